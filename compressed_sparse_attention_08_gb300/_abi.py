@@ -32,10 +32,14 @@ EXPORTED_SYMBOLS = (
     "dsv4_sparse_attn_decode", "dsv4_csa_decode_workspace_size", "dsv4_csa_decode",
     "dsv4_status_string", "dsv4_read_error_word", "dsv4_last_launch_count", "dsv4_max_comp",
     "dsv4_test_wait_fault", "dsv4_copy_async",
+    "dsv4_norm_rope_append", "dsv4_paged_attn_workspace_size", "dsv4_paged_attn",
+    "dsv4_paged_attn_weights_workspace_size", "dsv4_paged_attn_weights",
+    "dsv4_paged_evict_workspace_size", "dsv4_paged_evict",
 )
 
 P = ctypes.c_void_p
 I = ctypes.c_int
+L = ctypes.c_longlong
 
 
 class CompressArgs(ctypes.Structure):
@@ -72,6 +76,39 @@ class AttnArgs(ctypes.Structure):
                 ("win_rows", I), ("ratio", I), ("scale", ctypes.c_float), ("out_rope_pos", P),
                 ("out_rope_dim", I), ("out_rope_theta", ctypes.c_double), ("kv_fp8", I),
                 ("kv_nope", P), ("kv_scale", P), ("kv_rope", P), ("kv_rope_dim", I)]
+
+
+class NormRopeArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("k", P), ("v", P), ("q_out", P), ("k_pages", P), ("v_pages", P),
+                ("slots", P), ("pos", P), ("gamma_q", P), ("gamma_k", P),
+                ("q_stride", L), ("k_stride", L), ("v_stride", L), ("q_out_stride", L),
+                ("tokens", I), ("heads", I), ("kv_heads", I), ("dim", I), ("page_size", I),
+                ("num_pages", I), ("rope_dim", I), ("eps", ctypes.c_float),
+                ("rope_theta", ctypes.c_double)]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("k_pages", P), ("v_pages", P), ("block_table", P), ("cu_q", P),
+                ("kv_len", P), ("sink", P), ("out", P), ("lse", P), ("out_rope_pos", P),
+                ("q_stride", L), ("batch", I), ("total_q", I), ("heads", I), ("kv_heads", I),
+                ("dim", I), ("page_size", I), ("num_pages", I), ("max_pages", I), ("max_q", I),
+                ("window", I), ("scale", ctypes.c_float), ("out_rope_dim", I),
+                ("out_rope_theta", ctypes.c_double)]
+
+
+class PagedWeightsArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("lse", P), ("k_pages", P), ("block_table", P), ("cu_q", P),
+                ("kv_len", P), ("acc_in", P), ("acc", P), ("q_stride", L), ("batch", I),
+                ("total_q", I), ("heads", I), ("kv_heads", I), ("dim", I), ("page_size", I),
+                ("num_pages", I), ("max_pages", I), ("max_q", I), ("window", I), ("acc_rows", I),
+                ("scale", ctypes.c_float)]
+
+
+class PagedEvictArgs(ctypes.Structure):
+    _fields_ = [("k_pages", P), ("v_pages", P), ("block_table", P), ("out_table", P),
+                ("kv_len", P), ("kv_len_out", P), ("acc", P), ("acc_out", P), ("keep", P),
+                ("batch", I), ("kv_heads", I), ("dim", I), ("page_size", I), ("num_pages", I),
+                ("max_pages", I), ("out_pages", I), ("acc_rows", I), ("budget", I), ("recent", I)]
 
 
 class CsaArgs(ctypes.Structure):
@@ -132,6 +169,15 @@ def library():
         lib.dsv4_test_wait_fault.restype = I
         lib.dsv4_copy_async.argtypes = [P, P, ctypes.c_size_t, P]
         lib.dsv4_copy_async.restype = I
+        lib.dsv4_norm_rope_append.argtypes = [ctypes.POINTER(NormRopeArgs), P]
+        lib.dsv4_norm_rope_append.restype = I
+        for name, st in (("dsv4_paged_attn", PagedAttnArgs), ("dsv4_paged_attn_weights", PagedWeightsArgs),
+                         ("dsv4_paged_evict", PagedEvictArgs)):
+            size = getattr(lib, name + "_workspace_size")
+            size.argtypes = [ctypes.POINTER(st)]
+            size.restype = ctypes.c_size_t
+            getattr(lib, name).argtypes = [ctypes.POINTER(st), P, ctypes.c_size_t, P]
+            getattr(lib, name).restype = I
         for f in ("dsv4_compress", "dsv4_indexer_topk", "dsv4_index_score", "dsv4_topk", "dsv4_sparse_attn_decode",
                   "dsv4_csa_decode", "dsv4_read_error_word"):
             getattr(lib, f).restype = I
@@ -437,3 +483,213 @@ def dsv4_test_wait_fault(which, wait_limit_us=0):
     copy unissued so its bounded wait runs out after wait_limit_us microseconds (0: the
     default 2 s); DSV4_WAIT_FAULT_NONE restores normal launches."""
     _check(library().dsv4_test_wait_fault(int(which), int(wait_limit_us)), "dsv4_test_wait_fault")
+
+
+# ------------------------------------------------------------------ the paged cache
+# Prepared argument structs, as for dsv4_csa_decode: a serving loop builds them once over its
+# buffers and issues the same call every step. A struct holds its tensors, and the call runs on
+# the device they are on.
+def _heads_ptr(t, name, optional=False):
+    """bf16 [tokens, heads, dim] whose tokens may be further apart than their heads (a part of a
+    fused projection): (pointer, token stride in elements)."""
+    if t is None:
+        if optional:
+            return None, 0
+        raise ValueError(f"{name} is required")
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim]")
+    n, h, d = t.shape
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if n > 1 else h * d
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _held(args, *tensors):
+    """Keeps the tensors with the struct; all must be on one device."""
+    kept = [t for t in tensors if t is not None]
+    if any(t.device != kept[0].device for t in kept):
+        raise ValueError("all tensors must be on one device")
+    args.tensors = kept
+    args.device = kept[0].device.index
+    return args
+
+
+def _on_device(args, stream, call):
+    """call(stream) with the struct's device current, on its current stream unless one is given."""
+    import torch
+    if args.device == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(args.device):
+        return call(_stream(stream))
+
+
+def _ws_ptr(args, ws):
+    if ws.device.index != args.device:
+        raise ValueError("ws must be on the tensors' device")
+    return _ptr(ws, None, "ws")
+
+
+def norm_rope_args(q, q_out, pos, *, k=None, k_pages=None, v=None, v_pages=None, slots=None,
+                   gamma_q=None, gamma_k=None, rope_dim=64, eps=1e-6, rope_theta=10000.0):
+    """q bf16 [T, H, D] -> q_out (may be q); k bf16 [T, KV, D] -> row slots[t] (int64 [T], page *
+    page_size + slot, negative: not stored) of k_pages bf16 [pages, page_size, KV, D]; v likewise,
+    unchanged. pos int64 [T]. q or k may be None."""
+    bf16, f32, i32, i64 = _dt()
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q or k is required")
+    T, _, D = some.shape
+    H = 0 if q is None else q.shape[1]
+    KV = 0 if k is None else k.shape[1]
+    _shape(q, (T, H, D), "q")
+    _shape(q_out, (T, H, D), "q_out")
+    _shape(k, (T, KV, D), "k")
+    _shape(v, (T, KV, D), "v")
+    _shape(pos, (T,), "pos")
+    _shape(slots, (T,), "slots")
+    _shape(gamma_q, (D,), "gamma_q")
+    _shape(gamma_k, (D,), "gamma_k")
+    if k is not None:
+        if k_pages is None or slots is None:
+            raise ValueError("k needs k_pages and slots")
+        _shape(k_pages, (*k_pages.shape[:2], KV, D), "k_pages")
+        _shape(v_pages, k_pages.shape, "v_pages")
+    elif v is not None:
+        raise ValueError("v needs k")
+    qp, qs = _heads_ptr(q, "q", True)
+    op, os_ = _heads_ptr(q_out, "q_out", q is None)
+    kp, ks = _heads_ptr(k, "k", True)
+    vp, vs = _heads_ptr(v, "v", True)
+    a = NormRopeArgs(qp, kp, vp, op, _ptr(k_pages, bf16, "k_pages", True), _ptr(v_pages, bf16, "v_pages", True),
+                     _ptr(slots, i64, "slots", True), _ptr(pos, i64, "pos"), _ptr(gamma_q, f32, "gamma_q", True),
+                     _ptr(gamma_k, f32, "gamma_k", True), qs, ks, vs, os_, T, H, KV, D,
+                     0 if k_pages is None else k_pages.shape[1], 0 if k_pages is None else k_pages.shape[0],
+                     rope_dim, eps, rope_theta)
+    return _held(a, q, q_out, pos, k, k_pages, v, v_pages, slots, gamma_q, gamma_k)
+
+
+def dsv4_norm_rope_append(args, *, stream=None):
+    """RMSNorm per head, RoPE and the append to the pages, from a norm_rope_args struct."""
+    _check(_on_device(args, stream, lambda s: library().dsv4_norm_rope_append(ctypes.byref(args), s)),
+           "dsv4_norm_rope_append")
+
+
+def _paged(q, k_pages, block_table, cu_q, kv_len):
+    bf16, f32, i32, i64 = _dt()
+    qp, qs = _heads_ptr(q, "q")
+    T, H, D = q.shape
+    if k_pages.dim() != 4 or k_pages.shape[3] != D:
+        raise ValueError("k_pages must be [num_pages, page_size, kv_heads, dim]")
+    B = kv_len.shape[0]
+    _shape(block_table, (B, block_table.shape[-1]), "block_table")
+    _shape(cu_q, (B + 1,), "cu_q")
+    _shape(kv_len, (B,), "kv_len")
+    return qp, qs, T, H, D, B, k_pages.shape[0], k_pages.shape[1], k_pages.shape[2], block_table.shape[1]
+
+
+def paged_attn_args(q, out, k_pages, block_table, cu_q, kv_len, *, v_pages=None, max_q=None,
+                    sink=None, lse=None, window=0, scale=None, out_rope_pos=None, out_rope_dim=64,
+                    out_rope_theta=10000.0):
+    """q bf16 [T, H, D], out bf16 [T, H, D], k_pages (v_pages) bf16 [pages, page_size, KV, D],
+    block_table int32 [B, max_pages], cu_q int32 [B + 1], kv_len int32 [B], sink fp32 [H], lse
+    fp32 [T, H], out_rope_pos int64 [T]. max_q: the most tokens of one sequence (default T)."""
+    bf16, f32, i32, i64 = _dt()
+    qp, qs, T, H, D, B, n, ps, KV, mp = _paged(q, k_pages, block_table, cu_q, kv_len)
+    _shape(out, (T, H, D), "out")
+    _shape(v_pages, k_pages.shape, "v_pages")
+    _shape(sink, (H,), "sink")
+    _shape(lse, (T, H), "lse")
+    _shape(out_rope_pos, (T,), "out_rope_pos")
+    a = PagedAttnArgs(qp, _ptr(k_pages, bf16, "k_pages"), _ptr(v_pages, bf16, "v_pages", True),
+                      _ptr(block_table, i32, "block_table"), _ptr(cu_q, i32, "cu_q"), _ptr(kv_len, i32, "kv_len"),
+                      _ptr(sink, f32, "sink", True), _ptr(out, bf16, "out"), _ptr(lse, f32, "lse", True),
+                      _ptr(out_rope_pos, i64, "out_rope_pos", True), qs, B, T, H, KV, D, ps, n, mp,
+                      max(1, T if max_q is None else max_q), window, 1.0 / math.sqrt(D) if scale is None else scale,
+                      out_rope_dim if out_rope_pos is not None else 0, out_rope_theta)
+    return _held(a, q, out, k_pages, v_pages, block_table, cu_q, kv_len, sink, lse, out_rope_pos)
+
+
+def dsv4_paged_attn_workspace_size(args):
+    return int(library().dsv4_paged_attn_workspace_size(ctypes.byref(args)))
+
+
+def dsv4_paged_attn(args, ws, *, stream=None):
+    """Attention of the new tokens over their sequences' pages, from a paged_attn_args struct."""
+    _check(_on_device(args, stream, lambda s: library().dsv4_paged_attn(
+        ctypes.byref(args), _ws_ptr(args, ws), ws.numel() * ws.element_size(), s)), "dsv4_paged_attn")
+
+
+def paged_weights_args(q, lse, k_pages, block_table, cu_q, kv_len, acc, *, acc_in=None, max_q=None,
+                       window=0, scale=None):
+    """q, pages, tables and lengths as paged_attn_args, lse fp32 [T, H] as that call wrote it; acc
+    fp32 [B, rows] = acc_in (or 0) + the weights."""
+    bf16, f32, i32, i64 = _dt()
+    qp, qs, T, H, D, B, n, ps, KV, mp = _paged(q, k_pages, block_table, cu_q, kv_len)
+    _shape(lse, (T, H), "lse")
+    _shape(acc, (B, acc.shape[-1]), "acc")
+    _shape(acc_in, acc.shape, "acc_in")
+    a = PagedWeightsArgs(qp, _ptr(lse, f32, "lse"), _ptr(k_pages, bf16, "k_pages"), _ptr(block_table, i32, "block_table"),
+                         _ptr(cu_q, i32, "cu_q"), _ptr(kv_len, i32, "kv_len"), _ptr(acc_in, f32, "acc_in", True),
+                         _ptr(acc, f32, "acc"), qs, B, T, H, KV, D, ps, n, mp, max(1, T if max_q is None else max_q),
+                         window, acc.shape[1], 1.0 / math.sqrt(D) if scale is None else scale)
+    return _held(a, q, lse, k_pages, block_table, cu_q, kv_len, acc, acc_in)
+
+
+def dsv4_paged_attn_weights_workspace_size(args):
+    return int(library().dsv4_paged_attn_weights_workspace_size(ctypes.byref(args)))
+
+
+def dsv4_paged_attn_weights(args, ws, *, stream=None):
+    """The weight each cached row received, from a paged_weights_args struct."""
+    _check(_on_device(args, stream, lambda s: library().dsv4_paged_attn_weights(
+        ctypes.byref(args), _ws_ptr(args, ws), ws.numel() * ws.element_size(), s)), "dsv4_paged_attn_weights")
+
+
+def paged_evict_args(k_pages, block_table, kv_len, acc, keep, *, budget, recent, v_pages=None,
+                     out_table=None, kv_len_out=None, acc_out=None):
+    """Cut the caches to `budget` rows: acc fp32 [B, rows], keep int32 [B, budget]. out_table,
+    kv_len_out and acc_out default to block_table, kv_len and acc (in place)."""
+    bf16, f32, i32, i64 = _dt()
+    B = kv_len.shape[0]
+    out_table = block_table if out_table is None else out_table
+    kv_len_out = kv_len if kv_len_out is None else kv_len_out
+    acc_out = acc if acc_out is None else acc_out
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be [num_pages, page_size, kv_heads, dim]")
+    _shape(v_pages, k_pages.shape, "v_pages")
+    _shape(block_table, (B, block_table.shape[-1]), "block_table")
+    _shape(out_table, (B, out_table.shape[-1]), "out_table")
+    _shape(kv_len, (B,), "kv_len")
+    _shape(kv_len_out, (B,), "kv_len_out")
+    _shape(acc, (B, acc.shape[-1]), "acc")
+    _shape(acc_out, acc.shape, "acc_out")
+    _shape(keep, (B, budget), "keep")
+    n, ps, KV, D = k_pages.shape
+    a = PagedEvictArgs(_ptr(k_pages, bf16, "k_pages"), _ptr(v_pages, bf16, "v_pages", True),
+                       _ptr(block_table, i32, "block_table"), _ptr(out_table, i32, "out_table"),
+                       _ptr(kv_len, i32, "kv_len"), _ptr(kv_len_out, i32, "kv_len_out"), _ptr(acc, f32, "acc"),
+                       _ptr(acc_out, f32, "acc_out"), _ptr(keep, i32, "keep"), B, KV, D, ps, n, block_table.shape[1],
+                       out_table.shape[1], acc.shape[1], budget, recent)
+    return _held(a, k_pages, v_pages, block_table, out_table, kv_len, kv_len_out, acc, acc_out, keep)
+
+
+def dsv4_paged_evict_workspace_size(args):
+    return int(library().dsv4_paged_evict_workspace_size(ctypes.byref(args)))
+
+
+def dsv4_paged_evict(args, ws, *, stream=None):
+    """Eviction by accumulated weight, from a paged_evict_args struct."""
+    _check(_on_device(args, stream, lambda s: library().dsv4_paged_evict(
+        ctypes.byref(args), _ws_ptr(args, ws), ws.numel() * ws.element_size(), s)), "dsv4_paged_evict")

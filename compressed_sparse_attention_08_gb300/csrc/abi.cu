@@ -127,6 +127,85 @@ bool attn_ok(const dsv4_attn_args* a) {
     return true;
 }
 
+// What the paged calls share (include/dsv4.h, "Common rules").
+bool paged_ok(int batch, int kv_heads, int dim, int page_size, int num_pages, int max_pages) {
+    if (batch < 0 || batch > 2048 || kv_heads < 1 || kv_heads > 1024) return false;
+    if (dim != 128 && dim != 256 && dim != 512) return false;
+    if (page_size < 8 || page_size > 65536 || page_size % 8 != 0 || num_pages < 1 || max_pages < 1) return false;
+    const long long rows = static_cast<long long>(max_pages) * page_size;
+    return rows <= (1ll << 30) && rows * (batch > 0 ? batch : 1) < (1ll << 37);
+}
+bool heads_ok(int heads, int kv_heads) { return heads >= 1 && heads <= 1024 && kv_heads >= 1 && heads % kv_heads == 0; }
+bool stride_ok(long long stride, int heads, int dim) {
+    return stride >= static_cast<long long>(heads) * dim && stride % 8 == 0 && stride < (1ll << 38);
+}
+
+bool norm_rope_ok(const dsv4_norm_rope_args* a) {
+    if (!a || a->tokens < 0 || a->tokens > (1 << 24) || a->heads < 0 || a->heads > 1024 || a->kv_heads < 0 || a->kv_heads > 1024)
+        return false;
+    if (a->dim != 128 && a->dim != 256 && a->dim != 512) return false;
+    if (a->rope_dim < 0 || a->rope_dim > a->dim || a->rope_dim > 128 || (a->rope_dim & 1)) return false;
+    if (!(a->eps >= 0.f) || !std::isfinite(a->eps) || !std::isfinite(a->rope_theta) || a->rope_theta <= 0.0) return false;
+    if (!dev_ptr_ok(a->pos) || !opt_ptr_ok(a->gamma_q) || !opt_ptr_ok(a->gamma_k)) return false;
+    if (a->heads) {
+        if (!dev_ptr_ok(a->q) || !dev_ptr_ok(a->q_out) || !stride_ok(a->q_stride, a->heads, a->dim) ||
+            !stride_ok(a->q_out_stride, a->heads, a->dim))
+            return false;
+        if (a->q == a->q_out && a->q_stride != a->q_out_stride) return false;
+    } else if (a->q || a->q_out) {
+        return false;
+    }
+    if (a->kv_heads) {
+        if (!paged_ok(1, a->kv_heads, a->dim, a->page_size, a->num_pages, 1)) return false;
+        if (!dev_ptr_ok(a->k) || !dev_ptr_ok(a->k_pages) || !dev_ptr_ok(a->slots) || !stride_ok(a->k_stride, a->kv_heads, a->dim))
+            return false;
+        if ((a->v == nullptr) != (a->v_pages == nullptr)) return false;
+        if (a->v && (!dev_ptr_ok(a->v) || !dev_ptr_ok(a->v_pages) || !stride_ok(a->v_stride, a->kv_heads, a->dim))) return false;
+    } else if (a->k || a->v || a->k_pages || a->v_pages) {
+        return false;
+    }
+    return true;
+}
+
+bool paged_attn_ok(const dsv4_paged_attn_args* a) {
+    if (!a || !paged_ok(a->batch, a->kv_heads, a->dim, a->page_size, a->num_pages, a->max_pages)) return false;
+    if (!heads_ok(a->heads, a->kv_heads) || !stride_ok(a->q_stride, a->heads, a->dim)) return false;
+    if (a->total_q < 0 || a->total_q > (1 << 24) || a->max_q < 1 || a->window < 0 || !std::isfinite(a->scale)) return false;
+    if (!dev_ptr_ok(a->q) || !dev_ptr_ok(a->k_pages) || !opt_ptr_ok(a->v_pages) || !dev_ptr_ok(a->block_table) ||
+        !dev_ptr_ok(a->cu_q) || !dev_ptr_ok(a->kv_len) || !opt_ptr_ok(a->sink) || !dev_ptr_ok(a->out) || !opt_ptr_ok(a->lse) ||
+        !opt_ptr_ok(a->out_rope_pos))
+        return false;
+    if (a->v_pages && a->dim == 512) return false;       // (two tiles of 128 rows do not fit)
+    if (a->out_rope_pos &&
+        (a->out_rope_dim < 2 || (a->out_rope_dim & 1) || a->out_rope_dim > a->dim || a->out_rope_dim > 128 ||
+         !std::isfinite(a->out_rope_theta) || a->out_rope_theta <= 0.0))
+        return false;
+    return true;
+}
+
+bool paged_weights_ok(const dsv4_paged_weights_args* a) {
+    if (!a || !paged_ok(a->batch, a->kv_heads, a->dim, a->page_size, a->num_pages, a->max_pages)) return false;
+    if (!heads_ok(a->heads, a->kv_heads) || !stride_ok(a->q_stride, a->heads, a->dim)) return false;
+    if (a->total_q < 1 || a->total_q > (1 << 24) || a->max_q < 1 || a->window < 0 || a->acc_rows < 1 || !std::isfinite(a->scale))
+        return false;
+    return dev_ptr_ok(a->q) && dev_ptr_ok(a->lse) && dev_ptr_ok(a->k_pages) && dev_ptr_ok(a->block_table) &&
+           dev_ptr_ok(a->cu_q) && dev_ptr_ok(a->kv_len) && opt_ptr_ok(a->acc_in) && dev_ptr_ok(a->acc);
+}
+
+bool paged_evict_ok(const dsv4_paged_evict_args* a) {
+    if (!a || !paged_ok(a->batch, a->kv_heads, a->dim, a->page_size, a->num_pages, a->max_pages)) return false;
+    if (!dev_ptr_ok(a->k_pages) || !opt_ptr_ok(a->v_pages) || !dev_ptr_ok(a->block_table) || !dev_ptr_ok(a->out_table) ||
+        !dev_ptr_ok(a->kv_len) || !dev_ptr_ok(a->kv_len_out) || !dev_ptr_ok(a->acc) || !dev_ptr_ok(a->acc_out) ||
+        !dev_ptr_ok(a->keep))
+        return false;
+    if (a->out_pages < 1 || static_cast<long long>(a->out_pages) * a->page_size > (1ll << 30)) return false;
+    if (a->out_table == a->block_table && a->out_pages != a->max_pages) return false;
+    if (a->acc_rows < 1 || a->budget < 1 || a->budget > a->acc_rows ||
+        a->budget > static_cast<long long>(a->out_pages) * a->page_size || a->recent < 0 || a->recent > a->budget)
+        return false;
+    return true;
+}
+
 uint32_t* eword_of(void* ws) { return static_cast<uint32_t*>(ws); }
 uint8_t* body_of(void* ws) { return static_cast<uint8_t*>(ws) + kWsHeader; }
 
@@ -404,6 +483,50 @@ int dsv4_csa_decode(const dsv4_csa_args* a, void* ws, size_t ws_bytes, dsv4_stre
     if (a->index && (rc = launch_indexer(*a->index, body_of(ws), eword_of(ws), st, a->compress_keys)))
         return rc;
     return launch_attn(*a->attn, body_of(ws), eword_of(ws), st);
+}
+
+int dsv4_norm_rope_append(const dsv4_norm_rope_args* a, dsv4_stream_t stream) {
+    LaunchScope scope;
+    if (!norm_rope_ok(a)) return DSV4_ERR_INVALID_ARG;
+    if (int rc = device_check()) return rc;
+    return launch_norm_rope(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dsv4_paged_attn_workspace_size(const dsv4_paged_attn_args* a) {
+    if (!a) return 0;
+    return kWsHeader + paged_attn_ws_bytes(*a);
+}
+
+int dsv4_paged_attn(const dsv4_paged_attn_args* a, void* ws, size_t ws_bytes, dsv4_stream_t stream) {
+    LaunchScope scope;
+    if (!paged_attn_ok(a) || !dev_ptr_ok(ws) || ws_bytes < dsv4_paged_attn_workspace_size(a)) return DSV4_ERR_INVALID_ARG;
+    if (int rc = device_check()) return rc;
+    return launch_paged_attn(*a, body_of(ws), eword_of(ws), reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dsv4_paged_attn_weights_workspace_size(const dsv4_paged_weights_args* a) {
+    if (!a) return 0;
+    return kWsHeader + paged_weights_ws_bytes(*a);
+}
+
+int dsv4_paged_attn_weights(const dsv4_paged_weights_args* a, void* ws, size_t ws_bytes, dsv4_stream_t stream) {
+    LaunchScope scope;
+    if (!paged_weights_ok(a) || !dev_ptr_ok(ws) || ws_bytes < dsv4_paged_attn_weights_workspace_size(a))
+        return DSV4_ERR_INVALID_ARG;
+    if (int rc = device_check()) return rc;
+    return launch_paged_weights(*a, body_of(ws), eword_of(ws), reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dsv4_paged_evict_workspace_size(const dsv4_paged_evict_args* a) {
+    if (!a) return 0;
+    return kWsHeader + paged_evict_ws_bytes(*a);
+}
+
+int dsv4_paged_evict(const dsv4_paged_evict_args* a, void* ws, size_t ws_bytes, dsv4_stream_t stream) {
+    LaunchScope scope;
+    if (!paged_evict_ok(a) || !dev_ptr_ok(ws) || ws_bytes < dsv4_paged_evict_workspace_size(a)) return DSV4_ERR_INVALID_ARG;
+    if (int rc = device_check()) return rc;
+    return launch_paged_evict(*a, body_of(ws), eword_of(ws), reinterpret_cast<cudaStream_t>(stream));
 }
 
 int dsv4_read_error_word(void* ws, dsv4_stream_t stream, uint32_t* out) {

@@ -74,7 +74,29 @@ bool encode_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t
 bool encode_3d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t outer,
                     uint32_t box_inner, uint32_t box_mid);
 
+// `rank`-dimensional bf16 tensor: dims (innermost first), byte strides of dims 1 .. rank - 1, box;
+// 128-byte swizzle.
+bool encode_nd_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box);
+
 size_t attn_ws_bytes(const dsv4_attn_args& a);
 int launch_attn(const dsv4_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
+
+
+// The paged cache (norm_rope.cu, paged_attn.cu, paged_weights.cu, paged_evict.cu).
+int launch_norm_rope(const dsv4_norm_rope_args& a, cudaStream_t stream);
+size_t paged_attn_ws_bytes(const dsv4_paged_attn_args& a);
+int launch_paged_attn(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
+size_t paged_weights_ws_bytes(const dsv4_paged_weights_args& a);
+int launch_paged_weights(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
+size_t paged_evict_ws_bytes(const dsv4_paged_evict_args& a);
+int launch_paged_evict(const dsv4_paged_evict_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
+struct PagedGeom;
+PagedGeom paged_geom(const int32_t* table, const int32_t* cu_q, const int32_t* kv_len, int batch, int total_q, int max_pages,
+                     int page_size, int num_pages, int heads, int kv_heads, int window);
+// Queries [total_q, heads, D] with a token stride (elements), boxes of 64 channels x hb heads x tpt tokens.
+bool paged_query_map(CUtensorMap* map, const void* q, int D, int heads, int total_q, long long stride, int hb, int tpt);
+// A pool [num_pages, page_size, kv_heads, D], boxes of 64 channels x br slots of one head.
+bool paged_pool_map(CUtensorMap* map, const void* pages, int D, int kv_heads, int page_size, int num_pages, int br);
 
 }  // namespace dsv4

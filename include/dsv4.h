@@ -324,6 +324,146 @@ int dsv4_quantize_rows_fp8(const void* x, int rows, int dim, void* q, float* sca
                            dsv4_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * The paged cache. A pool of pages [num_pages, page_size, kv_heads, dim] holds the rows of many
+ * sequences; row r of sequence s is page block_table[s, r / page_size], slot r % page_size, and
+ * kv_len[s] rows are valid. Four calls work on it:
+ *   dsv4_norm_rope_append     norm and rotate a step's queries and keys, append the rows
+ *   dsv4_paged_attn           attention of each sequence's newest tokens over its rows
+ *   dsv4_paged_attn_weights   the attention weight each row received, accumulated
+ *   dsv4_paged_evict          keep the rows of most weight, compact the rest away
+ * Values are the key rows themselves (v_pages NULL: shared-KV attention, as in stage 4), or a
+ * second pool of the same shape. The pages have dense per-sequence buffers ([A]
+ * PERFORMANCE_AUDIT.md, the sliding-window cache; ARCHITECTURE_AND_MEMORY_AUDIT.md PART 2);
+ * the paged form and the eviction are this library's own.
+ *
+ * Common rules. dim: 128, 256 or 512 (512: shared-KV only). heads: a multiple of kv_heads,
+ * 1..1024. page_size: a multiple of 8, 8..65536. Sequence s owns the tokens
+ * cu_q[s] .. cu_q[s+1]-1 of the batch (cu_q[0] >= 0, not decreasing); tokens past cu_q[batch]
+ * are not read and their outputs are left as they were. These tokens are the newest of the
+ * cache: the t-th of n stands at row p = kv_len[s] - n + t and sees the rows
+ * [max(0, p + 1 - window), p + 1), or [0, p + 1) with window = 0. A token with p < 0 sees
+ * nothing. Only pages that hold a row some token of the call sees are read: entries of
+ * block_table past the rows in use, or before every window, may hold anything. Rows that some
+ * token sees must be finite for the others too (a tile's rows meet all its tokens in the tensor
+ * core, the ones a token does not see with weight 0); rows that none sees may hold anything.
+ * Counts outside their arrays are clamped and rows on a page outside the pool are hidden; both
+ * set DSV4_EWORD_BAD_INDEX. batch: 0..2048; batch * max_pages * page_size below 2^37.
+ */
+
+/* RMSNorm of queries and keys per head, RoPE in the same pass, rows appended to the pages.
+ *   y = x / sqrt(mean_d(x_d^2) + eps) * gamma
+ * then the last rope_dim channels rotated in interleaved pairs (2j, 2j+1) by the angle
+ * pos[t] * theta^(-2j/rope_dim), and one rounding to bf16: the arithmetic of stage 1, for every
+ * head of every token. k row (t, h) goes to slot slots[t] of the pool (flat: page * page_size +
+ * slot in the page), head h; v, when given, is stored beside it unchanged. A token whose slot
+ * is negative or past the pool stores nothing (its queries are still written).
+ * [B] single_shot_inference.py (unweighted RMSNorm of q per head, kv_norm, RoPE of the last 64
+ * dims, kv_cache.append_swa); [A] compressor_reduce.cu apply_kv_norm_kernel (eps 1e-6).
+ * Arithmetic: fp32 (angles in fp64). Two tokens must not name the same slot. */
+typedef struct dsv4_norm_rope_args {
+    const void* q;            /* bf16 [tokens, heads, dim], or NULL with heads = 0            */
+    const void* k;            /* bf16 [tokens, kv_heads, dim], or NULL with kv_heads = 0      */
+    const void* v;            /* bf16 [tokens, kv_heads, dim], or NULL                        */
+    void* q_out;              /* bf16 [tokens, heads, dim]; may be q itself (same stride)     */
+    void* k_pages;            /* bf16 [num_pages, page_size, kv_heads, dim]                   */
+    void* v_pages;            /* the same, or NULL when v is                                  */
+    const int64_t* slots;     /* int64 [tokens] (NULL when kv_heads = 0)                      */
+    const int64_t* pos;       /* int64 [tokens] positions                                     */
+    const float* gamma_q;     /* fp32 [dim], or NULL: 1                                       */
+    const float* gamma_k;     /* fp32 [dim], or NULL: 1                                       */
+    long long q_stride, k_stride, v_stride, q_out_stride; /* elements from token to token: multiples of 8, >= heads * dim */
+    int tokens, heads, kv_heads, dim, page_size, num_pages;
+    int rope_dim;             /* even, 0..min(dim, 128)                                       */
+    float eps;                /* 1e-6 on the pages                                            */
+    double rope_theta;        /* 10000 on the pages                                           */
+} dsv4_norm_rope_args;
+
+int dsv4_norm_rope_append(const dsv4_norm_rope_args* args, dsv4_stream_t stream);
+
+/* Attention over the paged rows, for single tokens and for chunks in one batch:
+ *   s_j = scale * q[t, h] . k_j,   m = max_j s_j (and sink[h]),
+ *   out[t, h] = sum_j e^(s_j - m) v_j / (sum_j e^(s_j - m) + e^(sink[h] - m))
+ *   lse[t, h] = m + log(that denominator)   (natural log, the sink included)
+ * Query head h reads KV head h / (heads / kv_heads). A token that sees nothing gets out 0 and
+ * lse = sink[h] (-inf without one). out_rope_*: the inverse RoPE of stage 4.
+ * Sources as stage 4. Arithmetic: bf16 tensor-core products, fp32 accumulation and softmax (P
+ * rounded to bf16 before the second product, the denominator from unrounded values), bf16
+ * output. The result does not depend on the order in which CTAs run. */
+typedef struct dsv4_paged_attn_args {
+    const void* q;            /* bf16 [total_q, heads, dim]                                   */
+    const void* k_pages;      /* bf16 [num_pages, page_size, kv_heads, dim]                   */
+    const void* v_pages;      /* the same, or NULL: the key rows are the values               */
+    const int32_t* block_table; /* int32 [batch, max_pages]                                   */
+    const int32_t* cu_q;      /* int32 [batch + 1]                                            */
+    const int32_t* kv_len;    /* int32 [batch], the new tokens' rows included                 */
+    const float* sink;        /* fp32 [heads], or NULL                                        */
+    void* out;                /* bf16 [total_q, heads, dim]                                   */
+    float* lse;               /* fp32 [total_q, heads], or NULL                               */
+    const int64_t* out_rope_pos; /* int64 [total_q], or NULL                                  */
+    long long q_stride;       /* elements from token to token: a multiple of 8, >= heads * dim */
+    int batch, total_q, heads, kv_heads, dim, page_size, num_pages, max_pages;
+    int max_q;                /* most tokens of one sequence (chooses the tile; not a limit)  */
+    int window;               /* 0: none                                                      */
+    float scale;              /* 1/sqrt(dim) on the pages                                     */
+    int out_rope_dim;         /* even, 2..min(dim, 128) when out_rope_pos is given            */
+    double out_rope_theta;
+} dsv4_paged_attn_args;
+
+/* The workspace does not depend on the lengths: the header and two partial tiles per SM. */
+size_t dsv4_paged_attn_workspace_size(const dsv4_paged_attn_args* args);
+int dsv4_paged_attn(const dsv4_paged_attn_args* args, void* ws, size_t ws_bytes, dsv4_stream_t stream);
+
+/* The attention weight that each cached row received from the call's tokens, over all heads:
+ *   acc[s, j] = acc_in[s, j] + sum_{t, h: t sees j} exp(scale * q[t, h] . k_j - lse[t, h])
+ * for j < kv_len[s] (the rest of acc is left as it was), with lse as dsv4_paged_attn wrote it
+ * for the same q, rows, window and scale. acc_in NULL: 0; acc_in may be acc. The order of the
+ * sum is fixed by the arguments and the lengths. fp32 accumulation. */
+typedef struct dsv4_paged_weights_args {
+    const void* q;            /* bf16 [total_q, heads, dim]                                   */
+    const float* lse;         /* fp32 [total_q, heads]                                        */
+    const void* k_pages;
+    const int32_t* block_table;
+    const int32_t* cu_q;
+    const int32_t* kv_len;
+    const float* acc_in;      /* fp32 [batch, acc_rows], or NULL                              */
+    float* acc;               /* fp32 [batch, acc_rows]                                       */
+    long long q_stride;
+    int batch, total_q, heads, kv_heads, dim, page_size, num_pages, max_pages;
+    int max_q, window;
+    int acc_rows;             /* rows past it are not accumulated (and flagged)               */
+    float scale;
+} dsv4_paged_weights_args;
+
+size_t dsv4_paged_attn_weights_workspace_size(const dsv4_paged_weights_args* args);
+int dsv4_paged_attn_weights(const dsv4_paged_weights_args* args, void* ws, size_t ws_bytes, dsv4_stream_t stream);
+
+/* Cuts each sequence's cache to `budget` rows. A sequence of n = kv_len[s] <= budget rows keeps
+ * them all. Otherwise it keeps its last `recent` rows and, of those before, the budget - recent
+ * with the greatest acc (equal: the lower row first; dsv4_topk's rule). The kept rows move, in
+ * their order, to rows 0 .. of the pages named by out_table: in place (out_table = block_table),
+ * or into pages that no sequence of the call reads. Their acc moves to acc_out likewise (acc_out
+ * may be acc), kv_len_out[s] gets their number (it may be kv_len), and keep[s, i] the former row
+ * of row i (-1 past the kept rows). acc_out past the kept rows is left as it was. acc must not
+ * be NaN. In place, sequences must not share pages. */
+typedef struct dsv4_paged_evict_args {
+    void* k_pages;            /* bf16 [num_pages, page_size, kv_heads, dim]                   */
+    void* v_pages;            /* the same, or NULL                                            */
+    const int32_t* block_table; /* int32 [batch, max_pages]                                   */
+    const int32_t* out_table; /* int32 [batch, out_pages]; may be block_table                 */
+    const int32_t* kv_len;    /* int32 [batch]                                                */
+    int32_t* kv_len_out;      /* int32 [batch]                                                */
+    const float* acc;         /* fp32 [batch, acc_rows]                                       */
+    float* acc_out;           /* fp32 [batch, acc_rows]                                       */
+    int32_t* keep;            /* int32 [batch, budget]                                        */
+    int batch, kv_heads, dim, page_size, num_pages, max_pages, out_pages;
+    int acc_rows;             /* >= max_pages * page_size is not required: longer sequences are clamped (and flagged) */
+    int budget, recent;       /* 1 <= budget <= acc_rows and out_pages * page_size; 0 <= recent <= budget */
+} dsv4_paged_evict_args;
+
+size_t dsv4_paged_evict_workspace_size(const dsv4_paged_evict_args* args);
+int dsv4_paged_evict(const dsv4_paged_evict_args* args, void* ws, size_t ws_bytes, dsv4_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * Test support: running the bounded-wait path on purpose. Not for a serving path.
  *
  * Every wait of a kernel on an asynchronous copy, or on another role of its CTA, is bounded

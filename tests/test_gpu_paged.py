@@ -1,0 +1,582 @@
+"""The paged cache on the GPU: norm + rotation + append, attention, weights and eviction against
+their plain 64-bit forms, at the sizes, layouts and masks where they can go wrong.
+
+Tolerances are derived in paged_reference.py from the roundings the kernels make (bf16 of P and
+of the output, fp32 sums); integers and moved rows are compared bit for bit.
+"""
+from __future__ import annotations
+
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+import paged_reference as ref  # noqa: E402
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from compressed_sparse_attention_08_gb300 import _build
+    _build.build()
+
+
+def lib():
+    import compressed_sparse_attention_08_gb300 as m
+    return m
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, *shape, std=1.0, dtype=BF):
+    return torch.empty(*shape, device="cuda", dtype=dtype).normal_(0.0, std, generator=g)
+
+
+def ws_for(n):
+    return torch.full((max(n, 256),), 0xA5, dtype=torch.uint8, device="cuda")     # (needs no initialisation)
+
+
+class Cache:
+    """Pages in random order; table entries past a sequence's rows (and before its window) name no page."""
+
+    def __init__(self, g, lens, page, kv, dim, shared=True, spare=3, first=None, poison=True):
+        self.lens, self.page = lens, page
+        per = max(1, max(-(-n // page) for n in lens))
+        need = [-(-n // page) for n in lens]
+        n = sum(need) + spare
+        self.k = normal(g, n, page, kv, dim)
+        self.v = None if shared else normal(g, n, page, kv, dim)
+        order = torch.randperm(n, generator=g, device="cuda").tolist()
+        table = [[(1 << 30) if i % 2 else -7 for i in range(per)] for _ in lens]
+        used = torch.zeros(n, page, dtype=torch.bool, device="cuda")
+        for s, c in enumerate(need):
+            for i in range(c):
+                table[s][i] = order.pop()
+            for j in range(lens[s]):
+                used[table[s][j // page], j % page] = True
+            if first is not None:                                     # rows before `first` are freed pages
+                for i in range(first[s] // page):
+                    used[table[s][i]] = False
+                    table[s][i] = -1
+        if poison:                                                    # what nobody sees holds NaN
+            for p in (self.k, self.v):
+                if p is not None:
+                    p[~used] = float("nan")
+        self.table = torch.tensor(table, dtype=torch.int32, device="cuda")
+        self.kv_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def cu_of(ns):
+    out = [0]
+    for n in ns:
+        out.append(out[-1] + n)
+    return out
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def attend(c, q, cu, *, window=0, sink=None, lse=True, max_q=None, pos=None, rope=64, scale=None, pad=0, ws=None):
+    m = lib()
+    T, H, D = q.shape
+    out = torch.full((T, H, D), 7.0, dtype=BF, device="cuda")
+    l = torch.full((T, H), 7.0, device="cuda") if lse else None
+    a = m.paged_attn_args(q, out, c.k, c.table, i32(cu), c.kv_len, v_pages=c.v, max_q=max_q, sink=sink, lse=l,
+                          window=window, scale=scale, out_rope_pos=pos, out_rope_dim=rope)
+    ws = ws_for(m.dsv4_paged_attn_workspace_size(a)) if ws is None else ws
+    m.dsv4_paged_attn(a, ws)
+    assert m.dsv4_read_error_word(ws) == (0, 0)
+    return out, l
+
+
+# ------------------------------------------------------------------ attention
+SHAPES = [(64, 1, 512, True), (8, 1, 128, True), (16, 1, 256, True), (32, 4, 128, False), (5, 5, 128, False),
+          (12, 2, 256, False), (1, 1, 512, True), (128, 1, 512, True), (96, 1, 128, True), (200, 1, 256, True)]
+
+
+@pytest.mark.parametrize("H, KV, D, shared", SHAPES)
+@pytest.mark.parametrize("page", [8, 48, 64])
+def test_single_tokens(H, KV, D, shared, page):
+    g = gen(H * 7 + D + page)
+    lens = [1, 2, 127, 128, 129, 300, 1000]
+    c = Cache(g, lens, page, KV, D, shared)
+    q = normal(g, len(lens), H, D, std=2.0)
+    sink = normal(g, H, dtype=torch.float32)
+    cu = cu_of([1] * len(lens))
+    out, lse = attend(c, q, cu, sink=sink, max_q=1)
+    ref.check_attention(out, lse, ref.attention(q, c.k, c.v, c.table, cu, lens, 1 / math.sqrt(D), sink=sink))
+
+
+@pytest.mark.parametrize("H, KV, D, shared", SHAPES)
+@pytest.mark.parametrize("window", [0, 1, 37, 128])
+def test_chunks(H, KV, D, shared, window):
+    """Ragged chunks: whole prompts, continued ones, empty ones, and chunks longer than a tile."""
+    g = gen(H + D + window)
+    ns, lens = [5, 0, 1, 33, 130, 7], [5, 0, 200, 140, 131, 500]
+    first = [max(0, L - n + 1 - window) if window else 0 for n, L in zip(ns, lens)]
+    c = Cache(g, lens, 16, KV, D, shared, first=first)
+    cu = cu_of(ns)
+    q = normal(g, cu[-1], H, D, std=2.0)
+    out, lse = attend(c, q, cu, window=window, max_q=max(ns))
+    ref.check_attention(out, lse, ref.attention(q, c.k, c.v, c.table, cu, lens, 1 / math.sqrt(D), window))
+
+
+@pytest.mark.parametrize("D, max_q", [(512, 1), (512, 100), (128, 1), (128, 100), (256, 100)])
+def test_tokens_that_see_nothing(D, max_q):
+    """More tokens than rows: the first tokens stand before the cache. Output 0, lse the sink's or -inf."""
+    g = gen(D)
+    ns, lens = [9, 4, 3], [4, 0, 3]
+    c = Cache(g, lens, 8, 1, D)
+    cu = cu_of(ns)
+    q = normal(g, cu[-1], 8, D)
+    for sink in (None, normal(g, 8, dtype=torch.float32)):
+        out, lse = attend(c, q, cu, sink=sink, max_q=max_q)
+        r = ref.attention(q, c.k, None, c.table, cu, lens, 1 / math.sqrt(D), sink=sink)
+        if sink is not None:
+            for t in list(range(5)) + list(range(9, 13)):
+                r[1][t] = sink.double()
+        ref.check_attention(out, lse, r)
+        assert (out[:5] == 0).all() and (out[9:13] == 0).all()
+
+
+@pytest.mark.parametrize("H, D, shared", [(64, 512, True), (64, 128, False), (16, 256, True)])
+def test_long_rows_are_split_and_merged(H, D, shared):
+    """One sequence over every CTA, and one long beside short ones; the peak of the scores late, early and flat."""
+    g = gen(3)
+    lens = [20000, 1, 700]
+    c = Cache(g, lens, 64, 1, D, shared)
+    q = normal(g, 3, H, D, std=2.0)
+    q[0, :8] *= 8                                   # scores of a few hundred: one row takes all
+    q[0, 8:16] = 0                                  # flat
+    pos = torch.tensor([5, 1 << 40, 123456], device="cuda")
+    cu = [0, 1, 2, 3]
+    sink = normal(g, H, dtype=torch.float32)
+    out, lse = attend(c, q, cu, sink=sink, max_q=1, pos=pos)
+    ref.check_attention(out, lse, ref.attention(q, c.k, c.v, c.table, cu, lens, 1 / math.sqrt(D), sink=sink, rope=64, pos=pos))
+
+
+@pytest.mark.parametrize("rope", [2, 64, 128])
+@pytest.mark.parametrize("H", [64, 6])
+def test_output_rotation(rope, H):
+    g = gen(rope)
+    ns, lens = [40, 1], [40, 333]
+    c = Cache(g, lens, 32, 1, 128)
+    cu = cu_of(ns)
+    q = normal(g, cu[-1], H, 128, std=2.0)
+    pos = torch.randint(0, 1 << 20, (cu[-1],), generator=g, device="cuda")
+    out, lse = attend(c, q, cu, pos=pos, rope=rope)
+    ref.check_attention(out, lse, ref.attention(q, c.k, None, c.table, cu, lens, 1 / math.sqrt(128), rope=rope, pos=pos))
+
+
+def test_scores_that_grow_along_the_cache():
+    """Each unit outruns the reference maximum of the one before: the running output is rescaled every time."""
+    g = gen(11)
+    lens, D, H = [1500], 512, 64
+    c = Cache(g, lens, 64, 1, D)
+    base = torch.ones(D, device="cuda")
+    for j in range(1500):
+        c.k[c.table[0, j // 64], j % 64, 0] = (c.k[c.table[0, j // 64], j % 64, 0].float() * 0.1 + base * (j / 100)).to(BF)
+    q = (normal(g, 3, H, D).float() * 0.1 + 1).to(BF)
+    q[:, H // 2:] *= -1
+    out, lse = attend(c, q, [0, 3])
+    ref.check_attention(out, lse, ref.attention(q, c.k, None, c.table, [0, 3], lens, 1 / math.sqrt(D)))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1.0])
+def test_scales(scale):
+    g = gen(5)
+    lens, ns = [300, 17], [2, 17]
+    c = Cache(g, lens, 16, 2, 128, False)
+    q = normal(g, 19, 8, 128)
+    out, lse = attend(c, q, cu_of(ns), scale=scale)
+    ref.check_attention(out, lse, ref.attention(q, c.k, c.v, c.table, cu_of(ns), lens, scale))
+
+
+def test_strided_queries_and_rows_behind_the_last_sequence():
+    """Queries inside a fused projection; tokens past cu_q[batch] keep what their outputs held."""
+    g = gen(6)
+    lens, ns = [100, 260], [3, 1]
+    c = Cache(g, lens, 16, 1, 128)
+    for extra in (0, 128, 8):
+        x = torch.empty(9, 8 * 128 + extra, device="cuda", dtype=BF).normal_(generator=g)
+        q = x[:, :1024].view(9, 8, 128) if extra == 0 else x.as_strided((9, 8, 128), (1024 + extra, 128, 1))
+        out, lse = attend(c, q, cu_of(ns), max_q=3)
+        r = ref.attention(q[:4], c.k, None, c.table, cu_of(ns), lens, 1 / math.sqrt(128))
+        ref.check_attention(out[:4], lse[:4], r)
+        assert (out[4:] == 7).all() and (lse[4:] == 7).all()
+
+
+def test_pages_past_32_bit_offsets():
+    """A pool of 6 GB: the rows of the sequence lie behind byte 2^32."""
+    m = lib()
+    g = gen(9)
+    n, page, D = 96000, 64, 512
+    k = torch.empty(n, page, 1, D, dtype=BF, device="cuda")
+    k[-40:] = normal(g, 40, page, 1, D)
+    table = torch.arange(n - 1, n - 33, -1, device="cuda").view(1, 32).to(torch.int32)
+    c = Cache.__new__(Cache)
+    c.k, c.v, c.table, c.kv_len, c.lens = k, None, table, i32([2000]), [2000]
+    q = normal(g, 1, 64, D, std=2.0)
+    out, lse = attend(c, q, [0, 1], max_q=1)
+    ref.check_attention(out, lse, ref.attention(q, k, None, table, [0, 1], [2000], 1 / math.sqrt(D)))
+    # and an append far behind
+    x = normal(g, 2, 1, D)
+    slots = torch.tensor([n * page - 1, (n - 36) * page + 5], device="cuda")
+    pos = torch.tensor([3, 4], device="cuda")
+    m.dsv4_norm_rope_append(m.norm_rope_args(None, None, pos, k=x, k_pages=k, slots=slots))
+    want = ref.norm_rope(x, None, pos, 64, 1e4, 1e-6)
+    got = k.view(-1, 1, D)[slots].double()
+    assert (got - want).abs().max() <= BF_TOL * want.abs().max()
+
+
+BF_TOL = 2.0 ** -8 + 2.0 ** -18
+
+
+def test_a_graph_serves_every_step_and_results_repeat():
+    """Captured once, replayed with other lengths and rows; two captures with a workspace of their own; bits repeat."""
+    m = lib()
+    g = gen(12)
+    lens = [900, 64, 5, 2000]
+    c = Cache(g, lens, 32, 1, 512, poison=False)
+    q = normal(g, 4, 64, 512, std=2.0)
+    out, lse = torch.empty_like(q), torch.empty(4, 64, device="cuda")
+    acc = torch.zeros(4, 2048, device="cuda")
+    cu = i32([0, 1, 2, 3, 4])
+    a = m.paged_attn_args(q, out, c.k, c.table, cu, c.kv_len, max_q=1, lse=lse)
+    b = m.paged_weights_args(q, lse, c.k, c.table, cu, c.kv_len, acc, max_q=1)
+    wa, wb = ws_for(m.dsv4_paged_attn_workspace_size(a)), ws_for(m.dsv4_paged_attn_weights_workspace_size(b))
+    m.dsv4_paged_attn(a, wa)
+    m.dsv4_paged_attn_weights(b, wb)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.dsv4_paged_attn(a, wa)
+        m.dsv4_paged_attn_weights(b, wb)
+    for step in range(3):
+        now = [max(1, n - 31 * step) for n in lens]
+        c.kv_len.copy_(i32(now))
+        q.copy_(normal(g, 4, 64, 512, std=2.0))
+        acc.fill_(-1)
+        graph.replay()
+        first = [x.clone() for x in (out, lse, acc)]
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip(first, (out, lse, acc)))
+        ref.check_attention(out, lse, ref.attention(q, c.k, None, c.table, [0, 1, 2, 3, 4], now, 1 / math.sqrt(512)))
+        want, tol = ref.weights(q, lse, c.k, c.table, [0, 1, 2, 3, 4], now, 1 / math.sqrt(512), torch.full_like(acc, -1), None)
+        assert ((acc.double() - want).abs() <= tol).all()
+        assert all((acc[s, n:] == -1).all() for s, n in enumerate(now))
+
+
+def test_streams():
+    """Two calls at once on two streams, each with its workspace, as one after the other."""
+    m = lib()
+    g = gen(13)
+    lens = [3000, 3000]
+    c = Cache(g, lens, 64, 1, 512)
+    qs = [normal(g, 2, 64, 512) for _ in range(2)]
+    want = [attend(c, q, [0, 1, 2], max_q=1) for q in qs]
+    side = [torch.cuda.Stream() for _ in qs]
+    calls = []
+    for q in qs:
+        out, lse = torch.empty_like(q), torch.empty(2, 64, device="cuda")
+        a = m.paged_attn_args(q, out, c.k, c.table, i32([0, 1, 2]), c.kv_len, max_q=1, lse=lse)
+        calls.append((a, ws_for(m.dsv4_paged_attn_workspace_size(a)), out, lse))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, (a, w, _, _) in zip(side, calls):
+            m.dsv4_paged_attn(a, w, stream=st)
+    torch.cuda.synchronize()
+    for (_, _, out, lse), (o, l) in zip(calls, want):
+        assert torch.equal(out, o) and torch.equal(lse, l)
+
+
+def test_many_sequences():
+    """More sequences than CTAs, some without tokens, some without rows."""
+    g = gen(14)
+    lens = [(i * 37) % 260 for i in range(1200)]
+    ns = [0 if i % 5 == 0 else (1 if lens[i] else 0) for i in range(1200)]
+    c = Cache(g, lens, 16, 1, 128, poison=False)
+    cu = cu_of(ns)
+    q = normal(g, cu[-1], 8, 128, std=2.0)
+    out, lse = attend(c, q, cu, max_q=1)
+    ref.check_attention(out, lse, ref.attention(q, c.k, None, c.table, cu, lens, 1 / math.sqrt(128)))
+
+
+def test_a_page_outside_the_pool_is_hidden_and_reported():
+    m = lib()
+    g = gen(15)
+    lens, D = [200, 90], 128
+    c = Cache(g, lens, 16, 1, D)
+    q = normal(g, 2, 8, D)
+    good = attend(c, q, [0, 1, 2], max_q=1)
+    c.table[0, 3] = 1 << 20
+    c.table[0, 12] = -1                              # the last page of the sequence
+    out, lse, acc = torch.empty_like(q), torch.empty(2, 8, device="cuda"), torch.zeros(2, 256, device="cuda")
+    a = m.paged_attn_args(q, out, c.k, c.table, i32([0, 1, 2]), c.kv_len, lse=lse)
+    ws = ws_for(m.dsv4_paged_attn_workspace_size(a))
+    m.dsv4_paged_attn(a, ws)
+    assert m.dsv4_read_error_word(ws) == (m.DSV4_ERR_BAD_INDEX, m.DSV4_EWORD_BAD_INDEX)
+    assert torch.equal(out[1], good[0][1])
+    seen = torch.tensor([j for j in range(200) if j // 16 not in (3, 12)], device="cuda")
+    k = c.k[c.table[0].long()[seen // 16], seen % 16, 0].double()
+    p = torch.softmax(q[0].double() @ k.t() / math.sqrt(D), -1)
+    assert ((out[0].double() - p @ k).abs() <= 2.0 ** -7 * (p @ k.abs()) + 2.0 ** -8 * (p @ k).abs()).all()
+    b = m.paged_weights_args(q, lse, c.k, c.table, i32([0, 1, 2]), c.kv_len, acc, max_q=1)
+    ws = ws_for(m.dsv4_paged_attn_weights_workspace_size(b))
+    m.dsv4_paged_attn_weights(b, ws)
+    assert m.dsv4_read_error_word(ws) == (m.DSV4_ERR_BAD_INDEX, m.DSV4_EWORD_BAD_INDEX)
+    assert (acc[0, 48:64] == 0).all() and (acc[0, 192:] == 0).all()
+    assert ((acc[0, seen].double() - p.sum(0)).abs() <= 1e-4 * p.sum(0)).all()
+    for bad_cu, bad_len in (([0, 1, 3], lens), ([0, 1, 2], [200, 99999]), ([0, 1, 2], [-4, 90]), ([0, 2, 1], lens)):
+        c.kv_len.copy_(i32(bad_len))
+        a = m.paged_attn_args(q, out, c.k, c.table, i32(bad_cu), c.kv_len, lse=lse)
+        ws = ws_for(m.dsv4_paged_attn_workspace_size(a))
+        m.dsv4_paged_attn(a, ws)
+        assert m.dsv4_read_error_word(ws)[1] == m.DSV4_EWORD_BAD_INDEX
+
+
+# ------------------------------------------------------------------ weights
+@pytest.mark.parametrize("H, KV, D, shared", SHAPES)
+@pytest.mark.parametrize("kind", ["step", "chunk", "window"])
+def test_weights(H, KV, D, shared, kind):
+    m = lib()
+    g = gen(H + D)
+    lens = [1, 127, 128, 1000, 333, 0]
+    ns = [1, 1, 1, 1, 1, 0] if kind == "step" else [1, 0, 130, 77, 333, 0]
+    window = 50 if kind == "window" else 0
+    first = [max(0, L - n + 1 - window) if window else 0 for n, L in zip(ns, lens)]
+    c = Cache(g, lens, 16, KV, D, True, first=first)
+    cu = cu_of(ns)
+    q = normal(g, cu[-1], H, D, std=2.0)
+    scale = 1 / math.sqrt(D)
+    lse = ref.attention(q, c.k, None, c.table, cu, lens, scale, window)[1].float()
+    acc_in = normal(g, len(lens), 1003, dtype=torch.float32).abs()
+    for src in (None, acc_in, "self"):
+        acc = acc_in.clone() if src == "self" else torch.full_like(acc_in, -3)
+        a_in = acc if src == "self" else src
+        a = m.paged_weights_args(q, lse, c.k, c.table, i32(cu), c.kv_len, acc, acc_in=a_in, max_q=max(ns), window=window)
+        want, tol = ref.weights(q, lse, c.k, c.table, cu, lens, scale, acc, None if src is None else acc_in, window)
+        ws = ws_for(m.dsv4_paged_attn_weights_workspace_size(a))
+        m.dsv4_paged_attn_weights(a, ws)
+        assert m.dsv4_read_error_word(ws) == (0, 0)
+        err = (acc.double() - want).abs()
+        assert (err <= tol).all(), (err / tol.clamp_min(1e-38)).max()
+
+
+def test_weights_with_more_tokens_than_announced():
+    """max_q chooses the tile and is not a limit: sequences with more tokens are answered alike."""
+    m = lib()
+    g = gen(21)
+    lens, ns = [400, 300], [9, 2]
+    c = Cache(g, lens, 16, 1, 512)
+    q = normal(g, 11, 64, 512, std=2.0)
+    lse = ref.attention(q, c.k, None, c.table, cu_of(ns), lens, 1 / math.sqrt(512))[1].float()
+    out, l = attend(c, q, cu_of(ns), max_q=1)
+    ref.check_attention(out, l, ref.attention(q, c.k, None, c.table, cu_of(ns), lens, 1 / math.sqrt(512)))
+    acc = torch.zeros(2, 400, device="cuda")
+    a = m.paged_weights_args(q, lse, c.k, c.table, i32(cu_of(ns)), c.kv_len, acc, max_q=1)
+    m.dsv4_paged_attn_weights(a, ws_for(m.dsv4_paged_attn_weights_workspace_size(a)))
+    want, tol = ref.weights(q, lse, c.k, c.table, cu_of(ns), lens, 1 / math.sqrt(512), torch.zeros_like(acc), None)
+    assert ((acc.double() - want).abs() <= tol).all()
+
+
+# ------------------------------------------------------------------ norm, rotation, append
+@pytest.mark.parametrize("tokens", [1, 3, 700])
+@pytest.mark.parametrize("H, KV, D, rope", [(64, 1, 512, 64), (5, 5, 128, 128), (32, 8, 256, 2), (0, 2, 128, 64), (7, 0, 256, 0)])
+@pytest.mark.parametrize("v", [False, True])
+def test_norm_rope_append(tokens, H, KV, D, rope, v):
+    m = lib()
+    g = gen(tokens + D)
+    v = v and KV > 0
+    x = normal(g, tokens, H + KV * (2 if v else 1) + 1, D, std=1.5)
+    x[0] *= 1e-3                                     # (eps counts)
+    q, k, vv = x[:, :H], x[:, H:H + KV], x[:, H + KV:H + 2 * KV]
+    gq, gk = normal(g, D, dtype=torch.float32), normal(g, D, dtype=torch.float32)
+    pos = torch.randint(0, 1 << 33, (tokens,), generator=g, device="cuda")
+    pos[0] = 0
+    n = tokens // 16 + 2
+    pages = normal(g, n, 16, max(KV, 1), D)
+    vpages = normal(g, n, 16, max(KV, 1), D)
+    before, vbefore = pages.clone(), vpages.clone()
+    slots = torch.randperm(n * 16, generator=g, device="cuda")[:tokens].contiguous()
+    slots[2::5] = -1
+    slots[3::50] = n * 16                            # past the pool: not stored
+    out = torch.empty(tokens, H, D, dtype=BF, device="cuda")
+    for gam in ((gq, gk), (None, None)):
+        pages.copy_(before)
+        vpages.copy_(vbefore)
+        a = m.norm_rope_args(q if H else None, out if H else None, pos, k=k if KV else None, k_pages=pages if KV else None,
+                             v=vv if v else None, v_pages=vpages if v else None, slots=slots if KV else None,
+                             gamma_q=gam[0], gamma_k=gam[1], rope_dim=rope, eps=1e-6)
+        m.dsv4_norm_rope_append(a)
+        kept = (slots >= 0) & (slots < n * 16)
+        pairs = [(out, q, gam[0])] if H else []
+        if KV:
+            pairs.append((pages.view(-1, KV, D)[slots[kept]], k, gam[1]))
+            left = torch.ones(n * 16, dtype=torch.bool, device="cuda")
+            left[slots[kept]] = False
+            assert torch.equal(pages.view(-1, KV, D)[left], before.view(-1, KV, D)[left])
+            if v:
+                assert torch.equal(vpages.view(-1, KV, D)[slots[kept]], vv[kept])
+                assert torch.equal(vpages.view(-1, KV, D)[left], vbefore.view(-1, KV, D)[left])
+            else:
+                assert torch.equal(vpages, vbefore)
+        for got, src, gamma in pairs:
+            want = ref.norm_rope(src, gamma, pos, rope, 1e4, 1e-6)
+            if got is not out:
+                want = want[kept]
+            # one rounding to bf16, and a few fp32 steps of the pair's length (sum of squares, root, product, turn)
+            size = want.abs()
+            if rope:
+                r = torch.hypot(want[..., -rope::2], want[..., -rope + 1::2]).repeat_interleave(2, -1)
+                size = torch.cat([size[..., :D - rope], r], -1)
+            tol = ref.BF16_STEP * want.abs() + (D / 8 + 16) * ref.F32_STEP * size + 1e-30
+            assert ((got.double() - want).abs() <= tol).all()
+
+
+def test_norm_rope_in_place():
+    m = lib()
+    g = gen(2)
+    x = normal(g, 50, 9, 256)
+    q = x[:, :8]
+    pos = torch.arange(50, device="cuda")
+    out = torch.empty(50, 8, 256, dtype=BF, device="cuda")
+    m.dsv4_norm_rope_append(m.norm_rope_args(q, out, pos))
+    keep = x[:, 8].clone()
+    m.dsv4_norm_rope_append(m.norm_rope_args(q, q, pos))
+    assert torch.equal(q, out) and torch.equal(x[:, 8], keep)
+
+
+# ------------------------------------------------------------------ eviction
+@pytest.mark.parametrize("KV, D, shared, page", [(1, 512, True, 64), (3, 128, False, 16), (8, 256, False, 48), (5, 128, True, 8)])
+@pytest.mark.parametrize("budget, recent", [(100, 20), (64, 64), (50, 0), (1, 0), (1, 1), (1500, 100)])
+@pytest.mark.parametrize("place", ["in", "out", "acc"])
+def test_evict(KV, D, shared, page, budget, recent, place):
+    """In place, into other pages, and into other pages with the weights in place."""
+    m = lib()
+    g = gen(budget + recent + D)
+    lens = [0, 1, budget, budget + 1, 1700, 333, max(1, budget - 1)]
+    c = Cache(g, lens, page, KV, D, shared, spare=2 + len(lens) * (-(-budget // page)), poison=False)
+    rows = 1801
+    acc = normal(g, len(lens), rows, dtype=torch.float32).abs()
+    acc = (acc * 4).round() / 4                      # ties, zeros
+    kept = ref.evict(lens, acc, budget, recent)
+    if place == "in":
+        per = -(-max(budget, max(lens)) // page)
+        table = torch.full((len(lens), per), 0, dtype=torch.int32, device="cuda")
+        table[:, :c.table.shape[1]] = c.table
+        c.table = table                              # (room for the budget; unused entries are not read)
+        out_table, acc_out, len_out = table, acc, c.kv_len
+    else:
+        free = sorted(set(range(c.k.shape[0])) - set(c.table.flatten().tolist()))
+        per = -(-budget // page)
+        out_table = i32(free[:len(lens) * per]).view(len(lens), per)
+        acc_out = acc if place == "acc" else torch.full_like(acc, -9)
+        len_out = torch.full_like(c.kv_len, -9)
+    old_acc, old_out = acc.clone(), acc_out.clone()
+    want_k = c.k.clone()
+    want_v = None if c.v is None else c.v.clone()
+    for s, r in enumerate(kept):
+        if not r:
+            continue
+        src = torch.tensor(r, device="cuda")
+        dst = torch.arange(len(r), device="cuda")
+        a, b = c.table[s].long()[src // page], out_table[s].long()[dst // page]
+        want_k[b, dst % page] = c.k[a, src % page]
+        if c.v is not None:
+            want_v[b, dst % page] = c.v[a, src % page]
+    keep = torch.full((len(lens), budget), -5, dtype=torch.int32, device="cuda")
+    a = m.paged_evict_args(c.k, c.table, c.kv_len, acc, keep, budget=budget, recent=recent, v_pages=c.v, out_table=out_table,
+                           kv_len_out=len_out, acc_out=acc_out)
+    ws = ws_for(m.dsv4_paged_evict_workspace_size(a))
+    m.dsv4_paged_evict(a, ws)
+    assert m.dsv4_read_error_word(ws) == (0, 0)
+    assert len_out.tolist() == [len(r) for r in kept]
+    assert torch.equal(c.k, want_k) and (c.v is None or torch.equal(c.v, want_v))
+    for s, r in enumerate(kept):
+        assert keep[s].tolist() == r + [-1] * (budget - len(r))
+        assert torch.equal(acc_out[s, :len(r)], old_acc[s, r])
+        assert torch.equal(acc_out[s, len(r):], old_out[s, len(r):])
+
+
+def test_evict_long_rows():
+    """Rows long enough for the top-k over a cluster, in place, twice (the second cuts further)."""
+    m = lib()
+    g = gen(31)
+    lens, page, D = [70000, 40000, 100], 64, 128
+    c = Cache(g, lens, page, 1, D, poison=False)
+    acc = (normal(g, 3, 70016, dtype=torch.float32).abs() * 64).round() / 64
+    for budget, recent in ((33000, 128), (1000, 0)):
+        now = c.kv_len.tolist()
+        kept = ref.evict(now, acc.cpu(), budget, recent)
+        flat = [c.k[c.table[s].long()[torch.tensor(r, device="cuda") // page], torch.tensor(r, device="cuda") % page] for s, r in enumerate(kept)]
+        old = acc.clone()
+        keep = torch.empty(3, budget, dtype=torch.int32, device="cuda")
+        a = m.paged_evict_args(c.k, c.table, c.kv_len, acc, keep, budget=budget, recent=recent)
+        ws = ws_for(m.dsv4_paged_evict_workspace_size(a))
+        m.dsv4_paged_evict(a, ws)
+        assert m.dsv4_read_error_word(ws) == (0, 0)
+        assert c.kv_len.tolist() == [len(r) for r in kept]
+        for s, r in enumerate(kept):
+            assert keep[s, :len(r)].tolist() == r and (keep[s, len(r):] == -1).all()
+            assert torch.equal(ref.rows_of(c.k, c.table, s, len(r)), flat[s])
+            assert torch.equal(acc[s, :len(r)], old[s, r])
+
+
+# ------------------------------------------------------------------ together
+def test_a_serving_loop():
+    """Prefill in chunks, then single tokens, with weights accumulated and the cache cut to a budget on the way: every
+    step's attention equals the plain form over the rows that are then in the cache."""
+    m = lib()
+    g = gen(41)
+    B, H, D, page, budget, recent = 3, 16, 128, 16, 200, 32
+    pool = 80
+    k = torch.full((pool, page, 1, D), float("nan"), dtype=BF, device="cuda")
+    table = torch.randperm(pool, generator=g, device="cuda")[:B * 26].view(B, 26).to(torch.int32).contiguous()
+    lens, seen = [0] * B, [0] * B
+    acc = torch.zeros(B, 26 * page, device="cuda")
+    keep = torch.empty(B, budget, dtype=torch.int32, device="cuda")
+    kv_len = torch.zeros(B, dtype=torch.int32, device="cuda")
+    e = m.paged_evict_args(k, table, kv_len, acc, keep, budget=budget, recent=recent)
+    we = ws_for(m.dsv4_paged_evict_workspace_size(e))
+    for step in range(9):
+        ns = [150, 7, 0] if step == 0 else [90, 140, 129] if step == 1 else [1, 1, 1]
+        T = sum(ns)
+        x = normal(g, T, H + 1, D, std=1.5)
+        at = [(s, t) for s in range(B) for t in range(ns[s])]
+        pos = torch.tensor([seen[s] + t for s, t in at], device="cuda")
+        row = [lens[s] + t for s, t in at]
+        slots = torch.tensor([int(table[s, r // page]) * page + r % page for (s, _), r in zip(at, row)], device="cuda")
+        q = torch.empty(T, H, D, dtype=BF, device="cuda")
+        m.dsv4_norm_rope_append(m.norm_rope_args(x[:, :H], q, pos, k=x[:, H:], k_pages=k, slots=slots))
+        lens = [a + b for a, b in zip(lens, ns)]
+        seen = [a + b for a, b in zip(seen, ns)]
+        kv_len.copy_(i32(lens))
+        cu = cu_of(ns)
+        out, lse = torch.empty_like(q), torch.empty(T, H, device="cuda")
+        a = m.paged_attn_args(q, out, k, table, i32(cu), kv_len, lse=lse, max_q=max(ns), out_rope_pos=pos)
+        b = m.paged_weights_args(q, lse, k, table, i32(cu), kv_len, acc, acc_in=acc, max_q=max(ns))
+        old = acc.clone()
+        m.dsv4_paged_attn(a, ws_for(m.dsv4_paged_attn_workspace_size(a)))
+        m.dsv4_paged_attn_weights(b, ws_for(m.dsv4_paged_attn_weights_workspace_size(b)))
+        ref.check_attention(out, lse, ref.attention(q, k, None, table, cu, lens, 1 / math.sqrt(D), rope=64, pos=pos))
+        want, tol = ref.weights(q, lse, k, table, cu, lens, 1 / math.sqrt(D), old, old)
+        assert ((acc.double() - want).abs() <= tol).all()
+        if step % 2:
+            kept = ref.evict(lens, acc.cpu(), budget, recent)
+            m.dsv4_paged_evict(e, we)
+            lens = kv_len.tolist()
+            assert lens == [len(r) for r in kept]
+            assert all(keep[s, :len(r)].tolist() == r for s, r in enumerate(kept))
+            for s in range(B):
+                acc[s, lens[s]:] = 0                 # rows that the next tokens fill start without weight
