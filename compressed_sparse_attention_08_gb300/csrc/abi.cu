@@ -127,13 +127,17 @@ bool attn_ok(const dsv4_attn_args* a) {
     return true;
 }
 
+// Lengths, tables and per-row numbers are read one by one: their own alignment is enough.
+bool num_ok(const void* p, size_t size) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % size == 0; }
+bool opt_num_ok(const void* p, size_t size) { return p == nullptr || num_ok(p, size); }
+
 // What the paged calls share (include/dsv4.h, "Common rules").
 bool paged_ok(int batch, int kv_heads, int dim, int page_size, int num_pages, int max_pages) {
     if (batch < 0 || batch > 2048 || kv_heads < 1 || kv_heads > 1024) return false;
     if (dim != 128 && dim != 256 && dim != 512) return false;
     if (page_size < 8 || page_size > 65536 || page_size % 8 != 0 || num_pages < 1 || max_pages < 1) return false;
     const long long rows = static_cast<long long>(max_pages) * page_size;
-    return rows <= (1ll << 30) && rows * (batch > 0 ? batch : 1) < (1ll << 37);
+    return rows <= (1ll << 29) && rows * (batch > 0 ? batch : 1) < (1ll << 37);
 }
 bool heads_ok(int heads, int kv_heads) { return heads >= 1 && heads <= 1024 && kv_heads >= 1 && heads % kv_heads == 0; }
 bool stride_ok(long long stride, int heads, int dim) {
@@ -146,7 +150,7 @@ bool norm_rope_ok(const dsv4_norm_rope_args* a) {
     if (a->dim != 128 && a->dim != 256 && a->dim != 512) return false;
     if (a->rope_dim < 0 || a->rope_dim > a->dim || a->rope_dim > 128 || (a->rope_dim & 1)) return false;
     if (!(a->eps >= 0.f) || !std::isfinite(a->eps) || !std::isfinite(a->rope_theta) || a->rope_theta <= 0.0) return false;
-    if (!dev_ptr_ok(a->pos) || !opt_ptr_ok(a->gamma_q) || !opt_ptr_ok(a->gamma_k)) return false;
+    if (!num_ok(a->pos, 8) || !opt_ptr_ok(a->gamma_q) || !opt_ptr_ok(a->gamma_k)) return false;
     if (a->heads) {
         if (!dev_ptr_ok(a->q) || !dev_ptr_ok(a->q_out) || !stride_ok(a->q_stride, a->heads, a->dim) ||
             !stride_ok(a->q_out_stride, a->heads, a->dim))
@@ -157,7 +161,7 @@ bool norm_rope_ok(const dsv4_norm_rope_args* a) {
     }
     if (a->kv_heads) {
         if (!paged_ok(1, a->kv_heads, a->dim, a->page_size, a->num_pages, 1)) return false;
-        if (!dev_ptr_ok(a->k) || !dev_ptr_ok(a->k_pages) || !dev_ptr_ok(a->slots) || !stride_ok(a->k_stride, a->kv_heads, a->dim))
+        if (!dev_ptr_ok(a->k) || !dev_ptr_ok(a->k_pages) || !num_ok(a->slots, 8) || !stride_ok(a->k_stride, a->kv_heads, a->dim))
             return false;
         if ((a->v == nullptr) != (a->v_pages == nullptr)) return false;
         if (a->v && (!dev_ptr_ok(a->v) || !dev_ptr_ok(a->v_pages) || !stride_ok(a->v_stride, a->kv_heads, a->dim))) return false;
@@ -171,9 +175,9 @@ bool paged_attn_ok(const dsv4_paged_attn_args* a) {
     if (!a || !paged_ok(a->batch, a->kv_heads, a->dim, a->page_size, a->num_pages, a->max_pages)) return false;
     if (!heads_ok(a->heads, a->kv_heads) || !stride_ok(a->q_stride, a->heads, a->dim)) return false;
     if (a->total_q < 0 || a->total_q > (1 << 24) || a->max_q < 1 || a->window < 0 || !std::isfinite(a->scale)) return false;
-    if (!dev_ptr_ok(a->q) || !dev_ptr_ok(a->k_pages) || !opt_ptr_ok(a->v_pages) || !dev_ptr_ok(a->block_table) ||
-        !dev_ptr_ok(a->cu_q) || !dev_ptr_ok(a->kv_len) || !opt_ptr_ok(a->sink) || !dev_ptr_ok(a->out) || !opt_ptr_ok(a->lse) ||
-        !opt_ptr_ok(a->out_rope_pos))
+    if (!dev_ptr_ok(a->q) || !dev_ptr_ok(a->k_pages) || !opt_ptr_ok(a->v_pages) || !num_ok(a->block_table, 4) ||
+        !num_ok(a->cu_q, 4) || !num_ok(a->kv_len, 4) || !opt_num_ok(a->sink, 4) || !dev_ptr_ok(a->out) || !opt_num_ok(a->lse, 4) ||
+        !opt_num_ok(a->out_rope_pos, 8))
         return false;
     if (a->v_pages && a->dim == 512) return false;       // (two tiles of 128 rows do not fit)
     if (a->out_rope_pos &&
@@ -188,17 +192,17 @@ bool paged_weights_ok(const dsv4_paged_weights_args* a) {
     if (!heads_ok(a->heads, a->kv_heads) || !stride_ok(a->q_stride, a->heads, a->dim)) return false;
     if (a->total_q < 1 || a->total_q > (1 << 24) || a->max_q < 1 || a->window < 0 || a->acc_rows < 1 || !std::isfinite(a->scale))
         return false;
-    return dev_ptr_ok(a->q) && dev_ptr_ok(a->lse) && dev_ptr_ok(a->k_pages) && dev_ptr_ok(a->block_table) &&
-           dev_ptr_ok(a->cu_q) && dev_ptr_ok(a->kv_len) && opt_ptr_ok(a->acc_in) && dev_ptr_ok(a->acc);
+    return dev_ptr_ok(a->q) && num_ok(a->lse, 4) && dev_ptr_ok(a->k_pages) && num_ok(a->block_table, 4) &&
+           num_ok(a->cu_q, 4) && num_ok(a->kv_len, 4) && opt_num_ok(a->acc_in, 4) && num_ok(a->acc, 4);
 }
 
 bool paged_evict_ok(const dsv4_paged_evict_args* a) {
     if (!a || !paged_ok(a->batch, a->kv_heads, a->dim, a->page_size, a->num_pages, a->max_pages)) return false;
-    if (!dev_ptr_ok(a->k_pages) || !opt_ptr_ok(a->v_pages) || !dev_ptr_ok(a->block_table) || !dev_ptr_ok(a->out_table) ||
-        !dev_ptr_ok(a->kv_len) || !dev_ptr_ok(a->kv_len_out) || !dev_ptr_ok(a->acc) || !dev_ptr_ok(a->acc_out) ||
-        !dev_ptr_ok(a->keep))
+    if (!dev_ptr_ok(a->k_pages) || !opt_ptr_ok(a->v_pages) || !num_ok(a->block_table, 4) || !num_ok(a->out_table, 4) ||
+        !num_ok(a->kv_len, 4) || !num_ok(a->kv_len_out, 4) || !num_ok(a->acc, 4) || !num_ok(a->acc_out, 4) ||
+        !num_ok(a->keep, 4))
         return false;
-    if (a->out_pages < 1 || static_cast<long long>(a->out_pages) * a->page_size > (1ll << 30)) return false;
+    if (a->out_pages < 1 || static_cast<long long>(a->out_pages) * a->page_size > (1ll << 29)) return false;
     if (a->out_table == a->block_table && a->out_pages != a->max_pages) return false;
     if (a->acc_rows < 1 || a->budget < 1 || a->budget > a->acc_rows ||
         a->budget > static_cast<long long>(a->out_pages) * a->page_size || a->recent < 0 || a->recent > a->budget)

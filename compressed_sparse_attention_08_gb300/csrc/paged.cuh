@@ -29,6 +29,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The inverse of float_to_key.
+__device__ __forceinline__ float key_to_float(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
 struct PagedGeom {
     const int32_t* table;                // [batch, max_pages]
     const int32_t* cu_q;                 // [batch + 1]
@@ -80,8 +85,7 @@ __device__ __forceinline__ int paged_tile_units(const PagedGeom& g, const PagedS
 }
 
 struct PagedSched {
-    long long total, u0;                 // all units, this CTA's first
-    long long left;                      // this CTA's units
+    long long total, u0, u1;             // all units, this CTA's [u0, u1)
     int ge;                              // CTAs with work
     int s, tt, inner, k;                 // where u0 lies
 };
@@ -129,21 +133,26 @@ __device__ void paged_schedule(const PagedGeom& g, int min_units, long long* pre
             if (s < g.batch) pref[s] = v;
             carry = __shfl_sync(~0u, v, 31);
         }
-        __syncwarp();
-        const long long T = carry;
+    }
+    __syncthreads();
+    // Warp 0 finds where this CTA's units start, warp 1 where the next CTA's do. A border inside a
+    // tile of few units moves to the tile's end: a partial result costs about a unit's time on
+    // either side, more than the imbalance of at most 2 units or 1/32 of a share.
+    if (warp < 2) {
+        const long long T = g.batch > 0 ? pref[g.batch - 1] : 0;
         const long long most = T / min_units < 1 ? 1 : T / min_units;
         const int ge = most < static_cast<long long>(gridDim.x) ? static_cast<int>(most) : static_cast<int>(gridDim.x);
-        const int c = blockIdx.x;
-        const long long u0 = T * c / ge, u1 = T * (c + 1) / ge;
+        const long long share32 = T / ge / 32, small = share32 > 2 ? share32 : 2;
+        const int c = static_cast<int>(blockIdx.x) + warp;
+        long long u = c < ge ? T * c / ge : T;
         int s = 0, tt = 0, inner = 0, k = 0;
-        const bool work = c < ge && u1 > u0;
-        if (work) {
-            int hi = g.batch - 1;                    // the first sequence whose units end past u0
+        if (u < T && u > 0) {
+            int hi = g.batch - 1;                    // the first sequence whose units end past u
             while (s < hi) {
                 const int mid = (s + hi) >> 1;
-                if (pref[mid] > u0) hi = mid; else s = mid + 1;
+                if (pref[mid] > u) hi = mid; else s = mid + 1;
             }
-            const long long rem = u0 - (s ? pref[s - 1] : 0);
+            const long long rem = u - (s ? pref[s - 1] : 0);
             bool dummy = false;
             const PagedSeq q = paged_seq(g, s, dummy);
             const int nt = (q.n + g.tpt - 1) / g.tpt;
@@ -164,12 +173,29 @@ __device__ void paged_schedule(const PagedGeom& g, int min_units, long long* pre
                     tt = tt0 + f;
                     inner = static_cast<int>(r / nf);
                     k = static_cast<int>(r - static_cast<long long>(inner) * nf);
+                    if (k > 0 && nf <= small) {      // the next tile's start
+                        u += nf - k;
+                        k = 0;
+                        if (++inner == mult) { inner = 0; ++tt; }
+                    }
                     break;
                 }
                 cum += __shfl_sync(~0u, v, 31);
             }
         }
-        if (lane == 0) *out = PagedSched{T, u0, work ? u1 - u0 : 0, ge, s, tt, inner, k};
+        if (lane == 0) {
+            if (warp == 0) {
+                out->total = T;
+                out->u0 = u;
+                out->ge = ge;
+                out->s = s;
+                out->tt = tt;
+                out->inner = inner;
+                out->k = k;
+            } else {
+                out->u1 = u;
+            }
+        }
     }
     __syncthreads();
 }
@@ -191,7 +217,7 @@ struct PagedWalk {
     long long left;
     PagedSeq q;
     __device__ PagedWalk(const PagedGeom& geom, const PagedSched& sc)
-        : g(geom), s(sc.s), tt(sc.tt), inner(sc.inner), k(sc.k), left(sc.left), q{0, 0, 0} {
+        : g(geom), s(sc.s), tt(sc.tt), inner(sc.inner), k(sc.k), left(sc.u1 - sc.u0), q{0, 0, 0} {
         bool dummy = false;
         if (left > 0) q = paged_seq(g, s, dummy);
     }

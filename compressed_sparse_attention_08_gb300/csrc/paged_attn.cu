@@ -50,23 +50,41 @@ struct PagedAttnParams {
     double or_freq[64];                  // theta^(-2j / out_rope_dim)
 };
 
+constexpr int kMaxSlots = 8;
+template <int N>
+struct PagedCtl {
+    uint64_t q_full, q_empty, full[kMaxSlots], empty[kMaxSlots], s_full[2], s_empty[2], p_full, pv_done;
+    PagedSched sched;
+    alignas(16) float m[N];              // reference maxima (base-2 units)
+    alignas(16) float f[N];              // factors
+    uint32_t top[N];                     // a unit's maxima as ordered keys
+    unsigned char tok[N];                // the column's token in the tile, 255: no query
+    unsigned bad[8];
+    uint32_t tmem, err;
+    int abort;
+};
+
+// Shared memory: a ring of slots of 128 cache rows x 128 channels (two swizzled boxes), in which
+// a K or V tile takes MT slots, so a slot is loaded again as soon as the product that reads it is
+// done; the queries; P; and a few arrays per query.
 template <int D_, int N_>
 struct PCfg {
     static constexpr int D = D_, N = N_;
-    static constexpr int NB = D / 64, MT = D / 128;
+    static constexpr int MT = D / 128;
     static constexpr int BOX = kPT * 128;                    // 128 rows x 64 channels
-    static constexpr int TILE = NB * BOX;
-    static constexpr int QBOX = N * 128, QB = NB * QBOX;
+    static constexpr int SLOT = 2 * BOX;
+    static constexpr int QBOX = N * 128, QB = 2 * MT * QBOX;
     static constexpr int PB = kPT * N * 2;
-    // after the tiles: reference maxima, factors, row bounds and offsets per query, partial sums
-    static constexpr int SMALL = N * 4 * 5 + 4 * N * 4 + 512;
-    static constexpr int ST_FIT = (232448 - 1024 - QB - PB - SMALL) / TILE;
-    static constexpr int ST = ST_FIT > 6 ? 6 : ST_FIT;       // ring of K / V tiles
-    static constexpr int OFF_Q = ST * TILE, OFF_P = OFF_Q + QB, OFF_S = OFF_P + PB;
-    static constexpr int SMEM = OFF_S + SMALL + 1024;
+    static constexpr int ST_FIT = (232448 - sizeof(PagedCtl<N>) - QB - PB) / SLOT;
+    static constexpr int ST = ST_FIT > 8 ? 8 : ST_FIT;
+    // With two tiles in the ring the scores of a unit are formed before the product with V of the
+    // unit before; otherwise (512 channels) the two take turns and share the ring slot by slot.
+    static constexpr bool AHEAD = ST >= 2 * MT;
+    static constexpr int OFF_Q = ST * SLOT, OFF_P = OFF_Q + QB, OFF_C = OFF_P + PB;
+    static constexpr int SMEM = OFF_C + sizeof(PagedCtl<N>);
     static constexpr int TCOLS = 512;
     static constexpr int OCOL = 2 * N;
-    static_assert(ST >= 1 && OCOL + MT * N <= 512, "one tile, and both accumulators in TMEM");
+    static_assert(ST >= MT && SMEM <= 232448 && OCOL + MT * N <= 512, "one tile, and both accumulators in TMEM");
 };
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -112,48 +130,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedAttnParams p) {
     using C = PCfg<D, N>;
-    constexpr int ST = C::ST, NB = C::NB, MT = C::MT, NC = N / 64;   // NC: 32-column pieces per thread
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint32_t tmem_slot, s_err;
-    __shared__ volatile int abort_flag;
-    __shared__ PagedSched sched;
-    __shared__ uint64_t q_full, q_empty, full[ST], empty[ST], s_full[2], s_empty[2], p_full, pv_done;
-    __shared__ unsigned s_bad[8];
-    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int ST = C::ST, MT = C::MT, NC = N / 64;               // NC: 32-column pieces per thread
+    extern __shared__ __align__(1024) uint8_t sm[];
+    PagedCtl<N>& ctl = *reinterpret_cast<PagedCtl<N>*>(sm + C::OFF_C);
     uint8_t* sQ = sm + C::OFF_Q;
     uint8_t* sP = sm + C::OFF_P;
-    float* s_m = reinterpret_cast<float*>(sm + C::OFF_S);            // reference maxima (base-2 units)
-    float* s_f = s_m + N;
-    int* s_hi = reinterpret_cast<int*>(s_f + N);
-    int* s_lo = s_hi + N;
-    int* s_off = s_lo + N;                                           // output offsets, -1: no query
-    float* red = reinterpret_cast<float*>(s_off + N);                // [4][N]
+    float *s_m = ctl.m, *s_f = ctl.f;
+    volatile int* abort_flag = &ctl.abort;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        mbar_init(&q_full, 1);
-        mbar_init(&q_empty, 1);
-        for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], kSoftWarps); }
-        mbar_init(&p_full, kSoftWarps);
-        mbar_init(&pv_done, 1);
-        abort_flag = 0;
-        s_err = 0;
+        mbar_init(&ctl.q_full, 1);
+        mbar_init(&ctl.q_empty, 1);
+        for (int i = 0; i < ST; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&ctl.s_full[i], 1); mbar_init(&ctl.s_empty[i], kSoftWarps); }
+        mbar_init(&ctl.p_full, kSoftWarps);
+        mbar_init(&ctl.pv_done, 1);
+        ctl.abort = 0;
+        ctl.err = 0;
         fence_barrier_init();
     }
-    if (warp == 2) tmem_alloc(&tmem_slot, C::TCOLS);
+    if (tid < N) ctl.top[tid] = 0;
+    if (warp == 2) tmem_alloc(&ctl.tmem, C::TCOLS);
     pdl_trigger();
     pdl_wait();                          // lengths, queries and rows may come from the kernel before
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    paged_schedule<kThreads>(p.g, p.min_units, reinterpret_cast<long long*>(sm), &sched, &s_err);
+    const uint32_t tmem = ctl.tmem;
+    paged_schedule<kThreads>(p.g, p.min_units, reinterpret_cast<long long*>(sm), &ctl.sched, &ctl.err);
     // the schedule's scratch is overwritten by TMA next
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
 
     const PagedGeom& g = p.g;
+    const PagedSched& sched = ctl.sched;
     const int parts = p.shared ? 1 : 2;
     if (warp == 0) {
         // ---------------------------------------------------------------- pages and queries
@@ -164,97 +175,104 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         uint32_t ring = 0, u = 0, seg = 0;
         bool dead = false;
         while (!dead && w.next(sg)) {
-            if (seg > 0) dead = __any_sync(~0u, !mbar_wait(&q_empty, (seg - 1) & 1, &abort_flag, p.wait_ns));
+            if (seg > 0) dead = __any_sync(~0u, !mbar_wait(&ctl.q_empty, (seg - 1) & 1, abort_flag, p.wait_ns));
             if (dead) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&q_full, qbytes);
-                for (int b = 0; b < NB; ++b)
-                    tma_load_3d(sQ + b * C::QBOX, &qmap, &q_full, b * 64, sg.head0, sg.tok0);
+                mbar_arrive_expect_tx(&ctl.q_full, qbytes);
+                for (int b = 0; b < 2 * MT; ++b)
+                    tma_load_3d(sQ + b * C::QBOX, &qmap, &ctl.q_full, b * 64, sg.head0, sg.tok0);
             }
             ++seg;
             for (int k = sg.kb; k < sg.ke && !dead; ++k, ++u) {
                 const PagedTile t = paged_tile_boxes(g, sg, sg.row0 + k * kPT, lane);
-                for (int part = 0; part < parts; ++part, ++ring) {
-                    const uint32_t slot = ring % ST;
-                    if (ring >= ST) dead = !mbar_wait(&empty[slot], (ring / ST - 1) & 1, &abort_flag, p.wait_ns);
-                    dead = __any_sync(~0u, dead);
-                    if (dead) break;
-                    if (lane == 0) {
-                        if (part == 0) {
-                            s_bad[u & 7] = t.bad;
-                            if (t.bad) atomicOr(&s_err, DSV4_EWORD_BAD_INDEX);
-                        }
-                        const uint32_t bytes = static_cast<uint32_t>(__popc(t.ok)) * g.br * D * 2;
-                        if (bytes) mbar_arrive_expect_tx(&full[slot], bytes);
-                        else mbar_arrive(&full[slot]);
-                    }
-                    __syncwarp();
+                const uint32_t bytes = static_cast<uint32_t>(__popc(t.ok)) * g.br * 256;
+                for (int part = 0; part < parts && !dead; ++part) {
                     const CUtensorMap* map = part ? &vmap : &kmap;
-                    uint8_t* tile = sm + slot * C::TILE;
-                    for (int i0 = 0; i0 < NB * pieces; i0 += 32) {
-                        const int i = i0 + lane, piece = i & (pieces - 1), box = i / pieces;
+                    for (int mt = 0; mt < MT; ++mt, ++ring) {
+                        const uint32_t slot = ring % ST;
+                        if (ring >= ST)
+                            dead = __any_sync(~0u, !mbar_wait(&ctl.empty[slot], (ring / ST - 1) & 1, abort_flag, p.wait_ns));
+                        if (dead) break;
+                        if (lane == 0) {
+                            if (part == 0 && mt == 0) {
+                                ctl.bad[u & 7] = t.bad;
+                                if (t.bad) atomicOr(&ctl.err, DSV4_EWORD_BAD_INDEX);
+                            }
+                            if (bytes) mbar_arrive_expect_tx(&ctl.full[slot], bytes);
+                            else mbar_arrive(&ctl.full[slot]);
+                        }
+                        __syncwarp();
+                        uint8_t* dst = sm + slot * C::SLOT;
+                        // lane: piece lane % pieces of box lane / pieces (two boxes, at most 16 pieces)
+                        const int piece = lane & (pieces - 1), box = lane / pieces;
                         const int page = __shfl_sync(~0u, t.page, piece), at = __shfl_sync(~0u, t.slot, piece);
-                        if (box < NB && ((t.ok >> piece) & 1))
-                            tma_load_4d(tile + box * C::BOX + piece * g.br * 128, map, &full[slot], box * 64, sg.kvh, at,
-                                        page);
+                        if (box < 2 && ((t.ok >> piece) & 1))
+                            tma_load_4d(dst + box * C::BOX + piece * g.br * 128, map, &ctl.full[slot], mt * 128 + box * 64,
+                                        sg.kvh, at, page);
                     }
                 }
             }
         }
         if (dead && lane == 0) {                     // a wait ran out: let the copies in flight land
-            atomicOr(&s_err, DSV4_EWORD_TIMEOUT);
-            abort_flag = 1;
-            if (seg) mbar_wait(&q_full, (seg - 1) & 1, nullptr, 100000000ull);
+            atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
+            ctl.abort = 1;
+            if (seg) mbar_wait(&ctl.q_full, (seg - 1) & 1, nullptr, 100000000ull);
             for (uint32_t r = ring > ST ? ring - ST : 0; r < ring; ++r)
-                mbar_wait(&full[r % ST], (r / ST) & 1, nullptr, 100000000ull);
+                mbar_wait(&ctl.full[r % ST], (r / ST) & 1, nullptr, 100000000ull);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- tensor core
         if (lane == 0) {
             PagedWalk w(g, sched);
             PagedSeg sg;
-            uint32_t u = 0, seg = 0;
+            uint32_t u = 0, seg = 0, pend_u = 0;
             bool dead = false, pend = false, pend_first = false;
-            uint32_t pend_u = 0;
             const uint32_t q0 = smem_u32(sQ), p0 = smem_u32(sP), t0 = smem_u32(sm);
             const uint32_t idS = idesc_bf16_f32(kPT, N), idO = idS | (1u << 15) | (1u << 16);
-            auto pv = [&](uint32_t x, bool first) {
-                const uint32_t r = p.shared ? x : 2 * x + 1, slot = r % ST;
-                if (!mbar_wait(&p_full, x & 1, &abort_flag, p.wait_ns)) return false;
-                if (!p.shared && !mbar_wait(&full[slot], (r / ST) & 1, &abort_flag, p.wait_ns)) return false;
-                tc_fence_after();
-                const uint32_t a0 = t0 + slot * C::TILE;
+            auto pv = [&](uint32_t x, bool first) {  // O^T += V^T P^T of unit x
+                if (!mbar_wait(&ctl.p_full, x & 1, abort_flag, p.wait_ns)) return false;
+                uint32_t r = (p.shared ? x : 2 * x + 1) * MT;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
+                for (int mt = 0; mt < MT; ++mt, ++r) {
+                    const uint32_t slot = r % ST;
+                    if (!p.shared && !mbar_wait(&ctl.full[slot], (r / ST) & 1, abort_flag, p.wait_ns)) return false;
+                    tc_fence_after();
+                    const uint32_t a0 = t0 + slot * C::SLOT;
 #pragma unroll
                     for (int kk = 0; kk < kPT / 16; ++kk)
                         umma_bf16(tmem + static_cast<uint32_t>(C::OCOL + mt * N),
-                                  sdesc_mnmajor_sw128(a0 + 2 * mt * C::BOX + kk * 2048, C::BOX, 1024u),
+                                  sdesc_mnmajor_sw128(a0 + kk * 2048, C::BOX, 1024u),
                                   sdesc_mnmajor_sw128(p0 + kk * 2048, kPT * 128, 1024u), idO,
                                   (!first || kk > 0) ? 1u : 0u);
+                    umma_commit(&ctl.empty[slot]);
                 }
-                umma_commit(&empty[slot]);
-                umma_commit(&pv_done);
+                umma_commit(&ctl.pv_done);
                 return true;
             };
             while (!dead && w.next(sg)) {
-                dead = !mbar_wait(&q_full, seg & 1, &abort_flag, p.wait_ns);
+                dead = !mbar_wait(&ctl.q_full, seg & 1, abort_flag, p.wait_ns);
                 ++seg;
                 for (int k = sg.kb; k < sg.ke && !dead; ++k, ++u) {
-                    const uint32_t r = p.shared ? u : 2 * u, slot = r % ST;
-                    dead = !mbar_wait(&full[slot], (r / ST) & 1, &abort_flag, p.wait_ns);
-                    if (!dead && u >= 2) dead = !mbar_wait(&s_empty[u & 1], ((u >> 1) - 1) & 1, &abort_flag, p.wait_ns);
-                    if (dead) break;
-                    tc_fence_after();
-                    const uint32_t a0 = t0 + slot * C::TILE;
+                    if (u >= 2) dead = !mbar_wait(&ctl.s_empty[u & 1], ((u >> 1) - 1) & 1, abort_flag, p.wait_ns);
+                    uint32_t r = (p.shared ? u : 2 * u) * MT;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        umma_bf16(tmem + (u & 1) * N, sdesc_kmajor_sw128(a0 + (kk >> 2) * C::BOX + (kk & 3) * 32),
-                                  sdesc_kmajor_sw128(q0 + (kk >> 2) * C::QBOX + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
-                    umma_commit(&s_full[u & 1]);
-                    if (!p.shared) umma_commit(&empty[slot]);
-                    if (k + 1 == sg.ke) umma_commit(&q_empty);
-                    if constexpr (ST == 1) {
+                    for (int mt = 0; mt < MT; ++mt, ++r) {       // S^T = K Q^T
+                        const uint32_t slot = r % ST;
+                        dead = dead || !mbar_wait(&ctl.full[slot], (r / ST) & 1, abort_flag, p.wait_ns);
+                        if (dead) break;
+                        tc_fence_after();
+                        const uint32_t a0 = t0 + slot * C::SLOT, b0 = q0 + mt * 2 * C::QBOX;
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_bf16(tmem + (u & 1) * N, sdesc_kmajor_sw128(a0 + (kk >> 2) * C::BOX + (kk & 3) * 32),
+                                      sdesc_kmajor_sw128(b0 + (kk >> 2) * C::QBOX + (kk & 3) * 32), idS,
+                                      (mt > 0 || kk > 0) ? 1u : 0u);
+                        if (!p.shared) umma_commit(&ctl.empty[slot]);
+                    }
+                    if (dead) break;
+                    umma_commit(&ctl.s_full[u & 1]);
+                    if (k + 1 == sg.ke) umma_commit(&ctl.q_empty);
+                    if constexpr (!C::AHEAD) {
                         dead = !pv(u, k == sg.kb);
                     } else {
                         if (pend) dead = !pv(pend_u, pend_first);
@@ -266,8 +284,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             }
             if (!dead && pend) dead = !pv(pend_u, pend_first);
             if (dead) {
-                atomicOr(&s_err, DSV4_EWORD_TIMEOUT);
-                abort_flag = 1;
+                atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
+                ctl.abort = 1;
             }
         }
     } else if (warp >= 4) {
@@ -288,70 +306,79 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 const int t = c / g.hb, h = c - t * g.hb;
                 const bool ok = t < sg.tn && h < sg.hv;
                 s_m[c] = ok ? -INFINITY : INFINITY;                  // (a column without a query gets P = 0)
-                s_hi[c] = ok ? paged_hi(sg.q, sg.t0 + t) : 0;
-                s_lo[c] = ok ? paged_lo(g, sg.q, sg.t0 + t) : 0;
-                s_off[c] = ok ? (t * g.H + h) * D : -1;
+                ctl.tok[c] = ok ? t : 255;
             }
             soft_sync();
+            const int base = sg.q.L - sg.q.n + sg.t0;                // row of the tile's first token
             float lacc[NC][32];                                      // this row's P per query, summed over the units
 #pragma unroll
             for (int n = 0; n < NC; ++n)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) lacc[n][i] = 0.f;
             for (int k = sg.kb; k < sg.ke; ++k, ++u) {
-                if (!dead) dead = !mbar_wait(&s_full[u & 1], (u >> 1) & 1, &abort_flag, p.wait_ns);
+                if (!dead) dead = !mbar_wait(&ctl.s_full[u & 1], (u >> 1) & 1, abort_flag, p.wait_ns);
                 tc_fence_after();
                 const int j0 = sg.row0 + k * kPT, j = j0 + row;
-                const unsigned bad = *reinterpret_cast<volatile unsigned*>(&s_bad[u & 7]);
+                const unsigned bad = *reinterpret_cast<volatile unsigned*>(&ctl.bad[u & 7]);
                 const bool edge = j0 < sg.lo_u || j0 + kPT > sg.hi_u || bad != 0;
                 const bool masked = edge || j0 < sg.lo_max || j0 + kPT > sg.hi_min;
                 const bool live = j >= sg.lo_u && j < sg.hi_u && !((bad >> (row / g.br)) & 1);
+                // this row is seen by the tile's tokens t_lo .. t_hi
+                const int t_lo = live ? j - base : 1, t_hi = live ? (g.window > 0 ? j - base + g.window - 1 : 254) : 0;
                 const uint32_t scol = lane_base + (u & 1) * N + c0;
-                float x[NC][32];
-                float mx = -INFINITY;
+                float x[32];
                 auto load_scores = [&](int n) {
                     uint32_t r[32];
                     DSV4_TMEM_LD_32x32b_X32(scol + n * 32, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[n][i] = __uint_as_float(r[i]);
+                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
                 };
                 auto hide = [&](int n) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int c = c0 + n * 32 + i;
-                        if (!live || j >= s_hi[c] || j < s_lo[c]) x[n][i] = -INFINITY;
+                    for (int i = 0; i < 32; i += 4) {
+                        const uint32_t t4 = *reinterpret_cast<const uint32_t*>(ctl.tok + c0 + n * 32 + i);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const int t = (t4 >> (8 * b)) & 255;
+                            if (t < t_lo || t > t_hi) x[i + b] = -INFINITY;
+                        }
                     }
                 };
-#pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    load_scores(n);
+                auto less_ref = [&](int n) {         // base-2 scores relative to the references
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
                         const float4 m4 = *reinterpret_cast<const float4*>(s_m + c0 + n * 32 + i);
-                        x[n][i] = fmaf(x[n][i], p.scale2, -m4.x);
-                        x[n][i + 1] = fmaf(x[n][i + 1], p.scale2, -m4.y);
-                        x[n][i + 2] = fmaf(x[n][i + 2], p.scale2, -m4.z);
-                        x[n][i + 3] = fmaf(x[n][i + 3], p.scale2, -m4.w);
+                        x[i] = fmaf(x[i], p.scale2, -m4.x);
+                        x[i + 1] = fmaf(x[i + 1], p.scale2, -m4.y);
+                        x[i + 2] = fmaf(x[i + 2], p.scale2, -m4.z);
+                        x[i + 3] = fmaf(x[i + 3], p.scale2, -m4.w);
                     }
                     if (masked) hide(n);
+                };
+                float mx = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, x[n][i]);
+                for (int n = 0; n < NC; ++n) {
+                    load_scores(n);
+                    less_ref(n);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, x[i]);
                 }
-                bool rescale = false;
+                bool rescale = false, again = NC > 1;
                 if (soft_sync_or(mx > kSpan)) {
                     // some score outruns its reference: reduce the unit's maxima and move the references
+                    again = true;
 #pragma unroll
                     for (int n = 0; n < NC; ++n) {
                         load_scores(n);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[n][i] *= p.scale2;
+                        for (int i = 0; i < 32; ++i) x[i] *= p.scale2;
                         if (masked) hide(n);
-                        red[q4 * N + c0 + n * 32 + lane] = lanes_reduce<true>(x[n], lane);
+                        atomicMax(&ctl.top[c0 + n * 32 + lane], float_to_key(lanes_reduce<true>(x, lane)));
                     }
                     soft_sync();
                     for (int c = st; c < N; c += kSoftThreads) {
-                        const float cm = fmaxf(fmaxf(red[c], red[N + c]), fmaxf(red[2 * N + c], red[3 * N + c]));
+                        const float cm = key_to_float(ctl.top[c]);
                         const float mo = s_m[c];
                         float f = 1.f;
                         if (cm > mo) {
@@ -360,25 +387,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                             rescale = k > sg.kb;
                         }
                         s_f[c] = f;
+                        ctl.top[c] = 0;
                     }
                     rescale = soft_sync_or(rescale);
+                    if (rescale) {
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) {
-                        load_scores(n);
+                        for (int n = 0; n < NC; ++n)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int c = c0 + n * 32 + i;
-                            lacc[n][i] *= s_f[c];
-                            x[n][i] = fmaf(x[n][i], p.scale2, -s_m[c]);
-                        }
-                        if (masked) hide(n);
+                            for (int i = 0; i < 32; ++i) lacc[n][i] *= s_f[c0 + n * 32 + i];
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[u & 1]);
                 // P and O are free once the product before is done
-                if (!dead && u > 0) dead = !mbar_wait(&pv_done, (u - 1) & 1, &abort_flag, p.wait_ns);
+                if (!dead && u > 0) dead = !mbar_wait(&ctl.pv_done, (u - 1) & 1, abort_flag, p.wait_ns);
                 if (rescale) {
                     tc_fence_after();
 #pragma unroll
@@ -396,14 +416,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     }
                     DSV4_TMEM_WAIT_ST();
                 }
-                // P = 2^(s - m) in bf16 (rounded: the tensor core takes bf16; the sum below stays
-                // in fp32), the MN-major operand: row j's 64 queries are one 128-byte line
+                // P = 2^(s - m) in bf16 (rounded: the tensor core takes bf16; the sum stays in fp32),
+                // the MN-major operand: row j's 64 queries are one 128-byte line
 #pragma unroll
                 for (int n = 0; n < NC; ++n) {
+                    if (again) {
+                        load_scores(n);
+                        less_ref(n);
+                    }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        x[n][i] = ex2(x[n][i]);
-                        lacc[n][i] += x[n][i];
+                        x[i] = ex2(x[i]);
+                        lacc[n][i] += x[i];
                     }
                     const int cb = c0 + n * 32;                      // first column of the piece
                     uint8_t* prow = sP + (cb >> 6) * (kPT * 128) + (row >> 3) * 1024 + (row & 7) * 128;
@@ -411,31 +435,36 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     for (int i = 0; i < 4; ++i) {
                         const int c16 = ((cb & 63) >> 3) + i;
                         *reinterpret_cast<uint4*>(prow + ((c16 ^ (row & 7)) << 4)) =
-                            make_uint4(pack2(x[n][8 * i], x[n][8 * i + 1]), pack2(x[n][8 * i + 2], x[n][8 * i + 3]),
-                                       pack2(x[n][8 * i + 4], x[n][8 * i + 5]), pack2(x[n][8 * i + 6], x[n][8 * i + 7]));
+                            make_uint4(pack2(x[8 * i], x[8 * i + 1]), pack2(x[8 * i + 2], x[8 * i + 3]),
+                                       pack2(x[8 * i + 4], x[8 * i + 5]), pack2(x[8 * i + 6], x[8 * i + 7]));
                     }
                 }
                 if (edge) {
                     // rows of the tile that nobody may see (past the cache, before the window, of a
                     // page that was not loaded) hold anything: as V they must not meet P = 0
-                    const uint32_t r = p.shared ? u : 2 * u + 1, slot = r % ST;
-                    if (!p.shared && !dead) dead = !mbar_wait(&full[slot], (r / ST) & 1, &abort_flag, p.wait_ns);
-                    if (!live) {
-                        for (int b = half * (NB / 2); b < (half + 1) * (NB / 2); ++b) {
-                            uint4* z = reinterpret_cast<uint4*>(sm + slot * C::TILE + b * C::BOX + row * 128);
+                    uint32_t r = (p.shared ? u : 2 * u + 1) * MT;
+                    for (int mt = 0; mt < MT; ++mt, ++r) {
+                        const uint32_t slot = r % ST;
+                        if (!p.shared && !dead) dead = !mbar_wait(&ctl.full[slot], (r / ST) & 1, abort_flag, p.wait_ns);
+                        if (!live) {
+                            uint4* z = reinterpret_cast<uint4*>(sm + slot * C::SLOT + half * C::BOX + row * 128);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) z[i] = make_uint4(0, 0, 0, 0);
+                            for (int i = 0; i < 8; ++i) z[i ^ (row & 7)] = make_uint4(0, 0, 0, 0);   // (eight rows, eight banks)
                         }
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full);
+                if (lane == 0) {
+                    mbar_arrive(&ctl.s_empty[u & 1]);
+                    mbar_arrive(&ctl.p_full);
+                }
             }
             // ---------------------------------------------------------------- the tile's results
-            if (!dead) dead = !mbar_wait(&pv_done, (u - 1) & 1, &abort_flag, p.wait_ns);
+            if (!dead) dead = !mbar_wait(&ctl.pv_done, (u - 1) & 1, abort_flag, p.wait_ns);
             tc_fence_after();
+            float* red = reinterpret_cast<float*>(sP);               // [4][N] (P is read)
 #pragma unroll
             for (int n = 0; n < NC; ++n) red[q4 * N + c0 + n * 32 + lane] = lanes_reduce<false>(lacc[n], lane);
             soft_sync();
@@ -444,11 +473,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             for (int c = st; c < N; c += kSoftThreads) {
                 const float l = (red[c] + red[N + c]) + (red[2 * N + c] + red[3 * N + c]);
                 const float m = s_m[c];
-                const int off = s_off[c];
+                const int t = ctl.tok[c];
                 if (whole) {
                     float f = 0.f;
-                    if (off >= 0) {
-                        const int t = c / g.hb, h = sg.head0 + c - t * g.hb;
+                    if (t != 255) {
+                        const int h = sg.head0 + c - t * g.hb;
                         const float snk = p.sink ? p.sink[h] * kLog2e : -INFINITY;
                         const float M = fmaxf(m, snk);
                         const float e = m == -INFINITY ? 0.f : exp2f(m - M);
@@ -461,9 +490,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     s_f[c] = f;
                 } else {
                     float* ml = p.part_ml + (static_cast<size_t>(slot2) * N + c) * 2;
-                    ml[0] = off >= 0 ? m : -INFINITY;
+                    ml[0] = t != 255 ? m : -INFINITY;
                     ml[1] = l;
-                    s_f[c] = 1.f;
                 }
             }
             soft_sync();
@@ -479,14 +507,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     if (!whole) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (s_off[cb + i] >= 0) po[(cb + i) * D + mt * 128 + row] = __uint_as_float(r[i]);
+                            if (ctl.tok[cb + i] != 255) po[(cb + i) * D + mt * 128 + row] = __uint_as_float(r[i]);
                         continue;
                     }
                     // two columns at a time: even lanes write the first, odd lanes the second, each
                     // a pair of neighbouring channels
                     const int d = mt * 128 + (row & ~1), pair = (d - (D - 2 * p.or_pairs)) >> 1;
                     const bool rot = p.orp && d >= D - 2 * p.or_pairs;
-                    int rtok = -1;
+                    int rt = -1;
                     float2 cs = make_float2(1.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
@@ -496,16 +524,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         const float b = f1 == 0.f ? 0.f : __uint_as_float(r[i + 1]) * f1;
                         const float got = __shfl_xor_sync(~0u, (lane & 1) ? a : b, 1);
                         float e = (lane & 1) ? got : a, o = (lane & 1) ? b : got;
-                        const int c = cb + i + (lane & 1), off = s_off[c];
-                        if (off < 0) continue;
+                        const int c = cb + i + (lane & 1), t = ctl.tok[c];
+                        if (t == 255) continue;
                         if (rot) {
-                            const int tok = sg.tok0 + c / g.hb;
-                            if (tok != rtok) { cs = out_rope_cs(p, tok, pair); rtok = tok; }
+                            if (t != rt) { cs = out_rope_cs(p, sg.tok0 + t, pair); rt = t; }
                             const float e0 = e;
                             e = e0 * cs.x + o * cs.y;
                             o = -e0 * cs.y + o * cs.x;
                         }
-                        *reinterpret_cast<uint32_t*>(ob + off + d) = pack2(e, o);
+                        *reinterpret_cast<uint32_t*>(ob + (t * g.H + c - t * g.hb) * D + d) = pack2(e, o);
                     }
                 }
             }
@@ -523,8 +550,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             at += sg.ke - sg.kb;
         }
         if (dead && lane == 0) {
-            atomicOr(&s_err, DSV4_EWORD_TIMEOUT);
-            abort_flag = 1;
+            atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
+            ctl.abort = 1;
         }
         if (st == 0) {
             int* d = p.desc + blockIdx.x * 8;
@@ -535,75 +562,129 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     __syncthreads();
     tc_fence_after();
     if (warp == 2) tmem_dealloc(tmem, C::TCOLS);
-    if (tid == 0) p.err[blockIdx.x] = s_err;
+    if (tid == 0) p.err[blockIdx.x] = ctl.err;
 }
 
-// Merges the partial results of the row tiles that several CTAs worked on: one block per (tile,
-// query), its threads over channels x groups of partials. Also gathers the error bits.
+// Merges the partial results of the row tiles that several CTAs worked on, and gathers the error
+// bits. An item is one query of such a tile. Tiles cut into up to kWarpParts parts (borders
+// between CTAs) take a warp per item, its lanes over the channels; tiles over more CTAs (a few
+// long rows) a block per item, its threads over channels x groups of parts, so that all the
+// loads of an item are in flight at once.
 constexpr int kMergeThreads = 512;
+template <int D> constexpr int kWarpParts = D == 512 ? 4 : 8;
+
+struct MergeItem { int first, parts, tok, h, c; };
+
+// e^(m - top) of the parts this lane holds (part lane, lane + 32, ..), and the denominator's inverse.
+template <int N>
+__device__ __forceinline__ size_t part_slot(int first, int i, int c) {
+    return static_cast<size_t>(i ? (first + i) * 2 : first * 2 + 1) * N + c;
+}
+template <int N, int PL>
+__device__ __forceinline__ float merge_factors(const PagedAttnParams& p, const MergeItem& it, int lane, float (&w)[PL]) {
+    float l[PL], M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < PL; ++k) {
+        const int i = lane + 32 * k;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (i < it.parts) ml = *reinterpret_cast<const float2*>(p.part_ml + part_slot<N>(it.first, i, it.c) * 2);
+        w[k] = ml.x;
+        l[k] = ml.y;
+        M = fmaxf(M, ml.x);
+    }
+#pragma unroll
+    for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
+    const float snk = p.sink ? p.sink[it.h] * kLog2e : -INFINITY;
+    const float top = fmaxf(M, snk);
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < PL; ++k) {
+        w[k] = w[k] == -INFINITY ? 0.f : exp2f(w[k] - top);
+        sum += w[k] * l[k];
+    }
+#pragma unroll
+    for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
+    const float den = sum + (snk == -INFINITY ? 0.f : exp2f(snk - top));
+    if (lane == 0 && p.lse)
+        p.lse[static_cast<size_t>(it.tok) * p.g.H + it.h] = top == -INFINITY ? -INFINITY : top * kLn2 + logf(den);
+    return M == -INFINITY ? 0.f : 1.f / den;
+}
+
+// Four neighbouring channels of a merged output: factor, inverse rotation, bf16.
+template <int D>
+__device__ __forceinline__ void merge_store(const PagedAttnParams& p, const MergeItem& it, int ch, float4 a, float f) {
+    float o[4] = {a.x * f, a.y * f, a.z * f, a.w * f};
+    if (p.orp && ch >= D - 2 * p.or_pairs - 2) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const int pair = (ch + i - (D - 2 * p.or_pairs)) >> 1;
+            if (pair >= 0) {
+                const float2 cs = out_rope_cs(p, it.tok, pair);
+                const float e0 = o[i], o0 = o[i + 1];
+                o[i] = e0 * cs.x + o0 * cs.y;
+                o[i + 1] = -e0 * cs.y + o0 * cs.x;
+            }
+        }
+    }
+    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(it.tok) * p.g.H + it.h) * D + ch) =
+        make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+}
+
 template <int D, int N>
 __global__ void __launch_bounds__(kMergeThreads)
 paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int ctas, uint32_t* eword) {
-    constexpr int LD = D / 4, GR = kMergeThreads / LD;
-    __shared__ int starts[160 + 8];
-    __shared__ float wgt[512];
+    constexpr int LD = D / 4, GR = kMergeThreads / LD, WV = D / 128, PL = 5;
+    __shared__ int few[160], many[160], n_few, n_many;
+    __shared__ float wgt[32 * PL];
     __shared__ float4 acc[GR][LD];
-    __shared__ float bc[2];
-    __shared__ int n_starts;
+    __shared__ float s_inv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     if (warp == 0) {                     // the tiles to merge, by the CTA that starts each
-        int n = 0;
+        int a = 0, b = 0;
         uint32_t err = 0;
         for (int c0 = 0; c0 < ctas; c0 += 32) {
             const int c = c0 + lane;
-            const bool is = c < ctas && p.desc[c * 8] > 0;
+            const int np = c < ctas ? p.desc[c * 8] : 0;
             if (c < ctas) err |= p.err[c];
-            const unsigned b = __ballot_sync(~0u, is);
-            if (is) starts[n + __popc(b & ((1u << lane) - 1))] = c;
-            n += __popc(b);
+            const unsigned lt = (1u << lane) - 1;
+            const unsigned f = __ballot_sync(~0u, np > 0 && np <= kWarpParts<D>), m = __ballot_sync(~0u, np > kWarpParts<D>);
+            if ((f >> lane) & 1) few[a + __popc(f & lt)] = c;
+            if ((m >> lane) & 1) many[b + __popc(m & lt)] = c;
+            a += __popc(f);
+            b += __popc(m);
         }
         err = __reduce_or_sync(~0u, err);
-        if (lane == 0) n_starts = n;
-        if (lane == 0 && blockIdx.x == 0) *eword = err;
+        if (lane == 0) {
+            n_few = a;
+            n_many = b;
+            if (blockIdx.x == 0) *eword = err;
+        }
     }
     __syncthreads();
-    const PagedGeom& g = p.g;
-    for (int item = blockIdx.x; item < n_starts * N; item += gridDim.x) {
-        const int first = starts[item / N], c = item % N;
+    auto item = [&](int first, int c, MergeItem& it) {
         const int* d = p.desc + first * 8;
-        const int np = d[0], t = c / g.hb, hh = c - t * g.hb;
-        if (t >= d[2] || hh >= d[4]) continue;
-        const int h = d[3] + hh, tok = d[1] + t;
-        auto slot = [&](int i) { return static_cast<size_t>(i ? (first + i) * 2 : first * 2 + 1) * N + c; };
+        const int t = c / p.g.hb, hh = c - t * p.g.hb;
+        it = MergeItem{first, d[0], d[1] + t, d[3] + hh, c};
+        return t < d[2] && hh < d[4];
+    };
+    MergeItem it;
+    for (int x = blockIdx.x; x < n_many * N; x += gridDim.x) {
+        if (!item(many[x / N], x % N, it)) continue;
         if (warp == 0) {
-            float M = -INFINITY;
-            for (int i = lane; i < np; i += 32) M = fmaxf(M, p.part_ml[slot(i) * 2]);
-            for (int w = 16; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, w));
-            const float snk = p.sink ? p.sink[h] * kLog2e : -INFINITY;
-            const float top = fmaxf(M, snk);
-            float l = 0.f;
-            for (int i = lane; i < np; i += 32) {
-                const float m = p.part_ml[slot(i) * 2];
-                const float e = m == -INFINITY ? 0.f : exp2f(m - top);
-                wgt[i] = e;
-                l += e * p.part_ml[slot(i) * 2 + 1];
-            }
-            for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(~0u, l, w);
-            if (lane == 0) {
-                const float den = l + (snk == -INFINITY ? 0.f : exp2f(snk - top));
-                bc[0] = M == -INFINITY ? 0.f : 1.f / den;
-                if (p.lse)
-                    p.lse[static_cast<size_t>(tok) * g.H + h] = top == -INFINITY ? -INFINITY : top * kLn2 + logf(den);
-            }
+            float w[PL];
+            const float inv = merge_factors<N, PL>(p, it, lane, w);
+#pragma unroll
+            for (int k = 0; k < PL; ++k) wgt[lane + 32 * k] = w[k];
+            if (lane == 0) s_inv = inv;
         }
         __syncthreads();
         const int dl = tid % LD, gr = tid / LD;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int i = gr; i < np; i += GR) {
+        for (int i = gr; i < it.parts; i += GR) {
             const float e = wgt[i];
-            const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * D + dl * 4);
+            const float4 v = *reinterpret_cast<const float4*>(p.part_o + part_slot<N>(it.first, i, it.c) * D + dl * 4);
             if (e != 0.f) {
                 a.x = fmaf(e, v.x, a.x); a.y = fmaf(e, v.y, a.y);
                 a.z = fmaf(e, v.z, a.z); a.w = fmaf(e, v.w, a.w);
@@ -612,30 +693,40 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int ctas, uint32_t
         acc[gr][dl] = a;
         __syncthreads();
         if (gr == 0) {
-            float o[4] = {a.x, a.y, a.z, a.w};
             for (int i = 1; i < GR; ++i) {
                 const float4 v = acc[i][dl];
-                o[0] += v.x; o[1] += v.y; o[2] += v.z; o[3] += v.w;
+                a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
             }
-            const float f = bc[0];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] *= f;
-            if (p.orp) {
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const int ch = dl * 4 + i, pair = (ch - (D - 2 * p.or_pairs)) >> 1;
-                    if (ch >= D - 2 * p.or_pairs) {
-                        const float2 cs = out_rope_cs(p, tok, pair);
-                        const float e0 = o[i], o0 = o[i + 1];
-                        o[i] = e0 * cs.x + o0 * cs.y;
-                        o[i + 1] = -e0 * cs.y + o0 * cs.x;
-                    }
-                }
-            }
-            *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(tok) * g.H + h) * D + dl * 4) =
-                make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+            merge_store<D>(p, it, dl * 4, a, s_inv);
         }
         __syncthreads();
+    }
+    constexpr int WB = kMergeThreads / 32;
+    for (int x = blockIdx.x * WB + warp; x < n_few * N; x += gridDim.x * WB) {
+        if (!item(few[x / N], x % N, it)) continue;
+        float4 v[kWarpParts<D>][WV];        // every load first
+#pragma unroll
+        for (int i = 0; i < kWarpParts<D>; ++i)
+#pragma unroll
+            for (int k = 0; k < WV; ++k)
+                if (i < it.parts)
+                    v[i][k] = *reinterpret_cast<const float4*>(p.part_o + part_slot<N>(it.first, i, it.c) * D + k * 128 + lane * 4);
+        float w[1];
+        const float inv = merge_factors<N, 1>(p, it, lane, w);
+        float4 a[WV] = {};
+#pragma unroll
+        for (int i = 0; i < kWarpParts<D>; ++i) {
+            const float e = __shfl_sync(~0u, w[0], i);
+            if (i < it.parts && e != 0.f) {
+#pragma unroll
+                for (int k = 0; k < WV; ++k) {
+                    a[k].x = fmaf(e, v[i][k].x, a[k].x); a[k].y = fmaf(e, v[i][k].y, a[k].y);
+                    a[k].z = fmaf(e, v[i][k].z, a[k].z); a[k].w = fmaf(e, v[i][k].w, a[k].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < WV; ++k) merge_store<D>(p, it, k * 128 + lane * 4, a[k], inv);
     }
 }
 
@@ -672,7 +763,7 @@ int run(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_
     p.sink = a.sink;
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.lse = a.lse;
-    p.scale2 = a.scale * kLog2e;
+    p.scale2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.orp = a.out_rope_pos;
     p.or_pairs = a.out_rope_pos ? a.out_rope_dim / 2 : 0;
     for (int j = 0; j < p.or_pairs; ++j) p.or_freq[j] = std::pow(a.out_rope_theta, -2.0 * j / a.out_rope_dim);
@@ -708,7 +799,7 @@ PagedGeom paged_geom(const int32_t* table, const int32_t* cu_q, const int32_t* k
     g.H = heads;
     g.KV = kv_heads;
     g.G = heads / kv_heads;
-    g.window = window;
+    g.window = static_cast<long long>(max_pages) * page_size <= window ? 0 : window;   // (no effect: none)
     g.br = paged_box_rows(page_size);
     return g;
 }

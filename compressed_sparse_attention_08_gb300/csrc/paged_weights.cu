@@ -23,7 +23,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8, kSoftThreads = 256, kSoftBar = 1;
 constexpr int kN = 128;                  // query columns
-constexpr int kSB = 4;                   // score buffers (TMEM)
+constexpr int kSB = 4;                   // accumulators (TMEM)
 constexpr int kMaxSplit = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -46,6 +46,11 @@ struct WCfg {
     static constexpr int BOX = kPT * 128;                    // 128 rows (or queries) x 64 channels
     static constexpr int RES = NB * BOX;                     // the operand that stays
     static constexpr int RS = D == 512 ? 5 : 8;              // ring boxes
+    // The tensor core's running fp32 sum is cut, not rounded, at every step, which pulls scores
+    // towards 0: by 1.1e-6 on average at scores of 3 with 512 channels in one sum (measured), which
+    // the weights show in full. Two sums of 256 channels, added in fp32, leave half of it.
+    static constexpr int SUMS = D == 512 ? 2 : 1;
+    static constexpr int SB = kSB / SUMS;                    // score buffers
     static constexpr int OFF_R = RES, OFF_S = RES + RS * BOX;
     static constexpr int OFF_PF = OFF_S + 2 * kN * 4 * 3 + 2 * kPT * 4;   // tiles before each sequence
     static constexpr int SMALL = OFF_PF - OFF_S + kPagedMaxBatch * 4;
@@ -172,12 +177,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ PagedWeightsParams p) {
     using C = WCfg<D>;
-    constexpr int NB = C::NB, RS = C::RS;
+    constexpr int NB = C::NB, RS = C::RS, SB = C::SB, SUMS = C::SUMS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_slot, s_err;
     __shared__ volatile int abort_flag;
     __shared__ WSched sched;
-    __shared__ uint64_t res_full, res_empty, full[RS], empty[RS], s_full[kSB], s_empty[kSB];
+    __shared__ uint64_t res_full, res_empty, full[RS], empty[RS], s_full[SB], s_empty[SB];
     __shared__ unsigned s_bad[16];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* sR = sm + C::OFF_R;
@@ -192,7 +197,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         mbar_init(&res_full, 1);
         mbar_init(&res_empty, 1);
         for (int i = 0; i < RS; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < kSB; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], kSoftWarps); }
+        for (int i = 0; i < SB; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], kSoftWarps); }
         abort_flag = 0;
         s_err = 0;
         fence_barrier_init();
@@ -298,8 +303,8 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                             ++res;
                             if (dead) break;
                         }
-                        const uint32_t sb = u % kSB;
-                        if (u >= kSB) dead = !mbar_wait(&s_empty[sb], (u / kSB - 1) & 1, &abort_flag, p.wait_ns);
+                        const uint32_t sb = u % SB;
+                        if (u >= SB) dead = !mbar_wait(&s_empty[sb], (u / SB - 1) & 1, &abort_flag, p.wait_ns);
                         for (int b = 0; b < NB && !dead; ++b, ++ring) {
                             const uint32_t slot = ring % RS;
                             dead = !mbar_wait(&full[slot], (ring / RS) & 1, &abort_flag, p.wait_ns);
@@ -309,8 +314,8 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                             const uint32_t a0 = keep_q ? strm : stay, b0 = keep_q ? stay : strm;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16(tmem + sb * kN, sdesc_kmajor_sw128(a0 + kk * 32), sdesc_kmajor_sw128(b0 + kk * 32),
-                                          id, (b > 0 || kk > 0) ? 1u : 0u);
+                                umma_bf16(tmem + (sb * SUMS + b / (NB / SUMS)) * kN, sdesc_kmajor_sw128(a0 + kk * 32),
+                                          sdesc_kmajor_sw128(b0 + kk * 32), id, (b % (NB / SUMS) > 0 || kk > 0) ? 1u : 0u);
                             umma_commit(&empty[slot]);
                         }
                         if (!dead) umma_commit(&s_full[sb]);
@@ -355,7 +360,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     };
                     fetch(0);
                     for (int x = 0; x < n; ++x, ++u) {
-                        const uint32_t sb = u % kSB;
+                        const uint32_t sb = u % SB;
                         float* l2 = s_l + (u & 1) * kN;
                         int *hi = s_hi + (u & 1) * kN, *lo = s_lo + (u & 1) * kN;
                         if (st < kN) { l2[st] = nl; hi[st] = nhi; lo[st] = nlo; }
@@ -364,7 +369,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         const int tt = it.tt0 + x / g.nhb, blk = x - x / g.nhb * g.nhb;
                         const int t0 = tt * g.tpt, tn = min(g.tpt, it.q.n - t0);
                         const int cols = (tn - 1) * g.hb + min(g.hb, g.G - blk * g.hb);
-                        if (!dead) dead = !mbar_wait(&s_full[sb], (u / kSB) & 1, &abort_flag, p.wait_ns);
+                        if (!dead) dead = !mbar_wait(&s_full[sb], (u / SB) & 1, &abort_flag, p.wait_ns);
                         tc_fence_after();
                         const unsigned bad = *reinterpret_cast<volatile unsigned*>(&s_bad[u & 15]);
                         const bool live = j < rows && !((bad >> (row / g.br)) & 1);
@@ -376,8 +381,17 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                             const int c0 = (2 * pc + half) * 32;
                             if (c0 >= cols) break;
                             uint32_t r[32];
-                            DSV4_TMEM_LD_32x32b_X32(lane_base + sb * kN + c0, r);
-                            tmem_wait_ld();
+                            DSV4_TMEM_LD_32x32b_X32(lane_base + sb * SUMS * kN + c0, r);
+                            if constexpr (SUMS == 2) {
+                                uint32_t r2[32];
+                                DSV4_TMEM_LD_32x32b_X32(lane_base + (sb * SUMS + 1) * kN + c0, r2);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
+                            } else {
+                                tmem_wait_ld();
+                            }
                             float part = 0.f;
                             if (open && c0 + 32 <= cols) {
 #pragma unroll
@@ -487,7 +501,7 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
     p.err = reinterpret_cast<uint32_t*>(p.head + 2 + 4 * ctas);
     // one row tile per sequence: the queries stay
     p.keep_q = p.g.nhb == 1 && a.max_q <= p.g.tpt;
-    p.scale2 = a.scale * kLog2e;
+    p.scale2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.wait_ns = kDefaultWaitNs;
     auto kern = paged_weights_kernel<D>;
     if (once_per_device(reinterpret_cast<const void*>(kern), kAttrLaunch, [kern] {

@@ -347,7 +347,9 @@ int dsv4_quantize_rows_fp8(const void* x, int rows, int dim, void* q, float* sca
  * token sees must be finite for the others too (a tile's rows meet all its tokens in the tensor
  * core, the ones a token does not see with weight 0); rows that none sees may hold anything.
  * Counts outside their arrays are clamped and rows on a page outside the pool are hidden; both
- * set DSV4_EWORD_BAD_INDEX. batch: 0..2048; batch * max_pages * page_size below 2^37.
+ * set DSV4_EWORD_BAD_INDEX. batch: 0..2048; max_pages *
+ * page_size: at most 2^29 (times batch: below 2^37). Lengths, tables, positions, lse, sink and acc need
+ * the alignment of their type only (a table may be a slice of a larger one).
  */
 
 /* RMSNorm of queries and keys per head, RoPE in the same pass, rows appended to the pages.

@@ -59,7 +59,7 @@ def _evict(**over):
 COMMON = [dict(dim=64), dict(dim=384), dict(kv_heads=0), dict(page_size=0), dict(page_size=12), dict(page_size=65544),
           dict(num_pages=0)]
 TABLES = COMMON + [dict(batch=-1), dict(batch=2049), dict(max_pages=0), dict(max_pages=1 << 25),
-                   dict(batch=2048, max_pages=1 << 24), dict(block_table=None), dict(kv_len=_p(5, 4))]
+                   dict(batch=2048, max_pages=1 << 24), dict(block_table=None), dict(kv_len=_p(5, 2))]
 QUERIES = [dict(heads=0), dict(heads=1025), dict(heads=6, kv_heads=4), dict(q_stride=512 * 64 - 8), dict(q_stride=512 * 64 + 4),
            dict(total_q=-1), dict(max_q=0), dict(window=-1), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None),
            dict(cu_q=None), dict(k_pages=_p(2, 8))]
@@ -77,7 +77,7 @@ def test_norm_rope_rejects_on_host(lib, bad):
 
 @pytest.mark.parametrize("bad", TABLES + QUERIES + [
     dict(v_pages=_p(10)),                           # K and V apart at 512 channels: not offered
-    dict(out=None), dict(lse=_p(8, 4)), dict(sink=_p(6, 8)), dict(out_rope_dim=0), dict(out_rope_dim=65),
+    dict(out=None), dict(lse=_p(8, 2)), dict(sink=_p(6, 2)), dict(out_rope_pos=_p(9, 4)), dict(out_rope_dim=0), dict(out_rope_dim=65),
     dict(out_rope_dim=130), dict(out_rope_theta=-1.0)])
 def test_attention_rejects_on_host(lib, bad):
     assert lib.dsv4_paged_attn(ctypes.byref(_attn(**bad)), _p(20), 1 << 40, None) == 1, bad
@@ -89,7 +89,7 @@ def test_weights_reject_on_host(lib, bad):
 
 
 @pytest.mark.parametrize("bad", TABLES + [
-    dict(out_table=None), dict(kv_len_out=None), dict(acc=None), dict(acc_out=_p(7, 4)), dict(keep=None), dict(out_pages=0),
+    dict(out_table=None), dict(kv_len_out=None), dict(acc=None), dict(acc_out=_p(7, 2)), dict(keep=None), dict(out_pages=0),
     dict(out_table=_p(2), out_pages=8),             # in place: one table, one width
     dict(acc_rows=0), dict(budget=0), dict(budget=513), dict(budget=1025, out_pages=32), dict(recent=-1), dict(recent=501)])
 def test_evict_rejects_on_host(lib, bad):
