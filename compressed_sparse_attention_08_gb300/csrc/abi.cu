@@ -179,7 +179,6 @@ bool paged_attn_ok(const dsv4_paged_attn_args* a) {
         !num_ok(a->cu_q, 4) || !num_ok(a->kv_len, 4) || !opt_num_ok(a->sink, 4) || !dev_ptr_ok(a->out) || !opt_num_ok(a->lse, 4) ||
         !opt_num_ok(a->out_rope_pos, 8))
         return false;
-    if (a->v_pages && a->dim == 512) return false;       // (two tiles of 128 rows do not fit)
     if (a->out_rope_pos &&
         (a->out_rope_dim < 2 || (a->out_rope_dim & 1) || a->out_rope_dim > a->dim || a->out_rope_dim > 128 ||
          !std::isfinite(a->out_rope_theta) || a->out_rope_theta <= 0.0))

@@ -80,6 +80,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Whether the phase is complete, without waiting (mbarrier.try_wait may suspend the thread).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // The time limit of a bounded wait unless a test shortens it (dsv4_test_wait_fault).
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 
@@ -290,6 +301,10 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 
 // 32 registers per thread -> 32 lanes x 32 consecutive 32-bit TMEM columns (the inverse of
 // the x32 load); tcgen05.wait::st orders the stores before a later tcgen05 operation reads them.
+#define DSV4_TMEM_ST_32x32b_X8(taddr, r)                                                      \
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"      \
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),          \
+                    "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory")
 #define DSV4_TMEM_ST_32x32b_X32(taddr, r)                                                     \
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "                               \
                  "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"                     \
@@ -369,6 +384,14 @@ __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
 __device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
+__device__ __forceinline__ void add_f32x2(uint64_t& acc, uint64_t a) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(a));
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
 __device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint64_t a, uint64_t b) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
@@ -406,6 +429,15 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 }
 __device__ __forceinline__ void red_cluster_add(uint32_t addr, uint32_t v) {
     asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// One lane of a converged warp (true in that lane). A role whose whole warp follows its control
+// flow and lets the elected lane issue keeps the operands of tcgen05.mma in uniform registers: 54
+// cycles per product against 65 where one lane runs alone.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Named barrier `id` (1..15) over `count` threads (a multiple of 32) of the CTA.

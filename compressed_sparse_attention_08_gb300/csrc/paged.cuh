@@ -6,7 +6,7 @@
 // the sequence stands at row p = kv_len[s] - n_s + t and sees the rows [max(0, p + 1 - window),
 // p + 1) (window 0: from row 0).
 //
-// Work is cut into units of 128 cache rows x one row tile: a row tile is `tpt` tokens times
+// Work is cut into units of `unit` (128 or 64) cache rows x one row tile: a row tile is `tpt` tokens times
 // `hb` query heads of one KV head (at most N rows, the tensor-core tile). All units of a call
 // form one line, in the order (sequence, token tile, KV head and head block, rows), and CTA c
 // of g takes the units [T c / g, T (c + 1) / g): every CTA has the same amount of work whatever
@@ -19,7 +19,6 @@
 
 namespace dsv4 {
 
-constexpr int kPT = 128;                 // cache rows per unit
 constexpr int kPagedMaxBatch = 2048;
 
 // 2^x by the hardware's approximation (relative error about 2^-22, results below 2^-126 are 0).
@@ -42,19 +41,30 @@ struct PagedGeom {
     int H, KV, G;                        // query heads, KV heads, query heads per KV head
     int hb, nhb, tpt;                    // heads per row tile, head blocks per KV head, tokens per row tile
     int window;                          // 0: none
-    int br;                              // cache rows per TMA box: a power of two that divides page_size, <= 128
+    int unit;                            // cache rows per unit
+    int br;                              // cache rows per TMA box: a power of two that divides page_size, <= unit
 };
 
-// Row tiles of at most N rows for groups of G heads.
+// Row tiles of at most N rows for groups of G heads: whole groups, or the split of a group into
+// equal blocks that fills the tiles best (64 heads in tiles of 96: three tokens of 32).
 inline void paged_tile(PagedGeom& g, int N) {
-    g.hb = g.G < N ? g.G : N;
-    g.nhb = (g.G + N - 1) / N;
-    g.tpt = N / g.hb;
+    double best = -1.0;
+    const int least = (g.G + N - 1) / N;
+    for (int k = least; k < least + 4 && k <= g.G; ++k) {
+        const int hb = (g.G + k - 1) / k, nhb = (g.G + hb - 1) / hb, tpt = N / hb;
+        const double fill = static_cast<double>(g.G) * tpt / (static_cast<double>(nhb) * N);
+        if (fill > best + 0.05) {
+            best = fill;
+            g.hb = hb;
+            g.nhb = nhb;
+            g.tpt = tpt;
+        }
+    }
 }
 
-inline int paged_box_rows(int page_size) {
+inline int paged_box_rows(int page_size, int unit) {
     const int low = page_size & -page_size;
-    return low < kPT ? low : kPT;
+    return low < unit ? low : unit;
 }
 
 struct PagedSeq { int q0, n, L; };       // first token, tokens, cache rows
@@ -77,11 +87,11 @@ __device__ __forceinline__ int paged_lo(const PagedGeom& g, const PagedSeq& q, i
     return g.window > 0 ? max(q.L - q.n + t + 1 - g.window, 0) : 0;
 }
 
-// Units of token tile tt: the 128-row blocks that some token of it sees (at least one, so that
+// Units of token tile tt: the blocks of `unit` rows that some token of it sees (at least one, so that
 // tokens that see nothing are still answered).
 __device__ __forceinline__ int paged_tile_units(const PagedGeom& g, const PagedSeq& q, int tt) {
     const int t0 = tt * g.tpt, t1 = min(t0 + g.tpt, q.n) - 1;
-    return max((paged_hi(q, t1) + kPT - 1) / kPT - paged_lo(g, q, t0) / kPT, 1);
+    return max((paged_hi(q, t1) + g.unit - 1) / g.unit - paged_lo(g, q, t0) / g.unit, 1);
 }
 
 struct PagedSched {
@@ -90,10 +100,11 @@ struct PagedSched {
     int s, tt, inner, k;                 // where u0 lies
 };
 
-// Whole block of NT threads; `pref` is scratch for `batch` counts in shared memory. At least
-// `min_units` units go to each CTA with work. Returns with the result visible to the block.
+// The share of worker `self` of `count`. Whole block of NT threads; `pref` is scratch for `batch` counts in shared memory. At least
+// `min_units` units go to each worker with work. Returns with the result visible to the block.
 template <int NT>
-__device__ void paged_schedule(const PagedGeom& g, int min_units, long long* pref, PagedSched* out, uint32_t* err) {
+__device__ void paged_schedule(const PagedGeom& g, int self, int count, int min_units, long long* pref, PagedSched* out,
+                               uint32_t* err) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int mult = g.KV * g.nhb;
     bool bad = false;
@@ -141,9 +152,9 @@ __device__ void paged_schedule(const PagedGeom& g, int min_units, long long* pre
     if (warp < 2) {
         const long long T = g.batch > 0 ? pref[g.batch - 1] : 0;
         const long long most = T / min_units < 1 ? 1 : T / min_units;
-        const int ge = most < static_cast<long long>(gridDim.x) ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+        const int ge = most < count ? static_cast<int>(most) : count;
         const long long share32 = T / ge / 32, small = share32 > 2 ? share32 : 2;
-        const int c = static_cast<int>(blockIdx.x) + warp;
+        const int c = self + warp;
         long long u = c < ge ? T * c / ge : T;
         int s = 0, tt = 0, inner = 0, k = 0;
         if (u < T && u > 0) {
@@ -207,7 +218,7 @@ struct PagedSeg {
     int kvh, head0, hv;                  // KV head, first query head, query heads
     int lo_u, hi_u;                      // rows that some token sees
     int lo_max, hi_min;                  // rows that every token sees
-    int row0;                            // first row of unit 0 (a multiple of 128)
+    int row0;                            // first row of unit 0 (a multiple of `unit`)
     int n, kb, ke;                       // the tile's units, this CTA's [kb, ke)
 };
 
@@ -243,8 +254,8 @@ struct PagedWalk {
         o.hi_u = paged_hi(q, t0 + o.tn - 1);
         o.lo_max = paged_lo(g, q, t0 + o.tn - 1);
         o.hi_min = paged_hi(q, t0);
-        o.row0 = o.lo_u / kPT * kPT;
-        o.n = max((o.hi_u + kPT - 1) / kPT - o.lo_u / kPT, 1);
+        o.row0 = o.lo_u / g.unit * g.unit;
+        o.n = max((o.hi_u + g.unit - 1) / g.unit - o.lo_u / g.unit, 1);
         o.kb = k;
         const long long take = left < o.n - k ? left : o.n - k;
         o.ke = k + static_cast<int>(take);
@@ -255,24 +266,28 @@ struct PagedWalk {
     }
 };
 
-// One tile of 128 cache rows: which of its boxes of `br` rows hold visible rows, and where they
-// lie. Whole warp; lane i (< 128 / br) answers for box i. `bad` lanes name a page that is not
-// in the pool: their rows are hidden.
-struct PagedTile { int page, slot; unsigned ok, bad; };
-__device__ __forceinline__ PagedTile paged_tile_boxes(const PagedGeom& g, const PagedSeg& sg, int row, int lane) {
-    PagedTile t{0, 0, 0, 0};
-    const int r = row + lane * g.br;
-    bool need = lane < kPT / g.br && r < sg.hi_u && r + g.br > sg.lo_u;
-    if (need) {
+// One tile of `unit` cache rows as boxes of `br` rows: lanes 2i and 2i + 1 answer for box i (the
+// two 64-channel halves of a slot). The page is only looked up here; paged_boxes uses it.
+struct PagedLook { int page, slot; bool need; };
+__device__ __forceinline__ PagedLook paged_look(const PagedGeom& g, const PagedSeg& sg, int row, int lane) {
+    PagedLook t{0, 0, false};
+    const int i = lane >> 1, r = row + i * g.br;
+    t.need = i < g.unit / g.br && r < sg.hi_u && r + g.br > sg.lo_u;   // holds rows that some token sees
+    if (t.need) {
         const int pg = r / g.page_size;
         t.slot = r - pg * g.page_size;
         t.page = g.table[static_cast<size_t>(sg.s) * g.max_pages + pg];
     }
-    const bool ok = need && t.page >= 0 && t.page < g.num_pages;
-    t.ok = __ballot_sync(~0u, ok);
-    t.bad = __ballot_sync(~0u, need && !ok);
     return t;
 }
+// Whole warp: the lanes with something to load, and (bits 2i) the boxes on pages that are not in
+// the pool: their rows are hidden.
+struct PagedBoxes { unsigned ok, bad; };
+__device__ __forceinline__ PagedBoxes paged_boxes(const PagedGeom& g, const PagedLook& t) {
+    const bool in = t.page >= 0 && t.page < g.num_pages;
+    return PagedBoxes{__ballot_sync(~0u, t.need && in), __ballot_sync(~0u, t.need && !in) & 0x55555555u};
+}
+__device__ __forceinline__ bool paged_bad_row(const PagedGeom& g, unsigned bad, int row) { return (bad >> (2 * (row / g.br))) & 1; }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
                                             int w) {

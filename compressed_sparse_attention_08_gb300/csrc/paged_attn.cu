@@ -9,14 +9,25 @@
 // RoPE of the output). The pages keep dense per-sequence buffers; the paged form is this
 // library's own.
 //
-// One persistent CTA per SM walks its share of the work line (paged.cuh). Both products have the
-// cache rows or the channels on the tensor core's 128 lanes and the queries on its columns:
-// S^T = K Q^T (128 rows x N queries, one unit) and O^T += V^T P^T (128 channels per tile x N).
-// So the number of query columns N is free (64 or 128), a single token's 64 heads fill a tile,
-// and one shared-memory copy of a shared KV row serves as K (K-major) and as V (MN-major).
-// Roles: warp 0 moves pages by TMA into a ring of 128-row tiles, warp 1 issues tcgen05.mma,
-// warps 4-11 do the softmax (a thread holds one cache row and half of the queries). The scores
-// have two TMEM buffers, so S^T of unit u + 1 runs under the softmax of unit u.
+// Persistent CTAs walk their shares of the work line (paged.cuh). Both products have the cache
+// rows or the channels on the tensor core's 128 lanes and the queries on its columns: S^T = K Q^T
+// (128 rows x N queries, one unit) and O^T += V^T P^T (128 channels per tile x N). So the number of
+// query columns N is free (64 or 128), a single token's 64 heads fill a tile, and one
+// shared-memory copy of a shared KV row serves as K (K-major) and as V (MN-major).
+// Roles: warps 0, 2 and 3 move pages by TMA into a ring (a warp issues a box in 70 to 120 cycles,
+// however small: three share the boxes of each slot), warp 1 issues tcgen05.mma, warps 4-19 do the
+// softmax (a thread holds one cache row and a quarter of the queries; with 8 warps its chain of
+// steps, not the tensor core, set the pace). The scores have two TMEM buffers, so S^T of unit
+// u + 1 runs under the softmax of unit u.
+//
+// 512 channels: a tile is 128 KB and the ring holds no second one beside it. Kept for both products,
+// it made loads, products and softmax take turns (7000 cycles per unit, of which the tensor core
+// worked 3300). So the rows come in twice, as K and as V, in the order of use K0 K1 V0 K2 V1 ..:
+// L2 has them the second time, and nothing waits for a whole tile (5700 cycles per unit; shared
+// memory then moves 640 KB per unit, 5100 cycles at the 128 bytes a cycle that it has). Slower were
+// units of 64 rows, of which two fit the ring (S^T with M = 64 costs as much as with M = 128),
+// and two CTAs with 256 channels each that exchange scores and P through distributed shared memory
+// (which moved about 12 bytes a cycle).
 #include <cmath>
 
 #include "internal.h"
@@ -25,8 +36,10 @@
 namespace dsv4 {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kSoftWarps = 8, kSoftThreads = 256, kSoftBar = 1;
+constexpr int kThreads = 640;
+constexpr int kLoadWarps = 3;
+constexpr int kGroups = 4;                       // softmax: groups of 4 warps, one per quarter of the columns
+constexpr int kSoftWarps = 16, kSoftThreads = 512, kSoftBar = 1;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // A query's reference maximum moves only when a score exceeds it by more than kSpan (base-2
 // units): P = 2^(s - m) then stays far inside the fp32 and bf16 range, and o does not depend on
@@ -38,10 +51,10 @@ struct PagedAttnParams {
     const float* sink;                   // [H] or null
     __nv_bfloat16* out;                  // [total_q, H, D]
     float* lse;                          // [total_q, H] or null
-    float* part_ml;                      // [2 * grid, N, 2]
-    float* part_o;                       // [2 * grid, N, D]
-    int* desc;                           // [grid, 8]
-    uint32_t* err;                       // [grid] error bits
+    float* part_ml;                      // [2 * workers, N, 2]
+    float* part_o;                       // [2 * workers, N, D]
+    int* desc;                           // [workers, 8]
+    uint32_t* err;                       // [CTAs] error bits
     float scale2;                        // scale * log2(e)
     const int64_t* orp;                  // [total_q] or null
     int or_pairs;
@@ -51,11 +64,13 @@ struct PagedAttnParams {
 };
 
 constexpr int kMaxSlots = 8;
+constexpr int kPT = 128;                 // cache rows per unit
 template <int N>
 struct PagedCtl {
-    uint64_t q_full, q_empty, full[kMaxSlots], empty[kMaxSlots], s_full[2], s_empty[2], p_full, pv_done;
+    uint64_t q_full, q_empty, full[kMaxSlots], empty[kMaxSlots], s_full[2], s_empty[2], p_full[2], pv_done[2];
+    uint64_t v_ready, v_clean;           // V apart from K: an edge unit's rows have come, and are cleared
     PagedSched sched;
-    alignas(16) float m[N];              // reference maxima (base-2 units)
+    alignas(16) float nm[N];             // reference maxima (base-2 units), negated
     alignas(16) float f[N];              // factors
     uint32_t top[N];                     // a unit's maxima as ordered keys
     unsigned char tok[N];                // the column's token in the tile, 255: no query
@@ -64,8 +79,8 @@ struct PagedCtl {
     int abort;
 };
 
-// Shared memory: a ring of slots of 128 cache rows x 128 channels (two swizzled boxes), in which
-// a K or V tile takes MT slots, so a slot is loaded again as soon as the product that reads it is
+// Shared memory: a ring of slots of 128 cache rows x 128 channels (two swizzled boxes), in which a
+// K or V tile takes MT slots, so a slot is loaded again as soon as the product that reads it is
 // done; the queries; P; and a few arrays per query.
 template <int D_, int N_>
 struct PCfg {
@@ -74,29 +89,47 @@ struct PCfg {
     static constexpr int BOX = kPT * 128;                    // 128 rows x 64 channels
     static constexpr int SLOT = 2 * BOX;
     static constexpr int QBOX = N * 128, QB = 2 * MT * QBOX;
-    static constexpr int PB = kPT * N * 2;
-    static constexpr int ST_FIT = (232448 - sizeof(PagedCtl<N>) - QB - PB) / SLOT;
-    static constexpr int ST = ST_FIT > 8 ? 8 : ST_FIT;
-    // With two tiles in the ring the scores of a unit are formed before the product with V of the
-    // unit before; otherwise (512 channels) the two take turns and share the ring slot by slot.
-    static constexpr bool AHEAD = ST >= 2 * MT;
-    static constexpr int OFF_Q = ST * SLOT, OFF_P = OFF_Q + QB, OFF_C = OFF_P + PB;
+    static constexpr int PB = kPT * N * 2, PN = D == 512 ? 2 : 1;    // P, and how many (two where the products are long)
+    static constexpr int ST_FIT = (232448 - sizeof(PagedCtl<N>) - QB - PN * PB) / SLOT;
+    static constexpr int ST = ST_FIT > kMaxSlots ? kMaxSlots : ST_FIT;
+    static constexpr int OFF_Q = ST * SLOT, OFF_P = OFF_Q + QB, OFF_C = OFF_P + PN * PB;
     static constexpr int SMEM = OFF_C + sizeof(PagedCtl<N>);
     static constexpr int TCOLS = 512;
     static constexpr int OCOL = 2 * N;
-    static_assert(ST >= MT && SMEM <= 232448 && OCOL + MT * N <= 512, "one tile, and both accumulators in TMEM");
+    static_assert(ST >= MT && SMEM <= 232448 && OCOL + MT * N <= 512, "one tile, and all accumulators in TMEM");
+    static constexpr bool KEEP = ST >= 2 * MT;               // a shared K/V tile stays for both products
 };
+
+// Whether the unit that starts at row j0 holds rows that no token of the tile sees.
+__device__ __forceinline__ bool unit_edge(const PagedGeom& g, const PagedSeg& sg, int j0, unsigned bad) {
+    return j0 < sg.lo_u || j0 + g.unit > sg.hi_u || bad != 0;
+}
+
+// Places of unit u's tiles in the order of loading, in tiles, of `units` in all: K0 K1 V0 K2 V1 ..,
+// or one tile for both.
+__device__ __forceinline__ uint32_t k_place(bool keep, uint32_t u) { return keep ? u : (u ? 2 * u - 1 : 0); }
+__device__ __forceinline__ uint32_t v_place(bool keep, uint32_t u, uint32_t units) {
+    return keep ? u : (u + 1 == units ? 2 * u + 1 : 2 * u + 2);
+}
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 32 values per lane, reduced over the warp's lanes: lane i returns the reduction of value i.
-template <bool kMax>
-__device__ __forceinline__ float lanes_reduce(float (&v)[32], int lane) {
+// K values per lane, reduced over the warp's lanes: lane i returns the reduction of value i mod K
+// (K: 8, 16 or 32).
+template <bool kMax, int K>
+__device__ __forceinline__ float lanes_reduce(float (&v)[K], int lane) {
 #pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) {
+    for (int w = 16; w >= K; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const float got = __shfl_xor_sync(0xffffffffu, v[i], w);
+            v[i] = kMax ? fmaxf(v[i], got) : v[i] + got;
+        }
+#pragma unroll
+    for (int w = K / 2; w >= 1; w >>= 1) {
         const bool upper = (lane & w) != 0;
 #pragma unroll
         for (int i = 0; i < w; ++i) {
@@ -118,11 +151,26 @@ __device__ __forceinline__ bool soft_sync_or(bool x) {
 }
 __device__ __forceinline__ void soft_sync() { named_bar_sync(kSoftBar, kSoftThreads); }
 
-// (cos, sin) of the inverse rotation of pair j of token tok.
-__device__ __forceinline__ float2 out_rope_cs(const PagedAttnParams& p, int tok, int j) {
+// (cos, sin) of the inverse rotation of pair j of token tok. Not inlined: sixteen copies of it in
+// the output loops pushed the code around them out of the instruction cache.
+__device__ __noinline__ float2 out_rope_angle(double a) {
     float sn, cs;
-    sincosf(reduced_angle(static_cast<double>(p.orp[tok]) * p.or_freq[j]), &sn, &cs);
+    sincosf(reduced_angle(a), &sn, &cs);
     return make_float2(cs, sn);
+}
+__device__ __forceinline__ float2 out_rope_cs(const PagedAttnParams& p, int tok, int j) {
+    return out_rope_angle(static_cast<double>(p.orp[tok]) * p.or_freq[j]);
+}
+
+// NT TMEM columns of this thread's lane.
+template <int NT>
+__device__ __forceinline__ void tmem_cols(uint32_t addr, uint32_t (&r)[NT]) {
+    if constexpr (NT == 32) {
+        DSV4_TMEM_LD_32x32b_X32(addr, r);
+    } else {
+        static_assert(NT == 16, "columns per thread");
+        DSV4_TMEM_LD_32x32b_X16(addr, r);
+    }
 }
 
 template <int D, int N>
@@ -130,22 +178,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedAttnParams p) {
     using C = PCfg<D, N>;
-    constexpr int ST = C::ST, MT = C::MT, NC = N / 64;               // NC: 32-column pieces per thread
+    constexpr int ST = C::ST, MT = C::MT;
+    constexpr int NE = N / kGroups;                                  // scores of a unit per softmax thread: one row
+    constexpr bool LATE = NE <= 16;
     extern __shared__ __align__(1024) uint8_t sm[];
     PagedCtl<N>& ctl = *reinterpret_cast<PagedCtl<N>*>(sm + C::OFF_C);
     uint8_t* sQ = sm + C::OFF_Q;
     uint8_t* sP = sm + C::OFF_P;
-    float *s_m = ctl.m, *s_f = ctl.f;
+    float *s_nm = ctl.nm, *s_f = ctl.f;
     volatile int* abort_flag = &ctl.abort;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int worker = blockIdx.x, workers = gridDim.x;
     if (tid == 0) {
-        mbar_init(&ctl.q_full, 1);
+        tma_prefetch_desc(&qmap);
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+        mbar_init(&ctl.q_full, kLoadWarps);
         mbar_init(&ctl.q_empty, 1);
-        for (int i = 0; i < ST; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&ctl.s_full[i], 1); mbar_init(&ctl.s_empty[i], kSoftWarps); }
-        mbar_init(&ctl.p_full, kSoftWarps);
-        mbar_init(&ctl.pv_done, 1);
+        for (int i = 0; i < ST; ++i) { mbar_init(&ctl.full[i], kLoadWarps); mbar_init(&ctl.empty[i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.s_full[i], 1);
+            mbar_init(&ctl.s_empty[i], kSoftWarps);
+            mbar_init(&ctl.p_full[i], kSoftWarps);
+            mbar_init(&ctl.pv_done[i], 1);
+        }
+        mbar_init(&ctl.v_ready, 1);
+        mbar_init(&ctl.v_clean, kSoftWarps);
         ctl.abort = 0;
         ctl.err = 0;
         fence_barrier_init();
@@ -158,61 +217,82 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
-    paged_schedule<kThreads>(p.g, p.min_units, reinterpret_cast<long long*>(sm), &ctl.sched, &ctl.err);
+    paged_schedule<kThreads>(p.g, worker, workers, p.min_units, reinterpret_cast<long long*>(sm), &ctl.sched, &ctl.err);
     // the schedule's scratch is overwritten by TMA next
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
 
     const PagedGeom& g = p.g;
     const PagedSched& sched = ctl.sched;
-    const int parts = p.shared ? 1 : 2;
-    if (warp == 0) {
+    const bool keep = C::KEEP && p.shared;               // K rows stay in place as V
+    const uint32_t units = static_cast<uint32_t>(sched.u1 - sched.u0);
+    if (warp == 0 || warp == 2 || warp == 3) {
         // ---------------------------------------------------------------- pages and queries
+        // Three warps walk the same slots and take turns with the boxes; all arrive on each slot (so
+        // none falls a round behind), warp 0 with the bytes.
+        const int mine = warp == 0 ? 0 : warp - 1;
         PagedWalk w(g, sched);
         PagedSeg sg;
-        const int pieces = kPT / g.br;
         const uint32_t qbytes = static_cast<uint32_t>(g.hb) * g.tpt * D * 2;
-        uint32_t ring = 0, u = 0, seg = 0;
-        bool dead = false;
-        while (!dead && w.next(sg)) {
-            if (seg > 0) dead = __any_sync(~0u, !mbar_wait(&ctl.q_empty, (seg - 1) & 1, abort_flag, p.wait_ns));
-            if (dead) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&ctl.q_full, qbytes);
-                for (int b = 0; b < 2 * MT; ++b)
-                    tma_load_3d(sQ + b * C::QBOX, &qmap, &ctl.q_full, b * 64, sg.head0, sg.tok0);
-            }
-            ++seg;
-            for (int k = sg.kb; k < sg.ke && !dead; ++k, ++u) {
-                const PagedTile t = paged_tile_boxes(g, sg, sg.row0 + k * kPT, lane);
-                const uint32_t bytes = static_cast<uint32_t>(__popc(t.ok)) * g.br * 256;
-                for (int part = 0; part < parts && !dead; ++part) {
-                    const CUtensorMap* map = part ? &vmap : &kmap;
-                    for (int mt = 0; mt < MT; ++mt, ++ring) {
-                        const uint32_t slot = ring % ST;
-                        if (ring >= ST)
-                            dead = __any_sync(~0u, !mbar_wait(&ctl.empty[slot], (ring / ST - 1) & 1, abort_flag, p.wait_ns));
-                        if (dead) break;
-                        if (lane == 0) {
-                            if (part == 0 && mt == 0) {
-                                ctl.bad[u & 7] = t.bad;
-                                if (t.bad) atomicOr(&ctl.err, DSV4_EWORD_BAD_INDEX);
-                            }
-                            if (bytes) mbar_arrive_expect_tx(&ctl.full[slot], bytes);
-                            else mbar_arrive(&ctl.full[slot]);
-                        }
-                        __syncwarp();
-                        uint8_t* dst = sm + slot * C::SLOT;
-                        // lane: piece lane % pieces of box lane / pieces (two boxes, at most 16 pieces)
-                        const int piece = lane & (pieces - 1), box = lane / pieces;
-                        const int page = __shfl_sync(~0u, t.page, piece), at = __shfl_sync(~0u, t.slot, piece);
-                        if (box < 2 && ((t.ok >> piece) & 1))
-                            tma_load_4d(dst + box * C::BOX + piece * g.br * 128, map, &ctl.full[slot], mt * 128 + box * 64,
-                                        sg.kvh, at, page);
+        const int piece = lane >> 1, box = lane & 1;
+        uint32_t ring = 0, seg = 0;
+        bool dead = false, more = w.next(sg);
+        int turn = lane % kLoadWarps;                // this lane's box falls to warp `turn`
+        PagedLook cur{0, 0, false}, prev{0, 0, false};
+        if (more) cur = paged_look(g, sg, sg.row0 + sg.kb * kPT, lane);
+        int prev_h = 0, k = more ? sg.kb : 0;
+        // one tile (K, or V of the unit before) into the next MT slots
+        auto load = [&](const CUtensorMap* map, const PagedLook& t, int kvh, int unit) {
+            const PagedBoxes bx = paged_boxes(g, t);
+            const uint32_t bytes = static_cast<uint32_t>(__popc(bx.ok)) * g.br * 128;
+#pragma unroll 1
+            for (int mt = 0; mt < MT; ++mt, ++ring) {
+                const uint32_t slot = ring % ST;
+                if (ring >= ST)
+                    dead = __any_sync(~0u, !mbar_wait(&ctl.empty[slot], (ring / ST - 1) & 1, abort_flag, p.wait_ns));
+                if (dead) return;
+                if (lane == 0) {
+                    if (mine == 0 && mt == 0 && unit >= 0) {
+                        ctl.bad[unit & 7] = bx.bad;
+                        if (bx.bad) atomicOr(&ctl.err, DSV4_EWORD_BAD_INDEX);
                     }
+                    if (mine == 0 && bytes) mbar_arrive_expect_tx(&ctl.full[slot], bytes);
+                    else mbar_arrive(&ctl.full[slot]);
                 }
+                if (turn == mine && ((bx.ok >> lane) & 1))
+                    tma_load_4d(sm + slot * C::SLOT + box * C::BOX + piece * g.br * 128, map, &ctl.full[slot], mt * 128 + box * 64,
+                                kvh, t.slot, t.page);
+                turn = turn + 1 == kLoadWarps ? 0 : turn + 1;
             }
+        };
+        for (int u = 0; !dead && more; ++u) {
+            if (k == sg.kb) {                        // a new row tile
+                if (seg > 0) dead = __any_sync(~0u, !mbar_wait(&ctl.q_empty, (seg - 1) & 1, abort_flag, p.wait_ns));
+                if (dead) break;
+                if (lane == 0) {
+                    if (mine == 0) mbar_arrive_expect_tx(&ctl.q_full, qbytes);
+                    else mbar_arrive(&ctl.q_full);
+#pragma unroll 1
+                    for (int b = mine; b < 2 * MT; b += kLoadWarps)
+                        tma_load_3d(sQ + b * C::QBOX, &qmap, &ctl.q_full, b * 64, sg.head0, sg.tok0);
+                }
+                ++seg;
+            }
+            // the pages of the next unit are looked up while this one's copies wait
+            const int kvh = sg.kvh;
+            PagedLook next{0, 0, false};
+            if (++k >= sg.ke) {
+                more = w.next(sg);
+                k = more ? sg.kb : 0;
+            }
+            if (more) next = paged_look(g, sg, sg.row0 + k * kPT, lane);
+            load(&kmap, cur, kvh, u);
+            if (!keep && !dead && u > 0) load(&vmap, prev, prev_h, -1);
+            prev = cur;
+            prev_h = kvh;
+            cur = next;
         }
+        if (!keep && !dead && units > 0) load(&vmap, prev, prev_h, -1);
         if (dead && lane == 0) {                     // a wait ran out: let the copies in flight land
             atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
             ctl.abort = 1;
@@ -222,122 +302,160 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- tensor core
-        if (lane == 0) {
-            PagedWalk w(g, sched);
-            PagedSeg sg;
-            uint32_t u = 0, seg = 0, pend_u = 0;
-            bool dead = false, pend = false, pend_first = false;
-            const uint32_t q0 = smem_u32(sQ), p0 = smem_u32(sP), t0 = smem_u32(sm);
-            const uint32_t idS = idesc_bf16_f32(kPT, N), idO = idS | (1u << 15) | (1u << 16);
-            auto pv = [&](uint32_t x, bool first) {  // O^T += V^T P^T of unit x
-                if (!mbar_wait(&ctl.p_full, x & 1, abort_flag, p.wait_ns)) return false;
-                uint32_t r = (p.shared ? x : 2 * x + 1) * MT;
+        PagedWalk w(g, sched);
+        PagedSeg sg;
+        uint32_t u = 0, seg = 0, pend_u = 0;
+        uint32_t edges = 0;
+        bool dead = false, pend = false, pend_first = false, pend_edge = false;
+        const bool one = elect_one();
+        // (the warp stays together: a wait that runs out does so for all lanes)
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return !__any_sync(~0u, !mbar_wait(bar, parity & 1, abort_flag, p.wait_ns)); };
+        const uint32_t q0 = smem_u32(sQ), t0 = smem_u32(sm);
+        const uint32_t idS = idesc_bf16_f32(kPT, N), idO = idesc_bf16_f32(128, N) | (1u << 15) | (1u << 16);
+        const uint64_t pdesc0 = sdesc_mnmajor_sw128(smem_u32(sP), kPT * 128, 1024u);
+        // (descriptors advance by 16-byte units)
+        auto pv = [&](uint32_t x, bool first, bool edge) {           // O^T += V^T P^T of unit x
+            if (!wait(&ctl.p_full[x & 1], x >> 1)) return false;
+            uint32_t r = v_place(keep, x, units) * MT;
+            if (!keep && edge) {                     // its rows come, and those that nobody sees are cleared
+                for (int mt = 0; mt < MT; ++mt)
+                    if (!wait(&ctl.full[(r + mt) % ST], (r + mt) / ST)) return false;
+                if (lane == 0) mbar_arrive(&ctl.v_ready);
+                if (!wait(&ctl.v_clean, edges)) return false;
+                ++edges;
+            }
+            const uint64_t pdesc = pdesc0 + (x % C::PN) * (C::PB / 16);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt, ++r) {
-                    const uint32_t slot = r % ST;
-                    if (!p.shared && !mbar_wait(&ctl.full[slot], (r / ST) & 1, abort_flag, p.wait_ns)) return false;
-                    tc_fence_after();
-                    const uint32_t a0 = t0 + slot * C::SLOT;
+            for (int mt = 0; mt < MT; ++mt, ++r) {
+                const uint32_t slot = r % ST;
+                if (!keep && !wait(&ctl.full[slot], r / ST)) return false;
+                tc_fence_after();
+                const uint64_t a = sdesc_mnmajor_sw128(t0 + slot * C::SLOT, C::BOX, 1024u);
+                const uint32_t d = tmem + static_cast<uint32_t>(C::OCOL + mt * N);
+                if (one) {
 #pragma unroll
                     for (int kk = 0; kk < kPT / 16; ++kk)
-                        umma_bf16(tmem + static_cast<uint32_t>(C::OCOL + mt * N),
-                                  sdesc_mnmajor_sw128(a0 + kk * 2048, C::BOX, 1024u),
-                                  sdesc_mnmajor_sw128(p0 + kk * 2048, kPT * 128, 1024u), idO,
-                                  (!first || kk > 0) ? 1u : 0u);
+                        umma_bf16(d, a + kk * 128, pdesc + kk * 128, idO, kk > 0 ? 1u : (first ? 0u : 1u));
                     umma_commit(&ctl.empty[slot]);
                 }
-                umma_commit(&ctl.pv_done);
-                return true;
-            };
-            while (!dead && w.next(sg)) {
-                dead = !mbar_wait(&ctl.q_full, seg & 1, abort_flag, p.wait_ns);
-                ++seg;
-                for (int k = sg.kb; k < sg.ke && !dead; ++k, ++u) {
-                    if (u >= 2) dead = !mbar_wait(&ctl.s_empty[u & 1], ((u >> 1) - 1) & 1, abort_flag, p.wait_ns);
-                    uint32_t r = (p.shared ? u : 2 * u) * MT;
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt, ++r) {       // S^T = K Q^T
-                        const uint32_t slot = r % ST;
-                        dead = dead || !mbar_wait(&ctl.full[slot], (r / ST) & 1, abort_flag, p.wait_ns);
-                        if (dead) break;
-                        tc_fence_after();
-                        const uint32_t a0 = t0 + slot * C::SLOT, b0 = q0 + mt * 2 * C::QBOX;
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            umma_bf16(tmem + (u & 1) * N, sdesc_kmajor_sw128(a0 + (kk >> 2) * C::BOX + (kk & 3) * 32),
-                                      sdesc_kmajor_sw128(b0 + (kk >> 2) * C::QBOX + (kk & 3) * 32), idS,
-                                      (mt > 0 || kk > 0) ? 1u : 0u);
-                        if (!p.shared) umma_commit(&ctl.empty[slot]);
-                    }
-                    if (dead) break;
-                    umma_commit(&ctl.s_full[u & 1]);
-                    if (k + 1 == sg.ke) umma_commit(&ctl.q_empty);
-                    if constexpr (!C::AHEAD) {
-                        dead = !pv(u, k == sg.kb);
-                    } else {
-                        if (pend) dead = !pv(pend_u, pend_first);
-                        pend = true;
-                        pend_u = u;
-                        pend_first = k == sg.kb;
+                __syncwarp();
+            }
+            if (one) umma_commit(&ctl.pv_done[x & 1]);
+            __syncwarp();
+            return true;
+        };
+        while (!dead && w.next(sg)) {
+            dead = !wait(&ctl.q_full, seg);
+            ++seg;
+            for (int k = sg.kb; k < sg.ke && !dead; ++k, ++u) {
+                uint32_t r = k_place(keep, u) * MT;
+                if (pend && keep) {
+                    // Whichever can start: this unit's scores (first, if both), or the product with V
+                    // of the unit before, whose slots this unit's rows may be waiting for. (Rows that
+                    // come in twice have their order.)
+                    const uint32_t last = r + MT - 1;
+                    const uint64_t t_start = global_timer_ns();
+                    for (uint32_t it = 1;; ++it) {
+                        if (__all_sync(~0u, mbar_test(&ctl.full[last % ST], (last / ST) & 1))) break;
+                        if (__all_sync(~0u, mbar_test(&ctl.p_full[pend_u & 1], (pend_u >> 1) & 1))) {
+                            dead = !pv(pend_u, pend_first, pend_edge);
+                            pend = false;
+                            break;
+                        }
+                        if ((it & 255u) == 0u &&
+                            __any_sync(~0u, *abort_flag != 0 || global_timer_ns() - t_start > p.wait_ns)) { dead = true; break; }
                     }
                 }
-            }
-            if (!dead && pend) dead = !pv(pend_u, pend_first);
-            if (dead) {
-                atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
-                ctl.abort = 1;
+                if (!dead && u >= 2) dead = !wait(&ctl.s_empty[u & 1], (u >> 1) - 1);
+                const uint32_t d = tmem + (u & 1) * N;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt, ++r) {           // S^T = K Q^T
+                    const uint32_t slot = r % ST;
+                    dead = dead || !wait(&ctl.full[slot], r / ST);
+                    if (dead) break;
+                    tc_fence_after();
+                    const uint64_t a = sdesc_kmajor_sw128(t0 + slot * C::SLOT), b = sdesc_kmajor_sw128(q0 + mt * 2 * C::QBOX);
+                    if (one) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_bf16(d, a + (kk >> 2) * (C::BOX / 16) + (kk & 3) * 2, b + (kk >> 2) * (C::QBOX / 16) + (kk & 3) * 2,
+                                      idS, mt > 0 || kk > 0 ? 1u : 0u);
+                        if (!keep) umma_commit(&ctl.empty[slot]);
+                    }
+                    __syncwarp();
+                }
+                if (dead) break;
+                if (one) {
+                    umma_commit(&ctl.s_full[u & 1]);
+                    if (k + 1 == sg.ke) umma_commit(&ctl.q_empty);
+                }
+                __syncwarp();
+                if (pend) dead = !pv(pend_u, pend_first, pend_edge);
+                pend = true;
+                pend_u = u;
+                pend_first = k == sg.kb;
+                pend_edge = unit_edge(g, sg, sg.row0 + k * kPT, ctl.bad[u & 7]);
             }
         }
-    } else if (warp >= 4) {
+        if (!dead && pend) dead = !pv(pend_u, pend_first, pend_edge);
+        if (dead && lane == 0) {
+            atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
+            ctl.abort = 1;
+        }
+    } else {
         // ---------------------------------------------------------------- softmax and output
         PagedWalk w(g, sched);
         PagedSeg sg;
-        const int st = tid - 128, q4 = warp & 3, half = (warp - 4) >> 2;
-        const int row = q4 * 32 + lane;                              // cache row of the unit, channel of an O tile
-        const int c0 = half * (N / 2);                               // first query column of this thread
+        const int st = tid - 128, q4 = warp & 3, grp = (warp - 4) >> 2;
+        const int c0 = grp * (N / kGroups);                          // columns of this thread's group
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-        uint32_t u = 0;
+        const int row = q4 * 32 + lane;                              // cache row of the unit, channel of an O tile
+        const uint64_t scale22 = pack_f32x2(p.scale2, p.scale2);
+        auto pv_over = [&](uint32_t x) { return mbar_wait(&ctl.pv_done[x & 1], (x >> 1) & 1, abort_flag, p.wait_ns); };
+        uint32_t u = 0, edges = 0;
         bool dead = false;
         int d_parts = 0, d_tok = 0, d_tn = 0, d_head = 0, d_hv = 0;
         long long at = sched.u0;                                     // first unit of the segment on the line
         while (w.next(sg)) {
             soft_sync();                                             // the tile before is written out
-            for (int c = st; c < N; c += kSoftThreads) {
-                const int t = c / g.hb, h = c - t * g.hb;
+            if (st < N) {
+                const int t = st / g.hb, h = st - t * g.hb;
                 const bool ok = t < sg.tn && h < sg.hv;
-                s_m[c] = ok ? -INFINITY : INFINITY;                  // (a column without a query gets P = 0)
-                ctl.tok[c] = ok ? t : 255;
+                s_nm[st] = ok ? INFINITY : -INFINITY;                // (a column without a query gets P = 0)
+                ctl.tok[st] = ok ? t : 255;
             }
             soft_sync();
             const int base = sg.q.L - sg.q.n + sg.t0;                // row of the tile's first token
-            float lacc[NC][32];                                      // this row's P per query, summed over the units
+            float sink = -INFINITY;                                  // of column st (read now, needed at the end)
+            if (p.sink && st < N && ctl.tok[st] != 255) sink = p.sink[sg.head0 + st - ctl.tok[st] * g.hb] * kLog2e;
+            uint64_t lacc[NE / 2];                                   // this row's P per query (pairs), summed over the units
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) lacc[n][i] = 0.f;
+            for (int i = 0; i < NE / 2; ++i) lacc[i] = 0ull;
             for (int k = sg.kb; k < sg.ke; ++k, ++u) {
                 if (!dead) dead = !mbar_wait(&ctl.s_full[u & 1], (u >> 1) & 1, abort_flag, p.wait_ns);
                 tc_fence_after();
-                const int j0 = sg.row0 + k * kPT, j = j0 + row;
+                const int j0 = sg.row0 + k * kPT;
                 const unsigned bad = *reinterpret_cast<volatile unsigned*>(&ctl.bad[u & 7]);
-                const bool edge = j0 < sg.lo_u || j0 + kPT > sg.hi_u || bad != 0;
+                const bool edge = unit_edge(g, sg, j0, bad);
                 const bool masked = edge || j0 < sg.lo_max || j0 + kPT > sg.hi_min;
-                const bool live = j >= sg.lo_u && j < sg.hi_u && !((bad >> (row / g.br)) & 1);
-                // this row is seen by the tile's tokens t_lo .. t_hi
-                const int t_lo = live ? j - base : 1, t_hi = live ? (g.window > 0 ? j - base + g.window - 1 : 254) : 0;
+                auto live = [&](int r) { return j0 + r >= sg.lo_u && j0 + r < sg.hi_u && !paged_bad_row(g, bad, r); };
                 const uint32_t scol = lane_base + (u & 1) * N + c0;
-                float x[32];
-                auto load_scores = [&](int n) {
-                    uint32_t r[32];
-                    DSV4_TMEM_LD_32x32b_X32(scol + n * 32, r);
+                float x[NE];
+                auto scores = [&] {
+                    uint32_t raw[NE];
+                    tmem_cols<NE>(scol, raw);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+                    for (int i = 0; i < NE; ++i) x[i] = __uint_as_float(raw[i]);
                 };
-                auto hide = [&](int n) {
+                auto hide = [&] {
+                    // this row is seen by the tile's tokens t_lo .. t_hi
+                    const bool on = live(row);
+                    const int t_lo = on ? j0 + row - base : 1;
+                    const int t_hi = on ? (g.window > 0 ? j0 + row - base + g.window - 1 : 254) : 0;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const uint32_t t4 = *reinterpret_cast<const uint32_t*>(ctl.tok + c0 + n * 32 + i);
+                    for (int i = 0; i < NE; i += 4) {
+                        const uint32_t t4 = *reinterpret_cast<const uint32_t*>(ctl.tok + c0 + i);
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
                             const int t = (t4 >> (8 * b)) & 255;
@@ -345,140 +463,158 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         }
                     }
                 };
-                auto less_ref = [&](int n) {         // base-2 scores relative to the references
+                auto less_ref = [&] {                // base-2 scores relative to the references
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 m4 = *reinterpret_cast<const float4*>(s_m + c0 + n * 32 + i);
-                        x[i] = fmaf(x[i], p.scale2, -m4.x);
-                        x[i + 1] = fmaf(x[i + 1], p.scale2, -m4.y);
-                        x[i + 2] = fmaf(x[i + 2], p.scale2, -m4.z);
-                        x[i + 3] = fmaf(x[i + 3], p.scale2, -m4.w);
+                    for (int i = 0; i < NE; i += 4) {
+                        ulonglong2 y = *reinterpret_cast<const ulonglong2*>(s_nm + c0 + i);
+                        uint64_t y0 = y.x, y1 = y.y;
+                        fma_f32x2(y0, pack_f32x2(x[i], x[i + 1]), scale22);
+                        fma_f32x2(y1, pack_f32x2(x[i + 2], x[i + 3]), scale22);
+                        unpack_f32x2(y0, x[i], x[i + 1]);
+                        unpack_f32x2(y1, x[i + 2], x[i + 3]);
                     }
-                    if (masked) hide(n);
+                    if (masked) hide();
                 };
-                float mx = -INFINITY;
+                // P = 2^(s - m) in bf16 (rounded: the tensor core takes bf16; the sum stays in fp32),
+                // the MN-major operand: a cache row's 64 queries are one 128-byte line
+                uint8_t* pbuf = sP + (u % C::PN) * C::PB;
+                auto put = [&] {
+                    // its place is free once the product that read it is done
+                    if (!dead && u >= C::PN) dead = !pv_over(u - C::PN);
 #pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    load_scores(n);
-                    less_ref(n);
+                    for (int i = 0; i < NE; ++i) x[i] = ex2(x[i]);
+                    uint8_t* line = pbuf + (c0 >> 6) * (kPT * 128) + (row >> 3) * 1024 + (row & 7) * 128;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, x[i]);
+                    for (int i = 0; i < NE / 8; ++i)
+                        *reinterpret_cast<uint4*>(line + (((((c0 & 63) >> 3) + i) ^ (row & 7)) << 4)) =
+                            make_uint4(pack2(x[8 * i], x[8 * i + 1]), pack2(x[8 * i + 2], x[8 * i + 3]),
+                                       pack2(x[8 * i + 4], x[8 * i + 5]), pack2(x[8 * i + 6], x[8 * i + 7]));
+                };
+                auto add_up = [&] {
+#pragma unroll
+                    for (int i = 0; i < NE; i += 2) add_f32x2(lacc[i / 2], pack_f32x2(x[i], x[i + 1]));
+                };
+                auto outrun = [&] {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < NE; i += 2) mx[(i >> 1) & 3] = fmaxf(fmaxf(x[i], x[i + 1]), mx[(i >> 1) & 3]);
+                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kSpan;
+                };
+                // A unit that outruns the references (the warps vote; a tile's first unit always) moves them.
+                // With few scores per thread the vote comes after P, so that the warps need not wait for
+                // one another between their steps, and P is formed again where it was too soon; with many,
+                // what is held across the vote would not fit.
+                bool rescale = false, over = k == sg.kb;
+                if (!over) {
+                    scores();
+                    less_ref();
+                    const bool mine = outrun();
+                    if (LATE) put();
+                    over = soft_sync_or(mine);
                 }
-                bool rescale = false, again = NC > 1;
-                if (soft_sync_or(mx > kSpan)) {
-                    // some score outruns its reference: reduce the unit's maxima and move the references
-                    again = true;
+                if (over) {                          // the unit's maxima, and the references above theirs
+                    scores();
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) {
-                        load_scores(n);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] *= p.scale2;
-                        if (masked) hide(n);
-                        atomicMax(&ctl.top[c0 + n * 32 + lane], float_to_key(lanes_reduce<true>(x, lane)));
-                    }
+                    for (int i = 0; i < NE; ++i) x[i] *= p.scale2;
+                    if (masked) hide();
+                    const float top = lanes_reduce<true>(x, lane);
+                    atomicMax(&ctl.top[c0 + (lane & (NE - 1))], float_to_key(top));
                     soft_sync();
-                    for (int c = st; c < N; c += kSoftThreads) {
-                        const float cm = key_to_float(ctl.top[c]);
-                        const float mo = s_m[c];
+                    if (st < N) {
+                        const float cm = key_to_float(ctl.top[st]);
+                        const float mo = -s_nm[st];
                         float f = 1.f;
                         if (cm > mo) {
                             f = mo == -INFINITY ? 0.f : ex2(mo - cm);
-                            s_m[c] = cm;
+                            s_nm[st] = -cm;
                             rescale = k > sg.kb;
                         }
-                        s_f[c] = f;
-                        ctl.top[c] = 0;
+                        s_f[st] = f;
+                        ctl.top[st] = 0;
                     }
                     rescale = soft_sync_or(rescale);
                     if (rescale) {
 #pragma unroll
-                        for (int n = 0; n < NC; ++n)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) lacc[n][i] *= s_f[c0 + n * 32 + i];
+                        for (int i = 0; i < NE; i += 2)
+                            lacc[i / 2] = mul_f32x2(lacc[i / 2], *reinterpret_cast<const uint64_t*>(s_f + c0 + i));
                     }
+                    scores();
+                    less_ref();
                 }
-                // P and O are free once the product before is done
-                if (!dead && u > 0) dead = !mbar_wait(&ctl.pv_done, (u - 1) & 1, abort_flag, p.wait_ns);
-                if (rescale) {
+                if (!LATE || over) put();
+                add_up();
+                if (rescale) {                       // O^T by the factors of the references that moved
+                    if (!dead) dead = !pv_over(u - 1);
                     tc_fence_after();
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) {
-                        for (int mt = 0; mt < MT; ++mt) {
-                            uint32_t r[32];
-                            const uint32_t ta = lane_base + C::OCOL + mt * N + c0 + n * 32;
-                            DSV4_TMEM_LD_32x32b_X32(ta, r);
+#pragma unroll 1
+                    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll 1
+                        for (int c = c0; c < c0 + N / kGroups; c += 8) {
+                            uint32_t r[8];
+                            const uint32_t ta = lane_base + C::OCOL + mt * N + c;
+                            DSV4_TMEM_LD_32x32b_X8(ta, r);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                r[i] = __float_as_uint(__uint_as_float(r[i]) * s_f[c0 + n * 32 + i]);
-                            DSV4_TMEM_ST_32x32b_X32(ta, r);
+                            for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * s_f[c + i]);
+                            DSV4_TMEM_ST_32x32b_X8(ta, r);
                         }
                     }
                     DSV4_TMEM_WAIT_ST();
                 }
-                // P = 2^(s - m) in bf16 (rounded: the tensor core takes bf16; the sum stays in fp32),
-                // the MN-major operand: row j's 64 queries are one 128-byte line
+                // Rows of the tile that nobody may see (past the cache, before the window, of a page that was
+                // not loaded) hold anything: as V they must not meet P = 0.
+                auto clear_rows = [&] {
+                    const int zr = st & (kPT - 1);
+                    if (live(zr)) return;
+#pragma unroll 1
+                    for (int b = st / kPT; b < 2 * MT; b += kSoftThreads / kPT) {
+                        const uint32_t slot = (v_place(keep, u, units) * MT + (b >> 1)) % ST;
+                        uint4* z = reinterpret_cast<uint4*>(sm + slot * C::SLOT + (b & 1) * C::BOX + zr * 128);
 #pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    if (again) {
-                        load_scores(n);
-                        less_ref(n);
+                        for (int i = 0; i < 8; ++i) z[i ^ (zr & 7)] = make_uint4(0, 0, 0, 0);    // (eight rows, eight banks)
                     }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        x[i] = ex2(x[i]);
-                        lacc[n][i] += x[i];
-                    }
-                    const int cb = c0 + n * 32;                      // first column of the piece
-                    uint8_t* prow = sP + (cb >> 6) * (kPT * 128) + (row >> 3) * 1024 + (row & 7) * 128;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c16 = ((cb & 63) >> 3) + i;
-                        *reinterpret_cast<uint4*>(prow + ((c16 ^ (row & 7)) << 4)) =
-                            make_uint4(pack2(x[8 * i], x[8 * i + 1]), pack2(x[8 * i + 2], x[8 * i + 3]),
-                                       pack2(x[8 * i + 4], x[8 * i + 5]), pack2(x[8 * i + 6], x[8 * i + 7]));
-                    }
-                }
-                if (edge) {
-                    // rows of the tile that nobody may see (past the cache, before the window, of a
-                    // page that was not loaded) hold anything: as V they must not meet P = 0
-                    uint32_t r = (p.shared ? u : 2 * u + 1) * MT;
-                    for (int mt = 0; mt < MT; ++mt, ++r) {
-                        const uint32_t slot = r % ST;
-                        if (!p.shared && !dead) dead = !mbar_wait(&ctl.full[slot], (r / ST) & 1, abort_flag, p.wait_ns);
-                        if (!live) {
-                            uint4* z = reinterpret_cast<uint4*>(sm + slot * C::SLOT + half * C::BOX + row * 128);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) z[i ^ (row & 7)] = make_uint4(0, 0, 0, 0);   // (eight rows, eight banks)
-                        }
-                    }
-                }
+                };
+                if (edge && keep) clear_rows();
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&ctl.s_empty[u & 1]);
-                    mbar_arrive(&ctl.p_full);
+                    mbar_arrive(&ctl.p_full[u & 1]);
+                }
+                if (edge && !keep) {
+                    if (!dead) dead = !mbar_wait(&ctl.v_ready, edges & 1, abort_flag, p.wait_ns);
+                    ++edges;
+                    clear_rows();
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.v_clean);
                 }
             }
             // ---------------------------------------------------------------- the tile's results
-            if (!dead) dead = !mbar_wait(&ctl.pv_done, (u - 1) & 1, abort_flag, p.wait_ns);
+            if (!dead) dead = !pv_over(u - 1);
             tc_fence_after();
             float* red = reinterpret_cast<float*>(sP);               // [4][N] (P is read)
+            {
+                float l[NE];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) red[q4 * N + c0 + n * 32 + lane] = lanes_reduce<false>(lacc[n], lane);
+                for (int i = 0; i < NE; i += 2) unpack_f32x2(lacc[i / 2], l[i], l[i + 1]);
+                const float sum = lanes_reduce<false>(l, lane);
+                if (lane < NE) red[q4 * N + c0 + lane] = sum;
+            }
             soft_sync();
             const bool whole = sg.kb == 0 && sg.ke == sg.n;
-            const int slot2 = blockIdx.x * 2 + (sg.kb > 0 ? 0 : 1);
-            for (int c = st; c < N; c += kSoftThreads) {
+            const int slot2 = worker * 2 + (sg.kb > 0 ? 0 : 1);
+            if (st < N) {
+                const int c = st;
                 const float l = (red[c] + red[N + c]) + (red[2 * N + c] + red[3 * N + c]);
-                const float m = s_m[c];
+                const float m = -s_nm[c];
                 const int t = ctl.tok[c];
                 if (whole) {
                     float f = 0.f;
                     if (t != 255) {
                         const int h = sg.head0 + c - t * g.hb;
-                        const float snk = p.sink ? p.sink[h] * kLog2e : -INFINITY;
+                        const float snk = sink;
                         const float M = fmaxf(m, snk);
                         const float e = m == -INFINITY ? 0.f : exp2f(m - M);
                         const float den = l * e + (snk == -INFINITY ? 0.f : exp2f(snk - M));
@@ -495,53 +631,61 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 }
             }
             soft_sync();
+            const int cols = (sg.tn - 1) * g.hb + sg.hv;             // (no query behind them)
             float* po = p.part_o + static_cast<size_t>(slot2) * N * D;
             __nv_bfloat16* ob = p.out + (static_cast<size_t>(sg.tok0) * g.H + sg.head0) * D;
+            const int r0 = D - 2 * p.or_pairs;
+#pragma unroll 1
+            for (int cb = c0; cb < c0 + NE && cb < cols; cb += 16) {
+                // Two columns at a time: even lanes write the first, odd lanes the second, each a pair
+                // of neighbouring channels.
+                float f[16];
+                int off[8], tok[8];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                const int cb = c0 + n * 32;
+                for (int i = 0; i < 16; ++i) f[i] = s_f[cb + i];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = cb + 2 * i + (lane & 1), t = ctl.tok[c];
+                    tok[i] = t;
+                    off[i] = t == 255 ? -1 : (t * g.H + c - t * g.hb) * D;
+                }
+#pragma unroll 1
                 for (int mt = 0; mt < MT; ++mt) {
-                    uint32_t r[32];
-                    DSV4_TMEM_LD_32x32b_X32(lane_base + C::OCOL + mt * N + cb, r);
+                    uint32_t r[16];
+                    DSV4_TMEM_LD_32x32b_X16(lane_base + C::OCOL + mt * N + cb, r);
                     tmem_wait_ld();
                     if (!whole) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (ctl.tok[cb + i] != 255) po[(cb + i) * D + mt * 128 + row] = __uint_as_float(r[i]);
+                        for (int i = 0; i < 16; ++i) po[(cb + i) * D + mt * 128 + row] = __uint_as_float(r[i]);
                         continue;
                     }
-                    // two columns at a time: even lanes write the first, odd lanes the second, each
-                    // a pair of neighbouring channels
-                    const int d = mt * 128 + (row & ~1), pair = (d - (D - 2 * p.or_pairs)) >> 1;
-                    const bool rot = p.orp && d >= D - 2 * p.or_pairs;
+                    const int d = mt * 128 + (row & ~1);             // this lane's pair of channels
+                    const bool rot = p.orp && d >= r0;
                     int rt = -1;
                     float2 cs = make_float2(1.f, 0.f);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
+                    for (int i = 0; i < 8; ++i) {
                         // (a factor of 0 stands for a query that sees nothing: O may hold anything)
-                        const float f0 = s_f[cb + i], f1 = s_f[cb + i + 1];
-                        const float a = f0 == 0.f ? 0.f : __uint_as_float(r[i]) * f0;
-                        const float b = f1 == 0.f ? 0.f : __uint_as_float(r[i + 1]) * f1;
+                        const float a = f[2 * i] == 0.f ? 0.f : __uint_as_float(r[2 * i]) * f[2 * i];
+                        const float b = f[2 * i + 1] == 0.f ? 0.f : __uint_as_float(r[2 * i + 1]) * f[2 * i + 1];
                         const float got = __shfl_xor_sync(~0u, (lane & 1) ? a : b, 1);
                         float e = (lane & 1) ? got : a, o = (lane & 1) ? b : got;
-                        const int c = cb + i + (lane & 1), t = ctl.tok[c];
-                        if (t == 255) continue;
-                        if (rot) {
-                            if (t != rt) { cs = out_rope_cs(p, sg.tok0 + t, pair); rt = t; }
+                        if (rot && tok[i] != 255) {
+                            if (tok[i] != rt) { cs = out_rope_cs(p, sg.tok0 + tok[i], (d - r0) >> 1); rt = tok[i]; }
                             const float e0 = e;
                             e = e0 * cs.x + o * cs.y;
                             o = -e0 * cs.y + o * cs.x;
                         }
-                        *reinterpret_cast<uint32_t*>(ob + (t * g.H + c - t * g.hb) * D + d) = pack2(e, o);
+                        if (off[i] >= 0) *reinterpret_cast<uint32_t*>(ob + off[i] + d) = pack2(e, o);
                     }
                 }
             }
-            if (!whole && sg.kb == 0) {                              // this CTA starts the tile: it is merged under its number
+            if (!whole && sg.kb == 0) {                              // this worker starts the tile: it is merged under its number
                 const long long end = at + sg.n, T = sched.total;
                 int last = static_cast<int>((end * sched.ge - 1) / T);
                 while (last + 1 < sched.ge && T * (last + 1) / sched.ge < end) ++last;
                 while (T * last / sched.ge >= end) --last;
-                d_parts = last - static_cast<int>(blockIdx.x) + 1;
+                d_parts = last - worker + 1;
                 d_tok = sg.tok0;
                 d_tn = sg.tn;
                 d_head = sg.head0;
@@ -554,7 +698,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             ctl.abort = 1;
         }
         if (st == 0) {
-            int* d = p.desc + blockIdx.x * 8;
+            int* d = p.desc + worker * 8;
             d[0] = d_parts; d[1] = d_tok; d[2] = d_tn; d[3] = d_head; d[4] = d_hv;
         }
     }
@@ -730,7 +874,8 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int ctas, uint32_t
     }
 }
 
-// Query columns per row tile: 128 where chunks fill them and the accumulators fit.
+// Query columns per row tile: 64 for single tokens and small groups; else as many as the
+// accumulators and two K/V tiles leave room for.
 int tile_queries(const dsv4_paged_attn_args& a) {
     const long long rows = static_cast<long long>(a.max_q) * (a.heads / a.kv_heads);
     return a.dim == 512 || rows <= 64 ? 64 : 128;
@@ -746,12 +891,18 @@ int run(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_
     using C = PCfg<D, N>;
     PagedAttnParams p{};
     p.g = paged_geom(a.block_table, a.cu_q, a.kv_len, a.batch, a.total_q, a.max_pages, a.page_size, a.num_pages, a.heads,
-                     a.kv_heads, a.window);
+                     a.kv_heads, a.window, kPT);
     paged_tile(p.g, N);
     CUtensorMap qmap, kmap, vmap;
     if (!paged_query_map(&qmap, a.q, D, a.heads, a.total_q, a.q_stride, p.g.hb, p.g.tpt) ||
-        !paged_pool_map(&kmap, a.k_pages, D, a.kv_heads, a.page_size, a.num_pages, p.g.br) ||
-        !paged_pool_map(&vmap, a.v_pages ? a.v_pages : a.k_pages, D, a.kv_heads, a.page_size, a.num_pages, p.g.br))
+        !paged_pool_map(&kmap, a.k_pages, D, a.kv_heads, a.page_size, a.num_pages, p.g.br))
+        return DSV4_ERR_LAUNCH;
+    if (!a.v_pages) vmap = kmap;
+    else if (!paged_pool_map(&vmap, a.v_pages, D, a.kv_heads, a.page_size, a.num_pages, p.g.br)) return DSV4_ERR_LAUNCH;
+    auto kern = paged_attn_kernel<D, N>;
+    if (once_per_device(reinterpret_cast<const void*>(kern), kAttrLaunch, [kern] {
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        }) != cudaSuccess)
         return DSV4_ERR_LAUNCH;
     const int ctas = attn_ctas();
     const size_t ml = align_up(static_cast<size_t>(ctas) * 2 * N * 2 * 4, 256);
@@ -770,15 +921,11 @@ int run(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_
     p.shared = a.v_pages == nullptr;
     p.min_units = 2;
     p.wait_ns = kDefaultWaitNs;
-    auto kern = paged_attn_kernel<D, N>;
-    if (once_per_device(reinterpret_cast<const void*>(kern), kAttrLaunch, [kern] {
-            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        }) != cudaSuccess)
-        return DSV4_ERR_LAUNCH;
     count_launch();
     if (launch_k(kern, dim3(ctas), dim3(kThreads), C::SMEM, st, true, qmap, kmap, vmap, p) != cudaSuccess) return DSV4_ERR_LAUNCH;
     count_launch();
-    if (launch_k(paged_merge_kernel<D, N>, dim3(ctas * 2), dim3(kMergeThreads), 0, st, true, p, ctas, eword) != cudaSuccess)
+    if (launch_k(paged_merge_kernel<D, N>, dim3(ctas * 2), dim3(kMergeThreads), 0, st, true, p, ctas, eword) !=
+        cudaSuccess)
         return DSV4_ERR_LAUNCH;
     return DSV4_OK;
 }
@@ -786,7 +933,7 @@ int run(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_
 }  // namespace
 
 PagedGeom paged_geom(const int32_t* table, const int32_t* cu_q, const int32_t* kv_len, int batch, int total_q, int max_pages,
-                     int page_size, int num_pages, int heads, int kv_heads, int window) {
+                     int page_size, int num_pages, int heads, int kv_heads, int window, int unit) {
     PagedGeom g{};
     g.table = table;
     g.cu_q = cu_q;
@@ -800,7 +947,8 @@ PagedGeom paged_geom(const int32_t* table, const int32_t* cu_q, const int32_t* k
     g.KV = kv_heads;
     g.G = heads / kv_heads;
     g.window = static_cast<long long>(max_pages) * page_size <= window ? 0 : window;   // (no effect: none)
-    g.br = paged_box_rows(page_size);
+    g.unit = unit;
+    g.br = paged_box_rows(page_size, unit);
     return g;
 }
 
@@ -821,8 +969,8 @@ bool paged_pool_map(CUtensorMap* map, const void* pages, int D, int kv_heads, in
 }
 
 size_t paged_attn_ws_bytes(const dsv4_paged_attn_args& a) {
-    const size_t n = static_cast<size_t>(attn_ctas()) * 2 * tile_queries(a);
-    return align_up(n * 2 * 4, 256) + n * a.dim * 4 + static_cast<size_t>(attn_ctas()) * 9 * 4;
+    const size_t ctas = attn_ctas(), n = ctas * 2 * tile_queries(a);
+    return align_up(n * 2 * 4, 256) + n * a.dim * 4 + ctas * 9 * 4;
 }
 
 int launch_paged_attn(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t st) {

@@ -23,6 +23,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8, kSoftThreads = 256, kSoftBar = 1;
 constexpr int kN = 128;                  // query columns
+constexpr int kPT = 128;                 // cache rows per tile
 constexpr int kSB = 4;                   // accumulators (TMEM)
 constexpr int kMaxSplit = 64;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -218,7 +219,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         WWalk w(p, pref, sched);
         WItem it;
         PagedSeg sg{};
-        const int pieces = kPT / g.br;
+        const int piece = lane >> 1;
         const uint32_t qbox = static_cast<uint32_t>(g.hb) * g.tpt * 128;
         uint32_t ring = 0, res = 0, unit = 0;
         WStay stays;
@@ -226,13 +227,13 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         while (!dead && w.next(it)) {
             if (it.tt1 <= it.tt0) continue;
             w.bounds(it, sg);
-            const PagedTile t = paged_tile_boxes(g, sg, it.row0, lane);
+            const PagedLook t = paged_look(g, sg, it.row0, lane);
+            const PagedBoxes bx = paged_boxes(g, t);
             auto k_box = [&](uint8_t* dst, uint64_t* bar, int kvh, int b) {   // whole warp; the bytes are announced
-                const int piece = lane & (pieces - 1);
-                if (lane < pieces && ((t.ok >> piece) & 1))
+                if ((lane & 1) == 0 && ((bx.ok >> lane) & 1))
                     tma_load_4d(dst + piece * g.br * 128, &kmap, bar, b * 64, kvh, t.slot, t.page);
             };
-            const uint32_t kbox = static_cast<uint32_t>(__popc(t.ok)) * g.br * 128;
+            const uint32_t kbox = static_cast<uint32_t>(__popc(bx.ok)) * g.br * 64;
             for (int kvh = 0; kvh < g.KV && !dead; ++kvh) {
                 for (int x = it.tt0 * g.nhb; x < it.tt1 * g.nhb && !dead; ++x, ++unit) {
                     const int tt = x / g.nhb, blk = x - tt * g.nhb;
@@ -254,8 +255,8 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         ++res;
                     }
                     if (lane == 0) {
-                        s_bad[unit & 15] = t.bad;
-                        if (t.bad) atomicOr(&s_err, DSV4_EWORD_BAD_INDEX);
+                        s_bad[unit & 15] = bx.bad;
+                        if (bx.bad) atomicOr(&s_err, DSV4_EWORD_BAD_INDEX);
                     }
                     for (int b = 0; b < NB; ++b, ++ring) {
                         const uint32_t slot = ring % RS;
@@ -372,7 +373,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         if (!dead) dead = !mbar_wait(&s_full[sb], (u / SB) & 1, &abort_flag, p.wait_ns);
                         tc_fence_after();
                         const unsigned bad = *reinterpret_cast<volatile unsigned*>(&s_bad[u & 15]);
-                        const bool live = j < rows && !((bad >> (row / g.br)) & 1);
+                        const bool live = j < rows && !paged_bad_row(g, bad, row);
                         // every token of the tile sees every row of the unit
                         const bool open = it.row0 + kPT <= paged_hi(it.q, t0) &&
                                           it.row0 >= paged_lo(g, it.q, t0 + tn - 1);
@@ -485,7 +486,7 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
     using C = WCfg<D>;
     PagedWeightsParams p{};
     p.g = paged_geom(a.block_table, a.cu_q, a.kv_len, a.batch, a.total_q, a.max_pages, a.page_size, a.num_pages, a.heads,
-                     a.kv_heads, a.window);
+                     a.kv_heads, a.window, kPT);
     paged_tile(p.g, kN);
     CUtensorMap qmap, kmap;
     if (!paged_query_map(&qmap, a.q, D, a.heads, a.total_q, a.q_stride, p.g.hb, p.g.tpt) ||

@@ -336,7 +336,7 @@ int dsv4_quantize_rows_fp8(const void* x, int rows, int dim, void* q, float* sca
  * PERFORMANCE_AUDIT.md, the sliding-window cache; ARCHITECTURE_AND_MEMORY_AUDIT.md PART 2);
  * the paged form and the eviction are this library's own.
  *
- * Common rules. dim: 128, 256 or 512 (512: shared-KV only). heads: a multiple of kv_heads,
+ * Common rules. dim: 128, 256 or 512. heads: a multiple of kv_heads,
  * 1..1024. page_size: a multiple of 8, 8..65536. Sequence s owns the tokens
  * cu_q[s] .. cu_q[s+1]-1 of the batch (cu_q[0] >= 0, not decreasing); tokens past cu_q[batch]
  * are not read and their outputs are left as they were. These tokens are the newest of the

@@ -101,7 +101,8 @@ def attend(c, q, cu, *, window=0, sink=None, lse=True, max_q=None, pos=None, rop
 
 # ------------------------------------------------------------------ attention
 SHAPES = [(64, 1, 512, True), (8, 1, 128, True), (16, 1, 256, True), (32, 4, 128, False), (5, 5, 128, False),
-          (12, 2, 256, False), (1, 1, 512, True), (128, 1, 512, True), (96, 1, 128, True), (200, 1, 256, True)]
+          (12, 2, 256, False), (1, 1, 512, True), (128, 1, 512, True), (96, 1, 128, True), (200, 1, 256, True),
+          (24, 3, 512, False)]
 
 
 @pytest.mark.parametrize("H, KV, D, shared", SHAPES)

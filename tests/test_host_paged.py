@@ -76,7 +76,7 @@ def test_norm_rope_rejects_on_host(lib, bad):
 
 
 @pytest.mark.parametrize("bad", TABLES + QUERIES + [
-    dict(v_pages=_p(10)),                           # K and V apart at 512 channels: not offered
+    dict(v_pages=_p(10, 8)),
     dict(out=None), dict(lse=_p(8, 2)), dict(sink=_p(6, 2)), dict(out_rope_pos=_p(9, 4)), dict(out_rope_dim=0), dict(out_rope_dim=65),
     dict(out_rope_dim=130), dict(out_rope_theta=-1.0)])
 def test_attention_rejects_on_host(lib, bad):
