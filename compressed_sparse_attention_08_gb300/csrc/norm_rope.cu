@@ -12,7 +12,8 @@
 // few tokens, a share of one token's heads): the token's angles are formed once (fp64, Cody-
 // Waite reduced) into shared memory while the first rows are already on their way; a row lies
 // in 16 or 32 lanes, 8 channels (one 16-byte load) per lane and vector, so its pairs stay inside
-// a thread and the sum of squares takes four or five shuffles.
+// a thread and the sum of squares takes four or five shuffles. Six such loads per thread are in
+// flight at once.
 #include <cmath>
 
 #include "internal.h"
@@ -22,6 +23,7 @@ namespace dsv4 {
 namespace {
 
 constexpr int kT = 256, kMaxPairs = 64;
+constexpr int kLoads = 6;                // 16-byte loads of a thread in flight
 
 struct NormRopeParams {
     const __nv_bfloat16 *q, *k, *v;
@@ -45,6 +47,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int LR = D >= 256 ? 32 : 16;               // lanes per row
     constexpr int VL = D / (8 * LR);                     // 16-byte vectors per lane
     constexpr int RP = kT / LR;                          // rows per pass
+    constexpr int U = kLoads / VL;                       // passes whose loads are in flight together
     __shared__ float2 cs[kMaxPairs];
     const int tid = threadIdx.x, sub = tid / LR, l = tid % LR;
     const int tok = blockIdx.x / p.split, part = blockIdx.x - tok * p.split;
@@ -52,18 +55,22 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     const int r1 = static_cast<int>(static_cast<long long>(p.rows) * (part + 1) / p.split);
     pdl_trigger();
     pdl_wait();
+    uint4 x[U][VL];
     // rows of a token: its query heads, its keys, its values
-    auto load = [&](int r, uint4 (&x)[VL]) {
-        const __nv_bfloat16* src;
-        if (r < p.heads) src = p.q + tok * p.q_stride + static_cast<long long>(r) * D;
-        else if (r < p.heads + p.kv_heads) src = p.k + tok * p.k_stride + static_cast<long long>(r - p.heads) * D;
-        else src = p.v + tok * p.v_stride + static_cast<long long>(r - p.heads - p.kv_heads) * D;
+    auto load = [&](int base) {
 #pragma unroll
-        for (int i = 0; i < VL; ++i) x[i] = *reinterpret_cast<const uint4*>(src + (i * LR + l) * 8);
+        for (int u = 0; u < U; ++u) {
+            const int r = base + u * RP;
+            if (r >= r1) continue;
+            const __nv_bfloat16* src;
+            if (r < p.heads) src = p.q + tok * p.q_stride + static_cast<long long>(r) * D;
+            else if (r < p.heads + p.kv_heads) src = p.k + tok * p.k_stride + static_cast<long long>(r - p.heads) * D;
+            else src = p.v + tok * p.v_stride + static_cast<long long>(r - p.heads - p.kv_heads) * D;
+#pragma unroll
+            for (int i = 0; i < VL; ++i) x[u][i] = *reinterpret_cast<const uint4*>(src + (i * LR + l) * 8);
+        }
     };
-    uint4 x[VL], nx[VL];
-    int r = r0 + sub;
-    if (r < r1) load(r, x);
+    load(r0 + sub);
     const long long slot = p.slots ? p.slots[tok] : -1;
     if (tid < p.pairs) {
         float sn, c;
@@ -72,39 +79,42 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     }
     __syncthreads();
     const int rope0 = D - 2 * p.pairs;
-    for (; __any_sync(~0u, r < r1); r += RP) {
-        if (r + RP < r1) load(r + RP, nx);
-        const bool on = r < r1, is_q = r < p.heads, is_v = r >= p.heads + p.kv_heads;
-        float f[VL][8], ss = 0.f;
+    for (int base = r0 + sub; __any_sync(~0u, base < r1); base += U * RP) {
 #pragma unroll
-        for (int i = 0; i < VL; ++i) {
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int u = 0; u < U; ++u) {
+            const int r = base + u * RP;
+            const bool on = r < r1, is_q = r < p.heads, is_v = r >= p.heads + p.kv_heads;
+            if (!__any_sync(~0u, on)) break;
+            float f[VL][8], ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[i][2 * j] = bf16_lo(w[j]);
-                f[i][2 * j + 1] = bf16_hi(w[j]);
-                ss = fmaf(f[i][2 * j], f[i][2 * j], ss);
-                ss = fmaf(f[i][2 * j + 1], f[i][2 * j + 1], ss);
+            for (int i = 0; i < VL; ++i) {
+                const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[i][2 * j] = bf16_lo(w[j]);
+                    f[i][2 * j + 1] = bf16_hi(w[j]);
+                    ss = fmaf(f[i][2 * j], f[i][2 * j], ss);
+                    ss = fmaf(f[i][2 * j + 1], f[i][2 * j + 1], ss);
+                }
             }
-        }
 #pragma unroll
-        for (int w = LR / 2; w; w >>= 1) ss += __shfl_xor_sync(~0u, ss, w);
-        const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-        __nv_bfloat16* dst = nullptr;
-        if (on) {
-            if (is_q) {
-                dst = p.q_out + tok * p.q_out_stride + static_cast<long long>(r) * D;
-            } else if (slot >= 0 && slot < p.n_slots) {
-                const int h = r - p.heads - (is_v ? p.kv_heads : 0);
-                dst = (is_v ? p.v_pages : p.k_pages) + (slot * p.kv_heads + h) * D;
+            for (int w = LR / 2; w; w >>= 1) ss += __shfl_xor_sync(~0u, ss, w);
+            const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
+            __nv_bfloat16* dst = nullptr;
+            if (on) {
+                if (is_q) {
+                    dst = p.q_out + tok * p.q_out_stride + static_cast<long long>(r) * D;
+                } else if (slot >= 0 && slot < p.n_slots) {
+                    const int h = r - p.heads - (is_v ? p.kv_heads : 0);
+                    dst = (is_v ? p.v_pages : p.k_pages) + (slot * p.kv_heads + h) * D;
+                }
             }
-        }
-        if (dst) {
+            if (!dst) continue;
             const float* gamma = is_q ? p.gamma_q : p.gamma_k;
 #pragma unroll
             for (int i = 0; i < VL; ++i) {
                 const int c0 = (i * LR + l) * 8;
-                uint4 y = x[i];
+                uint4 y = x[u][i];
                 if (!is_v) {
                     float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
                     if (gamma) {
@@ -131,8 +141,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
                 *reinterpret_cast<uint4*>(dst + c0) = y;
             }
         }
-#pragma unroll
-        for (int i = 0; i < VL; ++i) x[i] = nx[i];
+        load(base + U * RP);
     }
 }
 

@@ -710,167 +710,112 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
 }
 
 // Merges the partial results of the row tiles that several CTAs worked on, and gathers the error
-// bits. An item is one query of such a tile. Tiles cut into up to kWarpParts parts (borders
-// between CTAs) take a warp per item, its lanes over the channels; tiles over more CTAs (a few
-// long rows) a block per item, its threads over channels x groups of parts, so that all the
-// loads of an item are in flight at once.
-constexpr int kMergeThreads = 512;
-template <int D> constexpr int kWarpParts = D == 512 ? 4 : 8;
+// bits. An item is 128 channels of one query of such a tile: one warp, four channels per lane, so
+// that one sequence's 64 queries over all CTAs and many short tiles alike spread over the device,
+// and eight parts' loads are in flight at once. (A block per query took three times as long.)
+constexpr int kMergeThreads = 256;
 
-struct MergeItem { int first, parts, tok, h, c; };
-
-// e^(m - top) of the parts this lane holds (part lane, lane + 32, ..), and the denominator's inverse.
-template <int N>
-__device__ __forceinline__ size_t part_slot(int first, int i, int c) {
+__device__ __forceinline__ size_t part_slot(int first, int i, int N, int c) {
     return static_cast<size_t>(i ? (first + i) * 2 : first * 2 + 1) * N + c;
-}
-template <int N, int PL>
-__device__ __forceinline__ float merge_factors(const PagedAttnParams& p, const MergeItem& it, int lane, float (&w)[PL]) {
-    float l[PL], M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < PL; ++k) {
-        const int i = lane + 32 * k;
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (i < it.parts) ml = *reinterpret_cast<const float2*>(p.part_ml + part_slot<N>(it.first, i, it.c) * 2);
-        w[k] = ml.x;
-        l[k] = ml.y;
-        M = fmaxf(M, ml.x);
-    }
-#pragma unroll
-    for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
-    const float snk = p.sink ? p.sink[it.h] * kLog2e : -INFINITY;
-    const float top = fmaxf(M, snk);
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < PL; ++k) {
-        w[k] = w[k] == -INFINITY ? 0.f : exp2f(w[k] - top);
-        sum += w[k] * l[k];
-    }
-#pragma unroll
-    for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
-    const float den = sum + (snk == -INFINITY ? 0.f : exp2f(snk - top));
-    if (lane == 0 && p.lse)
-        p.lse[static_cast<size_t>(it.tok) * p.g.H + it.h] = top == -INFINITY ? -INFINITY : top * kLn2 + logf(den);
-    return M == -INFINITY ? 0.f : 1.f / den;
-}
-
-// Four neighbouring channels of a merged output: factor, inverse rotation, bf16.
-template <int D>
-__device__ __forceinline__ void merge_store(const PagedAttnParams& p, const MergeItem& it, int ch, float4 a, float f) {
-    float o[4] = {a.x * f, a.y * f, a.z * f, a.w * f};
-    if (p.orp && ch >= D - 2 * p.or_pairs - 2) {
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            const int pair = (ch + i - (D - 2 * p.or_pairs)) >> 1;
-            if (pair >= 0) {
-                const float2 cs = out_rope_cs(p, it.tok, pair);
-                const float e0 = o[i], o0 = o[i + 1];
-                o[i] = e0 * cs.x + o0 * cs.y;
-                o[i + 1] = -e0 * cs.y + o0 * cs.x;
-            }
-        }
-    }
-    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(it.tok) * p.g.H + it.h) * D + ch) =
-        make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
 }
 
 template <int D, int N>
 __global__ void __launch_bounds__(kMergeThreads)
 paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int ctas, uint32_t* eword) {
-    constexpr int LD = D / 4, GR = kMergeThreads / LD, WV = D / 128, PL = 5;
-    __shared__ int few[160], many[160], n_few, n_many;
-    __shared__ float wgt[32 * PL];
-    __shared__ float4 acc[GR][LD];
-    __shared__ float s_inv;
+    constexpr int CH = D / 128, PL = 5;  // chunks of a query; parts per lane (at most 160)
+    __shared__ int starts[160], d_s[160][5], n_starts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
-    if (warp == 0) {                     // the tiles to merge, by the CTA that starts each
-        int a = 0, b = 0;
+    // the tiles to merge, by the CTA that starts each
+    if (warp == 0) {
+        int n = 0;
         uint32_t err = 0;
         for (int c0 = 0; c0 < ctas; c0 += 32) {
             const int c = c0 + lane;
             const int np = c < ctas ? p.desc[c * 8] : 0;
             if (c < ctas) err |= p.err[c];
-            const unsigned lt = (1u << lane) - 1;
-            const unsigned f = __ballot_sync(~0u, np > 0 && np <= kWarpParts<D>), m = __ballot_sync(~0u, np > kWarpParts<D>);
-            if ((f >> lane) & 1) few[a + __popc(f & lt)] = c;
-            if ((m >> lane) & 1) many[b + __popc(m & lt)] = c;
-            a += __popc(f);
-            b += __popc(m);
+            const unsigned m = __ballot_sync(~0u, np > 0);
+            if (np > 0) starts[n + __popc(m & ((1u << lane) - 1))] = c;
+            n += __popc(m);
         }
         err = __reduce_or_sync(~0u, err);
         if (lane == 0) {
-            n_few = a;
-            n_many = b;
+            n_starts = n;
             if (blockIdx.x == 0) *eword = err;
         }
+    } else if (tid - 32 < ctas) {
+        for (int c = tid - 32; c < ctas; c += kMergeThreads - 32)
+            for (int i = 0; i < 5; ++i) d_s[c][i] = p.desc[c * 8 + i];
     }
     __syncthreads();
-    auto item = [&](int first, int c, MergeItem& it) {
-        const int* d = p.desc + first * 8;
-        const int t = c / p.g.hb, hh = c - t * p.g.hb;
-        it = MergeItem{first, d[0], d[1] + t, d[3] + hh, c};
-        return t < d[2] && hh < d[4];
-    };
-    MergeItem it;
-    for (int x = blockIdx.x; x < n_many * N; x += gridDim.x) {
-        if (!item(many[x / N], x % N, it)) continue;
-        if (warp == 0) {
-            float w[PL];
-            const float inv = merge_factors<N, PL>(p, it, lane, w);
-#pragma unroll
-            for (int k = 0; k < PL; ++k) wgt[lane + 32 * k] = w[k];
-            if (lane == 0) s_inv = inv;
-        }
-        __syncthreads();
-        const int dl = tid % LD, gr = tid / LD;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int i = gr; i < it.parts; i += GR) {
-            const float e = wgt[i];
-            const float4 v = *reinterpret_cast<const float4*>(p.part_o + part_slot<N>(it.first, i, it.c) * D + dl * 4);
-            if (e != 0.f) {
-                a.x = fmaf(e, v.x, a.x); a.y = fmaf(e, v.y, a.y);
-                a.z = fmaf(e, v.z, a.z); a.w = fmaf(e, v.w, a.w);
-            }
-        }
-        acc[gr][dl] = a;
-        __syncthreads();
-        if (gr == 0) {
-            for (int i = 1; i < GR; ++i) {
-                const float4 v = acc[i][dl];
-                a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-            }
-            merge_store<D>(p, it, dl * 4, a, s_inv);
-        }
-        __syncthreads();
-    }
     constexpr int WB = kMergeThreads / 32;
-    for (int x = blockIdx.x * WB + warp; x < n_few * N; x += gridDim.x * WB) {
-        if (!item(few[x / N], x % N, it)) continue;
-        float4 v[kWarpParts<D>][WV];        // every load first
+    for (int x = blockIdx.x * WB + warp; x < n_starts * N * CH; x += gridDim.x * WB) {
+        const int first = starts[x / (N * CH)], rest = x % (N * CH), c = rest / CH, ch = (rest % CH) * 128 + lane * 4;
+        const int* d = d_s[first];
+        const int np = d[0], t = c / p.g.hb, hh = c - t * p.g.hb;
+        if (t >= d[2] || hh >= d[4]) continue;
+        const int h = d[3] + hh, tok = d[1] + t;
+        float w[PL], l[PL], M = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kWarpParts<D>; ++i)
+        for (int k = 0; k < PL; ++k) {
+            const int i = lane + 32 * k;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (i < np) ml = *reinterpret_cast<const float2*>(p.part_ml + part_slot(first, i, N, c) * 2);
+            w[k] = ml.x;
+            l[k] = ml.y;
+            M = fmaxf(M, ml.x);
+        }
+        const float snk = p.sink ? p.sink[h] * kLog2e : -INFINITY;
+        float4 v[8];                     // (the first parts' loads do not wait for the factors)
+        const float* po = p.part_o + ch;
 #pragma unroll
-            for (int k = 0; k < WV; ++k)
-                if (i < it.parts)
-                    v[i][k] = *reinterpret_cast<const float4*>(p.part_o + part_slot<N>(it.first, i, it.c) * D + k * 128 + lane * 4);
-        float w[1];
-        const float inv = merge_factors<N, 1>(p, it, lane, w);
-        float4 a[WV] = {};
+        for (int i = 0; i < 8; ++i)
+            if (i < np) v[i] = *reinterpret_cast<const float4*>(po + part_slot(first, i, N, c) * D);
 #pragma unroll
-        for (int i = 0; i < kWarpParts<D>; ++i) {
-            const float e = __shfl_sync(~0u, w[0], i);
-            if (i < it.parts && e != 0.f) {
+        for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
+        const float top = fmaxf(M, snk);
+        float sum = 0.f;
 #pragma unroll
-                for (int k = 0; k < WV; ++k) {
-                    a[k].x = fmaf(e, v[i][k].x, a[k].x); a[k].y = fmaf(e, v[i][k].y, a[k].y);
-                    a[k].z = fmaf(e, v[i][k].z, a[k].z); a[k].w = fmaf(e, v[i][k].w, a[k].w);
+        for (int k = 0; k < PL; ++k) {
+            w[k] = w[k] == -INFINITY ? 0.f : exp2f(w[k] - top);
+            sum += w[k] * l[k];
+        }
+#pragma unroll
+        for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
+        const float den = sum + (snk == -INFINITY ? 0.f : exp2f(snk - top));
+        if (ch == 0 && p.lse)
+            p.lse[static_cast<size_t>(tok) * p.g.H + h] = top == -INFINITY ? -INFINITY : top * kLn2 + logf(den);
+        const float f = M == -INFINITY ? 0.f : 1.f / den;
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i0 = 0; i0 < np; i0 += 8) {
+            float wk = w[0];
+#pragma unroll
+            for (int k = 1; k < PL; ++k)
+                if (i0 >= 32 * k) wk = w[k];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float e = __shfl_sync(~0u, wk, (i0 + i) & 31);
+                if (i0 + i < np && e != 0.f) {       // (a part that saw nothing may hold anything)
+                    o[0] = fmaf(e, v[i].x, o[0]); o[1] = fmaf(e, v[i].y, o[1]);
+                    o[2] = fmaf(e, v[i].z, o[2]); o[3] = fmaf(e, v[i].w, o[3]);
                 }
             }
-        }
 #pragma unroll
-        for (int k = 0; k < WV; ++k) merge_store<D>(p, it, k * 128 + lane * 4, a[k], inv);
+            for (int i = 0; i < 8; ++i)
+                if (i0 + 8 + i < np) v[i] = *reinterpret_cast<const float4*>(po + part_slot(first, i0 + 8 + i, N, c) * D);
+        }
+        const int r0 = D - 2 * p.or_pairs;
+#pragma unroll 1
+        for (int i = 0; i < 4; i += 2) {
+            float e = (i ? o[2] : o[0]) * f, b = (i ? o[3] : o[1]) * f;
+            if (p.orp && ch + i >= r0) {
+                const float2 cs = out_rope_cs(p, tok, (ch + i - r0) >> 1);
+                const float e0 = e;
+                e = e0 * cs.x + b * cs.y;
+                b = -e0 * cs.y + b * cs.x;
+            }
+            *reinterpret_cast<uint32_t*>(p.out + (static_cast<size_t>(tok) * p.g.H + h) * D + ch + i) = pack2(e, b);
+        }
     }
 }
 
@@ -924,7 +869,7 @@ int run(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_
     count_launch();
     if (launch_k(kern, dim3(ctas), dim3(kThreads), C::SMEM, st, true, qmap, kmap, vmap, p) != cudaSuccess) return DSV4_ERR_LAUNCH;
     count_launch();
-    if (launch_k(paged_merge_kernel<D, N>, dim3(ctas * 2), dim3(kMergeThreads), 0, st, true, p, ctas, eword) !=
+    if (launch_k(paged_merge_kernel<D, N>, dim3(ctas * 4), dim3(kMergeThreads), 0, st, true, p, ctas, eword) !=
         cudaSuccess)
         return DSV4_ERR_LAUNCH;
     return DSV4_OK;

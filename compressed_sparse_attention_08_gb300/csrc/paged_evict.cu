@@ -58,10 +58,17 @@ evict_plan_kernel(const int32_t* kv_len, int32_t* len, int32_t* n_old, int32_t* 
     if (threadIdx.x == 0) *eword = err;
 }
 
-// grid: (slices x pools, row blocks, batch)
+// Grid: (slices x pools, row blocks, batch). A CTA takes kRows rows at a time: the places of the
+// rows first (their pages are looked up once per row, by a thread of its own), then every load of
+// the block, then its stores. Few registers, so that many CTAs' loads are in flight (with the
+// places worked out by every thread the copy ran at 3 TB/s).
+// In place a CTA goes through all rows of its slice of the channels, a larger block at a time.
+template <bool IN_PLACE> constexpr int kRows = IN_PLACE ? 512 : 64;
 template <bool IN_PLACE>
 __global__ void __launch_bounds__(kT)
 evict_move_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int R = kRows<IN_PLACE>, RT = (R + kT - 1) / kT;      // rows of a block, per thread
+    __shared__ long long s_src[R], s_dst[R];
     const int tid = threadIdx.x, b = blockIdx.z;
     const int slices = (p.row16 + p.slice - 1) / p.slice;
     const int pool = blockIdx.x / slices, sl = blockIdx.x - pool * slices;
@@ -72,55 +79,67 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
     const int r0 = static_cast<int>(blockIdx.y) * p.rows_cta, r1 = min(r0 + p.rows_cta, kept);
     const bool lists = pool == 0 && sl == 0;            // this CTA also moves the weights and writes the list
     uint4* rows = pool ? p.v : p.k;
-    const int32_t* idx = p.idx + static_cast<size_t>(b) * (k_old > 0 ? k_old : 1);
-    const int32_t* tin = p.table + static_cast<size_t>(b) * p.max_pages;
-    const int32_t* tout = p.out_table + static_cast<size_t>(b) * p.out_pages;
-    const float* acc = p.acc + static_cast<size_t>(b) * p.acc_rows;
     const int per = kT / p.slice;                       // rows per step
     const int sub = tid / p.slice, col = sl * p.slice + tid % p.slice;
-    const bool mine = sub < per && col < p.row16, first = mine && tid % p.slice == 0;
-    bool bad = false;
-    for (int base = r0; base < r1; base += per * kU) {
-        uint4 x[kU];
-        float w[kU];
-        long long dst[kU];
-        int src[kU];
+    const bool mine = sub < per && col < p.row16;
+    for (int base = r0; base < r1; base += R) {
+        int src[RT];
+        float w[RT];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int i = base + u * per + sub;
-            dst[u] = -1;
-            src[u] = -1;
-            if (!mine || i >= r1) continue;
-            src[u] = i < kept_old ? idx[i] : n_old + i - kept_old;
+        for (int k = 0; k < RT; ++k) {
+            const int j = tid + k * kT, i = base + j;
+            src[k] = -1;
+            if (j >= R) continue;
+            long long from = -1, to = -1;
+            if (i < r1) {
+                const int s = i < kept_old ? p.idx[static_cast<size_t>(b) * (k_old > 0 ? k_old : 1) + i] : n_old + i - kept_old;
+                src[k] = s;
+                if (lists) w[k] = p.acc[static_cast<size_t>(b) * p.acc_rows + s];
+                if (!(IN_PLACE && p.same && s == i)) {
+                    const int pi = s / p.page_size, po = i / p.page_size;
+                    const int a = p.table[static_cast<size_t>(b) * p.max_pages + pi];
+                    const int c = p.out_table[static_cast<size_t>(b) * p.out_pages + po];
+                    if (a < 0 || a >= p.num_pages || c < 0 || c >= p.num_pages) {
+                        flag_error(p.eword, DSV4_EWORD_BAD_INDEX);
+                    } else {
+                        from = (static_cast<long long>(a) * p.page_size + s - pi * p.page_size) * p.row16;
+                        to = (static_cast<long long>(c) * p.page_size + i - po * p.page_size) * p.row16;
+                    }
+                }
+            }
+            s_src[j] = from;
+            s_dst[j] = to;
         }
+        __syncthreads();
+        for (int j0 = 0; j0 < R; j0 += per * kU) {
+            uint4 x[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            if (src[u] < 0) continue;
-            const int i = base + u * per + sub;
-            if (lists && first) w[u] = acc[src[u]];
-            if (IN_PLACE && p.same && src[u] == i) continue;
-            const int pi = src[u] / p.page_size, po = i / p.page_size;
-            const int a = tin[pi], c = tout[po];
-            if (a < 0 || a >= p.num_pages || c < 0 || c >= p.num_pages) { bad = true; continue; }
-            x[u] = rows[(static_cast<long long>(a) * p.page_size + src[u] - pi * p.page_size) * p.row16 + col];
-            dst[u] = (static_cast<long long>(c) * p.page_size + i - po * p.page_size) * p.row16 + col;
-        }
-        if (IN_PLACE) __syncthreads();                  // every row of the block is read
+            for (int u = 0; u < kU; ++u) {
+                const int j = j0 + u * per + sub;
+                if (mine && j < R && s_src[j] >= 0) x[u] = rows[s_src[j] + col];
+            }
+            if (IN_PLACE) __syncthreads();              // these rows are read (the ones after lie further up)
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            if (dst[u] >= 0) rows[dst[u]] = x[u];
-            if (lists && first && src[u] >= 0) {
-                const int i = base + u * per + sub;
-                p.acc_out[static_cast<size_t>(b) * p.acc_rows + i] = w[u];
-                p.keep[static_cast<size_t>(b) * p.budget + i] = src[u];
+            for (int u = 0; u < kU; ++u) {
+                const int j = j0 + u * per + sub;
+                if (mine && j < R && s_src[j] >= 0) rows[s_dst[j] + col] = x[u];
             }
         }
+        if (lists) {                                    // (in place: every weight of the block is read by now)
+#pragma unroll
+            for (int k = 0; k < RT; ++k) {
+                const int i = base + tid + k * kT;
+                if (src[k] < 0) continue;
+                p.acc_out[static_cast<size_t>(b) * p.acc_rows + i] = w[k];
+                p.keep[static_cast<size_t>(b) * p.budget + i] = src[k];
+            }
+        }
+        __syncthreads();
     }
     if (lists) {
         const int e = min(r0 + p.rows_cta, p.budget);
         for (int i = max(r0, kept) + tid; i < e; i += kT) p.keep[static_cast<size_t>(b) * p.budget + i] = -1;
     }
-    if (bad) flag_error(p.eword, DSV4_EWORD_BAD_INDEX);
 }
 
 struct Layout { size_t len, n_old, idx, topk, end; };
@@ -206,7 +225,7 @@ int launch_paged_evict(const dsv4_paged_evict_args& a, uint8_t* ws, uint32_t* ew
         p.rows_cta = a.budget;
     } else {
         p.slice = p.row16 < 64 ? p.row16 : 64;
-        p.rows_cta = kT / p.slice * kU;
+        p.rows_cta = kRows<false>;
         while ((a.budget + p.rows_cta - 1) / p.rows_cta > 65535) p.rows_cta *= 2;
     }
     const unsigned slices = static_cast<unsigned>((p.row16 + p.slice - 1) / p.slice);
