@@ -55,6 +55,11 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     const int r1 = static_cast<int>(static_cast<long long>(p.rows) * (part + 1) / p.split);
     pdl_trigger();
     pdl_wait();
+    // a weight's 8 channels from c as pairs, or ones
+    auto gamma_of = [](const float* gamma, int c, uint64_t (&g)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = gamma ? *reinterpret_cast<const uint64_t*>(gamma + c + 2 * j) : pack_f32x2(1.f, 1.f);
+    };
     uint4 x[U][VL];
     // rows of a token: its query heads, its keys, its values
     auto load = [&](int base) {
@@ -79,27 +84,33 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     }
     __syncthreads();
     const int rope0 = D - 2 * p.pairs;
+    uint64_t gq[VL][4];
+#pragma unroll
+    for (int i = 0; i < VL; ++i) gamma_of(p.gamma_q, (i * LR + l) * 8, gq[i]);
     for (int base = r0 + sub; __any_sync(~0u, base < r1); base += U * RP) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int r = base + u * RP;
             const bool on = r < r1, is_q = r < p.heads, is_v = r >= p.heads + p.kv_heads;
             if (!__any_sync(~0u, on)) break;
-            float f[VL][8], ss = 0.f;
+            uint64_t f[VL][4], ss2 = 0ull;               // channel pairs
 #pragma unroll
             for (int i = 0; i < VL; ++i) {
                 const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    f[i][2 * j] = bf16_lo(w[j]);
-                    f[i][2 * j + 1] = bf16_hi(w[j]);
-                    ss = fmaf(f[i][2 * j], f[i][2 * j], ss);
-                    ss = fmaf(f[i][2 * j + 1], f[i][2 * j + 1], ss);
+                    f[i][j] = pack_f32x2(bf16_lo(w[j]), bf16_hi(w[j]));
+                    fma_f32x2(ss2, f[i][j], f[i][j]);
                 }
             }
+            float sa, sb;
+            unpack_f32x2(ss2, sa, sb);
+            float ss = sa + sb;
 #pragma unroll
             for (int w = LR / 2; w; w >>= 1) ss += __shfl_xor_sync(~0u, ss, w);
-            const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
+            // (the hardware's reciprocal root: within 2 units of the last place, the output has 16 fewer bits)
+            const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+            const uint64_t inv2 = pack_f32x2(inv, inv);
             __nv_bfloat16* dst = nullptr;
             if (on) {
                 if (is_q) {
@@ -110,23 +121,23 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
                 }
             }
             if (!dst) continue;
-            const float* gamma = is_q ? p.gamma_q : p.gamma_k;
 #pragma unroll
             for (int i = 0; i < VL; ++i) {
                 const int c0 = (i * LR + l) * 8;
                 uint4 y = x[u][i];
                 if (!is_v) {
-                    float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-                    if (gamma) {
-                        const float4 a = *reinterpret_cast<const float4*>(gamma + c0);
-                        const float4 b = *reinterpret_cast<const float4*>(gamma + c0 + 4);
-                        g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w;
-                        g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
+                    uint64_t g[4];
+                    if (is_q) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) g[j] = gq[i][j];
+                    } else {
+                        gamma_of(p.gamma_k, c0, g);
                     }
                     uint32_t o[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        float e = f[i][2 * j] * inv * g[2 * j], d = f[i][2 * j + 1] * inv * g[2 * j + 1];
+                        float e, d;
+                        unpack_f32x2(mul_f32x2(mul_f32x2(f[i][j], inv2), g[j]), e, d);
                         const int pr = (c0 + 2 * j - rope0) >> 1;
                         if (pr >= 0) {
                             const float2 t = cs[pr];

@@ -14,8 +14,8 @@
 // (128 rows x N queries, one unit) and O^T += V^T P^T (128 channels per tile x N). So the number of
 // query columns N is free (64 or 128), a single token's 64 heads fill a tile, and one
 // shared-memory copy of a shared KV row serves as K (K-major) and as V (MN-major).
-// Roles: warps 0, 2 and 3 move pages by TMA into a ring (a warp issues a box in 70 to 120 cycles,
-// however small: three share the boxes of each slot), warp 1 issues tcgen05.mma, warps 4-19 do the
+// Roles: warps 0, 2 and 3 move pages by TMA into a ring, a slot in turn each (a warp needs 300
+// cycles for a slot and 70 to 120 for each box in it, however small), warp 1 issues tcgen05.mma, warps 4-19 do the
 // softmax (a thread holds one cache row and a quarter of the queries; with 8 warps its chain of
 // steps, not the tensor core, set the pace). The scores have two TMEM buffers, so S^T of unit
 // u + 1 runs under the softmax of unit u.
@@ -196,7 +196,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         tma_prefetch_desc(&vmap);
         mbar_init(&ctl.q_full, kLoadWarps);
         mbar_init(&ctl.q_empty, 1);
-        for (int i = 0; i < ST; ++i) { mbar_init(&ctl.full[i], kLoadWarps); mbar_init(&ctl.empty[i], 1); }
+        for (int i = 0; i < ST; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.s_full[i], 1);
             mbar_init(&ctl.s_empty[i], kSoftWarps);
@@ -228,8 +228,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     const uint32_t units = static_cast<uint32_t>(sched.u1 - sched.u0);
     if (warp == 0 || warp == 2 || warp == 3) {
         // ---------------------------------------------------------------- pages and queries
-        // Three warps walk the same slots and take turns with the boxes; all arrive on each slot (so
-        // none falls a round behind), warp 0 with the bytes.
+        // Three warps walk the same slots and take them in turn.
         const int mine = warp == 0 ? 0 : warp - 1;
         PagedWalk w(g, sched);
         PagedSeg sg;
@@ -237,7 +236,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         const int piece = lane >> 1, box = lane & 1;
         uint32_t ring = 0, seg = 0;
         bool dead = false, more = w.next(sg);
-        int turn = lane % kLoadWarps;                // this lane's box falls to warp `turn`
         PagedLook cur{0, 0, false}, prev{0, 0, false};
         if (more) cur = paged_look(g, sg, sg.row0 + sg.kb * kPT, lane);
         int prev_h = 0, k = more ? sg.kb : 0;
@@ -247,22 +245,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             const uint32_t bytes = static_cast<uint32_t>(__popc(bx.ok)) * g.br * 128;
 #pragma unroll 1
             for (int mt = 0; mt < MT; ++mt, ++ring) {
+                if (ring % kLoadWarps != static_cast<uint32_t>(mine)) continue;
                 const uint32_t slot = ring % ST;
                 if (ring >= ST)
                     dead = __any_sync(~0u, !mbar_wait(&ctl.empty[slot], (ring / ST - 1) & 1, abort_flag, p.wait_ns));
                 if (dead) return;
                 if (lane == 0) {
-                    if (mine == 0 && mt == 0 && unit >= 0) {
+                    if (mt == 0 && unit >= 0) {
                         ctl.bad[unit & 7] = bx.bad;
                         if (bx.bad) atomicOr(&ctl.err, DSV4_EWORD_BAD_INDEX);
                     }
-                    if (mine == 0 && bytes) mbar_arrive_expect_tx(&ctl.full[slot], bytes);
+                    if (bytes) mbar_arrive_expect_tx(&ctl.full[slot], bytes);
                     else mbar_arrive(&ctl.full[slot]);
                 }
-                if (turn == mine && ((bx.ok >> lane) & 1))
+                __syncwarp();
+                if ((bx.ok >> lane) & 1)
                     tma_load_4d(sm + slot * C::SLOT + box * C::BOX + piece * g.br * 128, map, &ctl.full[slot], mt * 128 + box * 64,
                                 kvh, t.slot, t.page);
-                turn = turn + 1 == kLoadWarps ? 0 : turn + 1;
             }
         };
         for (int u = 0; !dead && more; ++u) {
@@ -298,7 +297,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             ctl.abort = 1;
             if (seg) mbar_wait(&ctl.q_full, (seg - 1) & 1, nullptr, 100000000ull);
             for (uint32_t r = ring > ST ? ring - ST : 0; r < ring; ++r)
-                mbar_wait(&ctl.full[r % ST], (r / ST) & 1, nullptr, 100000000ull);
+                if (r % kLoadWarps == static_cast<uint32_t>(mine)) mbar_wait(&ctl.full[r % ST], (r / ST) & 1, nullptr, 100000000ull);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- tensor core

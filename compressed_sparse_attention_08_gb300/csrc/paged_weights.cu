@@ -5,13 +5,14 @@
 //
 // The scores are formed as in paged_attn.cu: S^T = K Q^T on the tensor core, 128 cache rows on
 // the lanes and up to 128 queries on the columns, so a thread of the epilogue owns one cache row
-// and its sum over the queries stays in one register: no reduction over threads but the last one
-// over the two column halves, and a fixed order of addition. One of the operands stays in shared
-// memory while the other streams through a ring of 16 KB boxes (64 channels of 128 rows): with
-// one row tile of queries per sequence (single tokens) the queries stay and the rows stream,
+// and its sum over a quarter of the queries stays in registers: no reduction over threads but the
+// last one over the four quarters, and a fixed order of addition. One of the operands stays in
+// shared memory while the other streams through a ring of 16 KB boxes (64 channels of 128 rows):
+// with one row tile of queries per sequence (single tokens) the queries stay and the rows stream,
 // each read once; otherwise the rows of an item stay and the queries of every token that sees
-// them stream. An item is a tile of 128 cache rows; when there are fewer than two per CTA each
-// is split over the tokens, its partial sums in the workspace, added in order by the second kernel.
+// them stream. An item is a tile of 128 cache rows, or, where whole tiles would leave CTAs waiting
+// for others, a share of the tokens that see it; those partial sums lie in the workspace and the
+// second kernel adds them in order. Roles as in paged_attn.cu.
 #include <cmath>
 
 #include "internal.h"
@@ -20,12 +21,12 @@
 namespace dsv4 {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kSoftWarps = 8, kSoftThreads = 256, kSoftBar = 1;
+constexpr int kThreads = 640, kLoadWarps = 3, kGroups = 4;
+constexpr int kSoftWarps = 16, kSoftThreads = 512, kSoftBar = 1;
 constexpr int kN = 128;                  // query columns
 constexpr int kPT = 128;                 // cache rows per tile
 constexpr int kSB = 4;                   // accumulators (TMEM)
-constexpr int kMaxSplit = 64;
+constexpr int kMaxSplit = 64, kMaxShares = 8;    // shares per tile, and per CTA in all
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct PagedWeightsParams {
@@ -33,7 +34,7 @@ struct PagedWeightsParams {
     const float* lse;
     const float* acc_in;                 // or null
     float* acc;
-    float* part;                         // [2 * grid + 1, 128]
+    float* part;                         // [kMaxShares * grid, 128]
     int* head;                           // [0] tiles, [1] split, then per tile (sequence, first row)
     uint32_t* err;
     int acc_rows, keep_q;                // keep_q: the queries stay in shared memory
@@ -53,7 +54,7 @@ struct WCfg {
     static constexpr int SUMS = D == 512 ? 2 : 1;
     static constexpr int SB = kSB / SUMS;                    // score buffers
     static constexpr int OFF_R = RES, OFF_S = RES + RS * BOX;
-    static constexpr int OFF_PF = OFF_S + 2 * kN * 4 * 3 + 2 * kPT * 4;   // tiles before each sequence
+    static constexpr int OFF_PF = OFF_S + 2 * kN * 8 + kGroups * kPT * 4;   // tiles before each sequence
     static constexpr int SMALL = OFF_PF - OFF_S + kPagedMaxBatch * 4;
     static constexpr int SMEM = OFF_S + SMALL + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -99,14 +100,30 @@ __device__ void weight_schedule(const PagedWeightsParams& p, int* pref, WSched* 
             if (s < g.batch) pref[s] = v;
             carry = __shfl_sync(~0u, v, 31);
         }
-        if (lane == 0) {
-            int split = 1;
-            if (!p.keep_q && carry > 0 && carry < 2 * static_cast<int>(gridDim.x)) {
-                split = 2 * static_cast<int>(gridDim.x) / carry;
-                split = split < 1 ? 1 : (split > kMaxSplit ? kMaxSplit : split);
+        // The split with the shortest longest CTA: rounds of items, each a share of a tile and a
+        // fiftieth of one for loading its rows again. One split per lane.
+        float best = 1e30f;
+        int split = 1;
+        for (int n = lane + 1; n <= kMaxSplit; n += 32) {
+            const bool may = n == 1 || (!p.keep_q && static_cast<long long>(carry) * n <= kMaxShares * static_cast<int>(gridDim.x));
+            if (!may) continue;
+            const int rounds = (carry * n + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+            const float cost = n == 1 ? static_cast<float>(rounds) : rounds * (1.f / n + 0.02f);
+            if (cost < best) {
+                best = cost;
+                split = n;
             }
-            *out = WSched{carry, split};
         }
+#pragma unroll
+        for (int w = 16; w; w >>= 1) {
+            const float ob = __shfl_xor_sync(~0u, best, w);
+            const int os = __shfl_xor_sync(~0u, split, w);
+            if (ob < best || (ob == best && os < split)) {
+                best = ob;
+                split = os;
+            }
+        }
+        if (lane == 0) *out = WSched{carry, split};
     }
     __syncthreads();
 }
@@ -187,15 +204,16 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     __shared__ unsigned s_bad[16];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* sR = sm + C::OFF_R;
-    float* s_l = reinterpret_cast<float*>(sm + C::OFF_S);            // [2][N] lse in base-2 units
-    int* s_hi = reinterpret_cast<int*>(s_l + 2 * kN);
-    int* s_lo = s_hi + 2 * kN;
-    float* red = reinterpret_cast<float*>(s_lo + 2 * kN);            // [2][128]
+    float* s_nl = reinterpret_cast<float*>(sm + C::OFF_S);           // [2][N] lse in base-2 units, negated
+    int* s_tok = reinterpret_cast<int*>(s_nl + 2 * kN);              // [2][N] the column's token in the tile, -1: no query
+    float* red = reinterpret_cast<float*>(s_tok + 2 * kN);           // [4][128]
     int* pref = reinterpret_cast<int*>(sm + C::OFF_PF);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        mbar_init(&res_full, 1);
+        tma_prefetch_desc(&qmap);
+        tma_prefetch_desc(&kmap);
+        mbar_init(&res_full, kLoadWarps);
         mbar_init(&res_empty, 1);
         for (int i = 0; i < RS; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
         for (int i = 0; i < SB; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], kSoftWarps); }
@@ -214,65 +232,70 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 
     const PagedGeom& g = p.g;
     const bool keep_q = p.keep_q != 0;
-    if (warp == 0) {
+    if (warp == 0 || warp == 2 || warp == 3) {
         // ---------------------------------------------------------------- copies
+        // Three warps walk the same boxes and take them in turn.
+        const int mine = warp == 0 ? 0 : warp - 1;
         WWalk w(p, pref, sched);
         WItem it;
         PagedSeg sg{};
+        WStay stays;
         const int piece = lane >> 1;
         const uint32_t qbox = static_cast<uint32_t>(g.hb) * g.tpt * 128;
         uint32_t ring = 0, res = 0, unit = 0;
-        WStay stays;
         bool dead = false;
         while (!dead && w.next(it)) {
             if (it.tt1 <= it.tt0) continue;
             w.bounds(it, sg);
             const PagedLook t = paged_look(g, sg, it.row0, lane);
             const PagedBoxes bx = paged_boxes(g, t);
-            auto k_box = [&](uint8_t* dst, uint64_t* bar, int kvh, int b) {   // whole warp; the bytes are announced
-                if ((lane & 1) == 0 && ((bx.ok >> lane) & 1))
-                    tma_load_4d(dst + piece * g.br * 128, &kmap, bar, b * 64, kvh, t.slot, t.page);
-            };
             const uint32_t kbox = static_cast<uint32_t>(__popc(bx.ok)) * g.br * 64;
+            const bool piece_ok = (lane & 1) == 0 && ((bx.ok >> lane) & 1);
+            // 64 channels of the item's rows, or of a row tile's queries
+            auto load_k = [&](uint8_t* dst, uint64_t* bar, int kvh, int b) {
+                if (piece_ok) tma_load_4d(dst + piece * g.br * 128, &kmap, bar, b * 64, kvh, t.slot, t.page);
+            };
+            auto load_q = [&](uint8_t* dst, uint64_t* bar, int kvh, int b, int tt, int blk) {
+                if (lane == 0) tma_load_3d(dst, &qmap, bar, b * 64, kvh * g.G + blk * g.hb, it.q.q0 + tt * g.tpt);
+            };
             for (int kvh = 0; kvh < g.KV && !dead; ++kvh) {
                 for (int x = it.tt0 * g.nhb; x < it.tt1 * g.nhb && !dead; ++x, ++unit) {
                     const int tt = x / g.nhb, blk = x - tt * g.nhb;
                     if (stays.moved(keep_q, it, kvh, x)) {
                         if (res > 0) dead = __any_sync(~0u, !mbar_wait(&res_empty, (res - 1) & 1, &abort_flag, p.wait_ns));
                         if (dead) break;
-                        const uint32_t bytes = NB * (keep_q ? qbox : kbox);
                         if (lane == 0) {
-                            if (bytes) mbar_arrive_expect_tx(&res_full, bytes);
+                            const uint32_t bytes = NB * (keep_q ? qbox : kbox);
+                            if (mine == 0 && bytes) mbar_arrive_expect_tx(&res_full, bytes);
                             else mbar_arrive(&res_full);
                         }
                         __syncwarp();
-                        for (int b = 0; b < NB; ++b) {
-                            if (!keep_q) k_box(sm + b * C::BOX, &res_full, kvh, b);
-                            else if (lane == 0)
-                                tma_load_3d(sm + b * C::BOX, &qmap, &res_full, b * 64, kvh * g.G + blk * g.hb,
-                                            it.q.q0 + tt * g.tpt);
+#pragma unroll 1
+                        for (int b = mine; b < NB; b += kLoadWarps) {
+                            if (keep_q) load_q(sm + b * C::BOX, &res_full, kvh, b, tt, blk);
+                            else load_k(sm + b * C::BOX, &res_full, kvh, b);
                         }
                         ++res;
                     }
-                    if (lane == 0) {
-                        s_bad[unit & 15] = bx.bad;
-                        if (bx.bad) atomicOr(&s_err, DSV4_EWORD_BAD_INDEX);
-                    }
+#pragma unroll 1
                     for (int b = 0; b < NB; ++b, ++ring) {
+                        if (ring % kLoadWarps != static_cast<uint32_t>(mine)) continue;
                         const uint32_t slot = ring % RS;
                         if (ring >= RS)
                             dead = __any_sync(~0u, !mbar_wait(&empty[slot], (ring / RS - 1) & 1, &abort_flag, p.wait_ns));
                         if (dead) break;
                         const uint32_t bytes = keep_q ? kbox : qbox;
                         if (lane == 0) {
+                            if (b < kLoadWarps) {    // (the first of the unit's boxes that this warp takes)
+                                s_bad[unit & 15] = bx.bad;
+                                if (bx.bad) atomicOr(&s_err, DSV4_EWORD_BAD_INDEX);
+                            }
                             if (bytes) mbar_arrive_expect_tx(&full[slot], bytes);
                             else mbar_arrive(&full[slot]);
                         }
                         __syncwarp();
-                        if (keep_q) k_box(sR + slot * C::BOX, &full[slot], kvh, b);
-                        else if (lane == 0)
-                            tma_load_3d(sR + slot * C::BOX, &qmap, &full[slot], b * 64, kvh * g.G + blk * g.hb,
-                                        it.q.q0 + tt * g.tpt);
+                        if (keep_q) load_k(sR + slot * C::BOX, &full[slot], kvh, b);
+                        else load_q(sR + slot * C::BOX, &full[slot], kvh, b, tt, blk);
                     }
                 }
             }
@@ -282,134 +305,149 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             abort_flag = 1;
             if (res) mbar_wait(&res_full, (res - 1) & 1, nullptr, 100000000ull);
             for (uint32_t r = ring > RS ? ring - RS : 0; r < ring; ++r)
-                mbar_wait(&full[r % RS], (r / RS) & 1, nullptr, 100000000ull);
+                if (r % kLoadWarps == static_cast<uint32_t>(mine)) mbar_wait(&full[r % RS], (r / RS) & 1, nullptr, 100000000ull);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- tensor core
-        if (lane == 0) {
-            WWalk w(p, pref, sched);
-            WItem it;
-            uint32_t ring = 0, res = 0, u = 0;
-            WStay stays;
-            bool dead = false;
-            const uint32_t r0 = smem_u32(sm), g0 = smem_u32(sR);
-            const uint32_t id = idesc_bf16_f32(kPT, kN);
-            while (!dead && w.next(it)) {
-                if (it.tt1 <= it.tt0) continue;
-                for (int kvh = 0; kvh < g.KV && !dead; ++kvh) {
-                    for (int x = it.tt0 * g.nhb; x < it.tt1 * g.nhb && !dead; ++x, ++u) {
-                        if (stays.moved(keep_q, it, kvh, x)) {
-                            if (res > 0) umma_commit(&res_empty);
-                            dead = !mbar_wait(&res_full, res & 1, &abort_flag, p.wait_ns);
-                            ++res;
-                            if (dead) break;
-                        }
-                        const uint32_t sb = u % SB;
-                        if (u >= SB) dead = !mbar_wait(&s_empty[sb], (u / SB - 1) & 1, &abort_flag, p.wait_ns);
-                        for (int b = 0; b < NB && !dead; ++b, ++ring) {
-                            const uint32_t slot = ring % RS;
-                            dead = !mbar_wait(&full[slot], (ring / RS) & 1, &abort_flag, p.wait_ns);
-                            if (dead) break;
-                            tc_fence_after();
-                            const uint32_t stay = r0 + b * C::BOX, strm = g0 + slot * C::BOX;
-                            const uint32_t a0 = keep_q ? strm : stay, b0 = keep_q ? stay : strm;
+        WWalk w(p, pref, sched);
+        WItem it;
+        WStay stays;
+        uint32_t ring = 0, res = 0, u = 0;
+        bool dead = false;
+        const bool one = elect_one();
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return !__any_sync(~0u, !mbar_wait(bar, parity & 1, &abort_flag, p.wait_ns)); };
+        const uint32_t r0 = smem_u32(sm), g0 = smem_u32(sR);
+        const uint32_t id = idesc_bf16_f32(kPT, kN);
+        while (!dead && w.next(it)) {
+            if (it.tt1 <= it.tt0) continue;
+            for (int kvh = 0; kvh < g.KV && !dead; ++kvh) {
+                for (int x = it.tt0 * g.nhb; x < it.tt1 * g.nhb && !dead; ++x, ++u) {
+                    if (stays.moved(keep_q, it, kvh, x)) {
+                        if (res > 0 && one) umma_commit(&res_empty);
+                        __syncwarp();
+                        dead = !wait(&res_full, res);
+                        ++res;
+                        if (dead) break;
+                    }
+                    const uint32_t sb = u % SB;
+                    if (u >= SB) dead = !wait(&s_empty[sb], u / SB - 1);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b, ++ring) {
+                        const uint32_t slot = ring % RS;
+                        dead = dead || !wait(&full[slot], ring / RS);
+                        if (dead) break;
+                        tc_fence_after();
+                        const uint64_t stay = sdesc_kmajor_sw128(r0 + b * C::BOX), strm = sdesc_kmajor_sw128(g0 + slot * C::BOX);
+                        const uint64_t a0 = keep_q ? strm : stay, b0 = keep_q ? stay : strm;
+                        const uint32_t d = tmem + (sb * SUMS + b / (NB / SUMS)) * kN;
+                        if (one) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16(tmem + (sb * SUMS + b / (NB / SUMS)) * kN, sdesc_kmajor_sw128(a0 + kk * 32),
-                                          sdesc_kmajor_sw128(b0 + kk * 32), id, (b % (NB / SUMS) > 0 || kk > 0) ? 1u : 0u);
+                                umma_bf16(d, a0 + kk * 2, b0 + kk * 2, id, (b % (NB / SUMS) > 0 || kk > 0) ? 1u : 0u);
                             umma_commit(&empty[slot]);
                         }
-                        if (!dead) umma_commit(&s_full[sb]);
+                        __syncwarp();
                     }
+                    if (!dead && one) umma_commit(&s_full[sb]);
+                    __syncwarp();
                 }
             }
-            if (dead) {
-                atomicOr(&s_err, DSV4_EWORD_TIMEOUT);
-                abort_flag = 1;
-            }
         }
-    } else if (warp >= 4) {
+        if (dead && lane == 0) {
+            atomicOr(&s_err, DSV4_EWORD_TIMEOUT);
+            abort_flag = 1;
+        }
+    } else {
         // ---------------------------------------------------------------- weights
         WWalk w(p, pref, sched);
         WItem it;
-        PagedSeg sg{};
-        const int st = tid - 128, q4 = warp & 3, half = (warp - 4) >> 2;
-        const int row = q4 * 32 + lane;
+        const int st = tid - 128, q4 = warp & 3, grp = (warp - 4) >> 2;
+        const int row = q4 * 32 + lane, c0 = grp * (kN / kGroups);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+        const uint64_t scale22 = pack_f32x2(p.scale2, p.scale2);
+        const int ct = st / g.hb, ch = st - ct * g.hb;               // column st: token and head in the tile
         uint32_t u = 0;
         bool dead = false;
         while (w.next(it)) {
-            float sum = 0.f;
+            uint64_t sums[4] = {0ull, 0ull, 0ull, 0ull};
             const int n = (it.tt1 - it.tt0) * g.nhb, rows = weight_rows(p, it.q), j = it.row0 + row;
             if (n > 0) {
-                w.bounds(it, sg);
                 for (int kvh = 0; kvh < g.KV; ++kvh) {
-                    // column st of unit x: its lse (base-2 units) and bounds; no query: hidden
+                    // column st of unit x (its lse is read a unit ahead)
                     float nl = 0.f;
-                    int nhi = 0, nlo = 0;
+                    int tok = -1;
                     auto fetch = [&](int x) {
-                        nl = 0.f;
-                        nhi = nlo = 0;
+                        tok = -1;
                         if (st >= kN || x >= n) return;
                         const int tt = it.tt0 + x / g.nhb, blk = x - x / g.nhb * g.nhb;
-                        const int t = tt * g.tpt + st / g.hb, h = blk * g.hb + st % g.hb;
-                        if (st / g.hb < g.tpt && t < it.q.n && h < g.G) {
-                            nl = p.lse[static_cast<size_t>(it.q.q0 + t) * g.H + kvh * g.G + h] * kLog2e;
-                            nhi = paged_hi(it.q, t);
-                            nlo = paged_lo(g, it.q, t);
+                        const int t = tt * g.tpt + ct, h = blk * g.hb + ch;
+                        if (ct < g.tpt && t < it.q.n && h < g.G) {
+                            nl = p.lse[static_cast<size_t>(it.q.q0 + t) * g.H + kvh * g.G + h];
+                            tok = ct;
                         }
                     };
                     fetch(0);
                     for (int x = 0; x < n; ++x, ++u) {
                         const uint32_t sb = u % SB;
-                        float* l2 = s_l + (u & 1) * kN;
-                        int *hi = s_hi + (u & 1) * kN, *lo = s_lo + (u & 1) * kN;
-                        if (st < kN) { l2[st] = nl; hi[st] = nhi; lo[st] = nlo; }
+                        float* unl = s_nl + (u & 1) * kN;
+                        int* utok = s_tok + (u & 1) * kN;
+                        if (st < kN) {
+                            // (a query that saw nothing, lse -inf, has no weight to give)
+                            if (tok >= 0 && nl == -INFINITY) tok = -1;
+                            unl[st] = tok >= 0 ? -nl * kLog2e : -INFINITY;
+                            utok[st] = tok;
+                        }
                         soft_sync();
                         fetch(x + 1);
                         const int tt = it.tt0 + x / g.nhb, blk = x - x / g.nhb * g.nhb;
-                        const int t0 = tt * g.tpt, tn = min(g.tpt, it.q.n - t0);
-                        const int cols = (tn - 1) * g.hb + min(g.hb, g.G - blk * g.hb);
+                        const int t0 = tt * g.tpt, tn = min(g.tpt, it.q.n - t0), hv = min(g.hb, g.G - blk * g.hb);
+                        const int cols = (tn - 1) * g.hb + hv;       // (no query behind them)
+                        // every token of the tile sees every row of the unit, and every column has a query
+                        const bool open = it.row0 + kPT <= paged_hi(it.q, t0) && it.row0 >= paged_lo(g, it.q, t0 + tn - 1) &&
+                                          (hv == g.hb || tn == 1) && c0 + 32 <= cols;
                         if (!dead) dead = !mbar_wait(&s_full[sb], (u / SB) & 1, &abort_flag, p.wait_ns);
                         tc_fence_after();
-                        const unsigned bad = *reinterpret_cast<volatile unsigned*>(&s_bad[u & 15]);
-                        const bool live = j < rows && !paged_bad_row(g, bad, row);
-                        // every token of the tile sees every row of the unit
-                        const bool open = it.row0 + kPT <= paged_hi(it.q, t0) &&
-                                          it.row0 >= paged_lo(g, it.q, t0 + tn - 1);
-#pragma unroll
-                        for (int pc = 0; pc < 2; ++pc) {
-                            const int c0 = (2 * pc + half) * 32;
-                            if (c0 >= cols) break;
+                        if (c0 < cols) {
                             uint32_t r[32];
-                            DSV4_TMEM_LD_32x32b_X32(lane_base + sb * SUMS * kN + c0, r);
+                            const uint32_t scol = lane_base + sb * SUMS * kN + c0;
+                            DSV4_TMEM_LD_32x32b_X32(scol, r);
+                            uint64_t x2[16];
                             if constexpr (SUMS == 2) {
                                 uint32_t r2[32];
-                                DSV4_TMEM_LD_32x32b_X32(lane_base + (sb * SUMS + 1) * kN + c0, r2);
+                                DSV4_TMEM_LD_32x32b_X32(scol + kN, r2);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
-                            } else {
-                                tmem_wait_ld();
-                            }
-                            float part = 0.f;
-                            if (open && c0 + 32 <= cols) {
-#pragma unroll
-                                for (int i = 0; i < 32; i += 4) {
-                                    const float4 m4 = *reinterpret_cast<const float4*>(l2 + c0 + i);
-                                    part += ex2(fmaf(__uint_as_float(r[i]), p.scale2, -m4.x)) +
-                                            ex2(fmaf(__uint_as_float(r[i + 1]), p.scale2, -m4.y)) +
-                                            (ex2(fmaf(__uint_as_float(r[i + 2]), p.scale2, -m4.z)) +
-                                             ex2(fmaf(__uint_as_float(r[i + 3]), p.scale2, -m4.w)));
+                                for (int i = 0; i < 16; ++i) {
+                                    x2[i] = pack_f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                                    add_f32x2(x2[i], pack_f32x2(__uint_as_float(r2[2 * i]), __uint_as_float(r2[2 * i + 1])));
                                 }
                             } else {
+                                tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (j < hi[c0 + i] && j >= lo[c0 + i])
-                                        part += ex2(fmaf(__uint_as_float(r[i]), p.scale2, -l2[c0 + i]));
+                                for (int i = 0; i < 16; ++i)
+                                    x2[i] = pack_f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
                             }
-                            if (live) sum += part;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(unl + c0 + 2 * i);
+                                uint64_t a = m.x, b = m.y;
+                                fma_f32x2(a, x2[i], scale22);
+                                fma_f32x2(b, x2[i + 1], scale22);
+                                float e[4];
+                                unpack_f32x2(a, e[0], e[1]);
+                                unpack_f32x2(b, e[2], e[3]);
+                                if (!open) {
+                                    const unsigned bad = *reinterpret_cast<volatile unsigned*>(&s_bad[u & 15]);
+                                    const bool live = j < rows && !paged_bad_row(g, bad, row);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const int t = utok[c0 + 2 * i + k];
+                                        if (!live || t < 0 || j >= paged_hi(it.q, t0 + t) || j < paged_lo(g, it.q, t0 + t)) e[k] = -INFINITY;
+                                    }
+                                }
+                                add_f32x2(sums[i & 3], pack_f32x2(ex2(e[0]), ex2(e[1])));
+                                add_f32x2(sums[(i & 3) + 1], pack_f32x2(ex2(e[2]), ex2(e[3])));
+                            }
                         }
                         tc_fence_before();
                         __syncwarp();
@@ -417,11 +455,20 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     }
                 }
             }
-            red[half * kPT + row] = sum;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float a, b;
+                unpack_f32x2(sums[i], a, b);
+                sum += a + b;
+            }
+            red[grp * kPT + row] = sum;
             soft_sync();
             if (st < kPT) {
-                const float v = red[st] + red[kPT + st];
+                float v = (red[st] + red[kPT + st]) + (red[2 * kPT + st] + red[3 * kPT + st]);
                 const int jj = it.row0 + st;
+                // (a row on a page outside the pool: hidden; the units that all tokens see do not ask)
+                if (n > 0 && paged_bad_row(g, *reinterpret_cast<volatile unsigned*>(&s_bad[(u - 1) & 15]), st)) v = 0.f;
                 if (sched.split > 1) {
                     p.part[(static_cast<size_t>(it.tile) * sched.split + it.part) * kPT + st] = v;
                 } else if (jj < rows) {
@@ -498,8 +545,8 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
     p.acc = a.acc;
     p.acc_rows = a.acc_rows;
     p.part = reinterpret_cast<float*>(ws);
-    p.head = reinterpret_cast<int*>(ws + static_cast<size_t>(2 * ctas) * kPT * 4);
-    p.err = reinterpret_cast<uint32_t*>(p.head + 2 + 4 * ctas);
+    p.head = reinterpret_cast<int*>(ws + static_cast<size_t>(kMaxShares * ctas) * kPT * 4);
+    p.err = reinterpret_cast<uint32_t*>(p.head + 2 + kMaxShares * ctas);
     // one row tile per sequence: the queries stay
     p.keep_q = p.g.nhb == 1 && a.max_q <= p.g.tpt;
     p.scale2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
@@ -512,7 +559,7 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
     count_launch();
     if (launch_k(kern, dim3(ctas), dim3(kThreads), C::SMEM, st, true, qmap, kmap, p) != cudaSuccess) return DSV4_ERR_LAUNCH;
     count_launch();
-    return launch_k(paged_weights_sum_kernel, dim3(2 * ctas), dim3(kPT), 0, st, true, p, ctas, eword) == cudaSuccess
+    return launch_k(paged_weights_sum_kernel, dim3(kMaxShares / 2 * ctas), dim3(kPT), 0, st, true, p, ctas, eword) == cudaSuccess
                ? DSV4_OK : DSV4_ERR_LAUNCH;
 }
 
@@ -521,7 +568,7 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
 size_t paged_weights_ws_bytes(const dsv4_paged_weights_args& a) {
     (void)a;
     const size_t n = static_cast<size_t>(weight_ctas());
-    return 2 * n * kPT * 4 + (2 + 5 * n) * 4;
+    return kMaxShares * n * kPT * 4 + (2 + (kMaxShares + 1) * n) * 4;
 }
 
 int launch_paged_weights(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t st) {
