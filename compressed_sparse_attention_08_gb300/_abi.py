@@ -523,22 +523,28 @@ def _held(args, *tensors):
         raise ValueError("all tensors must be on one device")
     args.tensors = kept
     args.device = kept[0].device.index
+    args.ref = ctypes.byref(args)
     return args
 
 
-def _on_device(args, stream, call):
-    """call(stream) with the struct's device current, on its current stream unless one is given."""
+def _call(fn, args, stream, what, ws=None):
+    """fn on the struct (and a workspace), with the struct's device current, on its current stream
+    unless one is given."""
     import torch
-    if args.device == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(args.device):
-        return call(_stream(stream))
-
-
-def _ws_ptr(args, ws):
-    if ws.device.index != args.device:
-        raise ValueError("ws must be on the tensors' device")
-    return _ptr(ws, None, "ws")
+    dev = args.device
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _call(fn, args, stream, what, ws)
+    # (the raw handle: torch.cuda.current_stream() takes 3 us to wrap it)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if ws is None:
+        status = fn(args.ref, st)
+    else:
+        if ws.device.index != dev or not ws.is_contiguous():
+            raise ValueError("ws must be contiguous, on the tensors' device")
+        status = fn(args.ref, ws.data_ptr(), ws.numel() * ws.element_size(), st)
+    if status:
+        _check(status, what)
 
 
 def norm_rope_args(q, q_out, pos, *, k=None, k_pages=None, v=None, v_pages=None, slots=None,
@@ -582,8 +588,7 @@ def norm_rope_args(q, q_out, pos, *, k=None, k_pages=None, v=None, v_pages=None,
 
 def dsv4_norm_rope_append(args, *, stream=None):
     """RMSNorm per head, RoPE and the append to the pages, from a norm_rope_args struct."""
-    _check(_on_device(args, stream, lambda s: library().dsv4_norm_rope_append(ctypes.byref(args), s)),
-           "dsv4_norm_rope_append")
+    _call(library().dsv4_norm_rope_append, args, stream, "dsv4_norm_rope_append")
 
 
 def _paged(q, k_pages, block_table, cu_q, kv_len):
@@ -627,8 +632,7 @@ def dsv4_paged_attn_workspace_size(args):
 
 def dsv4_paged_attn(args, ws, *, stream=None):
     """Attention of the new tokens over their sequences' pages, from a paged_attn_args struct."""
-    _check(_on_device(args, stream, lambda s: library().dsv4_paged_attn(
-        ctypes.byref(args), _ws_ptr(args, ws), ws.numel() * ws.element_size(), s)), "dsv4_paged_attn")
+    _call(library().dsv4_paged_attn, args, stream, "dsv4_paged_attn", ws)
 
 
 def paged_weights_args(q, lse, k_pages, block_table, cu_q, kv_len, acc, *, acc_in=None, max_q=None,
@@ -653,8 +657,7 @@ def dsv4_paged_attn_weights_workspace_size(args):
 
 def dsv4_paged_attn_weights(args, ws, *, stream=None):
     """The weight each cached row received, from a paged_weights_args struct."""
-    _check(_on_device(args, stream, lambda s: library().dsv4_paged_attn_weights(
-        ctypes.byref(args), _ws_ptr(args, ws), ws.numel() * ws.element_size(), s)), "dsv4_paged_attn_weights")
+    _call(library().dsv4_paged_attn_weights, args, stream, "dsv4_paged_attn_weights", ws)
 
 
 def paged_evict_args(k_pages, block_table, kv_len, acc, keep, *, budget, recent, v_pages=None,
@@ -691,5 +694,4 @@ def dsv4_paged_evict_workspace_size(args):
 
 def dsv4_paged_evict(args, ws, *, stream=None):
     """Eviction by accumulated weight, from a paged_evict_args struct."""
-    _check(_on_device(args, stream, lambda s: library().dsv4_paged_evict(
-        ctypes.byref(args), _ws_ptr(args, ws), ws.numel() * ws.element_size(), s)), "dsv4_paged_evict")
+    _call(library().dsv4_paged_evict, args, stream, "dsv4_paged_evict", ws)
