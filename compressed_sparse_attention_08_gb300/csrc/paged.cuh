@@ -108,10 +108,13 @@ __device__ void paged_schedule(const PagedGeom& g, int self, int count, int min_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int mult = g.KV * g.nhb;
     bool bad = false;
-    for (int s0 = warp * 32; s0 < g.batch; s0 += NT) {
+    // (up to 32 sequences per warp at a time, a lane each; the whole warp goes over a long one's tiles)
+    const int step = min((g.batch + NT / 32 - 1) / (NT / 32), 32);
+    for (int s0 = warp * step; s0 < g.batch; s0 += NT / 32 * step) {
         const int s = s0 + lane;
+        const bool here = lane < step && s < g.batch;
         PagedSeq q{0, 0, 0};
-        if (s < g.batch) q = paged_seq(g, s, bad);
+        if (here) q = paged_seq(g, s, bad);
         const int nt = (q.n + g.tpt - 1) / g.tpt;
         long long units = 0;
         if (nt <= 4)
@@ -126,7 +129,7 @@ __device__ void paged_schedule(const PagedGeom& g, int self, int count, int min_
             for (int w = 16; w; w >>= 1) u += __shfl_xor_sync(~0u, u, w);
             if (lane == src) units = u;
         }
-        if (s < g.batch) pref[s] = units * mult;
+        if (here) pref[s] = units * mult;
     }
     if (bad) atomicOr(err, DSV4_EWORD_BAD_INDEX);
     __syncthreads();

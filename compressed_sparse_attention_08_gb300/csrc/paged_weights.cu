@@ -9,10 +9,11 @@
 // last one over the four quarters, and a fixed order of addition. One of the operands stays in
 // shared memory while the other streams through a ring of 16 KB boxes (64 channels of 128 rows):
 // with one row tile of queries per sequence (single tokens) the queries stay and the rows stream,
-// each read once; otherwise the rows of an item stay and the queries of every token that sees
-// them stream. An item is a tile of 128 cache rows, or, where whole tiles would leave CTAs waiting
-// for others, a share of the tokens that see it; those partial sums lie in the workspace and the
-// second kernel adds them in order. Roles as in paged_attn.cu.
+// each read once; otherwise the rows of a tile stay and the queries of every token that sees them
+// stream. A unit is a tile of 128 cache rows x one row tile of queries; as in the attention all
+// units form one line, (sequence, rows, KV head, row tile), and each CTA takes an equal piece of
+// it. A tile that crosses a border leaves partial sums in the workspace, at most two per CTA, which
+// the second kernel adds in order. Roles as in paged_attn.cu.
 #include <cmath>
 
 #include "internal.h"
@@ -26,7 +27,6 @@ constexpr int kSoftWarps = 16, kSoftThreads = 512, kSoftBar = 1;
 constexpr int kN = 128;                  // query columns
 constexpr int kPT = 128;                 // cache rows per tile
 constexpr int kSB = 4;                   // accumulators (TMEM)
-constexpr int kMaxSplit = 64, kMaxShares = 8;    // shares per tile, and per CTA in all
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct PagedWeightsParams {
@@ -34,8 +34,8 @@ struct PagedWeightsParams {
     const float* lse;
     const float* acc_in;                 // or null
     float* acc;
-    float* part;                         // [kMaxShares * grid, 128]
-    int* head;                           // [0] tiles, [1] split, then per tile (sequence, first row)
+    float* part;                         // [2 * grid, 128]
+    int* desc;                           // [grid, 4]: of the tile that a CTA starts and others finish
     uint32_t* err;
     int acc_rows, keep_q;                // keep_q: the queries stay in shared memory
     float scale2;
@@ -54,136 +54,190 @@ struct WCfg {
     static constexpr int SUMS = D == 512 ? 2 : 1;
     static constexpr int SB = kSB / SUMS;                    // score buffers
     static constexpr int OFF_R = RES, OFF_S = RES + RS * BOX;
-    static constexpr int OFF_PF = OFF_S + 2 * kN * 8 + kGroups * kPT * 4;   // tiles before each sequence
-    static constexpr int SMALL = OFF_PF - OFF_S + kPagedMaxBatch * 4;
+    static constexpr int SMALL = 2 * kN * 8 + kGroups * kPT * 4;
     static constexpr int SMEM = OFF_S + SMALL + 1024;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
 __device__ __forceinline__ void soft_sync() { named_bar_sync(kSoftBar, kSoftThreads); }
 
-// An item: a tile of cache rows of one sequence and a share of the token tiles that see it.
-struct WItem {
-    PagedSeq q;
-    int s, row0, tt0, tt1;               // token tiles [tt0, tt1)
-    int tile, part;
-};
-
 // Rows of a sequence that are accumulated: its length, at most acc_rows.
 __device__ __forceinline__ int weight_rows(const PagedWeightsParams& p, const PagedSeq& q) { return min(q.L, p.acc_rows); }
+__device__ __forceinline__ int weight_tiles(const PagedWeightsParams& p, const PagedSeq& q) {
+    return (weight_rows(p, q) + kPT - 1) / kPT;
+}
 
-struct WSched { int tiles, split; };
+// Token tiles [tt0, tt1) with a token that sees a row of the tile from row0: hi(t) > row0 and
+// lo(t) < row0 + 128.
+struct WSpan { int tt0, tt1; };
+__device__ __forceinline__ WSpan weight_span(const PagedGeom& g, const PagedSeq& q, int row0) {
+    const int base = q.L - q.n, a = max(row0 - base, 0);
+    int b = q.n;
+    if (g.window > 0) b = static_cast<int>(min(static_cast<long long>(b), static_cast<long long>(row0) + kPT - 1 + g.window - base));
+    if (a >= b) return WSpan{0, 0};
+    return WSpan{a / g.tpt, (b + g.tpt - 1) / g.tpt};
+}
+// Units of a tile (at least one, so that its rows are written).
+__device__ __forceinline__ int weight_units(const PagedGeom& g, const PagedSeq& q, int tile) {
+    const WSpan w = weight_span(g, q, tile * kPT);
+    return max((w.tt1 - w.tt0) * g.nhb * g.KV, 1);
+}
 
-// Tiles before each sequence, and the split. Whole block.
-__device__ void weight_schedule(const PagedWeightsParams& p, int* pref, WSched* out, uint32_t* err) {
+struct WSched {
+    long long total, u0, u1;             // all units, this CTA's [u0, u1)
+    int s, tile, k;                      // where u0 lies
+};
+
+// Whole block; `pref` is scratch for `batch` counts.
+__device__ void weight_schedule(const PagedWeightsParams& p, long long* pref, WSched* out, uint32_t* err) {
     const PagedGeom& g = p.g;
-    const int tid = threadIdx.x, lane = tid & 31;
+    constexpr int NW = kThreads / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int mult = g.nhb * g.KV;
     bool bad = false;
-    for (int s = tid; s < g.batch; s += kThreads) {
-        const PagedSeq q = paged_seq(g, s, bad);
-        bad |= q.L > p.acc_rows;
-        pref[s] = (weight_rows(p, q) + kPT - 1) / kPT;
+    const int step = min((g.batch + NW - 1) / NW, 32);
+    for (int s0 = warp * step; s0 < g.batch; s0 += NW * step) {
+        const int s = s0 + lane;
+        const bool here = lane < step && s < g.batch;
+        PagedSeq q{0, 0, 0};
+        if (here) {
+            q = paged_seq(g, s, bad);
+            bad |= q.L > p.acc_rows;
+        }
+        const int nt = weight_tiles(p, q);
+        long long units = 0;
+        const bool one = q.n > 0 && q.n <= g.tpt;    // one row tile: every tile from the first seen one
+        if (one) {
+            const int f = min(paged_lo(g, q, 0) / kPT, nt);
+            units = static_cast<long long>(nt - f) * mult + f;
+        } else if (nt <= 4) {
+            for (int t = 0; t < nt; ++t) units += weight_units(g, q, t);
+        }
+        for (unsigned big = __ballot_sync(~0u, !one && nt > 4); big; big &= big - 1) {
+            const int src = __ffs(big) - 1;
+            const PagedSeq b{0, __shfl_sync(~0u, q.n, src), __shfl_sync(~0u, q.L, src)};
+            const int bnt = weight_tiles(p, b);
+            long long u = 0;
+            for (int t = lane; t < bnt; t += 32) u += weight_units(g, b, t);
+#pragma unroll
+            for (int w = 16; w; w >>= 1) u += __shfl_xor_sync(~0u, u, w);
+            if (lane == src) units = u;
+        }
+        if (here) pref[s] = units;
     }
     if (bad) atomicOr(err, DSV4_EWORD_BAD_INDEX);
     __syncthreads();
-    if (tid < 32) {
-        int carry = 0;                   // (batch * rows / 128 fits: the host checks it)
+    if (warp == 0) {
+        long long carry = 0;
         for (int s0 = 0; s0 < g.batch; s0 += 32) {
             const int s = s0 + lane;
-            int v = s < g.batch ? pref[s] : 0;
+            long long v = s < g.batch ? pref[s] : 0;
 #pragma unroll
             for (int w = 1; w < 32; w <<= 1) {
-                const int o = __shfl_up_sync(~0u, v, w);
+                const long long o = __shfl_up_sync(~0u, v, w);
                 if (lane >= w) v += o;
             }
             v += carry;
             if (s < g.batch) pref[s] = v;
             carry = __shfl_sync(~0u, v, 31);
         }
-        // The split with the shortest longest CTA: rounds of items, each a share of a tile and a
-        // fiftieth of one for loading its rows again. One split per lane.
-        float best = 1e30f;
-        int split = 1;
-        for (int n = lane + 1; n <= kMaxSplit; n += 32) {
-            const bool may = n == 1 || (!p.keep_q && static_cast<long long>(carry) * n <= kMaxShares * static_cast<int>(gridDim.x));
-            if (!may) continue;
-            const int rounds = (carry * n + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-            const float cost = n == 1 ? static_cast<float>(rounds) : rounds * (1.f / n + 0.02f);
-            if (cost < best) {
-                best = cost;
-                split = n;
+        __syncwarp();
+        const long long T = carry, c = blockIdx.x, ge = min(T, static_cast<long long>(gridDim.x));
+        const long long u0 = c < ge ? T * c / ge : T, u1 = c < ge ? T * (c + 1) / ge : T;
+        int s = 0, tile = 0, k = 0;
+        if (u1 > u0) {
+            int hi = g.batch - 1;                    // the first sequence whose units end past u0
+            while (s < hi) {
+                const int mid = (s + hi) >> 1;
+                if (pref[mid] > u0) hi = mid; else s = mid + 1;
             }
-        }
+            long long rem = u0 - (s ? pref[s - 1] : 0);
+            bool dummy = false;
+            const PagedSeq q = paged_seq(g, s, dummy);
+            const int nt = weight_tiles(p, q);
+            const int f = q.n > 0 && q.n <= g.tpt ? min(paged_lo(g, q, 0) / kPT, nt) : 0;
+            if (q.n > 0 && q.n <= g.tpt) {
+                tile = rem < f ? static_cast<int>(rem) : f + static_cast<int>((rem - f) / mult);
+                k = rem < f ? 0 : static_cast<int>((rem - f) % mult);
+                rem = -1;
+            }
+            long long cum = 0;
+            for (int t0 = 0; t0 < nt && rem >= 0; t0 += 32) {
+                long long v = t0 + lane < nt ? weight_units(g, q, t0 + lane) : 0;
+                const long long own = v;
 #pragma unroll
-        for (int w = 16; w; w >>= 1) {
-            const float ob = __shfl_xor_sync(~0u, best, w);
-            const int os = __shfl_xor_sync(~0u, split, w);
-            if (ob < best || (ob == best && os < split)) {
-                best = ob;
-                split = os;
+                for (int w = 1; w < 32; w <<= 1) {
+                    const long long o = __shfl_up_sync(~0u, v, w);
+                    if (lane >= w) v += o;
+                }
+                const unsigned past = __ballot_sync(~0u, cum + v > rem);
+                if (past) {
+                    const int f = __ffs(past) - 1;
+                    tile = t0 + f;
+                    k = static_cast<int>(rem - cum - __shfl_sync(~0u, v - own, f));
+                    break;
+                }
+                cum += __shfl_sync(~0u, v, 31);
             }
         }
-        if (lane == 0) *out = WSched{carry, split};
+        if (lane == 0) *out = WSched{T, u0, u1, s, tile, k};
     }
     __syncthreads();
 }
 
+// A CTA's part [kb, ke) of a tile's n units: unit i is KV head i / nx, row tile x0 + i % nx (nx = 0:
+// nobody sees the rows).
+struct WItem {
+    PagedSeq q;
+    int s, row0, n, kb, ke, nx, x0;
+    int lo_u, hi_u;                      // rows that some token of the tile sees
+};
+
 struct WWalk {
     const PagedWeightsParams& p;
-    const int* pref;
-    WSched sc;
-    long long i;                         // item
-    int s;                               // the sequence of the item before
-    __device__ WWalk(const PagedWeightsParams& par, const int* pr, const WSched& sched)
-        : p(par), pref(pr), sc(sched), i(blockIdx.x), s(0) {}
-    // Items go round over the CTAs, so neighbours read the same queries at about the same time.
-    __device__ bool next(WItem& o) {
-        if (i >= static_cast<long long>(sc.tiles) * sc.split) return false;
-        const PagedGeom& g = p.g;
-        o.tile = static_cast<int>(i / sc.split);
-        o.part = static_cast<int>(i - static_cast<long long>(o.tile) * sc.split);
-        int lo = s, hi = g.batch - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (pref[mid] > o.tile) hi = mid; else lo = mid + 1;
-        }
-        s = lo;
+    int s, tile, k;
+    long long left;
+    PagedSeq q;
+    __device__ WWalk(const PagedWeightsParams& par, const WSched& sc)
+        : p(par), s(sc.s), tile(sc.tile), k(sc.k), left(sc.u1 - sc.u0), q{0, 0, 0} {
         bool dummy = false;
-        o.s = s;
-        o.q = paged_seq(g, s, dummy);
-        o.row0 = (o.tile - (s ? pref[s - 1] : 0)) * kPT;
-        // tokens t with hi(t) > row0 and lo(t) < row0 + 128
-        const long long base = static_cast<long long>(o.q.L) - o.q.n;
-        long long a = o.row0 - base, b = o.q.n;
-        if (a < 0) a = 0;
-        if (g.window > 0) {
-            const long long e = o.row0 + kPT - 1 + g.window - base;
-            if (e < b) b = e;
-        }
-        int t0 = static_cast<int>(a / g.tpt), t1 = b > a ? static_cast<int>((b + g.tpt - 1) / g.tpt) : t0;
-        if (a >= b) t1 = t0;
-        const int n = t1 - t0;
-        o.tt0 = t0 + static_cast<int>(static_cast<long long>(n) * o.part / sc.split);
-        o.tt1 = t0 + static_cast<int>(static_cast<long long>(n) * (o.part + 1) / sc.split);
-        i += gridDim.x;
-        return true;
+        if (left > 0) q = paged_seq(p.g, s, dummy);
     }
-    // the rows that some token of the item sees
-    __device__ void bounds(const WItem& o, PagedSeg& sg) const {
-        const int ta = o.tt0 * p.g.tpt, tb = min(o.tt1 * p.g.tpt, o.q.n) - 1;
-        sg.s = o.s;
-        sg.lo_u = paged_lo(p.g, o.q, ta);
-        sg.hi_u = min(paged_hi(o.q, tb), weight_rows(p, o.q));
+    __device__ bool next(WItem& o) {
+        if (left <= 0) return false;
+        const PagedGeom& g = p.g;
+        while (tile >= weight_tiles(p, q)) {         // the next sequence with rows
+            if (++s >= g.batch) return false;
+            tile = 0;
+            bool dummy = false;
+            q = paged_seq(g, s, dummy);
+        }
+        o.q = q;
+        o.s = s;
+        o.row0 = tile * kPT;
+        const WSpan w = weight_span(g, q, o.row0);
+        o.nx = (w.tt1 - w.tt0) * g.nhb;
+        o.x0 = w.tt0 * g.nhb;
+        o.n = max(o.nx * g.KV, 1);
+        o.lo_u = o.nx ? paged_lo(g, q, w.tt0 * g.tpt) : 0;
+        o.hi_u = o.nx ? min(paged_hi(q, min(w.tt1 * g.tpt, q.n) - 1), weight_rows(p, q)) : 0;
+        o.kb = k;
+        const long long take = left < o.n - k ? left : o.n - k;
+        o.ke = k + static_cast<int>(take);
+        left -= take;
+        k = 0;
+        ++tile;
+        return true;
     }
 };
 
-// What the resident operand holds: the queries of one row tile, or the rows of an item's KV head.
+// What the resident operand holds: the queries of one row tile, or the rows of a tile's KV head.
 struct WStay {
     int a = -1, h = -1, b = -1;
     __device__ bool moved(bool keep_q, const WItem& it, int kvh, int x) {
-        const int na = keep_q ? it.s : it.tile, nb = keep_q ? x : it.part;
-        if (a == na && h == kvh && b == nb) return false;
-        a = na;
+        const int nb = keep_q ? x : it.row0;
+        if (a == it.s && h == kvh && b == nb) return false;
+        a = it.s;
         h = kvh;
         b = nb;
         return true;
@@ -207,7 +261,6 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     float* s_nl = reinterpret_cast<float*>(sm + C::OFF_S);           // [2][N] lse in base-2 units, negated
     int* s_tok = reinterpret_cast<int*>(s_nl + 2 * kN);              // [2][N] the column's token in the tile, -1: no query
     float* red = reinterpret_cast<float*>(s_tok + 2 * kN);           // [4][128]
-    int* pref = reinterpret_cast<int*>(sm + C::OFF_PF);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -228,7 +281,10 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    weight_schedule(p, pref, &sched, &s_err);
+    weight_schedule(p, reinterpret_cast<long long*>(sm), &sched, &s_err);
+    // the schedule's scratch is overwritten by TMA next
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
 
     const PagedGeom& g = p.g;
     const bool keep_q = p.keep_q != 0;
@@ -236,7 +292,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         // ---------------------------------------------------------------- copies
         // Three warps walk the same boxes and take them in turn.
         const int mine = warp == 0 ? 0 : warp - 1;
-        WWalk w(p, pref, sched);
+        WWalk w(p, sched);
         WItem it;
         PagedSeg sg{};
         WStay stays;
@@ -245,8 +301,10 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         uint32_t ring = 0, res = 0, unit = 0;
         bool dead = false;
         while (!dead && w.next(it)) {
-            if (it.tt1 <= it.tt0) continue;
-            w.bounds(it, sg);
+            if (it.nx == 0) continue;
+            sg.s = it.s;
+            sg.lo_u = it.lo_u;
+            sg.hi_u = it.hi_u;
             const PagedLook t = paged_look(g, sg, it.row0, lane);
             const PagedBoxes bx = paged_boxes(g, t);
             const uint32_t kbox = static_cast<uint32_t>(__popc(bx.ok)) * g.br * 64;
@@ -258,45 +316,44 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             auto load_q = [&](uint8_t* dst, uint64_t* bar, int kvh, int b, int tt, int blk) {
                 if (lane == 0) tma_load_3d(dst, &qmap, bar, b * 64, kvh * g.G + blk * g.hb, it.q.q0 + tt * g.tpt);
             };
-            for (int kvh = 0; kvh < g.KV && !dead; ++kvh) {
-                for (int x = it.tt0 * g.nhb; x < it.tt1 * g.nhb && !dead; ++x, ++unit) {
-                    const int tt = x / g.nhb, blk = x - tt * g.nhb;
-                    if (stays.moved(keep_q, it, kvh, x)) {
-                        if (res > 0) dead = __any_sync(~0u, !mbar_wait(&res_empty, (res - 1) & 1, &abort_flag, p.wait_ns));
-                        if (dead) break;
-                        if (lane == 0) {
-                            const uint32_t bytes = NB * (keep_q ? qbox : kbox);
-                            if (mine == 0 && bytes) mbar_arrive_expect_tx(&res_full, bytes);
-                            else mbar_arrive(&res_full);
-                        }
-                        __syncwarp();
-#pragma unroll 1
-                        for (int b = mine; b < NB; b += kLoadWarps) {
-                            if (keep_q) load_q(sm + b * C::BOX, &res_full, kvh, b, tt, blk);
-                            else load_k(sm + b * C::BOX, &res_full, kvh, b);
-                        }
-                        ++res;
+            for (int i = it.kb; i < it.ke && !dead; ++i, ++unit) {
+                const int kvh = i / it.nx, x = it.x0 + i - kvh * it.nx;
+                const int tt = x / g.nhb, blk = x - tt * g.nhb;
+                if (stays.moved(keep_q, it, kvh, x)) {
+                    if (res > 0) dead = __any_sync(~0u, !mbar_wait(&res_empty, (res - 1) & 1, &abort_flag, p.wait_ns));
+                    if (dead) break;
+                    if (lane == 0) {
+                        const uint32_t bytes = NB * (keep_q ? qbox : kbox);
+                        if (mine == 0 && bytes) mbar_arrive_expect_tx(&res_full, bytes);
+                        else mbar_arrive(&res_full);
                     }
+                    __syncwarp();
 #pragma unroll 1
-                    for (int b = 0; b < NB; ++b, ++ring) {
-                        if (ring % kLoadWarps != static_cast<uint32_t>(mine)) continue;
-                        const uint32_t slot = ring % RS;
-                        if (ring >= RS)
-                            dead = __any_sync(~0u, !mbar_wait(&empty[slot], (ring / RS - 1) & 1, &abort_flag, p.wait_ns));
-                        if (dead) break;
-                        const uint32_t bytes = keep_q ? kbox : qbox;
-                        if (lane == 0) {
-                            if (b < kLoadWarps) {    // (the first of the unit's boxes that this warp takes)
-                                s_bad[unit & 15] = bx.bad;
-                                if (bx.bad) atomicOr(&s_err, DSV4_EWORD_BAD_INDEX);
-                            }
-                            if (bytes) mbar_arrive_expect_tx(&full[slot], bytes);
-                            else mbar_arrive(&full[slot]);
-                        }
-                        __syncwarp();
-                        if (keep_q) load_k(sR + slot * C::BOX, &full[slot], kvh, b);
-                        else load_q(sR + slot * C::BOX, &full[slot], kvh, b, tt, blk);
+                    for (int b = mine; b < NB; b += kLoadWarps) {
+                        if (keep_q) load_q(sm + b * C::BOX, &res_full, kvh, b, tt, blk);
+                        else load_k(sm + b * C::BOX, &res_full, kvh, b);
                     }
+                    ++res;
+                }
+#pragma unroll 1
+                for (int b = 0; b < NB; ++b, ++ring) {
+                    if (ring % kLoadWarps != static_cast<uint32_t>(mine)) continue;
+                    const uint32_t slot = ring % RS;
+                    if (ring >= RS)
+                        dead = __any_sync(~0u, !mbar_wait(&empty[slot], (ring / RS - 1) & 1, &abort_flag, p.wait_ns));
+                    if (dead) break;
+                    const uint32_t bytes = keep_q ? kbox : qbox;
+                    if (lane == 0) {
+                        if (b < kLoadWarps) {    // (the first of the unit's boxes that this warp takes)
+                            s_bad[unit & 15] = bx.bad;
+                            if (bx.bad) atomicOr(&s_err, DSV4_EWORD_BAD_INDEX);
+                        }
+                        if (bytes) mbar_arrive_expect_tx(&full[slot], bytes);
+                        else mbar_arrive(&full[slot]);
+                    }
+                    __syncwarp();
+                    if (keep_q) load_k(sR + slot * C::BOX, &full[slot], kvh, b);
+                    else load_q(sR + slot * C::BOX, &full[slot], kvh, b, tt, blk);
                 }
             }
         }
@@ -309,7 +366,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- tensor core
-        WWalk w(p, pref, sched);
+        WWalk w(p, sched);
         WItem it;
         WStay stays;
         uint32_t ring = 0, res = 0, u = 0;
@@ -319,38 +376,37 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         const uint32_t r0 = smem_u32(sm), g0 = smem_u32(sR);
         const uint32_t id = idesc_bf16_f32(kPT, kN);
         while (!dead && w.next(it)) {
-            if (it.tt1 <= it.tt0) continue;
-            for (int kvh = 0; kvh < g.KV && !dead; ++kvh) {
-                for (int x = it.tt0 * g.nhb; x < it.tt1 * g.nhb && !dead; ++x, ++u) {
-                    if (stays.moved(keep_q, it, kvh, x)) {
-                        if (res > 0 && one) umma_commit(&res_empty);
-                        __syncwarp();
-                        dead = !wait(&res_full, res);
-                        ++res;
-                        if (dead) break;
-                    }
-                    const uint32_t sb = u % SB;
-                    if (u >= SB) dead = !wait(&s_empty[sb], u / SB - 1);
+            if (it.nx == 0) continue;
+            for (int i = it.kb; i < it.ke && !dead; ++i, ++u) {
+                const int kvh = i / it.nx, x = it.x0 + i - kvh * it.nx;
+                if (stays.moved(keep_q, it, kvh, x)) {
+                    if (res > 0 && one) umma_commit(&res_empty);
+                    __syncwarp();
+                    dead = !wait(&res_full, res);
+                    ++res;
+                    if (dead) break;
+                }
+                const uint32_t sb = u % SB;
+                if (u >= SB) dead = !wait(&s_empty[sb], u / SB - 1);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b, ++ring) {
-                        const uint32_t slot = ring % RS;
-                        dead = dead || !wait(&full[slot], ring / RS);
-                        if (dead) break;
-                        tc_fence_after();
-                        const uint64_t stay = sdesc_kmajor_sw128(r0 + b * C::BOX), strm = sdesc_kmajor_sw128(g0 + slot * C::BOX);
-                        const uint64_t a0 = keep_q ? strm : stay, b0 = keep_q ? stay : strm;
-                        const uint32_t d = tmem + (sb * SUMS + b / (NB / SUMS)) * kN;
-                        if (one) {
+                for (int b = 0; b < NB; ++b, ++ring) {
+                    const uint32_t slot = ring % RS;
+                    dead = dead || !wait(&full[slot], ring / RS);
+                    if (dead) break;
+                    tc_fence_after();
+                    const uint64_t stay = sdesc_kmajor_sw128(r0 + b * C::BOX), strm = sdesc_kmajor_sw128(g0 + slot * C::BOX);
+                    const uint64_t a0 = keep_q ? strm : stay, b0 = keep_q ? stay : strm;
+                    const uint32_t d = tmem + (sb * SUMS + b / (NB / SUMS)) * kN;
+                    if (one) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16(d, a0 + kk * 2, b0 + kk * 2, id, (b % (NB / SUMS) > 0 || kk > 0) ? 1u : 0u);
-                            umma_commit(&empty[slot]);
-                        }
-                        __syncwarp();
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_bf16(d, a0 + kk * 2, b0 + kk * 2, id, (b % (NB / SUMS) > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit(&empty[slot]);
                     }
-                    if (!dead && one) umma_commit(&s_full[sb]);
                     __syncwarp();
                 }
+                if (!dead && one) umma_commit(&s_full[sb]);
+                __syncwarp();
             }
         }
         if (dead && lane == 0) {
@@ -359,7 +415,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         }
     } else {
         // ---------------------------------------------------------------- weights
-        WWalk w(p, pref, sched);
+        WWalk w(p, sched);
         WItem it;
         const int st = tid - 128, q4 = warp & 3, grp = (warp - 4) >> 2;
         const int row = q4 * 32 + lane, c0 = grp * (kN / kGroups);
@@ -368,92 +424,91 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         const int ct = st / g.hb, ch = st - ct * g.hb;               // column st: token and head in the tile
         uint32_t u = 0;
         bool dead = false;
+        int d_parts = 0, d_s = 0, d_row = 0;
+        long long at = sched.u0;                                     // first unit of the item on the line
         while (w.next(it)) {
             uint64_t sums[4] = {0ull, 0ull, 0ull, 0ull};
-            const int n = (it.tt1 - it.tt0) * g.nhb, rows = weight_rows(p, it.q), j = it.row0 + row;
-            if (n > 0) {
-                for (int kvh = 0; kvh < g.KV; ++kvh) {
-                    // column st of unit x (its lse is read a unit ahead)
-                    float nl = 0.f;
-                    int tok = -1;
-                    auto fetch = [&](int x) {
-                        tok = -1;
-                        if (st >= kN || x >= n) return;
-                        const int tt = it.tt0 + x / g.nhb, blk = x - x / g.nhb * g.nhb;
-                        const int t = tt * g.tpt + ct, h = blk * g.hb + ch;
-                        if (ct < g.tpt && t < it.q.n && h < g.G) {
-                            nl = p.lse[static_cast<size_t>(it.q.q0 + t) * g.H + kvh * g.G + h];
-                            tok = ct;
+            const int rows = weight_rows(p, it.q), j = it.row0 + row;
+            const int ke = it.nx ? it.ke : it.kb;                    // (nobody sees the rows: no unit)
+            // column st of unit i (its lse is read a unit ahead)
+            float nl = 0.f;
+            int tok = -1;
+            auto fetch = [&](int i) {
+                tok = -1;
+                if (st >= kN || i >= ke) return;
+                const int kvh = i / it.nx, x = it.x0 + i - kvh * it.nx, tt = x / g.nhb, blk = x - tt * g.nhb;
+                const int t = tt * g.tpt + ct, h = blk * g.hb + ch;
+                if (ct < g.tpt && t < it.q.n && h < g.G) {
+                    nl = p.lse[static_cast<size_t>(it.q.q0 + t) * g.H + kvh * g.G + h];
+                    tok = ct;
+                }
+            };
+            fetch(it.kb);
+            for (int i = it.kb; i < ke; ++i, ++u) {
+                const uint32_t sb = u % SB;
+                float* unl = s_nl + (u & 1) * kN;
+                int* utok = s_tok + (u & 1) * kN;
+                if (st < kN) {
+                    // (a query that saw nothing, lse -inf, has no weight to give)
+                    if (tok >= 0 && nl == -INFINITY) tok = -1;
+                    unl[st] = tok >= 0 ? -nl * kLog2e : -INFINITY;
+                    utok[st] = tok;
+                }
+                soft_sync();
+                fetch(i + 1);
+                const int x = it.x0 + i % it.nx, tt = x / g.nhb, blk = x - tt * g.nhb;
+                const int t0 = tt * g.tpt, tn = min(g.tpt, it.q.n - t0), hv = min(g.hb, g.G - blk * g.hb);
+                const int cols = (tn - 1) * g.hb + hv;       // (no query behind them)
+                // every token of the tile sees every row of the unit, and every column has a query
+                const bool open = it.row0 + kPT <= paged_hi(it.q, t0) && it.row0 >= paged_lo(g, it.q, t0 + tn - 1) &&
+                                  (hv == g.hb || tn == 1) && c0 + 32 <= cols;
+                if (!dead) dead = !mbar_wait(&s_full[sb], (u / SB) & 1, &abort_flag, p.wait_ns);
+                tc_fence_after();
+                if (c0 < cols) {
+                    uint32_t r[32];
+                    const uint32_t scol = lane_base + sb * SUMS * kN + c0;
+                    DSV4_TMEM_LD_32x32b_X32(scol, r);
+                    uint64_t x2[16];
+                    if constexpr (SUMS == 2) {
+                        uint32_t r2[32];
+                        DSV4_TMEM_LD_32x32b_X32(scol + kN, r2);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            x2[i] = pack_f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                            add_f32x2(x2[i], pack_f32x2(__uint_as_float(r2[2 * i]), __uint_as_float(r2[2 * i + 1])));
                         }
-                    };
-                    fetch(0);
-                    for (int x = 0; x < n; ++x, ++u) {
-                        const uint32_t sb = u % SB;
-                        float* unl = s_nl + (u & 1) * kN;
-                        int* utok = s_tok + (u & 1) * kN;
-                        if (st < kN) {
-                            // (a query that saw nothing, lse -inf, has no weight to give)
-                            if (tok >= 0 && nl == -INFINITY) tok = -1;
-                            unl[st] = tok >= 0 ? -nl * kLog2e : -INFINITY;
-                            utok[st] = tok;
-                        }
-                        soft_sync();
-                        fetch(x + 1);
-                        const int tt = it.tt0 + x / g.nhb, blk = x - x / g.nhb * g.nhb;
-                        const int t0 = tt * g.tpt, tn = min(g.tpt, it.q.n - t0), hv = min(g.hb, g.G - blk * g.hb);
-                        const int cols = (tn - 1) * g.hb + hv;       // (no query behind them)
-                        // every token of the tile sees every row of the unit, and every column has a query
-                        const bool open = it.row0 + kPT <= paged_hi(it.q, t0) && it.row0 >= paged_lo(g, it.q, t0 + tn - 1) &&
-                                          (hv == g.hb || tn == 1) && c0 + 32 <= cols;
-                        if (!dead) dead = !mbar_wait(&s_full[sb], (u / SB) & 1, &abort_flag, p.wait_ns);
-                        tc_fence_after();
-                        if (c0 < cols) {
-                            uint32_t r[32];
-                            const uint32_t scol = lane_base + sb * SUMS * kN + c0;
-                            DSV4_TMEM_LD_32x32b_X32(scol, r);
-                            uint64_t x2[16];
-                            if constexpr (SUMS == 2) {
-                                uint32_t r2[32];
-                                DSV4_TMEM_LD_32x32b_X32(scol + kN, r2);
-                                tmem_wait_ld();
+                    } else {
+                        tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    x2[i] = pack_f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                                    add_f32x2(x2[i], pack_f32x2(__uint_as_float(r2[2 * i]), __uint_as_float(r2[2 * i + 1])));
-                                }
-                            } else {
-                                tmem_wait_ld();
+                        for (int i = 0; i < 16; ++i)
+                            x2[i] = pack_f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                    }
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    x2[i] = pack_f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                            }
+                    for (int c = 0; c < 16; c += 2) {
+                        const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(unl + c0 + 2 * c);
+                        uint64_t a = m.x, b = m.y;
+                        fma_f32x2(a, x2[c], scale22);
+                        fma_f32x2(b, x2[c + 1], scale22);
+                        float e[4];
+                        unpack_f32x2(a, e[0], e[1]);
+                        unpack_f32x2(b, e[2], e[3]);
+                        if (!open) {
+                            const unsigned bad = *reinterpret_cast<volatile unsigned*>(&s_bad[u & 15]);
+                            const bool live = j < rows && !paged_bad_row(g, bad, row);
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(unl + c0 + 2 * i);
-                                uint64_t a = m.x, b = m.y;
-                                fma_f32x2(a, x2[i], scale22);
-                                fma_f32x2(b, x2[i + 1], scale22);
-                                float e[4];
-                                unpack_f32x2(a, e[0], e[1]);
-                                unpack_f32x2(b, e[2], e[3]);
-                                if (!open) {
-                                    const unsigned bad = *reinterpret_cast<volatile unsigned*>(&s_bad[u & 15]);
-                                    const bool live = j < rows && !paged_bad_row(g, bad, row);
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const int t = utok[c0 + 2 * i + k];
-                                        if (!live || t < 0 || j >= paged_hi(it.q, t0 + t) || j < paged_lo(g, it.q, t0 + t)) e[k] = -INFINITY;
-                                    }
-                                }
-                                add_f32x2(sums[i & 3], pack_f32x2(ex2(e[0]), ex2(e[1])));
-                                add_f32x2(sums[(i & 3) + 1], pack_f32x2(ex2(e[2]), ex2(e[3])));
+                            for (int k = 0; k < 4; ++k) {
+                                const int t = utok[c0 + 2 * c + k];
+                                if (!live || t < 0 || j >= paged_hi(it.q, t0 + t) || j < paged_lo(g, it.q, t0 + t)) e[k] = -INFINITY;
                             }
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s_empty[sb]);
+                        add_f32x2(sums[c & 3], pack_f32x2(ex2(e[0]), ex2(e[1])));
+                        add_f32x2(sums[(c & 3) + 1], pack_f32x2(ex2(e[2]), ex2(e[3])));
                     }
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[sb]);
             }
             float sum = 0.f;
 #pragma unroll
@@ -468,19 +523,29 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 float v = (red[st] + red[kPT + st]) + (red[2 * kPT + st] + red[3 * kPT + st]);
                 const int jj = it.row0 + st;
                 // (a row on a page outside the pool: hidden; the units that all tokens see do not ask)
-                if (n > 0 && paged_bad_row(g, *reinterpret_cast<volatile unsigned*>(&s_bad[(u - 1) & 15]), st)) v = 0.f;
-                if (sched.split > 1) {
-                    p.part[(static_cast<size_t>(it.tile) * sched.split + it.part) * kPT + st] = v;
+                if (it.nx && paged_bad_row(g, *reinterpret_cast<volatile unsigned*>(&s_bad[(u - 1) & 15]), st)) v = 0.f;
+                if (it.kb > 0 || it.ke < it.n) {
+                    p.part[static_cast<size_t>(blockIdx.x * 2 + (it.kb > 0 ? 0 : 1)) * kPT + st] = v;
                 } else if (jj < rows) {
                     const size_t o = static_cast<size_t>(it.s) * p.acc_rows + jj;
                     p.acc[o] = (p.acc_in ? p.acc_in[o] : 0.f) + v;
                 }
             }
-            if (st == 0 && sched.split > 1 && it.part == 0) {
-                p.head[2 + it.tile * 2] = it.s;
-                p.head[3 + it.tile * 2] = it.row0;
+            if (it.kb == 0 && it.ke < it.n) {        // this CTA starts the tile: its parts are added under its number
+                const long long end = at + it.n, T = sched.total, n = min(T, static_cast<long long>(gridDim.x));
+                int last = static_cast<int>((end * n - 1) / T);
+                while (last + 1 < n && T * (last + 1) / n < end) ++last;
+                while (T * last / n >= end) --last;
+                d_parts = last - static_cast<int>(blockIdx.x) + 1;
+                d_s = it.s;
+                d_row = it.row0;
             }
+            at += it.ke - it.kb;
             soft_sync();
+        }
+        if (st == 0) {
+            int* d = p.desc + blockIdx.x * 4;
+            d[0] = d_parts; d[1] = d_s; d[2] = d_row;
         }
         if (dead && lane == 0) {
             atomicOr(&s_err, DSV4_EWORD_TIMEOUT);
@@ -491,34 +556,28 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     __syncthreads();
     tc_fence_after();
     if (warp == 2) tmem_dealloc(tmem, kSB * kN);
-    if (tid == 0) {
-        p.err[blockIdx.x] = s_err;
-        if (blockIdx.x == 0) {
-            p.head[0] = sched.split > 1 ? sched.tiles : 0;
-            p.head[1] = sched.split;
-        }
-    }
+    if (tid == 0) p.err[blockIdx.x] = s_err;
 }
 
-// Adds the partial sums of split items in order, and gathers the error bits.
+// Adds the partial sums of the tiles that several CTAs worked on, in order, one block per CTA that
+// starts one, and gathers the error bits.
 __global__ void __launch_bounds__(kPT)
-paged_weights_sum_kernel(const __grid_constant__ PagedWeightsParams p, int ctas, uint32_t* eword) {
+paged_weights_sum_kernel(const __grid_constant__ PagedWeightsParams p, uint32_t* eword) {
     pdl_wait();
-    const int tid = threadIdx.x;
-    if (blockIdx.x == 0 && tid < 32) {
+    const int tid = threadIdx.x, c = blockIdx.x;
+    if (c == 0 && tid < 32) {
         uint32_t e = 0;
-        for (int c = tid; c < ctas; c += 32) e |= p.err[c];
+        for (int i = tid; i < static_cast<int>(gridDim.x); i += 32) e |= p.err[i];
         e = __reduce_or_sync(~0u, e);
         if (tid == 0) *eword = e;
     }
-    if (static_cast<int>(blockIdx.x) >= p.head[0]) return;
-    const int split = p.head[1], s = p.head[2 + blockIdx.x * 2], j = p.head[3 + blockIdx.x * 2] + tid;
+    const int parts = p.desc[c * 4], s = p.desc[c * 4 + 1], j = p.desc[c * 4 + 2] + tid;
+    if (parts == 0) return;
     bool dummy = false;
     if (j >= weight_rows(p, paged_seq(p.g, s, dummy))) return;
-    const float* src = p.part + static_cast<size_t>(blockIdx.x) * split * kPT + tid;
-    float v = 0.f;
+    float v = p.part[static_cast<size_t>(c * 2 + 1) * kPT + tid];
 #pragma unroll 8
-    for (int i = 0; i < split; ++i) v += src[i * kPT];
+    for (int i = 1; i < parts; ++i) v += p.part[static_cast<size_t>((c + i) * 2) * kPT + tid];
     const size_t o = static_cast<size_t>(s) * p.acc_rows + j;
     p.acc[o] = (p.acc_in ? p.acc_in[o] : 0.f) + v;
 }
@@ -545,8 +604,8 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
     p.acc = a.acc;
     p.acc_rows = a.acc_rows;
     p.part = reinterpret_cast<float*>(ws);
-    p.head = reinterpret_cast<int*>(ws + static_cast<size_t>(kMaxShares * ctas) * kPT * 4);
-    p.err = reinterpret_cast<uint32_t*>(p.head + 2 + kMaxShares * ctas);
+    p.desc = reinterpret_cast<int*>(ws + static_cast<size_t>(2 * ctas) * kPT * 4);
+    p.err = reinterpret_cast<uint32_t*>(p.desc + 4 * ctas);
     // one row tile per sequence: the queries stay
     p.keep_q = p.g.nhb == 1 && a.max_q <= p.g.tpt;
     p.scale2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
@@ -559,7 +618,7 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
     count_launch();
     if (launch_k(kern, dim3(ctas), dim3(kThreads), C::SMEM, st, true, qmap, kmap, p) != cudaSuccess) return DSV4_ERR_LAUNCH;
     count_launch();
-    return launch_k(paged_weights_sum_kernel, dim3(kMaxShares / 2 * ctas), dim3(kPT), 0, st, true, p, ctas, eword) == cudaSuccess
+    return launch_k(paged_weights_sum_kernel, dim3(ctas), dim3(kPT), 0, st, true, p, eword) == cudaSuccess
                ? DSV4_OK : DSV4_ERR_LAUNCH;
 }
 
@@ -568,7 +627,7 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
 size_t paged_weights_ws_bytes(const dsv4_paged_weights_args& a) {
     (void)a;
     const size_t n = static_cast<size_t>(weight_ctas());
-    return kMaxShares * n * kPT * 4 + (2 + (kMaxShares + 1) * n) * 4;
+    return 2 * n * kPT * 4 + 5 * n * 4;
 }
 
 int launch_paged_weights(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t st) {
