@@ -185,11 +185,12 @@ __device__ void weight_schedule(const PagedWeightsParams& p, long long* pref, WS
     __syncthreads();
 }
 
-// A CTA's part [kb, ke) of a tile's n units: unit i is KV head i / nx, row tile x0 + i % nx (nx = 0:
-// nobody sees the rows).
+// A CTA's part [kb, ke) of a tile's n units: KV head by KV head, token tile by token tile, head
+// block by head block (nx = 0: nobody sees the rows, and the one unit has no work).
 struct WItem {
     PagedSeq q;
-    int s, row0, n, kb, ke, nx, x0;
+    int s, row0, n, kb, ke, nx;
+    int tt0, tt1;                        // token tiles that see the rows
     int lo_u, hi_u;                      // rows that some token of the tile sees
 };
 
@@ -217,7 +218,8 @@ struct WWalk {
         o.row0 = tile * kPT;
         const WSpan w = weight_span(g, q, o.row0);
         o.nx = (w.tt1 - w.tt0) * g.nhb;
-        o.x0 = w.tt0 * g.nhb;
+        o.tt0 = w.tt0;
+        o.tt1 = w.tt1;
         o.n = max(o.nx * g.KV, 1);
         o.lo_u = o.nx ? paged_lo(g, q, w.tt0 * g.tpt) : 0;
         o.hi_u = o.nx ? min(paged_hi(q, min(w.tt1 * g.tpt, q.n) - 1), weight_rows(p, q)) : 0;
@@ -231,14 +233,34 @@ struct WWalk {
     }
 };
 
+// A unit of an item, counted on without divisions.
+struct WUnit {
+    int kvh, tt, blk;
+    __device__ WUnit(const PagedGeom& g, const WItem& it) {
+        const int nx = max(it.nx, 1);
+        kvh = it.kb / nx;
+        const int x = it.kb - kvh * nx;
+        tt = x / g.nhb;
+        blk = x - tt * g.nhb;
+        tt += it.tt0;
+    }
+    __device__ void step(const PagedGeom& g, const WItem& it) {
+        if (++blk < g.nhb) return;
+        blk = 0;
+        if (++tt < it.tt1) return;
+        tt = it.tt0;
+        ++kvh;
+    }
+};
+
 // What the resident operand holds: the queries of one row tile, or the rows of a tile's KV head.
 struct WStay {
     int a = -1, h = -1, b = -1;
-    __device__ bool moved(bool keep_q, const WItem& it, int kvh, int x) {
-        const int nb = keep_q ? x : it.row0;
-        if (a == it.s && h == kvh && b == nb) return false;
+    __device__ bool moved(bool keep_q, const PagedGeom& g, const WItem& it, const WUnit& c) {
+        const int nb = keep_q ? c.tt * g.nhb + c.blk : it.row0;
+        if (a == it.s && h == c.kvh && b == nb) return false;
         a = it.s;
-        h = kvh;
+        h = c.kvh;
         b = nb;
         return true;
     }
@@ -316,10 +338,10 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             auto load_q = [&](uint8_t* dst, uint64_t* bar, int kvh, int b, int tt, int blk) {
                 if (lane == 0) tma_load_3d(dst, &qmap, bar, b * 64, kvh * g.G + blk * g.hb, it.q.q0 + tt * g.tpt);
             };
-            for (int i = it.kb; i < it.ke && !dead; ++i, ++unit) {
-                const int kvh = i / it.nx, x = it.x0 + i - kvh * it.nx;
-                const int tt = x / g.nhb, blk = x - tt * g.nhb;
-                if (stays.moved(keep_q, it, kvh, x)) {
+            WUnit c(g, it);
+            for (int i = it.kb; i < it.ke && !dead; ++i, ++unit, c.step(g, it)) {
+                const int kvh = c.kvh, tt = c.tt, blk = c.blk;
+                if (stays.moved(keep_q, g, it, c)) {
                     if (res > 0) dead = __any_sync(~0u, !mbar_wait(&res_empty, (res - 1) & 1, &abort_flag, p.wait_ns));
                     if (dead) break;
                     if (lane == 0) {
@@ -377,9 +399,9 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         const uint32_t id = idesc_bf16_f32(kPT, kN);
         while (!dead && w.next(it)) {
             if (it.nx == 0) continue;
-            for (int i = it.kb; i < it.ke && !dead; ++i, ++u) {
-                const int kvh = i / it.nx, x = it.x0 + i - kvh * it.nx;
-                if (stays.moved(keep_q, it, kvh, x)) {
+            WUnit c(g, it);
+            for (int i = it.kb; i < it.ke && !dead; ++i, ++u, c.step(g, it)) {
+                if (stays.moved(keep_q, g, it, c)) {
                     if (res > 0 && one) umma_commit(&res_empty);
                     __syncwarp();
                     dead = !wait(&res_full, res);
@@ -433,17 +455,17 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             // column st of unit i (its lse is read a unit ahead)
             float nl = 0.f;
             int tok = -1;
-            auto fetch = [&](int i) {
+            auto fetch = [&](const WUnit& c, int i) {
                 tok = -1;
                 if (st >= kN || i >= ke) return;
-                const int kvh = i / it.nx, x = it.x0 + i - kvh * it.nx, tt = x / g.nhb, blk = x - tt * g.nhb;
-                const int t = tt * g.tpt + ct, h = blk * g.hb + ch;
+                const int t = c.tt * g.tpt + ct, h = c.blk * g.hb + ch;
                 if (ct < g.tpt && t < it.q.n && h < g.G) {
-                    nl = p.lse[static_cast<size_t>(it.q.q0 + t) * g.H + kvh * g.G + h];
+                    nl = p.lse[static_cast<size_t>(it.q.q0 + t) * g.H + c.kvh * g.G + h];
                     tok = ct;
                 }
             };
-            fetch(it.kb);
+            WUnit c(g, it);
+            fetch(c, it.kb);
             for (int i = it.kb; i < ke; ++i, ++u) {
                 const uint32_t sb = u % SB;
                 float* unl = s_nl + (u & 1) * kN;
@@ -455,13 +477,16 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     utok[st] = tok;
                 }
                 soft_sync();
-                fetch(i + 1);
-                const int x = it.x0 + i % it.nx, tt = x / g.nhb, blk = x - tt * g.nhb;
-                const int t0 = tt * g.tpt, tn = min(g.tpt, it.q.n - t0), hv = min(g.hb, g.G - blk * g.hb);
+                const int t0 = c.tt * g.tpt, tn = min(g.tpt, it.q.n - t0), hv = min(g.hb, g.G - c.blk * g.hb);
+                c.step(g, it);
+                fetch(c, i + 1);
                 const int cols = (tn - 1) * g.hb + hv;       // (no query behind them)
                 // every token of the tile sees every row of the unit, and every column has a query
                 const bool open = it.row0 + kPT <= paged_hi(it.q, t0) && it.row0 >= paged_lo(g, it.q, t0 + tn - 1) &&
                                   (hv == g.hb || tn == 1) && c0 + 32 <= cols;
+                // else, of the tile's tokens, those that see row j
+                const int from = j - (it.q.L - it.q.n) - t0, seen0 = max(from, 0);
+                const int seen1 = g.window > 0 && g.window - 1 < g.tpt - from ? from + g.window - 1 : g.tpt;
                 if (!dead) dead = !mbar_wait(&s_full[sb], (u / SB) & 1, &abort_flag, p.wait_ns);
                 tc_fence_after();
                 if (c0 < cols) {
@@ -494,13 +519,11 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         unpack_f32x2(a, e[0], e[1]);
                         unpack_f32x2(b, e[2], e[3]);
                         if (!open) {
-                            const unsigned bad = *reinterpret_cast<volatile unsigned*>(&s_bad[u & 15]);
-                            const bool live = j < rows && !paged_bad_row(g, bad, row);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int t = utok[c0 + 2 * c + k];
-                                if (!live || t < 0 || j >= paged_hi(it.q, t0 + t) || j < paged_lo(g, it.q, t0 + t)) e[k] = -INFINITY;
-                            }
+                            const int4 t = *reinterpret_cast<const int4*>(utok + c0 + 2 * c);
+                            if (t.x < seen0 || t.x > seen1) e[0] = -INFINITY;
+                            if (t.y < seen0 || t.y > seen1) e[1] = -INFINITY;
+                            if (t.z < seen0 || t.z > seen1) e[2] = -INFINITY;
+                            if (t.w < seen0 || t.w > seen1) e[3] = -INFINITY;
                         }
                         add_f32x2(sums[c & 3], pack_f32x2(ex2(e[0]), ex2(e[1])));
                         add_f32x2(sums[(c & 3) + 1], pack_f32x2(ex2(e[2]), ex2(e[3])));
@@ -522,7 +545,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             if (st < kPT) {
                 float v = (red[st] + red[kPT + st]) + (red[2 * kPT + st] + red[3 * kPT + st]);
                 const int jj = it.row0 + st;
-                // (a row on a page outside the pool: hidden; the units that all tokens see do not ask)
+                // (a row on a page outside the pool: hidden)
                 if (it.nx && paged_bad_row(g, *reinterpret_cast<volatile unsigned*>(&s_bad[(u - 1) & 15]), st)) v = 0.f;
                 if (it.kb > 0 || it.ke < it.n) {
                     p.part[static_cast<size_t>(blockIdx.x * 2 + (it.kb > 0 ? 0 : 1)) * kPT + st] = v;
