@@ -150,6 +150,7 @@ bool norm_rope_ok(const dsv4_norm_rope_args* a) {
     if (a->dim != 128 && a->dim != 256 && a->dim != 512) return false;
     if (a->rope_dim < 0 || a->rope_dim > a->dim || a->rope_dim > 128 || (a->rope_dim & 1)) return false;
     if (!(a->eps >= 0.f) || !std::isfinite(a->eps) || !std::isfinite(a->rope_theta) || a->rope_theta <= 0.0) return false;
+    if (a->tokens == 0) return true;                 // nothing to do: no array is looked at
     if (!num_ok(a->pos, 8) || !opt_ptr_ok(a->gamma_q) || !opt_ptr_ok(a->gamma_k)) return false;
     if (a->heads) {
         if (!dev_ptr_ok(a->q) || !dev_ptr_ok(a->q_out) || !stride_ok(a->q_stride, a->heads, a->dim) ||
@@ -175,6 +176,7 @@ bool paged_attn_ok(const dsv4_paged_attn_args* a) {
     if (!a || !paged_ok(a->batch, a->kv_heads, a->dim, a->page_size, a->num_pages, a->max_pages)) return false;
     if (!heads_ok(a->heads, a->kv_heads) || !stride_ok(a->q_stride, a->heads, a->dim)) return false;
     if (a->total_q < 0 || a->total_q > (1 << 24) || a->max_q < 1 || a->window < 0 || !std::isfinite(a->scale)) return false;
+    if (a->batch == 0 || a->total_q == 0) return true;   // nothing to do: no array is looked at
     if (!dev_ptr_ok(a->q) || !dev_ptr_ok(a->k_pages) || !opt_ptr_ok(a->v_pages) || !num_ok(a->block_table, 4) ||
         !num_ok(a->cu_q, 4) || !num_ok(a->kv_len, 4) || !opt_num_ok(a->sink, 4) || !dev_ptr_ok(a->out) || !opt_num_ok(a->lse, 4) ||
         !opt_num_ok(a->out_rope_pos, 8))
@@ -189,14 +191,17 @@ bool paged_attn_ok(const dsv4_paged_attn_args* a) {
 bool paged_weights_ok(const dsv4_paged_weights_args* a) {
     if (!a || !paged_ok(a->batch, a->kv_heads, a->dim, a->page_size, a->num_pages, a->max_pages)) return false;
     if (!heads_ok(a->heads, a->kv_heads) || !stride_ok(a->q_stride, a->heads, a->dim)) return false;
-    if (a->total_q < 1 || a->total_q > (1 << 24) || a->max_q < 1 || a->window < 0 || a->acc_rows < 1 || !std::isfinite(a->scale))
+    if (a->total_q < 0 || a->total_q > (1 << 24) || a->max_q < 1 || a->window < 0 || a->acc_rows < 1 || !std::isfinite(a->scale))
         return false;
-    return dev_ptr_ok(a->q) && num_ok(a->lse, 4) && dev_ptr_ok(a->k_pages) && num_ok(a->block_table, 4) &&
+    if (a->batch == 0) return true;
+    // (without tokens acc is acc_in, and there is no query to point to)
+    return (a->total_q == 0 || (dev_ptr_ok(a->q) && num_ok(a->lse, 4))) && dev_ptr_ok(a->k_pages) && num_ok(a->block_table, 4) &&
            num_ok(a->cu_q, 4) && num_ok(a->kv_len, 4) && opt_num_ok(a->acc_in, 4) && num_ok(a->acc, 4);
 }
 
 bool paged_evict_ok(const dsv4_paged_evict_args* a) {
     if (!a || !paged_ok(a->batch, a->kv_heads, a->dim, a->page_size, a->num_pages, a->max_pages)) return false;
+    if (a->batch == 0) return true;
     if (!dev_ptr_ok(a->k_pages) || !opt_ptr_ok(a->v_pages) || !num_ok(a->block_table, 4) || !num_ok(a->out_table, 4) ||
         !num_ok(a->kv_len, 4) || !num_ok(a->kv_len_out, 4) || !num_ok(a->acc, 4) || !num_ok(a->acc_out, 4) ||
         !num_ok(a->keep, 4))

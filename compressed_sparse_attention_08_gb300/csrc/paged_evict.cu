@@ -93,6 +93,12 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
             long long from = -1, to = -1;
             if (i < r1) {
                 const int s = i < kept_old ? p.idx[static_cast<size_t>(b) * (k_old > 0 ? k_old : 1) + i] : n_old + i - kept_old;
+                if (static_cast<unsigned>(s) >= static_cast<unsigned>(len)) {   // (a NaN weight: no choice of rows)
+                    flag_error(p.eword, DSV4_EWORD_BAD_INDEX);
+                    s_src[j] = s_dst[j] = -1;
+                    if (lists) p.keep[static_cast<size_t>(b) * p.budget + i] = -1;
+                    continue;
+                }
                 src[k] = s;
                 if (lists) w[k] = p.acc[static_cast<size_t>(b) * p.acc_rows + s];
                 if (!(IN_PLACE && p.same && s == i)) {

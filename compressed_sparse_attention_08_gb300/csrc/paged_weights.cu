@@ -618,9 +618,9 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
                      a.kv_heads, a.window, kPT);
     paged_tile(p.g, kN);
     CUtensorMap qmap, kmap;
-    if (!paged_query_map(&qmap, a.q, D, a.heads, a.total_q, a.q_stride, p.g.hb, p.g.tpt) ||
-        !paged_pool_map(&kmap, a.k_pages, D, a.kv_heads, a.page_size, a.num_pages, p.g.br))
-        return DSV4_ERR_LAUNCH;
+    if (!paged_pool_map(&kmap, a.k_pages, D, a.kv_heads, a.page_size, a.num_pages, p.g.br)) return DSV4_ERR_LAUNCH;
+    qmap = kmap;                         // (no tokens: never used)
+    if (a.total_q > 0 && !paged_query_map(&qmap, a.q, D, a.heads, a.total_q, a.q_stride, p.g.hb, p.g.tpt)) return DSV4_ERR_LAUNCH;
     const int ctas = weight_ctas();
     p.lse = a.lse;
     p.acc_in = a.acc_in;

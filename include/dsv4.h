@@ -347,7 +347,8 @@ int dsv4_quantize_rows_fp8(const void* x, int rows, int dim, void* q, float* sca
  * token sees must be finite for the others too (a tile's rows meet all its tokens in the tensor
  * core, the ones a token does not see with weight 0); rows that none sees may hold anything.
  * Counts outside their arrays are clamped and rows on a page outside the pool are hidden; both
- * set DSV4_EWORD_BAD_INDEX. batch: 0..2048; max_pages *
+ * set DSV4_EWORD_BAD_INDEX. Calls without sequences or without tokens are valid and need no
+ * arrays for them (the weights of a call without tokens are acc_in). batch: 0..2048; max_pages *
  * page_size: at most 2^29 (times batch: below 2^37). Lengths, tables, positions, lse, sink and acc need
  * the alignment of their type only (a table may be a slice of a larger one).
  */
@@ -458,7 +459,7 @@ typedef struct dsv4_paged_evict_args {
     float* acc_out;           /* fp32 [batch, acc_rows]                                       */
     int32_t* keep;            /* int32 [batch, budget]                                        */
     int batch, kv_heads, dim, page_size, num_pages, max_pages, out_pages;
-    int acc_rows;             /* >= max_pages * page_size is not required: longer sequences are clamped (and flagged) */
+    int acc_rows;             /* longer sequences are cut to it (and flagged)                 */
     int budget, recent;       /* 1 <= budget <= acc_rows and out_pages * page_size; 0 <= recent <= budget */
 } dsv4_paged_evict_args;
 

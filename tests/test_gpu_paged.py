@@ -581,3 +581,123 @@ def test_a_serving_loop():
             assert all(keep[s, :len(r)].tolist() == r for s, r in enumerate(kept))
             for s in range(B):
                 acc[s, lens[s]:] = 0                 # rows that the next tokens fill start without weight
+
+
+# ------------------------------------------------------------------ empty calls, many sequences, bad pages
+def test_calls_without_tokens_or_sequences():
+    """No token: attention and append leave everything alone and the weights are acc_in; no sequence: nothing."""
+    m = lib()
+    g = gen(40)
+    c = Cache(g, [70, 130], 16, 2, 128, False)
+    q = torch.empty(0, 8, 128, dtype=BF, device="cuda")
+    for table, cu, n in ((c.table, i32([0, 0, 0]), c.kv_len), (c.table[:0], i32([0]), c.kv_len[:0])):
+        lse = torch.empty(0, 8, device="cuda")
+        a = m.paged_attn_args(q, torch.empty_like(q), c.k, table, cu, n, v_pages=c.v, lse=lse)
+        ws = ws_for(m.dsv4_paged_attn_workspace_size(a))
+        m.dsv4_paged_attn(a, ws)
+        assert m.dsv4_read_error_word(ws) == (0, 0)
+        acc = torch.full((n.shape[0], 140), 7.0, device="cuda")
+        acc_in = torch.arange(140, device="cuda", dtype=torch.float32).repeat(n.shape[0], 1)
+        a = m.paged_weights_args(q, lse, c.k, table, cu, n, acc, acc_in=acc_in)
+        ws = ws_for(m.dsv4_paged_attn_weights_workspace_size(a))
+        m.dsv4_paged_attn_weights(a, ws)
+        assert m.dsv4_read_error_word(ws) == (0, 0)
+        for s, L in enumerate(c.lens[:n.shape[0]]):
+            assert torch.equal(acc[s, :L], acc_in[s, :L]) and (acc[s, L:] == 7).all()
+    before = c.k.clone()
+    a = m.norm_rope_args(q, torch.empty_like(q), torch.empty(0, dtype=torch.int64, device="cuda"), k=q[:, :2], k_pages=c.k,
+                         slots=torch.empty(0, dtype=torch.int64, device="cuda"))
+    m.dsv4_norm_rope_append(a)
+    torch.cuda.synchronize()
+    assert torch.equal(before.view(torch.int16), c.k.view(torch.int16))
+
+
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("longest", [1, 5, 70])
+def test_weights_of_many_sequences(window, longest):
+    """More sequences than the block has warps, some without tokens or rows, some with more rows than acc."""
+    m = lib()
+    g = gen(41)
+    r = torch.Generator().manual_seed(longest)
+    B, rows = 300, 500
+    lens = torch.randint(0, 700, (B,), generator=r).tolist()
+    ns = [min(int(n), L) for n, L in zip(torch.randint(0, longest + 1, (B,), generator=r), lens)]
+    c = Cache(g, lens, 8, 2, 128, True)
+    cu = cu_of(ns)
+    q = normal(g, cu[-1], 8, 128, std=2.0)
+    scale = 1 / math.sqrt(128)
+    lse = ref.attention(q, c.k, None, c.table, cu, lens, scale, window)[1].float()
+    acc = torch.full((B, 700), -3.0, device="cuda")
+    a = m.paged_weights_args(q, lse, c.k, c.table, i32(cu), c.kv_len, acc, max_q=longest, window=window)
+    ws = ws_for(m.dsv4_paged_attn_weights_workspace_size(a))
+    m.dsv4_paged_attn_weights(a, ws)
+    assert m.dsv4_read_error_word(ws) == (0, 0)
+    want, tol = ref.weights(q, lse, c.k, c.table, cu, lens, scale, torch.full_like(acc, -3.0), None, window)
+    assert ((acc.double() - want).abs() <= tol).all()
+    # an accumulator of fewer rows: the same, cut, and reported
+    short = torch.full((B, rows), -3.0, device="cuda")
+    a = m.paged_weights_args(q, lse, c.k, c.table, i32(cu), c.kv_len, short, max_q=longest, window=window)
+    m.dsv4_paged_attn_weights(a, ws)
+    assert m.dsv4_read_error_word(ws)[1] == m.DSV4_EWORD_BAD_INDEX
+    assert ((short.double() - want[:, :rows]).abs() <= tol[:, :rows]).all()
+
+
+def test_weights_hide_a_page_outside_the_pool():
+    m = lib()
+    g = gen(42)
+    for ns in ([1, 1], [90, 200]):
+        lens = [400, 300]
+        c = Cache(g, lens, 16, 1, 256)
+        cu = cu_of(ns)
+        q = normal(g, cu[-1], 16, 256, std=2.0)
+        lse = ref.attention(q, c.k, None, c.table, cu, lens, 1 / 16)[1].float()
+        want, tol = ref.weights(q, lse, c.k, c.table, cu, lens, 1 / 16, torch.zeros(2, 400, device="cuda"), None)
+        c.table[0, 3] = c.k.shape[0]                                 # rows 48 .. 63
+        c.table[1, 10] = -1                                          # rows 160 .. 175
+        want[0, 48:64] = 0
+        want[1, 160:176] = 0
+        acc = torch.zeros(2, 400, device="cuda")
+        a = m.paged_weights_args(q, lse, c.k, c.table, i32(cu), c.kv_len, acc, max_q=max(ns))
+        ws = ws_for(m.dsv4_paged_attn_weights_workspace_size(a))
+        m.dsv4_paged_attn_weights(a, ws)
+        assert m.dsv4_read_error_word(ws)[1] == m.DSV4_EWORD_BAD_INDEX
+        assert ((acc.double() - want).abs() <= tol).all()
+
+
+def test_tables_and_lengths_may_be_slices():
+    """Lengths, tables and accumulators at addresses of their type's alignment only."""
+    m = lib()
+    g = gen(43)
+    lens, ns = [333, 200, 45], [3, 1, 45]
+    c = Cache(g, lens, 16, 1, 128)
+    cu = cu_of(ns)
+
+    def shifted(t):
+        room = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        room[1:] = t.flatten()
+        return room[1:].view(t.shape)
+
+    q = normal(g, cu[-1], 8, 128, std=2.0)
+    out = torch.empty_like(q)
+    lse = shifted(torch.zeros(cu[-1], 8, device="cuda"))
+    sink = shifted(normal(g, 8, dtype=torch.float32))
+    table, cuq, n = shifted(c.table), shifted(i32(cu)), shifted(c.kv_len)
+    a = m.paged_attn_args(q, out, c.k, table, cuq, n, lse=lse, sink=sink)
+    ws = ws_for(m.dsv4_paged_attn_workspace_size(a))
+    m.dsv4_paged_attn(a, ws)
+    scale = 1 / math.sqrt(128)
+    ref.check_attention(out, lse, ref.attention(q, c.k, None, c.table, cu, lens, scale, sink=sink))
+    acc = shifted(torch.zeros(3, 333, device="cuda"))
+    a = m.paged_weights_args(q, lse, c.k, table, cuq, n, acc)
+    ws = ws_for(m.dsv4_paged_attn_weights_workspace_size(a))
+    m.dsv4_paged_attn_weights(a, ws)
+    want, tol = ref.weights(q, lse, c.k, c.table, cu, lens, scale, torch.zeros_like(acc), None)
+    assert ((acc.double() - want).abs() <= tol).all()
+    keep = shifted(torch.zeros(3, 50, dtype=torch.int32, device="cuda"))
+    rows, old = c.k[c.table[0, :21].long()].flatten(0, 1).clone(), acc.clone()
+    a = m.paged_evict_args(c.k, table, n, acc, keep, budget=50, recent=10)
+    m.dsv4_paged_evict(a, ws_for(m.dsv4_paged_evict_workspace_size(a)))
+    top = old[0, :323].topk(40).indices.sort().values
+    assert torch.equal(keep[0].long(), torch.cat([top, torch.arange(323, 333, device="cuda")]))
+    assert torch.equal(c.k[c.table[0, :4].long()].flatten(0, 1)[:50], rows[keep[0].long()])
+    assert n.tolist() == [50, 50, 45]
