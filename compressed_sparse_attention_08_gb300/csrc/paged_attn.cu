@@ -64,12 +64,14 @@ struct PagedAttnParams {
 };
 
 constexpr int kMaxSlots = 8;
+constexpr int kSegs = 8;                 // tiles described at a time (the loads run at most three ahead of the outputs)
 constexpr int kPT = 128;                 // cache rows per unit
 template <int N>
 struct PagedCtl {
     uint64_t q_full, q_empty, full[kMaxSlots], empty[kMaxSlots], s_full[2], s_empty[2], p_full[2], pv_done[2];
     uint64_t v_ready, v_clean;           // V apart from K: an edge unit's rows have come, and are cleared
     PagedSched sched;
+    PagedSeg segs[kSegs];                // the tiles, written by the load warps for the softmax
     alignas(16) float nm[N];             // reference maxima (base-2 units), negated
     alignas(16) float f[N];              // factors
     uint32_t top[N];                     // a unit's maxima as ordered keys
@@ -269,6 +271,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 if (seg > 0) dead = __any_sync(~0u, !mbar_wait(&ctl.q_empty, (seg - 1) & 1, abort_flag, p.wait_ns));
                 if (dead) break;
                 if (lane == 0) {
+                    if (mine == 0) ctl.segs[seg % kSegs] = sg;
                     if (mine == 0) mbar_arrive_expect_tx(&ctl.q_full, qbytes);
                     else mbar_arrive(&ctl.q_full);
 #pragma unroll 1
@@ -403,8 +406,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         }
     } else {
         // ---------------------------------------------------------------- softmax and output
-        PagedWalk w(g, sched);
-        PagedSeg sg;
         const int st = tid - 128, q4 = warp & 3, grp = (warp - 4) >> 2;
         const int c0 = grp * (N / kGroups);                          // columns of this thread's group
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
@@ -413,15 +414,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         auto pv_over = [&](uint32_t x) { return mbar_wait(&ctl.pv_done[x & 1], (x >> 1) & 1, abort_flag, p.wait_ns); };
         uint32_t u = 0, edges = 0;
         bool dead = false;
-        int d_parts = 0, d_tok = 0, d_tn = 0, d_head = 0, d_hv = 0;
-        long long at = sched.u0;                                     // first unit of the segment on the line
-        while (w.next(sg)) {
-            soft_sync();                                             // the tile before is written out
+        const int ct = st / g.hb;                                    // column st's token in a tile
+        int* desc = p.desc + worker * 8;
+        if (st == 0) desc[0] = 0;
+        for (uint32_t tile = 0; u < units; ++tile) {
+            // The tile's description stays in shared memory (walked here it took the registers that the
+            // scores need): its first scores come after it. All warps go on, or none.
+            if (!dead) dead = !mbar_wait(&ctl.s_full[u & 1], (u >> 1) & 1, abort_flag, p.wait_ns);
+            if (soft_sync_or(dead)) break;                           // (and the tile before is written out)
+            const PagedSeg& sg = ctl.segs[tile % kSegs];
             if (st < N) {
-                const int t = st / g.hb, h = st - t * g.hb;
-                const bool ok = t < sg.tn && h < sg.hv;
+                const int h = st - ct * g.hb;
+                const bool ok = ct < sg.tn && h < sg.hv;
                 s_nm[st] = ok ? INFINITY : -INFINITY;                // (a column without a query gets P = 0)
-                ctl.tok[st] = ok ? t : 255;
+                ctl.tok[st] = ok ? ct : 255;
             }
             soft_sync();
             const int base = sg.q.L - sg.q.n + sg.t0;                // row of the tile's first token
@@ -430,7 +436,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             uint64_t lacc[NE / 2];                                   // this row's P per query (pairs), summed over the units
 #pragma unroll
             for (int i = 0; i < NE / 2; ++i) lacc[i] = 0ull;
-            for (int k = sg.kb; k < sg.ke; ++k, ++u) {
+            const int kb = sg.kb, ke = sg.ke;
+            for (int k = kb; k < ke; ++k, ++u) {
                 if (!dead) dead = !mbar_wait(&ctl.s_full[u & 1], (u >> 1) & 1, abort_flag, p.wait_ns);
                 tc_fence_after();
                 const int j0 = sg.row0 + k * kPT;
@@ -503,7 +510,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 // With few scores per thread the vote comes after P, so that the warps need not wait for
                 // one another between their steps, and P is formed again where it was too soon; with many,
                 // what is held across the vote would not fit.
-                bool rescale = false, over = k == sg.kb;
+                bool rescale = false, over = k == kb;
                 if (!over) {
                     scores();
                     less_ref();
@@ -526,7 +533,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         if (cm > mo) {
                             f = mo == -INFINITY ? 0.f : ex2(mo - cm);
                             s_nm[st] = -cm;
-                            rescale = k > sg.kb;
+                            rescale = k > kb;
                         }
                         s_f[st] = f;
                         ctl.top[st] = 0;
@@ -638,14 +645,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             for (int cb = c0; cb < c0 + NE && cb < cols; cb += 16) {
                 // Two columns at a time: even lanes write the first, odd lanes the second, each a pair
                 // of neighbouring channels.
-                float f[16];
-                int off[8], tok[8];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = s_f[cb + i];
+                int off[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int c = cb + 2 * i + (lane & 1), t = ctl.tok[c];
-                    tok[i] = t;
                     off[i] = t == 255 ? -1 : (t * g.H + c - t * g.hb) * D;
                 }
 #pragma unroll 1
@@ -659,46 +662,50 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         continue;
                     }
                     const int d = mt * 128 + (row & ~1);             // this lane's pair of channels
-                    const bool rot = p.orp && d >= r0;
-                    int rt = -1;
-                    float2 cs = make_float2(1.f, 0.f);
+                    float e[8], o[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         // (a factor of 0 stands for a query that sees nothing: O may hold anything)
-                        const float a = f[2 * i] == 0.f ? 0.f : __uint_as_float(r[2 * i]) * f[2 * i];
-                        const float b = f[2 * i + 1] == 0.f ? 0.f : __uint_as_float(r[2 * i + 1]) * f[2 * i + 1];
+                        const float2 f = *reinterpret_cast<const float2*>(s_f + cb + 2 * i);
+                        const float a = f.x == 0.f ? 0.f : __uint_as_float(r[2 * i]) * f.x;
+                        const float b = f.y == 0.f ? 0.f : __uint_as_float(r[2 * i + 1]) * f.y;
                         const float got = __shfl_xor_sync(~0u, (lane & 1) ? a : b, 1);
-                        float e = (lane & 1) ? got : a, o = (lane & 1) ? b : got;
-                        if (rot && tok[i] != 255) {
-                            if (tok[i] != rt) { cs = out_rope_cs(p, sg.tok0 + tok[i], (d - r0) >> 1); rt = tok[i]; }
-                            const float e0 = e;
-                            e = e0 * cs.x + o * cs.y;
-                            o = -e0 * cs.y + o * cs.x;
-                        }
-                        if (off[i] >= 0) *reinterpret_cast<uint32_t*>(ob + off[i] + d) = pack2(e, o);
+                        e[i] = (lane & 1) ? got : a;
+                        o[i] = (lane & 1) ? b : got;
                     }
+                    if (p.orp && mt * 128 + q4 * 32 + 31 >= r0) {    // (a warp's 32 channels: apart, or the branches below cost all)
+                        int rt = 255;
+                        float2 cs = make_float2(1.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int t = ctl.tok[cb + 2 * i + (lane & 1)];
+                            if (d < r0 || t == 255) continue;
+                            if (t != rt) { cs = out_rope_cs(p, sg.tok0 + t, (d - r0) >> 1); rt = t; }
+                            const float e0 = e[i];
+                            e[i] = e0 * cs.x + o[i] * cs.y;
+                            o[i] = -e0 * cs.y + o[i] * cs.x;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (off[i] >= 0) *reinterpret_cast<uint32_t*>(ob + off[i] + d) = pack2(e[i], o[i]);
                 }
             }
-            if (!whole && sg.kb == 0) {                              // this worker starts the tile: it is merged under its number
-                const long long end = at + sg.n, T = sched.total;
+            if (st == 0 && !whole && sg.kb == 0) {                   // this worker starts the tile: it is merged under its number
+                const long long end = sched.u0 + u - sg.ke + sg.n, T = sched.total;
                 int last = static_cast<int>((end * sched.ge - 1) / T);
                 while (last + 1 < sched.ge && T * (last + 1) / sched.ge < end) ++last;
                 while (T * last / sched.ge >= end) --last;
-                d_parts = last - worker + 1;
-                d_tok = sg.tok0;
-                d_tn = sg.tn;
-                d_head = sg.head0;
-                d_hv = sg.hv;
+                desc[0] = last - worker + 1;
+                desc[1] = sg.tok0;
+                desc[2] = sg.tn;
+                desc[3] = sg.head0;
+                desc[4] = sg.hv;
             }
-            at += sg.ke - sg.kb;
         }
         if (dead && lane == 0) {
             atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
             ctl.abort = 1;
-        }
-        if (st == 0) {
-            int* d = p.desc + worker * 8;
-            d[0] = d_parts; d[1] = d_tok; d[2] = d_tn; d[3] = d_head; d[4] = d_hv;
         }
     }
     tc_fence_before();
