@@ -107,12 +107,10 @@ __device__ __forceinline__ bool unit_edge(const PagedGeom& g, const PagedSeg& sg
     return j0 < sg.lo_u || j0 + g.unit > sg.hi_u || bad != 0;
 }
 
-// Places of unit u's tiles in the order of loading, in tiles, of `units` in all: K0 K1 V0 K2 V1 ..,
-// or one tile for both.
-__device__ __forceinline__ uint32_t k_place(bool keep, uint32_t u) { return keep ? u : (u ? 2 * u - 1 : 0); }
-__device__ __forceinline__ uint32_t v_place(bool keep, uint32_t u, uint32_t units) {
-    return keep ? u : (u + 1 == units ? 2 * u + 1 : 2 * u + 2);
-}
+// Places of unit u's tiles in the order of loading, in tiles: K0 K1 V0 K2 V1 .. V_last for each
+// query tile, or one tile for both. (V_last before the next query tile's K0: its product ends this tile.)
+__device__ __forceinline__ uint32_t k_place(bool keep, uint32_t u, bool first) { return keep ? u : 2 * u - (first ? 0 : 1); }
+__device__ __forceinline__ uint32_t v_place(bool keep, uint32_t u, bool last) { return keep ? u : 2 * u + (last ? 1 : 2); }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -240,7 +238,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         bool dead = false, more = w.next(sg);
         PagedLook cur{0, 0, false}, prev{0, 0, false};
         if (more) cur = paged_look(g, sg, sg.row0 + sg.kb * kPT, lane);
-        int prev_h = 0, k = more ? sg.kb : 0;
+        int k = more ? sg.kb : 0;
         // one tile (K, or V of the unit before) into the next MT slots
         auto load = [&](const CUtensorMap* map, const PagedLook& t, int kvh, int unit) {
             const PagedBoxes bx = paged_boxes(g, t);
@@ -282,6 +280,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             }
             // the pages of the next unit are looked up while this one's copies wait
             const int kvh = sg.kvh;
+            const bool first = k == sg.kb, last = k + 1 == sg.ke;
             PagedLook next{0, 0, false};
             if (++k >= sg.ke) {
                 more = w.next(sg);
@@ -289,12 +288,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             }
             if (more) next = paged_look(g, sg, sg.row0 + k * kPT, lane);
             load(&kmap, cur, kvh, u);
-            if (!keep && !dead && u > 0) load(&vmap, prev, prev_h, -1);
+            if (!keep && !dead && !first) load(&vmap, prev, kvh, -1);
+            if (!keep && !dead && last) load(&vmap, cur, kvh, -1);
             prev = cur;
-            prev_h = kvh;
             cur = next;
         }
-        if (!keep && !dead && units > 0) load(&vmap, prev, prev_h, -1);
         if (dead && lane == 0) {                     // a wait ran out: let the copies in flight land
             atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
             ctl.abort = 1;
@@ -306,7 +304,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         // ---------------------------------------------------------------- tensor core
         PagedWalk w(g, sched);
         PagedSeg sg;
-        uint32_t u = 0, seg = 0, pend_u = 0;
+        uint32_t u = 0, seg = 0, pend_u = 0, pend_place = 0;
         uint32_t edges = 0;
         bool dead = false, pend = false, pend_first = false, pend_edge = false;
         const bool one = elect_one();
@@ -316,9 +314,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         const uint32_t idS = idesc_bf16_f32(kPT, N), idO = idesc_bf16_f32(128, N) | (1u << 15) | (1u << 16);
         const uint64_t pdesc0 = sdesc_mnmajor_sw128(smem_u32(sP), kPT * 128, 1024u);
         // (descriptors advance by 16-byte units)
-        auto pv = [&](uint32_t x, bool first, bool edge) {           // O^T += V^T P^T of unit x
+        auto pv = [&](uint32_t x, uint32_t place, bool first, bool edge) {   // O^T += V^T P^T of unit x
             if (!wait(&ctl.p_full[x & 1], x >> 1)) return false;
-            uint32_t r = v_place(keep, x, units) * MT;
+            uint32_t r = place * MT;
             if (!keep && edge) {                     // its rows come, and those that nobody sees are cleared
                 for (int mt = 0; mt < MT; ++mt)
                     if (!wait(&ctl.full[(r + mt) % ST], (r + mt) / ST)) return false;
@@ -350,7 +348,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             dead = !wait(&ctl.q_full, seg);
             ++seg;
             for (int k = sg.kb; k < sg.ke && !dead; ++k, ++u) {
-                uint32_t r = k_place(keep, u) * MT;
+                uint32_t r = k_place(keep, u, k == sg.kb) * MT;
                 if (pend && keep) {
                     // Whichever can start: this unit's scores (first, if both), or the product with V
                     // of the unit before, whose slots this unit's rows may be waiting for. (Rows that
@@ -360,7 +358,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     for (uint32_t it = 1;; ++it) {
                         if (__all_sync(~0u, mbar_test(&ctl.full[last % ST], (last / ST) & 1))) break;
                         if (__all_sync(~0u, mbar_test(&ctl.p_full[pend_u & 1], (pend_u >> 1) & 1))) {
-                            dead = !pv(pend_u, pend_first, pend_edge);
+                            dead = !pv(pend_u, pend_place, pend_first, pend_edge);
                             pend = false;
                             break;
                         }
@@ -392,14 +390,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     if (k + 1 == sg.ke) umma_commit(&ctl.q_empty);
                 }
                 __syncwarp();
-                if (pend) dead = !pv(pend_u, pend_first, pend_edge);
+                if (pend) dead = !pv(pend_u, pend_place, pend_first, pend_edge);
                 pend = true;
                 pend_u = u;
+                pend_place = v_place(keep, u, k + 1 == sg.ke);
                 pend_first = k == sg.kb;
                 pend_edge = unit_edge(g, sg, sg.row0 + k * kPT, ctl.bad[u & 7]);
             }
+            // the tile's last product first: its outputs are waited for, the next tile's scores are not
+            if (!dead && pend) dead = !pv(pend_u, pend_place, pend_first, pend_edge);
+            pend = false;
         }
-        if (!dead && pend) dead = !pv(pend_u, pend_first, pend_edge);
         if (dead && lane == 0) {
             atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
             ctl.abort = 1;
@@ -574,7 +575,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     if (live(zr)) return;
 #pragma unroll 1
                     for (int b = st / kPT; b < 2 * MT; b += kSoftThreads / kPT) {
-                        const uint32_t slot = (v_place(keep, u, units) * MT + (b >> 1)) % ST;
+                        const uint32_t slot = (v_place(keep, u, k + 1 == ke) * MT + (b >> 1)) % ST;
                         uint4* z = reinterpret_cast<uint4*>(sm + slot * C::SLOT + (b & 1) * C::BOX + zr * 128);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) z[i ^ (zr & 7)] = make_uint4(0, 0, 0, 0);    // (eight rows, eight banks)
