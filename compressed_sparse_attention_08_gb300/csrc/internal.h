@@ -93,7 +93,7 @@ size_t paged_evict_ws_bytes(const dsv4_paged_evict_args& a);
 int launch_paged_evict(const dsv4_paged_evict_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
 struct PagedGeom;
 PagedGeom paged_geom(const int32_t* table, const int32_t* cu_q, const int32_t* kv_len, int batch, int total_q, int max_pages,
-                     int page_size, int num_pages, int heads, int kv_heads, int window, int unit);
+                     int page_size, int num_pages, int heads, int kv_heads, int window);
 // Queries [total_q, heads, D] with a token stride (elements), boxes of 64 channels x hb heads x tpt tokens.
 bool paged_query_map(CUtensorMap* map, const void* q, int D, int heads, int total_q, long long stride, int hb, int tpt);
 // A pool [num_pages, page_size, kv_heads, D], boxes of 64 channels x br slots of one head.

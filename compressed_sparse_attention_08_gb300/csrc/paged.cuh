@@ -33,6 +33,8 @@ __device__ __forceinline__ float key_to_float(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
+constexpr int kUnit = 128;               // cache rows per unit
+
 struct PagedGeom {
     const int32_t* table;                // [batch, max_pages]
     const int32_t* cu_q;                 // [batch + 1]
@@ -41,8 +43,7 @@ struct PagedGeom {
     int H, KV, G;                        // query heads, KV heads, query heads per KV head
     int hb, nhb, tpt;                    // heads per row tile, head blocks per KV head, tokens per row tile
     int window;                          // 0: none
-    int unit;                            // cache rows per unit
-    int br;                              // cache rows per TMA box: a power of two that divides page_size, <= unit
+    int br, br_log2;                     // cache rows per TMA box: a power of two that divides page_size, <= kUnit
 };
 
 // Row tiles of at most N rows for groups of G heads: whole groups, or the split of a group into
@@ -62,9 +63,9 @@ inline void paged_tile(PagedGeom& g, int N) {
     }
 }
 
-inline int paged_box_rows(int page_size, int unit) {
+inline int paged_box_rows(int page_size) {
     const int low = page_size & -page_size;
-    return low < unit ? low : unit;
+    return low < kUnit ? low : kUnit;
 }
 
 struct PagedSeq { int q0, n, L; };       // first token, tokens, cache rows
@@ -91,7 +92,7 @@ __device__ __forceinline__ int paged_lo(const PagedGeom& g, const PagedSeq& q, i
 // tokens that see nothing are still answered).
 __device__ __forceinline__ int paged_tile_units(const PagedGeom& g, const PagedSeq& q, int tt) {
     const int t0 = tt * g.tpt, t1 = min(t0 + g.tpt, q.n) - 1;
-    return max((paged_hi(q, t1) + g.unit - 1) / g.unit - paged_lo(g, q, t0) / g.unit, 1);
+    return max((paged_hi(q, t1) + kUnit - 1) / kUnit - paged_lo(g, q, t0) / kUnit, 1);
 }
 
 struct PagedSched {
@@ -257,8 +258,8 @@ struct PagedWalk {
         o.hi_u = paged_hi(q, t0 + o.tn - 1);
         o.lo_max = paged_lo(g, q, t0 + o.tn - 1);
         o.hi_min = paged_hi(q, t0);
-        o.row0 = o.lo_u / g.unit * g.unit;
-        o.n = max((o.hi_u + g.unit - 1) / g.unit - o.lo_u / g.unit, 1);
+        o.row0 = o.lo_u / kUnit * kUnit;
+        o.n = max((o.hi_u + kUnit - 1) / kUnit - o.lo_u / kUnit, 1);
         o.kb = k;
         const long long take = left < o.n - k ? left : o.n - k;
         o.ke = k + static_cast<int>(take);
@@ -275,7 +276,7 @@ struct PagedLook { int page, slot; bool need; };
 __device__ __forceinline__ PagedLook paged_look(const PagedGeom& g, const PagedSeg& sg, int row, int lane) {
     PagedLook t{0, 0, false};
     const int i = lane >> 1, r = row + i * g.br;
-    t.need = i < g.unit / g.br && r < sg.hi_u && r + g.br > sg.lo_u;   // holds rows that some token sees
+    t.need = i < (kUnit >> g.br_log2) && r < sg.hi_u && r + g.br > sg.lo_u;   // holds rows that some token sees
     if (t.need) {
         const int pg = r / g.page_size;
         t.slot = r - pg * g.page_size;
@@ -290,7 +291,7 @@ __device__ __forceinline__ PagedBoxes paged_boxes(const PagedGeom& g, const Page
     const bool in = t.page >= 0 && t.page < g.num_pages;
     return PagedBoxes{__ballot_sync(~0u, t.need && in), __ballot_sync(~0u, t.need && !in) & 0x55555555u};
 }
-__device__ __forceinline__ bool paged_bad_row(const PagedGeom& g, unsigned bad, int row) { return (bad >> (2 * (row / g.br))) & 1; }
+__device__ __forceinline__ bool paged_bad_row(const PagedGeom& g, unsigned bad, int row) { return (bad >> (2 * (row >> g.br_log2))) & 1; }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
                                             int w) {

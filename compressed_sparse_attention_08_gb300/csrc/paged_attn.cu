@@ -65,7 +65,7 @@ struct PagedAttnParams {
 
 constexpr int kMaxSlots = 8;
 constexpr int kSegs = 8;                 // tiles described at a time (the loads run at most three ahead of the outputs)
-constexpr int kPT = 128;                 // cache rows per unit
+constexpr int kPT = kUnit;               // cache rows per unit
 template <int N>
 struct PagedCtl {
     uint64_t q_full, q_empty, full[kMaxSlots], empty[kMaxSlots], s_full[2], s_empty[2], p_full[2], pv_done[2];
@@ -104,7 +104,7 @@ struct PCfg {
 
 // Whether the unit that starts at row j0 holds rows that no token of the tile sees.
 __device__ __forceinline__ bool unit_edge(const PagedGeom& g, const PagedSeg& sg, int j0, unsigned bad) {
-    return j0 < sg.lo_u || j0 + g.unit > sg.hi_u || bad != 0;
+    return j0 < sg.lo_u || j0 + kUnit > sg.hi_u || bad != 0;
 }
 
 // Places of unit u's tiles in the order of loading, in tiles: K0 K1 V0 K2 V1 .. V_last for each
@@ -437,8 +437,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             uint64_t lacc[NE / 2];                                   // this row's P per query (pairs), summed over the units
 #pragma unroll
             for (int i = 0; i < NE / 2; ++i) lacc[i] = 0ull;
-            const int kb = sg.kb, ke = sg.ke;
-            for (int k = kb; k < ke; ++k, ++u) {
+            for (int k = sg.kb; k < sg.ke; ++k, ++u) {
                 if (!dead) dead = !mbar_wait(&ctl.s_full[u & 1], (u >> 1) & 1, abort_flag, p.wait_ns);
                 tc_fence_after();
                 const int j0 = sg.row0 + k * kPT;
@@ -511,7 +510,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 // With few scores per thread the vote comes after P, so that the warps need not wait for
                 // one another between their steps, and P is formed again where it was too soon; with many,
                 // what is held across the vote would not fit.
-                bool rescale = false, over = k == kb;
+                bool rescale = false, over = k == sg.kb;
                 if (!over) {
                     scores();
                     less_ref();
@@ -534,7 +533,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         if (cm > mo) {
                             f = mo == -INFINITY ? 0.f : ex2(mo - cm);
                             s_nm[st] = -cm;
-                            rescale = k > kb;
+                            rescale = k > sg.kb;
                         }
                         s_f[st] = f;
                         ctl.top[st] = 0;
@@ -575,7 +574,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     if (live(zr)) return;
 #pragma unroll 1
                     for (int b = st / kPT; b < 2 * MT; b += kSoftThreads / kPT) {
-                        const uint32_t slot = (v_place(keep, u, k + 1 == ke) * MT + (b >> 1)) % ST;
+                        const uint32_t slot = (v_place(keep, u, k + 1 == sg.ke) * MT + (b >> 1)) % ST;
                         uint4* z = reinterpret_cast<uint4*>(sm + slot * C::SLOT + (b & 1) * C::BOX + zr * 128);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) z[i ^ (zr & 7)] = make_uint4(0, 0, 0, 0);    // (eight rows, eight banks)
@@ -843,7 +842,7 @@ int run(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_
     using C = PCfg<D, N>;
     PagedAttnParams p{};
     p.g = paged_geom(a.block_table, a.cu_q, a.kv_len, a.batch, a.total_q, a.max_pages, a.page_size, a.num_pages, a.heads,
-                     a.kv_heads, a.window, kPT);
+                     a.kv_heads, a.window);
     paged_tile(p.g, N);
     CUtensorMap qmap, kmap, vmap;
     if (!paged_query_map(&qmap, a.q, D, a.heads, a.total_q, a.q_stride, p.g.hb, p.g.tpt) ||
@@ -885,7 +884,7 @@ int run(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_
 }  // namespace
 
 PagedGeom paged_geom(const int32_t* table, const int32_t* cu_q, const int32_t* kv_len, int batch, int total_q, int max_pages,
-                     int page_size, int num_pages, int heads, int kv_heads, int window, int unit) {
+                     int page_size, int num_pages, int heads, int kv_heads, int window) {
     PagedGeom g{};
     g.table = table;
     g.cu_q = cu_q;
@@ -899,8 +898,8 @@ PagedGeom paged_geom(const int32_t* table, const int32_t* cu_q, const int32_t* k
     g.KV = kv_heads;
     g.G = heads / kv_heads;
     g.window = static_cast<long long>(max_pages) * page_size <= window ? 0 : window;   // (no effect: none)
-    g.unit = unit;
-    g.br = paged_box_rows(page_size, unit);
+    g.br = paged_box_rows(page_size);
+    while ((1 << g.br_log2) < g.br) ++g.br_log2;
     return g;
 }
 

@@ -25,7 +25,7 @@ namespace {
 constexpr int kThreads = 640, kLoadWarps = 3, kGroups = 4;
 constexpr int kSoftWarps = 16, kSoftThreads = 512, kSoftBar = 1;
 constexpr int kN = 128;                  // query columns
-constexpr int kPT = 128;                 // cache rows per tile
+constexpr int kPT = kUnit;               // cache rows per tile
 constexpr int kSB = 4;                   // accumulators (TMEM)
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -615,7 +615,7 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
     using C = WCfg<D>;
     PagedWeightsParams p{};
     p.g = paged_geom(a.block_table, a.cu_q, a.kv_len, a.batch, a.total_q, a.max_pages, a.page_size, a.num_pages, a.heads,
-                     a.kv_heads, a.window, kPT);
+                     a.kv_heads, a.window);
     paged_tile(p.g, kN);
     CUtensorMap qmap, kmap;
     if (!paged_pool_map(&kmap, a.k_pages, D, a.kv_heads, a.page_size, a.num_pages, p.g.br)) return DSV4_ERR_LAUNCH;
