@@ -99,6 +99,7 @@ struct PagedSched {
     long long total, u0, u1;             // all units, this CTA's [u0, u1)
     int ge;                              // CTAs with work
     int s, tt, inner, k;                 // where u0 lies
+    PagedSeq q;                          // sequence s
 };
 
 // The share of worker `self` of `count`. Whole block of NT threads; `pref` is scratch for `batch` counts in shared memory. At least
@@ -161,6 +162,9 @@ __device__ void paged_schedule(const PagedGeom& g, int self, int count, int min_
         const int c = self + warp;
         long long u = c < ge ? T * c / ge : T;
         int s = 0, tt = 0, inner = 0, k = 0;
+        PagedSeq q{0, 0, 0};
+        bool dummy = false;
+        if (u == 0 && T > 0) q = paged_seq(g, 0, dummy);
         if (u < T && u > 0) {
             int hi = g.batch - 1;                    // the first sequence whose units end past u
             while (s < hi) {
@@ -168,8 +172,7 @@ __device__ void paged_schedule(const PagedGeom& g, int self, int count, int min_
                 if (pref[mid] > u) hi = mid; else s = mid + 1;
             }
             const long long rem = u - (s ? pref[s - 1] : 0);
-            bool dummy = false;
-            const PagedSeq q = paged_seq(g, s, dummy);
+            q = paged_seq(g, s, dummy);
             const int nt = (q.n + g.tpt - 1) / g.tpt;
             long long cum = 0;
             for (int tt0 = 0; tt0 < nt; tt0 += 32) {
@@ -207,6 +210,7 @@ __device__ void paged_schedule(const PagedGeom& g, int self, int count, int min_
                 out->tt = tt;
                 out->inner = inner;
                 out->k = k;
+                out->q = q;
             } else {
                 out->u1 = u;
             }
@@ -232,10 +236,7 @@ struct PagedWalk {
     long long left;
     PagedSeq q;
     __device__ PagedWalk(const PagedGeom& geom, const PagedSched& sc)
-        : g(geom), s(sc.s), tt(sc.tt), inner(sc.inner), k(sc.k), left(sc.u1 - sc.u0), q{0, 0, 0} {
-        bool dummy = false;
-        if (left > 0) q = paged_seq(g, s, dummy);
-    }
+        : g(geom), s(sc.s), tt(sc.tt), inner(sc.inner), k(sc.k), left(sc.u1 - sc.u0), q(sc.q) {}
     __device__ bool next(PagedSeg& o) {
         if (left <= 0) return false;
         while (tt * g.tpt >= q.n) {      // the next sequence with tokens

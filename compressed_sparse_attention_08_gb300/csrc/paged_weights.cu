@@ -86,6 +86,7 @@ __device__ __forceinline__ int weight_units(const PagedGeom& g, const PagedSeq& 
 struct WSched {
     long long total, u0, u1;             // all units, this CTA's [u0, u1)
     int s, tile, k;                      // where u0 lies
+    PagedSeq q;                          // sequence s
 };
 
 // Whole block; `pref` is scratch for `batch` counts.
@@ -145,6 +146,7 @@ __device__ void weight_schedule(const PagedWeightsParams& p, long long* pref, WS
         const long long T = carry, c = blockIdx.x, ge = min(T, static_cast<long long>(gridDim.x));
         const long long u0 = c < ge ? T * c / ge : T, u1 = c < ge ? T * (c + 1) / ge : T;
         int s = 0, tile = 0, k = 0;
+        PagedSeq q{0, 0, 0};
         if (u1 > u0) {
             int hi = g.batch - 1;                    // the first sequence whose units end past u0
             while (s < hi) {
@@ -153,7 +155,7 @@ __device__ void weight_schedule(const PagedWeightsParams& p, long long* pref, WS
             }
             long long rem = u0 - (s ? pref[s - 1] : 0);
             bool dummy = false;
-            const PagedSeq q = paged_seq(g, s, dummy);
+            q = paged_seq(g, s, dummy);
             const int nt = weight_tiles(p, q);
             const int f = q.n > 0 && q.n <= g.tpt ? min(paged_lo(g, q, 0) / kPT, nt) : 0;
             if (q.n > 0 && q.n <= g.tpt) {
@@ -180,7 +182,7 @@ __device__ void weight_schedule(const PagedWeightsParams& p, long long* pref, WS
                 cum += __shfl_sync(~0u, v, 31);
             }
         }
-        if (lane == 0) *out = WSched{T, u0, u1, s, tile, k};
+        if (lane == 0) *out = WSched{T, u0, u1, s, tile, k, q};
     }
     __syncthreads();
 }
@@ -200,10 +202,7 @@ struct WWalk {
     long long left;
     PagedSeq q;
     __device__ WWalk(const PagedWeightsParams& par, const WSched& sc)
-        : p(par), s(sc.s), tile(sc.tile), k(sc.k), left(sc.u1 - sc.u0), q{0, 0, 0} {
-        bool dummy = false;
-        if (left > 0) q = paged_seq(p.g, s, dummy);
-    }
+        : p(par), s(sc.s), tile(sc.tile), k(sc.k), left(sc.u1 - sc.u0), q(sc.q) {}
     __device__ bool next(WItem& o) {
         if (left <= 0) return false;
         const PagedGeom& g = p.g;
