@@ -23,11 +23,16 @@
 // 512 channels: a tile is 128 KB and the ring holds no second one beside it. Kept for both products,
 // it made loads, products and softmax take turns (7000 cycles per unit, of which the tensor core
 // worked 3300). So the rows come in twice, as K and as V, in the order of use K0 K1 V0 K2 V1 ..:
-// L2 has them the second time, and nothing waits for a whole tile (5700 cycles per unit; shared
-// memory then moves 640 KB per unit, 5100 cycles at the 128 bytes a cycle that it has). Slower were
+// L2 has them the second time, and nothing waits for a whole tile (5100 cycles per unit: shared
+// memory moves 640 KB per unit at the 128 bytes a cycle that it has). Slower were
 // units of 64 rows, of which two fit the ring (S^T with M = 64 costs as much as with M = 128),
 // and two CTAs with 256 channels each that exchange scores and P through distributed shared memory
 // (which moved about 12 bytes a cycle).
+//
+// Measured (64 heads x 512, K = V): 2,048 tokens behind 14K rows 3.96 ms, 1,040 TFLOP/s, bound by
+// shared memory; 16 single tokens over up to 8K rows 46 us (15 us of it HBM, the rest the start of cold
+// CTAs and the merge); 4 over up to 256K rows 176 us, 5.05 TB/s. 32 heads over 8 of 128, tokens and
+// chunks mixed: 228 us, 565 TFLOP/s, bound by a unit's chain of softmax steps.
 #include <cmath>
 
 #include "internal.h"

@@ -12,6 +12,8 @@
 // a row that was overwritten; a CTA therefore takes a slice of every row's channels (their
 // copies are independent) and walks all rows. Into other pages there is no such order, and
 // the rows are spread over CTAs too.
+// Measured: 4 sequences of up to 64K rows x 512 cut to 32K in 70 us (the move 50 us, 5.4 TB/s);
+// 3 of up to 1.5K rows 12 us, three dependent launches.
 #include "internal.h"
 #include "paged.cuh"
 
