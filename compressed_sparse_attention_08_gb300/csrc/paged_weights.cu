@@ -51,13 +51,14 @@ struct WCfg {
     static constexpr int D = D_, NB = D / 64;
     static constexpr int BOX = kPT * 128;                    // 128 rows (or queries) x 64 channels
     static constexpr int RES = NB * BOX;                     // the operand that stays
+    static constexpr int RB = D == 128 ? 2 : 1;              // and how many: with several KV heads it changes every unit
     static constexpr int RS = D == 512 ? 5 : 8;              // ring boxes
     // The tensor core's running fp32 sum is cut, not rounded, at every step, which pulls scores
     // towards 0: by 1.1e-6 on average at scores of 3 with 512 channels in one sum (measured), which
     // the weights show in full. Two sums of 256 channels, added in fp32, leave half of it.
     static constexpr int SUMS = D == 512 ? 2 : 1;
     static constexpr int SB = kSB / SUMS;                    // score buffers
-    static constexpr int OFF_R = RES, OFF_S = RES + RS * BOX;
+    static constexpr int OFF_R = RB * RES, OFF_S = OFF_R + RS * BOX;
     static constexpr int SMALL = 2 * kN * 8 + kGroups * kPT * 4;
     static constexpr int SMEM = OFF_S + SMALL + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -274,12 +275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ PagedWeightsParams p) {
     using C = WCfg<D>;
-    constexpr int NB = C::NB, RS = C::RS, SB = C::SB, SUMS = C::SUMS;
+    constexpr int NB = C::NB, RS = C::RS, RB = C::RB, SB = C::SB, SUMS = C::SUMS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_slot, s_err;
     __shared__ volatile int abort_flag;
     __shared__ WSched sched;
-    __shared__ uint64_t res_full, res_empty, full[RS], empty[RS], s_full[SB], s_empty[SB];
+    __shared__ uint64_t res_full[RB], res_empty[RB], full[RS], empty[RS], s_full[SB], s_empty[SB];
     __shared__ unsigned s_bad[16];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* sR = sm + C::OFF_R;
@@ -291,8 +292,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     if (tid == 0) {
         tma_prefetch_desc(&qmap);
         tma_prefetch_desc(&kmap);
-        mbar_init(&res_full, kLoadWarps);
-        mbar_init(&res_empty, 1);
+        for (int i = 0; i < RB; ++i) { mbar_init(&res_full[i], kLoadWarps); mbar_init(&res_empty[i], 1); }
         for (int i = 0; i < RS; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
         for (int i = 0; i < SB; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], kSoftWarps); }
         abort_flag = 0;
@@ -345,18 +345,19 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             for (int i = it.kb; i < it.ke && !dead; ++i, ++unit, c.step(g, it)) {
                 const int kvh = c.kvh, tt = c.tt, blk = c.blk;
                 if (stays.moved(keep_q, g, it, c)) {
-                    if (res > 0) dead = __any_sync(~0u, !mbar_wait(&res_empty, (res - 1) & 1, &abort_flag, p.wait_ns));
+                    const uint32_t rb = res % RB;
+                    if (res >= RB) dead = __any_sync(~0u, !mbar_wait(&res_empty[rb], (res / RB - 1) & 1, &abort_flag, p.wait_ns));
                     if (dead) break;
                     if (lane == 0) {
                         const uint32_t bytes = NB * (keep_q ? qbox : kbox);
-                        if (mine == 0 && bytes) mbar_arrive_expect_tx(&res_full, bytes);
-                        else mbar_arrive(&res_full);
+                        if (mine == 0 && bytes) mbar_arrive_expect_tx(&res_full[rb], bytes);
+                        else mbar_arrive(&res_full[rb]);
                     }
                     __syncwarp();
 #pragma unroll 1
                     for (int b = mine; b < NB; b += kLoadWarps) {
-                        if (keep_q) load_q(sm + b * C::BOX, &res_full, kvh, b, tt, blk);
-                        else load_k(sm + b * C::BOX, &res_full, kvh, b);
+                        if (keep_q) load_q(sm + rb * C::RES + b * C::BOX, &res_full[rb], kvh, b, tt, blk);
+                        else load_k(sm + rb * C::RES + b * C::BOX, &res_full[rb], kvh, b);
                     }
                     ++res;
                 }
@@ -385,7 +386,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         if (dead && lane == 0) {                     // a wait ran out: let the copies in flight land
             atomicOr(&s_err, DSV4_EWORD_TIMEOUT);
             abort_flag = 1;
-            if (res) mbar_wait(&res_full, (res - 1) & 1, nullptr, 100000000ull);
+            for (uint32_t r = res > RB ? res - RB : 0; r < res; ++r) mbar_wait(&res_full[r % RB], (r / RB) & 1, nullptr, 100000000ull);
             for (uint32_t r = ring > RS ? ring - RS : 0; r < ring; ++r)
                 if (r % kLoadWarps == static_cast<uint32_t>(mine)) mbar_wait(&full[r % RS], (r / RS) & 1, nullptr, 100000000ull);
         }
@@ -405,9 +406,9 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             WUnit c(g, it);
             for (int i = it.kb; i < it.ke && !dead; ++i, ++u, c.step(g, it)) {
                 if (stays.moved(keep_q, g, it, c)) {
-                    if (res > 0 && one) umma_commit(&res_empty);
+                    if (res > 0 && one) umma_commit(&res_empty[(res - 1) % RB]);
                     __syncwarp();
-                    dead = !wait(&res_full, res);
+                    dead = !wait(&res_full[res % RB], res / RB);
                     ++res;
                     if (dead) break;
                 }
@@ -419,7 +420,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     dead = dead || !wait(&full[slot], ring / RS);
                     if (dead) break;
                     tc_fence_after();
-                    const uint64_t stay = sdesc_kmajor_sw128(r0 + b * C::BOX), strm = sdesc_kmajor_sw128(g0 + slot * C::BOX);
+                    const uint64_t stay = sdesc_kmajor_sw128(r0 + (res - 1) % RB * C::RES + b * C::BOX), strm = sdesc_kmajor_sw128(g0 + slot * C::BOX);
                     const uint64_t a0 = keep_q ? strm : stay, b0 = keep_q ? stay : strm;
                     const uint32_t d = tmem + (sb * SUMS + b / (NB / SUMS)) * kN;
                     if (one) {
