@@ -51,8 +51,8 @@ struct WCfg {
     static constexpr int D = D_, NB = D / 64;
     static constexpr int BOX = kPT * 128;                    // 128 rows (or queries) x 64 channels
     static constexpr int RES = NB * BOX;                     // the operand that stays
-    static constexpr int RB = D == 128 ? 2 : 1;              // and how many: with several KV heads it changes every unit
-    static constexpr int RS = D == 512 ? 5 : 8;              // ring boxes
+    static constexpr int RB = D <= 256 ? 2 : 1;              // and how many (several KV heads: it changes every unit)
+    static constexpr int RS = D == 128 ? 8 : 5;              // ring boxes
     // The tensor core's running fp32 sum is cut, not rounded, at every step, which pulls scores
     // towards 0: by 1.1e-6 on average at scores of 3 with 512 channels in one sum (measured), which
     // the weights show in full. Two sums of 256 channels, added in fp32, leave half of it.
