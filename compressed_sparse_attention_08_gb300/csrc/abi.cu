@@ -132,9 +132,11 @@ bool num_ok(const void* p, size_t size) { return p != nullptr && reinterpret_cas
 bool opt_num_ok(const void* p, size_t size) { return p == nullptr || num_ok(p, size); }
 
 // What the paged calls share (include/dsv4.h, "Common rules").
+constexpr int kPagedMaxBatch = 2048;
+bool paged_dim_ok(int dim) { return dim == 128 || dim == 256 || dim == 512; }
 bool paged_ok(int batch, int kv_heads, int dim, int page_size, int num_pages, int max_pages) {
-    if (batch < 0 || batch > 2048 || kv_heads < 1 || kv_heads > 1024) return false;
-    if (dim != 128 && dim != 256 && dim != 512) return false;
+    if (batch < 0 || batch > kPagedMaxBatch || kv_heads < 1 || kv_heads > 1024) return false;
+    if (!paged_dim_ok(dim)) return false;
     if (page_size < 8 || page_size > 65536 || page_size % 8 != 0 || num_pages < 1 || max_pages < 1) return false;
     const long long rows = static_cast<long long>(max_pages) * page_size;
     return rows <= (1ll << 29) && rows * (batch > 0 ? batch : 1) < (1ll << 37);
@@ -170,6 +172,19 @@ bool norm_rope_ok(const dsv4_norm_rope_args* a) {
         return false;
     }
     return true;
+}
+
+// What the workspaces of the paged calls are sized by: 0 bytes for values that the call refuses (the
+// size is asked for first, so the sums here may not meet them).
+bool paged_attn_sizes_ok(const dsv4_paged_attn_args* a) {
+    return a->batch >= 0 && a->batch <= kPagedMaxBatch && heads_ok(a->heads, a->kv_heads) && paged_dim_ok(a->dim) && a->max_q >= 1;
+}
+bool paged_weights_sizes_ok(const dsv4_paged_weights_args* a) {
+    return a->batch >= 0 && a->batch <= kPagedMaxBatch && heads_ok(a->heads, a->kv_heads) && paged_dim_ok(a->dim);
+}
+bool paged_evict_sizes_ok(const dsv4_paged_evict_args* a) {
+    return a->batch >= 0 && a->batch <= kPagedMaxBatch && a->budget >= 1 && a->acc_rows >= a->budget && a->recent >= 0 &&
+           a->recent <= a->budget;
 }
 
 bool paged_attn_ok(const dsv4_paged_attn_args* a) {
@@ -501,7 +516,7 @@ int dsv4_norm_rope_append(const dsv4_norm_rope_args* a, dsv4_stream_t stream) {
 }
 
 size_t dsv4_paged_attn_workspace_size(const dsv4_paged_attn_args* a) {
-    if (!a) return 0;
+    if (!a || !paged_attn_sizes_ok(a)) return 0;
     return kWsHeader + paged_attn_ws_bytes(*a);
 }
 
@@ -513,7 +528,7 @@ int dsv4_paged_attn(const dsv4_paged_attn_args* a, void* ws, size_t ws_bytes, ds
 }
 
 size_t dsv4_paged_attn_weights_workspace_size(const dsv4_paged_weights_args* a) {
-    if (!a) return 0;
+    if (!a || !paged_weights_sizes_ok(a)) return 0;
     return kWsHeader + paged_weights_ws_bytes(*a);
 }
 
@@ -526,7 +541,7 @@ int dsv4_paged_attn_weights(const dsv4_paged_weights_args* a, void* ws, size_t w
 }
 
 size_t dsv4_paged_evict_workspace_size(const dsv4_paged_evict_args* a) {
-    if (!a) return 0;
+    if (!a || !paged_evict_sizes_ok(a)) return 0;
     return kWsHeader + paged_evict_ws_bytes(*a);
 }
 

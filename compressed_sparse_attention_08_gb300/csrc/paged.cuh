@@ -19,8 +19,6 @@
 
 namespace dsv4 {
 
-constexpr int kPagedMaxBatch = 2048;
-
 // 2^x by the hardware's approximation (relative error about 2^-22, results below 2^-126 are 0).
 __device__ __forceinline__ float ex2(float x) {
     float y;

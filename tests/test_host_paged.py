@@ -3,6 +3,8 @@ CUDA call, and workspaces are sized without one."""
 from __future__ import annotations
 
 import ctypes
+import subprocess
+import sys
 
 import pytest
 
@@ -109,6 +111,28 @@ def test_workspaces(lib, make, name):
     assert call(None, _p(20), need, None) == 1
     if make is not _evict:                          # lengths do not enter
         assert size(ctypes.byref(make(max_pages=1024, total_q=4000))) == need
+
+
+# what enters a workspace's size, at values that the calls refuse
+SIZED = [(_attn, "dsv4_paged_attn", x) for x in (
+    dict(kv_heads=0), dict(kv_heads=-1), dict(heads=0), dict(heads=1025), dict(heads=6, kv_heads=4), dict(dim=64), dict(dim=0),
+    dict(dim=-512), dict(max_q=0), dict(max_q=-5), dict(batch=-1), dict(batch=2049))]
+SIZED += [(_weights, "dsv4_paged_attn_weights", x) for x in (dict(kv_heads=0), dict(heads=0), dict(dim=64), dict(batch=-1))]
+SIZED += [(_evict, "dsv4_paged_evict", x) for x in (
+    dict(batch=-1), dict(batch=2049), dict(budget=0), dict(budget=-1, recent=-2), dict(recent=-1), dict(recent=501),
+    dict(acc_rows=0), dict(acc_rows=-1), dict(budget=1025), dict(budget=-(1 << 31), recent=1))]
+
+
+@pytest.mark.parametrize("make, name, bad", SIZED)
+def test_workspace_sizes_of_refused_counts(name, make, bad):
+    """A size is asked for before the call checks its arguments: it is 0 for counts that the call refuses. In a process of
+    its own, since a division by a count of 0 would end it."""
+    code = (f"import sys, ctypes; sys.path[:0] = {sys.path!r}; import test_host_paged as t\n"
+            f"from compressed_sparse_attention_08_gb300 import _abi\n"
+            f"print(_abi.library().{name}_workspace_size(ctypes.byref(t.{make.__name__}(**{bad!r}))))")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, f"ended with {r.returncode}: {r.stderr[-300:]}"
+    assert r.stdout.split()[-1] == "0"
 
 
 def test_binding_refuses_shapes_and_types():
