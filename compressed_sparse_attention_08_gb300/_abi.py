@@ -517,13 +517,13 @@ def _shape(t, shape, name):
 
 
 def _held(args, *tensors):
-    """Keeps the tensors with the struct; all must be on one device."""
+    """Keeps the tensors with the struct; all must be on one device. (Nothing here may refer back to the struct, a stored
+    byref included: the tensors would then live until the cyclic collector runs.)"""
     kept = [t for t in tensors if t is not None]
     if any(t.device != kept[0].device for t in kept):
         raise ValueError("all tensors must be on one device")
     args.tensors = kept
     args.device = kept[0].device.index
-    args.ref = ctypes.byref(args)
     return args
 
 
@@ -538,11 +538,11 @@ def _call(fn, args, stream, what, ws=None):
     # (the raw handle: torch.cuda.current_stream() takes 3 us to wrap it)
     st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
     if ws is None:
-        status = fn(args.ref, st)
+        status = fn(args, st)
     else:
         if ws.device.index != dev or not ws.is_contiguous():
             raise ValueError("ws must be contiguous, on the tensors' device")
-        status = fn(args.ref, ws.data_ptr(), ws.numel() * ws.element_size(), st)
+        status = fn(args, ws.data_ptr(), ws.numel() * ws.element_size(), st)
     if status:
         _check(status, what)
 

@@ -3,8 +3,10 @@ CUDA call, and workspaces are sized without one."""
 from __future__ import annotations
 
 import ctypes
+import gc
 import subprocess
 import sys
+import weakref
 
 import pytest
 
@@ -147,3 +149,28 @@ def test_binding_refuses_shapes_and_types():
         m.norm_rope_args(q, q, torch.zeros(2, dtype=torch.int64))
     with pytest.raises(ValueError, match="keep"):
         m.paged_evict_args(pages, t, n, torch.zeros(1, 32), torch.zeros(1, 9, dtype=torch.int32), budget=8, recent=0)
+
+
+def test_a_dropped_struct_frees_its_tensors():
+    """The struct holds its tensors, and nothing holds the struct: they go with it, without the cyclic collector."""
+    torch = pytest.importorskip("torch")
+    from compressed_sparse_attention_08_gb300 import _abi
+    t = torch.zeros(4)
+    held = weakref.ref(t)
+    a = _abi._held(_abi.PagedAttnArgs(), t)
+    del t
+    assert held() is not None
+    gc.disable()
+    try:
+        del a
+        assert held() is None
+    finally:
+        gc.enable()
+
+
+def test_a_struct_is_passed_as_it_is(lib):
+    """The calls take the struct itself (what the binding hands over)."""
+    a = _attn()
+    assert lib.dsv4_paged_attn_workspace_size(a) == lib.dsv4_paged_attn_workspace_size(ctypes.byref(a)) > 256
+    assert lib.dsv4_paged_attn(_attn(window=-1), _p(20), 1 << 40, None) == 1
+    assert lib.dsv4_norm_rope_append(_norm(eps=-1.0), None) == 1
