@@ -516,6 +516,16 @@ def _shape(t, shape, name):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _struct(cls, *values):
+    """cls(*values), whose counts must fit their 32 bits (ctypes would keep the low ones)."""
+    if len(values) != len(cls._fields_):
+        raise ValueError(f"{cls.__name__} has {len(cls._fields_)} fields, got {len(values)}")
+    for (name, kind), v in zip(cls._fields_, values):
+        if kind is I and not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} is out of range: {v}")
+    return cls(*values)
+
+
 def _held(args, *tensors):
     """Keeps the tensors with the struct; all must be on one device. (Nothing here may refer back to the struct, a stored
     byref included: the tensors would then live until the cyclic collector runs.)"""
@@ -578,11 +588,11 @@ def norm_rope_args(q, q_out, pos, *, k=None, k_pages=None, v=None, v_pages=None,
     op, os_ = _heads_ptr(q_out, "q_out", q is None)
     kp, ks = _heads_ptr(k, "k", True)
     vp, vs = _heads_ptr(v, "v", True)
-    a = NormRopeArgs(qp, kp, vp, op, _ptr(k_pages, bf16, "k_pages", True), _ptr(v_pages, bf16, "v_pages", True),
-                     _ptr(slots, i64, "slots", True), _ptr(pos, i64, "pos"), _ptr(gamma_q, f32, "gamma_q", True),
-                     _ptr(gamma_k, f32, "gamma_k", True), qs, ks, vs, os_, T, H, KV, D,
-                     0 if k_pages is None else k_pages.shape[1], 0 if k_pages is None else k_pages.shape[0],
-                     rope_dim, eps, rope_theta)
+    a = _struct(NormRopeArgs, qp, kp, vp, op, _ptr(k_pages, bf16, "k_pages", True), _ptr(v_pages, bf16, "v_pages", True),
+                _ptr(slots, i64, "slots", True), _ptr(pos, i64, "pos"), _ptr(gamma_q, f32, "gamma_q", True),
+                _ptr(gamma_k, f32, "gamma_k", True), qs, ks, vs, os_, T, H, KV, D,
+                0 if k_pages is None else k_pages.shape[1], 0 if k_pages is None else k_pages.shape[0],
+                rope_dim, eps, rope_theta)
     return _held(a, q, q_out, pos, k, k_pages, v, v_pages, slots, gamma_q, gamma_k)
 
 
@@ -617,12 +627,12 @@ def paged_attn_args(q, out, k_pages, block_table, cu_q, kv_len, *, v_pages=None,
     _shape(sink, (H,), "sink")
     _shape(lse, (T, H), "lse")
     _shape(out_rope_pos, (T,), "out_rope_pos")
-    a = PagedAttnArgs(qp, _ptr(k_pages, bf16, "k_pages"), _ptr(v_pages, bf16, "v_pages", True),
-                      _ptr(block_table, i32, "block_table"), _ptr(cu_q, i32, "cu_q"), _ptr(kv_len, i32, "kv_len"),
-                      _ptr(sink, f32, "sink", True), _ptr(out, bf16, "out"), _ptr(lse, f32, "lse", True),
-                      _ptr(out_rope_pos, i64, "out_rope_pos", True), qs, B, T, H, KV, D, ps, n, mp,
-                      max(1, T if max_q is None else max_q), window, 1.0 / math.sqrt(D) if scale is None else scale,
-                      out_rope_dim if out_rope_pos is not None else 0, out_rope_theta)
+    a = _struct(PagedAttnArgs, qp, _ptr(k_pages, bf16, "k_pages"), _ptr(v_pages, bf16, "v_pages", True),
+                _ptr(block_table, i32, "block_table"), _ptr(cu_q, i32, "cu_q"), _ptr(kv_len, i32, "kv_len"),
+                _ptr(sink, f32, "sink", True), _ptr(out, bf16, "out"), _ptr(lse, f32, "lse", True),
+                _ptr(out_rope_pos, i64, "out_rope_pos", True), qs, B, T, H, KV, D, ps, n, mp,
+                max(1, T if max_q is None else max_q), window, 1.0 / math.sqrt(D) if scale is None else scale,
+                out_rope_dim if out_rope_pos is not None else 0, out_rope_theta)
     return _held(a, q, out, k_pages, v_pages, block_table, cu_q, kv_len, sink, lse, out_rope_pos)
 
 
@@ -644,10 +654,10 @@ def paged_weights_args(q, lse, k_pages, block_table, cu_q, kv_len, acc, *, acc_i
     _shape(lse, (T, H), "lse")
     _shape(acc, (B, acc.shape[-1]), "acc")
     _shape(acc_in, acc.shape, "acc_in")
-    a = PagedWeightsArgs(qp, _ptr(lse, f32, "lse"), _ptr(k_pages, bf16, "k_pages"), _ptr(block_table, i32, "block_table"),
-                         _ptr(cu_q, i32, "cu_q"), _ptr(kv_len, i32, "kv_len"), _ptr(acc_in, f32, "acc_in", True),
-                         _ptr(acc, f32, "acc"), qs, B, T, H, KV, D, ps, n, mp, max(1, T if max_q is None else max_q),
-                         window, acc.shape[1], 1.0 / math.sqrt(D) if scale is None else scale)
+    a = _struct(PagedWeightsArgs, qp, _ptr(lse, f32, "lse"), _ptr(k_pages, bf16, "k_pages"), _ptr(block_table, i32, "block_table"),
+                _ptr(cu_q, i32, "cu_q"), _ptr(kv_len, i32, "kv_len"), _ptr(acc_in, f32, "acc_in", True),
+                _ptr(acc, f32, "acc"), qs, B, T, H, KV, D, ps, n, mp, max(1, T if max_q is None else max_q),
+                window, acc.shape[1], 1.0 / math.sqrt(D) if scale is None else scale)
     return _held(a, q, lse, k_pages, block_table, cu_q, kv_len, acc, acc_in)
 
 
@@ -680,11 +690,11 @@ def paged_evict_args(k_pages, block_table, kv_len, acc, keep, *, budget, recent,
     _shape(acc_out, acc.shape, "acc_out")
     _shape(keep, (B, budget), "keep")
     n, ps, KV, D = k_pages.shape
-    a = PagedEvictArgs(_ptr(k_pages, bf16, "k_pages"), _ptr(v_pages, bf16, "v_pages", True),
-                       _ptr(block_table, i32, "block_table"), _ptr(out_table, i32, "out_table"),
-                       _ptr(kv_len, i32, "kv_len"), _ptr(kv_len_out, i32, "kv_len_out"), _ptr(acc, f32, "acc"),
-                       _ptr(acc_out, f32, "acc_out"), _ptr(keep, i32, "keep"), B, KV, D, ps, n, block_table.shape[1],
-                       out_table.shape[1], acc.shape[1], budget, recent)
+    a = _struct(PagedEvictArgs, _ptr(k_pages, bf16, "k_pages"), _ptr(v_pages, bf16, "v_pages", True),
+                _ptr(block_table, i32, "block_table"), _ptr(out_table, i32, "out_table"),
+                _ptr(kv_len, i32, "kv_len"), _ptr(kv_len_out, i32, "kv_len_out"), _ptr(acc, f32, "acc"),
+                _ptr(acc_out, f32, "acc_out"), _ptr(keep, i32, "keep"), B, KV, D, ps, n, block_table.shape[1],
+                out_table.shape[1], acc.shape[1], budget, recent)
     return _held(a, k_pages, v_pages, block_table, out_table, kv_len, kv_len_out, acc, acc_out, keep)
 
 

@@ -174,3 +174,47 @@ def test_a_struct_is_passed_as_it_is(lib):
     assert lib.dsv4_paged_attn_workspace_size(a) == lib.dsv4_paged_attn_workspace_size(ctypes.byref(a)) > 256
     assert lib.dsv4_paged_attn(_attn(window=-1), _p(20), 1 << 40, None) == 1
     assert lib.dsv4_norm_rope_append(_norm(eps=-1.0), None) == 1
+
+
+@pytest.mark.parametrize("struct, name, value", [
+    ("PagedAttnArgs", "window", (1 << 32) + 5), ("PagedAttnArgs", "max_q", 1 << 31), ("PagedWeightsArgs", "window", -(1 << 31) - 1),
+    ("PagedWeightsArgs", "acc_rows", (1 << 32) + 512), ("PagedEvictArgs", "recent", 1 << 32), ("NormRopeArgs", "rope_dim", (1 << 32) + 64)])
+def test_counts_do_not_wrap(struct, name, value):
+    """A number past 32 bits is refused, not cut to its low bits (a window of 2^32 + 5 rows is not one of 5)."""
+    from compressed_sparse_attention_08_gb300 import _abi
+    cls = getattr(_abi, struct)
+    fields = [f for f, _ in cls._fields_]
+    values = [0] * len(fields)
+    for v in ((1 << 31) - 1, -(1 << 31)):
+        values[fields.index(name)] = v
+        assert getattr(_abi._struct(cls, *values), name) == v
+    values[fields.index(name)] = value
+    with pytest.raises(ValueError, match=name):
+        _abi._struct(cls, *values)
+    with pytest.raises(ValueError, match="fields"):
+        _abi._struct(cls, *values[:-1])
+
+
+def test_builders_do_not_wrap_counts(monkeypatch):
+    """The same through the builders, on tensors that only stand in for device ones."""
+    torch = pytest.importorskip("torch")
+    from compressed_sparse_attention_08_gb300 import _abi
+    monkeypatch.setattr(_abi, "_ptr", lambda t, *a, **k: None if t is None else ctypes.c_void_p(FAKE))
+    monkeypatch.setattr(_abi, "_heads_ptr", lambda t, *a, **k: (None, 0) if t is None else (ctypes.c_void_p(FAKE), t.stride(0)))
+    q = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    pages = torch.zeros(4, 16, 1, 128, dtype=torch.bfloat16)
+    table, cu, n = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    lse, acc, keep = torch.zeros(2, 8), torch.zeros(1, 32), torch.zeros(1, 8, dtype=torch.int32)
+    far = (1 << 32) + 5
+    assert _abi.paged_attn_args(q, q, pages, table, cu, n, window=5).window == 5
+    for bad in (dict(window=far), dict(max_q=far)):
+        with pytest.raises(ValueError, match="out of range"):
+            _abi.paged_attn_args(q, q, pages, table, cu, n, **bad)
+        with pytest.raises(ValueError, match="out of range"):
+            _abi.paged_weights_args(q, lse, pages, table, cu, n, acc, **bad)
+    with pytest.raises(ValueError, match="out of range"):
+        _abi.paged_attn_args(q, q, pages, table, cu, n, out_rope_pos=torch.zeros(2, dtype=torch.int64), out_rope_dim=far)
+    with pytest.raises(ValueError, match="out of range"):
+        _abi.paged_evict_args(pages, table, n, acc, keep, budget=8, recent=1 << 32)
+    with pytest.raises(ValueError, match="out of range"):
+        _abi.norm_rope_args(q, q, torch.zeros(2, dtype=torch.int64), rope_dim=far)
