@@ -50,6 +50,10 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // units): P = 2^(s - m) then stays far inside the fp32 and bf16 range, and o does not depend on
 // which m was used.
 constexpr float kSpan = 24.f;
+// A query's reference until a score moves it: lower than any score but finite, so that a score of
+// -inf gives P = 0 beside it, and not NaN. What a query sees is told by the bounds of its rows: a
+// reference that never moved may also stand for scores that are all NaN or -inf.
+constexpr float kUnset = -3.0e38f;
 
 struct PagedAttnParams {
     PagedGeom g;
@@ -432,7 +436,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             if (st < N) {
                 const int h = st - ct * g.hb;
                 const bool ok = ct < sg.tn && h < sg.hv;
-                s_nm[st] = ok ? INFINITY : -INFINITY;                // (a column without a query gets P = 0)
+                s_nm[st] = ok ? -kUnset : -INFINITY;                 // (a column without a query gets P = 0)
                 ctl.tok[st] = ok ? ct : 255;
             }
             soft_sync();
@@ -536,7 +540,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         const float mo = -s_nm[st];
                         float f = 1.f;
                         if (cm > mo) {
-                            f = mo == -INFINITY ? 0.f : ex2(mo - cm);
+                            f = ex2(mo - cm);                        // (0 from kUnset)
                             s_nm[st] = -cm;
                             rescale = k > sg.kb;
                         }
@@ -621,15 +625,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 const float l = (red[c] + red[N + c]) + (red[2 * N + c] + red[3 * N + c]);
                 const float m = -s_nm[c];
                 const int t = ctl.tok[c];
+                // No row of this part is the query's, by its bounds or because their pages are not in
+                // the pool (then the sum is 0).
+                const bool none = t == 255 || (l == 0.f && (ctl.err & DSV4_EWORD_BAD_INDEX)) ||
+                                  min(paged_hi(sg.q, sg.t0 + t), sg.row0 + sg.ke * kPT) <=
+                                      max(paged_lo(g, sg.q, sg.t0 + t), sg.row0 + sg.kb * kPT);
                 if (whole) {
                     float f = 0.f;
                     if (t != 255) {
                         const int h = sg.head0 + c - t * g.hb;
                         const float snk = sink;
-                        const float M = fmaxf(m, snk);
-                        const float e = m == -INFINITY ? 0.f : exp2f(m - M);
-                        const float den = l * e + (snk == -INFINITY ? 0.f : exp2f(snk - M));
-                        f = m == -INFINITY ? 0.f : e / den;
+                        const float M = none ? snk : fmaxf(m, snk);
+                        float den = snk == -INFINITY ? 0.f : exp2f(snk - M);
+                        if (!none) {
+                            const float e = exp2f(m - M);
+                            den += l * e;
+                            f = e / den;             // (0/0 where every score is -inf)
+                        }
                         if (p.lse)
                             p.lse[static_cast<size_t>(sg.tok0 + t) * g.H + h] =
                                 M == -INFINITY ? -INFINITY : M * kLn2 + logf(den);
@@ -637,7 +649,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     s_f[c] = f;
                 } else {
                     float* ml = p.part_ml + (static_cast<size_t>(slot2) * N + c) * 2;
-                    ml[0] = t != 255 ? m : -INFINITY;
+                    ml[0] = none ? -INFINITY : m;
                     ml[1] = l;
                 }
             }
@@ -796,7 +808,7 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int ctas, uint32_t
         const float den = sum + (snk == -INFINITY ? 0.f : exp2f(snk - top));
         if (ch == 0 && p.lse)
             p.lse[static_cast<size_t>(tok) * p.g.H + h] = top == -INFINITY ? -INFINITY : top * kLn2 + logf(den);
-        const float f = M == -INFINITY ? 0.f : 1.f / den;
+        const float f = M == -INFINITY ? 0.f : 1.f / den;            // (-inf: no part had a row of the query's)
         float o[4] = {0.f, 0.f, 0.f, 0.f};
         for (int i0 = 0; i0 < np; i0 += 8) {
             float wk = w[0];

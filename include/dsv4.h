@@ -389,7 +389,8 @@ int dsv4_norm_rope_append(const dsv4_norm_rope_args* args, dsv4_stream_t stream)
  *   out[t, h] = sum_j e^(s_j - m) v_j / (sum_j e^(s_j - m) + e^(sink[h] - m))
  *   lse[t, h] = m + log(that denominator)   (natural log, the sink included)
  * Query head h reads KV head h / (heads / kv_heads). A token that sees nothing gets out 0 and
- * lse = sink[h] (-inf without one). out_rope_*: the inverse RoPE of stage 4.
+ * lse = sink[h] (-inf without one). A NaN in a query gives NaN in its own out and lse and in no
+ * other's. out_rope_*: the inverse RoPE of stage 4.
  * Sources as stage 4. Arithmetic: bf16 tensor-core products, fp32 accumulation and softmax (P
  * rounded to bf16 before the second product, the denominator from unrounded values), bf16
  * output. The result does not depend on the order in which CTAs run. */

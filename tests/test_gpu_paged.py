@@ -701,3 +701,93 @@ def test_tables_and_lengths_may_be_slices():
     assert torch.equal(keep[0].long(), torch.cat([top, torch.arange(323, 333, device="cuda")]))
     assert torch.equal(c.k[c.table[0, :4].long()].flatten(0, 1)[:50], rows[keep[0].long()])
     assert n.tolist() == [50, 50, 45]
+
+
+# ------------------------------------------------------------------ values that are not finite
+def _but(r, mask):
+    """The reference's results of the queries in mask [T, H]."""
+    return tuple(x[mask] for x in r)
+
+
+@pytest.mark.parametrize("H, KV, D, shared", [(64, 1, 512, True), (8, 1, 128, True), (12, 2, 256, False), (32, 4, 128, False)])
+@pytest.mark.parametrize("kind", ["split", "step", "chunk", "window"])
+@pytest.mark.parametrize("with_sink", [False, True])
+def test_a_nan_query_answers_nan(H, KV, D, shared, kind, with_sink):
+    """Its output and lse are NaN, in one tile and over many CTAs, and so are the weights of the rows it sees; every other
+    query's results are as without it."""
+    m = lib()
+    g = gen(H + D)
+    lens = [20000, 300] if kind == "split" else [300, 77, 130, 1]
+    ns = [1] * len(lens) if kind in ("split", "step") else [150, 2, 130, 1]
+    window = 40 if kind == "window" else 0
+    c = Cache(g, lens, 16, KV, D, shared)
+    cu = cu_of(ns)
+    q = normal(g, cu[-1], H, D, std=2.0)
+    sink = normal(g, H, dtype=torch.float32) if with_sink else None
+    scale = 1 / math.sqrt(D)
+    r = ref.attention(q, c.k, c.v, c.table, cu, lens, scale, window, sink=sink)
+    sick = torch.zeros(cu[-1], H, dtype=torch.bool, device="cuda")
+    at = [(s, t, h) for s, t, h in ((0, 0, 3), (1, ns[1] - 1, H - 1), (0, ns[0] // 3, 0))]
+    for s, t, h in at:
+        sick[cu[s] + t, h] = True
+        q[cu[s] + t, h, (7 * h + t) % D] = float("nan")
+    out, lse = attend(c, q, cu, window=window, sink=sink, max_q=max(ns))
+    ref.check_attention(out[~sick], lse[~sick], _but(r, ~sick))
+    assert torch.isnan(out[sick].float()).all() and torch.isnan(lse[sick]).all()
+    acc = torch.full((len(lens), max(lens)), -3.0, device="cuda")
+    a = m.paged_weights_args(q, lse, c.k, c.table, i32(cu), c.kv_len, acc, max_q=max(ns), window=window)
+    ws = ws_for(m.dsv4_paged_attn_weights_workspace_size(a))
+    m.dsv4_paged_attn_weights(a, ws)
+    assert m.dsv4_read_error_word(ws) == (0, 0)
+    want = torch.full_like(acc, -3.0)
+    for s, L in enumerate(lens):
+        want[s, :L] = 0
+    for s, t, h in at:
+        lo, hi = ref.bounds(lens[s], ns[s], window)[t]
+        want[s, lo:hi] = float("nan")
+    assert torch.equal(torch.isnan(acc), torch.isnan(want))
+    well = q.clone()
+    well[sick] = 0                                   # (the weights of the others alone)
+    weights, tol = ref.weights(well, torch.where(sick, 1e4, lse), c.k, c.table, cu, lens, scale, torch.full_like(acc, -3.0), None,
+                               window)
+    sound = ~torch.isnan(acc)
+    assert ((acc.double() - weights).abs() <= tol)[sound].all()
+
+
+@pytest.mark.parametrize("D, max_q", [(512, 1), (128, 1), (128, 100), (256, 100)])
+@pytest.mark.parametrize("L", [300, 9000])
+def test_scores_of_minus_infinity(D, max_q, L):
+    """Scores that leave the range of fp32 downwards: rows that have them get no weight. A query with no other score has
+    0/0 for an output and lse -inf; with a sink, output 0 and the sink's lse."""
+    g = gen(D)
+    c = Cache(g, [L, L], 16, 1, D, False)
+    far = 256 if L == 300 else 8000
+    row = torch.arange(L, device="cuda")
+    for s in range(2):
+        page, slot = c.table[s].long()[row // 16], row % 16
+        c.k[page, slot, 0, 0] = torch.where(row < (far if s == 0 else L), -3e38, 0.0).to(BF)
+    q = normal(g, 2, 8, D)
+    q[..., 0] = 0
+    tame = q.clone()
+    q[:, ::2, 0] = 3e38                              # even heads: q . k past -3.4e38 where k's first channel is -3e38
+    scale = 1 / math.sqrt(D)
+    for sink in (None, normal(g, 8, dtype=torch.float32)):
+        out, lse = attend(c, q, [0, 1, 2], sink=sink, max_q=max_q)
+        # sequence 0, even heads: the rows from `far` on
+        page, slot = c.table[0].long()[row[far:] // 16], row[far:] % 16
+        k, v = c.k[page, slot, 0].double(), c.v[page, slot, 0].double()
+        z = tame[0, ::2].double() @ k.t() * scale
+        if sink is not None:
+            z = torch.cat([z, sink[::2].double()[:, None]], 1)
+        p = torch.softmax(z, 1)[:, :k.shape[0]]
+        # (bf16 rounding of P and of the output; a score's fp32 sum has at most 32 steps, each off by 2^-23 of a partial
+        # sum below 2^7, times the scale: below 2^-14, and 2^-12 with the exponentials and the sums)
+        tol = ref.BF16_STEP * (p @ v).abs() + (ref.BF16_STEP + 2.0 ** -12) * (p @ v.abs())
+        assert ((out[0, ::2].double() - p @ v).abs() <= tol).all()
+        assert ((lse[0, ::2].double() - torch.logsumexp(z, 1)).abs() <= 2.0 ** -12).all()
+        # sequence 1, even heads: nothing but -inf
+        if sink is None:
+            assert torch.isnan(out[1, ::2].float()).all() and (lse[1, ::2] == -math.inf).all()
+        else:
+            assert (out[1, ::2] == 0).all() and ((lse[1, ::2] - sink[::2]).abs() <= 2.0 ** -20 * (1 + sink[::2].abs())).all()
+        assert torch.isfinite(out[:, 1::2].float()).all() and torch.isfinite(lse[:, 1::2]).all()
