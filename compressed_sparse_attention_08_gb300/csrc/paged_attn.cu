@@ -171,6 +171,10 @@ __device__ __forceinline__ float2 out_rope_cs(const PagedAttnParams& p, int tok,
     return out_rope_angle(static_cast<double>(p.orp[tok]) * p.or_freq[j]);
 }
 
+// The lse of a query that sees nothing: its sink, as given (in base-2 units the type's lowest
+// values would leave the range).
+__device__ __forceinline__ float own_sink(const PagedAttnParams& p, int h) { return p.sink ? p.sink[h] : -INFINITY; }
+
 // NT TMEM columns of this thread's lane.
 template <int NT>
 __device__ __forceinline__ void tmem_cols(uint32_t addr, uint32_t (&r)[NT]) {
@@ -635,16 +639,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     if (t != 255) {
                         const int h = sg.head0 + c - t * g.hb;
                         const float snk = sink;
-                        const float M = none ? snk : fmaxf(m, snk);
-                        float den = snk == -INFINITY ? 0.f : exp2f(snk - M);
-                        if (!none) {
-                            const float e = exp2f(m - M);
-                            den += l * e;
-                            f = e / den;             // (0/0 where every score is -inf)
-                        }
+                        const float M = fmaxf(m, snk);
+                        const float e = exp2f(m - M);
+                        const float den = l * e + (snk == -INFINITY ? 0.f : exp2f(snk - M));
+                        if (!none) f = e / den;      // (0/0 where every score is -inf)
                         if (p.lse)
-                            p.lse[static_cast<size_t>(sg.tok0 + t) * g.H + h] =
-                                M == -INFINITY ? -INFINITY : M * kLn2 + logf(den);
+                            p.lse[static_cast<size_t>(sg.tok0 + t) * g.H + h] = none ? own_sink(p, h) : M * kLn2 + logf(den);
                     }
                     s_f[c] = f;
                 } else {
@@ -807,7 +807,7 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int ctas, uint32_t
         for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
         const float den = sum + (snk == -INFINITY ? 0.f : exp2f(snk - top));
         if (ch == 0 && p.lse)
-            p.lse[static_cast<size_t>(tok) * p.g.H + h] = top == -INFINITY ? -INFINITY : top * kLn2 + logf(den);
+            p.lse[static_cast<size_t>(tok) * p.g.H + h] = M == -INFINITY ? own_sink(p, h) : top * kLn2 + logf(den);
         const float f = M == -INFINITY ? 0.f : 1.f / den;            // (-inf: no part had a row of the query's)
         float o[4] = {0.f, 0.f, 0.f, 0.f};
         for (int i0 = 0; i0 < np; i0 += 8) {

@@ -791,3 +791,41 @@ def test_scores_of_minus_infinity(D, max_q, L):
         else:
             assert (out[1, ::2] == 0).all() and ((lse[1, ::2] - sink[::2]).abs() <= 2.0 ** -20 * (1 + sink[::2].abs())).all()
         assert torch.isfinite(out[:, 1::2].float()).all() and torch.isfinite(lse[:, 1::2]).all()
+
+
+@pytest.mark.parametrize("D, max_q", [(512, 1), (128, 100)])
+def test_the_lse_of_a_token_that_sees_nothing_is_its_sink(D, max_q):
+    """Bit for bit, the type's lowest value included; such a sink adds nothing where rows are seen."""
+    g = gen(D + 1)
+    ns, lens = [9, 4, 3], [4, 0, 3]
+    c = Cache(g, lens, 8, 1, D)
+    cu = cu_of(ns)
+    q = normal(g, cu[-1], 8, D)
+    sink = normal(g, 8, dtype=torch.float32)
+    sink[0], sink[1], sink[2] = torch.finfo(torch.float32).min, -3.0e38, -math.inf
+    out, lse = attend(c, q, cu, sink=sink, max_q=max_q)
+    blind = list(range(5)) + list(range(9, 13))
+    assert torch.equal(lse[blind], sink.expand(len(blind), 8)) and (out[blind] == 0).all()
+    seen = [t for t in range(cu[-1]) if t not in blind]
+    r = ref.attention(q, c.k, None, c.table, cu, lens, 1 / math.sqrt(D), sink=sink)
+    ref.check_attention(out[seen], lse[seen], tuple(x[seen] for x in r))
+
+
+def test_sinks_of_a_sequence_without_a_page_over_many_ctas():
+    """A long sequence none of whose pages lies in the pool, beside one that has rows: out 0, lse the sink, in the merge too."""
+    m = lib()
+    g = gen(77)
+    lens, D, H = [30000, 200], 128, 8
+    c = Cache(g, lens, 64, 1, D)
+    c.table[0] = -1
+    q = normal(g, 2, H, D)
+    sink = normal(g, H, dtype=torch.float32)
+    sink[1] = torch.finfo(torch.float32).min
+    out, lse = torch.empty_like(q), torch.empty(2, H, device="cuda")
+    a = m.paged_attn_args(q, out, c.k, c.table, i32([0, 1, 2]), c.kv_len, max_q=1, sink=sink, lse=lse)
+    ws = ws_for(m.dsv4_paged_attn_workspace_size(a))
+    m.dsv4_paged_attn(a, ws)
+    assert m.dsv4_read_error_word(ws)[1] == m.DSV4_EWORD_BAD_INDEX
+    assert (out[0] == 0).all() and torch.equal(lse[0], sink)
+    one = ref.attention(q[1:], c.k, None, c.table[1:], [0, 1], lens[1:], 1 / math.sqrt(D), sink=sink)
+    ref.check_attention(out[1:], lse[1:], one)
