@@ -301,4 +301,21 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
            "r"(smem_u32(bar)) : "memory");
 }
 
+// Waits (bounded) for the copies in flight into a ring of ST slots that kLoadWarps warps fill in
+// turn: slot r % ST by warp r % kLoadWarps, of which `end[w]` says where it stopped.
+constexpr int kLoadWarps = 3;
+constexpr unsigned long long kDrainNs = 100000000ull;
+template <int ST>
+__device__ __forceinline__ void ring_drain(uint64_t* full, const uint32_t (&end)[kLoadWarps]) {
+    const uint32_t last = max(max(end[0], end[1]), end[2]);
+    for (uint32_t i = last > ST ? last - ST : 0; i < last; ++i) {
+        uint32_t r = i;
+        if (r >= end[r % kLoadWarps]) {              // not issued: the slot's copy before it is the last
+            if (r < ST) continue;
+            r -= ST;
+        }
+        mbar_wait(&full[r % ST], (r / ST) & 1, nullptr, kDrainNs);
+    }
+}
+
 }  // namespace dsv4

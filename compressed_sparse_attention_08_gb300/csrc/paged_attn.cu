@@ -42,7 +42,6 @@ namespace dsv4 {
 namespace {
 
 constexpr int kThreads = 640;
-constexpr int kLoadWarps = 3;
 constexpr int kGroups = 4;                       // softmax: groups of 4 warps, one per quarter of the columns
 constexpr int kSoftWarps = 16, kSoftThreads = 512, kSoftBar = 1;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -79,6 +78,8 @@ template <int N>
 struct PagedCtl {
     uint64_t q_full, q_empty, full[kMaxSlots], empty[kMaxSlots], s_full[2], s_empty[2], p_full[2], pv_done[2];
     uint64_t v_ready, v_clean;           // V apart from K: an edge unit's rows have come, and are cleared
+    uint64_t drained;                    // products in flight when a wait ran out
+    uint32_t ring_end[kLoadWarps], seg_end[kLoadWarps];              // slots and query tiles that a load warp issued
     PagedSched sched;
     PagedSeg segs[kSegs];                // the tiles, written by the load warps for the softmax
     alignas(16) float nm[N];             // reference maxima (base-2 units), negated
@@ -218,6 +219,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         }
         mbar_init(&ctl.v_ready, 1);
         mbar_init(&ctl.v_clean, kSoftWarps);
+        mbar_init(&ctl.drained, 1);
         ctl.abort = 0;
         ctl.err = 0;
         fence_barrier_init();
@@ -306,12 +308,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             prev = cur;
             cur = next;
         }
-        if (dead && lane == 0) {                     // a wait ran out: let the copies in flight land
-            atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
-            ctl.abort = 1;
-            if (seg) mbar_wait(&ctl.q_full, (seg - 1) & 1, nullptr, 100000000ull);
-            for (uint32_t r = ring > ST ? ring - ST : 0; r < ring; ++r)
-                if (r % kLoadWarps == static_cast<uint32_t>(mine)) mbar_wait(&ctl.full[r % ST], (r / ST) & 1, nullptr, 100000000ull);
+        if (lane == 0) {
+            ctl.ring_end[mine] = ring;
+            ctl.seg_end[mine] = seg;
+            if (dead) {
+                atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
+                ctl.abort = 1;
+            }
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- tensor core
@@ -728,6 +731,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (ctl.abort) {
+        // A wait ran out in some role, and the others may have finished before it: the copies and
+        // products still in flight end (each wait bounded) before memory is given up.
+        if (warp == 1) {
+            if (elect_one()) umma_commit(&ctl.drained);
+            __syncwarp();
+            mbar_wait(&ctl.drained, 0, nullptr, kDrainNs);
+        }
+        if (tid == 0) {
+            const uint32_t seg = max(max(ctl.seg_end[0], ctl.seg_end[1]), ctl.seg_end[2]);
+            if (seg) mbar_wait(&ctl.q_full, (seg - 1) & 1, nullptr, kDrainNs);
+            ring_drain<ST>(ctl.full, ctl.ring_end);
+        }
+        __syncthreads();
+    }
     if (warp == 2) tmem_dealloc(tmem, C::TCOLS);
     if (tid == 0) p.err[blockIdx.x] = ctl.err;
 }

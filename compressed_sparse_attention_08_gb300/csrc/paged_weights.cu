@@ -26,7 +26,7 @@
 namespace dsv4 {
 namespace {
 
-constexpr int kThreads = 640, kLoadWarps = 3, kGroups = 4;
+constexpr int kThreads = 640, kGroups = 4;
 constexpr int kSoftWarps = 16, kSoftThreads = 512, kSoftBar = 1;
 constexpr int kN = 128;                  // query columns
 constexpr int kPT = kUnit;               // cache rows per tile
@@ -282,6 +282,8 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     __shared__ WSched sched;
     __shared__ uint64_t res_full[RB], res_empty[RB], full[RS], empty[RS], s_full[SB], s_empty[SB];
     __shared__ unsigned s_bad[16];
+    __shared__ uint64_t drained;                     // products in flight when a wait ran out
+    __shared__ uint32_t ring_end[kLoadWarps], res_end[kLoadWarps];   // boxes and resident operands that a load warp issued
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* sR = sm + C::OFF_R;
     float* s_nl = reinterpret_cast<float*>(sm + C::OFF_S);           // [2][N] lse in base-2 units, negated
@@ -295,6 +297,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         for (int i = 0; i < RB; ++i) { mbar_init(&res_full[i], kLoadWarps); mbar_init(&res_empty[i], 1); }
         for (int i = 0; i < RS; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
         for (int i = 0; i < SB; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], kSoftWarps); }
+        mbar_init(&drained, 1);
         abort_flag = 0;
         s_err = 0;
         fence_barrier_init();
@@ -383,12 +386,13 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 }
             }
         }
-        if (dead && lane == 0) {                     // a wait ran out: let the copies in flight land
-            atomicOr(&s_err, DSV4_EWORD_TIMEOUT);
-            abort_flag = 1;
-            for (uint32_t r = res > RB ? res - RB : 0; r < res; ++r) mbar_wait(&res_full[r % RB], (r / RB) & 1, nullptr, 100000000ull);
-            for (uint32_t r = ring > RS ? ring - RS : 0; r < ring; ++r)
-                if (r % kLoadWarps == static_cast<uint32_t>(mine)) mbar_wait(&full[r % RS], (r / RS) & 1, nullptr, 100000000ull);
+        if (lane == 0) {
+            ring_end[mine] = ring;
+            res_end[mine] = res;
+            if (dead) {
+                atomicOr(&s_err, DSV4_EWORD_TIMEOUT);
+                abort_flag = 1;
+            }
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- tensor core
@@ -582,6 +586,21 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (abort_flag) {
+        // A wait ran out in some role, and the others may have finished before it: the copies and
+        // products still in flight end (each wait bounded) before memory is given up.
+        if (warp == 1) {
+            if (elect_one()) umma_commit(&drained);
+            __syncwarp();
+            mbar_wait(&drained, 0, nullptr, kDrainNs);
+        }
+        if (tid == 0) {
+            const uint32_t res = max(max(res_end[0], res_end[1]), res_end[2]);
+            for (uint32_t r = res > RB ? res - RB : 0; r < res; ++r) mbar_wait(&res_full[r % RB], (r / RB) & 1, nullptr, kDrainNs);
+            ring_drain<RS>(full, ring_end);
+        }
+        __syncthreads();
+    }
     if (warp == 2) tmem_dealloc(tmem, kSB * kN);
     if (tid == 0) p.err[blockIdx.x] = s_err;
 }
