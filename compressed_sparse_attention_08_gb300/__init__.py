@@ -17,7 +17,7 @@ from ._abi import (  # noqa: F401
     dsv4_sparse_attn_workspace_size, dsv4_csa_decode, dsv4_csa_decode_workspace_size,
     dsv4_read_error_word, dsv4_status_string, dsv4_last_launch_count, dsv4_max_comp,
     dsv4_test_wait_fault, dsv4_copy_async, DSV4_WAIT_FAULT_NONE, DSV4_WAIT_FAULT_SCORER_STAGE,
-    DSV4_WAIT_FAULT_ATTN_QUERY, EXPORTED_SYMBOLS,
+    DSV4_WAIT_FAULT_ATTN_QUERY, DSV4_WAIT_FAULT_PAGED_ATTN, DSV4_WAIT_FAULT_PAGED_WEIGHTS, EXPORTED_SYMBOLS,
     norm_rope_args, dsv4_norm_rope_append, paged_attn_args, dsv4_paged_attn,
     dsv4_paged_attn_workspace_size, paged_weights_args, dsv4_paged_attn_weights,
     dsv4_paged_attn_weights_workspace_size, paged_evict_args, dsv4_paged_evict,

@@ -23,6 +23,8 @@ DSV4_EWORD_TIMEOUT = 0x2
 DSV4_WAIT_FAULT_NONE = 0
 DSV4_WAIT_FAULT_SCORER_STAGE = 1
 DSV4_WAIT_FAULT_ATTN_QUERY = 2
+DSV4_WAIT_FAULT_PAGED_ATTN = 4
+DSV4_WAIT_FAULT_PAGED_WEIGHTS = 8
 
 EXPORTED_SYMBOLS = (
     "dsv4_compress", "dsv4_compress_step", "dsv4_quantize_rows_fp8", "dsv4_indexer_topk_workspace_size",

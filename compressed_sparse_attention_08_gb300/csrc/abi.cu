@@ -325,8 +325,10 @@ const char* dsv4_status_string(int status) {
 int dsv4_last_launch_count(void) { return g_last_launches; }
 
 int dsv4_test_wait_fault(int which, uint32_t wait_limit_us) {
-    if (which < DSV4_WAIT_FAULT_NONE || which > DSV4_WAIT_FAULT_ATTN_QUERY || wait_limit_us > 2000000u)
-        return DSV4_ERR_INVALID_ARG;
+    const bool known = which == DSV4_WAIT_FAULT_NONE || which == DSV4_WAIT_FAULT_SCORER_STAGE ||
+                       which == DSV4_WAIT_FAULT_ATTN_QUERY || which == DSV4_WAIT_FAULT_PAGED_ATTN ||
+                       which == DSV4_WAIT_FAULT_PAGED_WEIGHTS;
+    if (!known || wait_limit_us > 2000000u) return DSV4_ERR_INVALID_ARG;
     g_wait_limit_us.store(wait_limit_us);
     g_wait_fault.store(which);
     return DSV4_OK;

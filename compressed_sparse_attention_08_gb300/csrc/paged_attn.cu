@@ -67,6 +67,7 @@ struct PagedAttnParams {
     const int64_t* orp;                  // [total_q] or null
     int or_pairs;
     int shared, min_units;
+    int fault;                           // test control: a CTA's first query tile is never copied
     unsigned long long wait_ns;
     double or_freq[64];                  // theta^(-2j / out_rope_dim)
 };
@@ -285,10 +286,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 if (dead) break;
                 if (lane == 0) {
                     if (mine == 0) ctl.segs[seg % kSegs] = sg;
-                    if (mine == 0) mbar_arrive_expect_tx(&ctl.q_full, qbytes);
-                    else mbar_arrive(&ctl.q_full);
+                    const bool skip = p.fault && seg == 0;
+                    if (!skip && mine == 0) mbar_arrive_expect_tx(&ctl.q_full, qbytes);
+                    else if (!skip) mbar_arrive(&ctl.q_full);
 #pragma unroll 1
-                    for (int b = mine; b < 2 * MT; b += kLoadWarps)
+                    for (int b = skip ? 2 * MT : mine; b < 2 * MT; b += kLoadWarps)
                         tma_load_3d(sQ + b * C::QBOX, &qmap, &ctl.q_full, b * 64, sg.head0, sg.tok0);
                 }
                 ++seg;
@@ -723,6 +725,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 desc[4] = sg.hv;
             }
         }
+        dead = __any_sync(~0u, dead);                                // (each lane waits for itself: any of them may run out)
         if (dead && lane == 0) {
             atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
             ctl.abort = 1;
@@ -741,7 +744,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         }
         if (tid == 0) {
             const uint32_t seg = max(max(ctl.seg_end[0], ctl.seg_end[1]), ctl.seg_end[2]);
-            if (seg) mbar_wait(&ctl.q_full, (seg - 1) & 1, nullptr, kDrainNs);
+            if (seg && !p.fault) mbar_wait(&ctl.q_full, (seg - 1) & 1, nullptr, kDrainNs);
             ring_drain<ST>(ctl.full, ctl.ring_end);
         }
         __syncthreads();
@@ -906,7 +909,9 @@ int run(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_
     for (int j = 0; j < p.or_pairs; ++j) p.or_freq[j] = std::pow(a.out_rope_theta, -2.0 * j / a.out_rope_dim);
     p.shared = a.v_pages == nullptr;
     p.min_units = 2;
-    p.wait_ns = kDefaultWaitNs;
+    const WaitCtl wc = wait_ctl(DSV4_WAIT_FAULT_PAGED_ATTN);
+    p.fault = wc.fault;
+    p.wait_ns = wc.wait_ns;
     count_launch();
     if (launch_k(kern, dim3(ctas), dim3(kThreads), C::SMEM, st, true, qmap, kmap, vmap, p) != cudaSuccess) return DSV4_ERR_LAUNCH;
     count_launch();

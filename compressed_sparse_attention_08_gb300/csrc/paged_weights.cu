@@ -42,6 +42,7 @@ struct PagedWeightsParams {
     int* desc;                           // [grid, 4]: of the tile that a CTA starts and others finish
     uint32_t* err;
     int acc_rows, keep_q;                // keep_q: the queries stay in shared memory
+    int fault;                           // test control: a CTA's first resident operand is never copied
     float scale2;
     unsigned long long wait_ns;
 };
@@ -351,14 +352,15 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     const uint32_t rb = res % RB;
                     if (res >= RB) dead = __any_sync(~0u, !mbar_wait(&res_empty[rb], (res / RB - 1) & 1, &abort_flag, p.wait_ns));
                     if (dead) break;
-                    if (lane == 0) {
+                    const bool skip = p.fault && res == 0;
+                    if (lane == 0 && !skip) {
                         const uint32_t bytes = NB * (keep_q ? qbox : kbox);
                         if (mine == 0 && bytes) mbar_arrive_expect_tx(&res_full[rb], bytes);
                         else mbar_arrive(&res_full[rb]);
                     }
                     __syncwarp();
 #pragma unroll 1
-                    for (int b = mine; b < NB; b += kLoadWarps) {
+                    for (int b = skip ? NB : mine; b < NB; b += kLoadWarps) {
                         if (keep_q) load_q(sm + rb * C::RES + b * C::BOX, &res_full[rb], kvh, b, tt, blk);
                         else load_k(sm + rb * C::RES + b * C::BOX, &res_full[rb], kvh, b);
                     }
@@ -578,6 +580,7 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             int* d = p.desc + blockIdx.x * 4;
             d[0] = d_parts; d[1] = d_s; d[2] = d_row;
         }
+        dead = __any_sync(~0u, dead);                                // (each lane waits for itself: any of them may run out)
         if (dead && lane == 0) {
             atomicOr(&s_err, DSV4_EWORD_TIMEOUT);
             abort_flag = 1;
@@ -596,7 +599,8 @@ paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         }
         if (tid == 0) {
             const uint32_t res = max(max(res_end[0], res_end[1]), res_end[2]);
-            for (uint32_t r = res > RB ? res - RB : 0; r < res; ++r) mbar_wait(&res_full[r % RB], (r / RB) & 1, nullptr, kDrainNs);
+            for (uint32_t r = res > RB ? res - RB : p.fault; r < res; ++r)     // (the test control's copy never comes)
+                mbar_wait(&res_full[r % RB], (r / RB) & 1, nullptr, kDrainNs);
             ring_drain<RS>(full, ring_end);
         }
         __syncthreads();
@@ -655,7 +659,9 @@ int run(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStre
     // one row tile per sequence: the queries stay
     p.keep_q = p.g.nhb == 1 && a.max_q <= p.g.tpt;
     p.scale2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-    p.wait_ns = kDefaultWaitNs;
+    const WaitCtl wc = wait_ctl(DSV4_WAIT_FAULT_PAGED_WEIGHTS);
+    p.fault = wc.fault;
+    p.wait_ns = wc.wait_ns;
     auto kern = paged_weights_kernel<D>;
     if (once_per_device(reinterpret_cast<const void*>(kern), kAttrLaunch, [kern] {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);

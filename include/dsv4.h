@@ -487,13 +487,19 @@ int dsv4_paged_evict(const dsv4_paged_evict_args* args, void* ws, size_t ws_byte
  *   DSV4_WAIT_FAULT_ATTN_QUERY: the split-form attention kernel (decode: fewer query rows,
  *     see dsv4_sparse_attn_workspace_size) issues no copy of its query tile; the wait before
  *     its first tensor-core product runs out.
+ *   DSV4_WAIT_FAULT_PAGED_ATTN: dsv4_paged_attn issues no copy of a CTA's first query tile; the
+ *     tensor-core warp's wait for it runs out, then those of the softmax and of the page loads.
+ *   DSV4_WAIT_FAULT_PAGED_WEIGHTS: dsv4_paged_attn_weights issues no copy of the first operand
+ *     that stays in shared memory; the same waits run out. (acc then holds no meaningful sums.)
  * [A] fmha_multitile_capi.cu (errors of the device path returned through C-ABI status codes,
  * never by trapping the process).
  */
 enum {
     DSV4_WAIT_FAULT_NONE = 0,
     DSV4_WAIT_FAULT_SCORER_STAGE = 1,
-    DSV4_WAIT_FAULT_ATTN_QUERY = 2
+    DSV4_WAIT_FAULT_ATTN_QUERY = 2,
+    DSV4_WAIT_FAULT_PAGED_ATTN = 4,
+    DSV4_WAIT_FAULT_PAGED_WEIGHTS = 8
 };
 int dsv4_test_wait_fault(int which, uint32_t wait_limit_us);
 

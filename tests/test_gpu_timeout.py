@@ -104,3 +104,94 @@ def test_attention_wait_times_out_then_recovers(m):
     assert ew == 0 and st == m.DSV4_OK
     _, ref, _ = oracle.sparse_attn(q, sink, kv, n_comp, idx, win, win_len, k, W, 4)
     assert_bf16_close(host_bf16(out), ref, "attention after a timed-out call")
+
+
+# ------------------------------------------------------------------ the paged cache
+def _paged_case(g, H, KV, D, ns, lens, page=16):
+    """(argument structs' inputs): queries, pages in order, tables and lengths of a small batch."""
+    per = -(-max(lens) // page)
+    k = torch.empty(per * len(lens), page, KV, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    v = torch.empty_like(k).normal_(generator=g)
+    table = torch.arange(per * len(lens), dtype=torch.int32, device="cuda").view(len(lens), per)
+    cu = torch.tensor([0] + ns, device="cuda").cumsum(0).to(torch.int32)
+    q = torch.empty(sum(ns), H, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    return q, k, v, table, cu, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+# single tokens with long and with short caches (the page loads wait for their ring, or are done by then), a chunk, rows
+# loaded twice (512 channels), several KV heads
+PAGED = [(16, 1, 512, [1, 1], [4000, 3000]), (8, 1, 128, [1, 1, 1], [100, 7, 64]), (64, 1, 512, [1], [90]),
+         (8, 2, 256, [150, 3], [900, 3]), (8, 8, 128, [200, 60], [1500, 60])]
+
+
+@pytest.mark.parametrize("H, KV, D, ns, lens", PAGED)
+@pytest.mark.parametrize("shared", [False, True])
+def test_paged_attention_wait_times_out_then_recovers(m, H, KV, D, ns, lens, shared):
+    """A CTA's first query tile is never loaded; the call ends with the timeout bit set, and the next normal call gives
+    what the call before it gave, bit for bit."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(73)
+    q, k, v, table, cu, n = _paged_case(g, H, KV, D, ns, lens)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[0], H, device="cuda")
+    a = m.paged_attn_args(q, out, k, table, cu, n, v_pages=None if shared else v, lse=lse, max_q=max(ns))
+    ws = torch.empty(max(m.dsv4_paged_attn_workspace_size(a), 256), dtype=torch.uint8, device="cuda")
+    m.dsv4_paged_attn(a, ws)
+    assert m.dsv4_read_error_word(ws) == (m.DSV4_OK, 0)
+    want = out.clone(), lse.clone()
+    for _ in range(3):
+        m.dsv4_test_wait_fault(m.DSV4_WAIT_FAULT_PAGED_ATTN, 1000)
+        m.dsv4_paged_attn(a, ws)
+        m.dsv4_test_wait_fault(m.DSV4_WAIT_FAULT_NONE, 0)
+        torch.cuda.synchronize()
+        st, ew = m.dsv4_read_error_word(ws)
+        assert ew & m.DSV4_EWORD_TIMEOUT, f"error word {ew:#x}: the wait did not run out"
+        assert st == m.DSV4_ERR_TIMEOUT
+        out.zero_()
+        lse.zero_()
+        m.dsv4_paged_attn(a, ws)
+        assert m.dsv4_read_error_word(ws) == (m.DSV4_OK, 0)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("H, KV, D, ns, lens", PAGED)
+def test_paged_weights_wait_times_out_then_recovers(m, H, KV, D, ns, lens):
+    """The first operand that stays (queries of single tokens, rows for chunks) is never loaded."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(74)
+    q, k, v, table, cu, n = _paged_case(g, H, KV, D, ns, lens)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[0], H, device="cuda")
+    a = m.paged_attn_args(q, out, k, table, cu, n, lse=lse, max_q=max(ns))
+    m.dsv4_paged_attn(a, torch.empty(m.dsv4_paged_attn_workspace_size(a), dtype=torch.uint8, device="cuda"))
+    acc_in = torch.rand(len(lens), max(lens), generator=g, device="cuda")
+    acc = torch.zeros_like(acc_in)
+    b = m.paged_weights_args(q, lse, k, table, cu, n, acc, acc_in=acc_in, max_q=max(ns))
+    ws = torch.empty(max(m.dsv4_paged_attn_weights_workspace_size(b), 256), dtype=torch.uint8, device="cuda")
+    m.dsv4_paged_attn_weights(b, ws)
+    assert m.dsv4_read_error_word(ws) == (m.DSV4_OK, 0)
+    want = acc.clone()
+    for _ in range(3):
+        m.dsv4_test_wait_fault(m.DSV4_WAIT_FAULT_PAGED_WEIGHTS, 1000)
+        m.dsv4_paged_attn_weights(b, ws)
+        m.dsv4_test_wait_fault(m.DSV4_WAIT_FAULT_NONE, 0)
+        torch.cuda.synchronize()
+        st, ew = m.dsv4_read_error_word(ws)
+        assert ew & m.DSV4_EWORD_TIMEOUT, f"error word {ew:#x}: the wait did not run out"
+        assert st == m.DSV4_ERR_TIMEOUT
+        acc.zero_()
+        m.dsv4_paged_attn_weights(b, ws)
+        assert m.dsv4_read_error_word(ws) == (m.DSV4_OK, 0)
+        assert torch.equal(acc, want)
+
+
+def test_a_control_of_one_kernel_leaves_the_others_alone(m):
+    """The paged kernels run as usual while another kernel's control is set."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(75)
+    q, k, v, table, cu, n = _paged_case(g, 8, 1, 128, [1, 1], [300, 40])
+    out, lse = torch.empty_like(q), torch.empty(2, 8, device="cuda")
+    a = m.paged_attn_args(q, out, k, table, cu, n, lse=lse, max_q=1)
+    ws = torch.empty(max(m.dsv4_paged_attn_workspace_size(a), 256), dtype=torch.uint8, device="cuda")
+    for which in (m.DSV4_WAIT_FAULT_SCORER_STAGE, m.DSV4_WAIT_FAULT_ATTN_QUERY, m.DSV4_WAIT_FAULT_PAGED_WEIGHTS):
+        m.dsv4_test_wait_fault(which, 1000)
+        m.dsv4_paged_attn(a, ws)
+        assert m.dsv4_read_error_word(ws) == (m.DSV4_OK, 0)

@@ -218,3 +218,15 @@ def test_builders_do_not_wrap_counts(monkeypatch):
         _abi.paged_evict_args(pages, table, n, acc, keep, budget=8, recent=1 << 32)
     with pytest.raises(ValueError, match="out of range"):
         _abi.norm_rope_args(q, q, torch.zeros(2, dtype=torch.int64), rope_dim=far)
+
+
+def test_wait_fault_controls(lib):
+    """The test control knows the four kernels with bounded waits on copies, and nothing between them."""
+    from compressed_sparse_attention_08_gb300 import _abi
+    known = [_abi.DSV4_WAIT_FAULT_NONE, _abi.DSV4_WAIT_FAULT_SCORER_STAGE, _abi.DSV4_WAIT_FAULT_ATTN_QUERY,
+             _abi.DSV4_WAIT_FAULT_PAGED_ATTN, _abi.DSV4_WAIT_FAULT_PAGED_WEIGHTS]
+    try:
+        assert [lib.dsv4_test_wait_fault(x, 1000) for x in range(-1, 20)] == [0 if x in known else 1 for x in range(-1, 20)]
+        assert all(lib.dsv4_test_wait_fault(x, 2000001) == 1 for x in known)
+    finally:
+        assert lib.dsv4_test_wait_fault(0, 0) == 0
