@@ -829,3 +829,182 @@ def test_sinks_of_a_sequence_without_a_page_over_many_ctas():
     assert (out[0] == 0).all() and torch.equal(lse[0], sink)
     one = ref.attention(q[1:], c.k, None, c.table[1:], [0, 1], lens[1:], 1 / math.sqrt(D), sink=sink)
     ref.check_attention(out[1:], lse[1:], one)
+
+
+# ------------------------------------------------------------------ large pages, bad pages and lengths in the eviction
+@pytest.mark.parametrize("page", [128, 256, 384, 2048])
+@pytest.mark.parametrize("H, KV, D, shared", [(64, 1, 512, True), (32, 4, 128, False), (16, 1, 256, True)])
+def test_pages_of_a_whole_unit_and_more(page, H, KV, D, shared):
+    m = lib()
+    g = gen(page + D)
+    lens, ns, window = [1, 127, 128, 700, 5000, 260], [1, 1, 90, 1, 1, 130], 0
+    scale = 1 / math.sqrt(D)
+    for window in (0, 100):
+        first = [max(0, L - n + 1 - window) if window else 0 for n, L in zip(ns, lens)]
+        c = Cache(g, lens, page, KV, D, shared, first=first)
+        cu = cu_of(ns)
+        q = normal(g, cu[-1], H, D, std=2.0)
+        out, lse = attend(c, q, cu, window=window, max_q=130)
+        ref.check_attention(out, lse, ref.attention(q, c.k, c.v, c.table, cu, lens, scale, window))
+        lse = ref.attention(q, c.k, None, c.table, cu, lens, scale, window)[1].float()
+        acc = torch.full((len(lens), 5000), -3.0, device="cuda")
+        a = m.paged_weights_args(q, lse, c.k, c.table, i32(cu), c.kv_len, acc, max_q=130, window=window)
+        want, tol = ref.weights(q, lse, c.k, c.table, cu, lens, scale, acc, None, window)
+        ws = ws_for(m.dsv4_paged_attn_weights_workspace_size(a))
+        m.dsv4_paged_attn_weights(a, ws)
+        assert m.dsv4_read_error_word(ws) == (0, 0)
+        assert ((acc.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("page", [128, 384])
+@pytest.mark.parametrize("n", [1, 70])
+def test_a_large_page_outside_the_pool_is_hidden(page, n):
+    """Whole units are hidden; a sequence with no other page answers as one that sees nothing."""
+    m = lib()
+    g = gen(page + n)
+    lens, ns, D, H = [3 * page + 50, page], [n, n], 128, 8
+    c = Cache(g, lens, page, 1, D)
+    q = normal(g, 2 * n, H, D)
+    c.table[0, 1] = c.k.shape[0]
+    c.table[1, 0] = -5
+    out, lse = torch.empty_like(q), torch.empty(2 * n, H, device="cuda")
+    cu = cu_of(ns)
+    a = m.paged_attn_args(q, out, c.k, c.table, i32(cu), c.kv_len, lse=lse, max_q=n)
+    ws = ws_for(m.dsv4_paged_attn_workspace_size(a))
+    m.dsv4_paged_attn(a, ws)
+    assert m.dsv4_read_error_word(ws) == (m.DSV4_ERR_BAD_INDEX, m.DSV4_EWORD_BAD_INDEX)
+    assert (out[n:] == 0).all() and (lse[n:] == -math.inf).all()
+    seen = torch.tensor([j for j in range(lens[0]) if j // page != 1], device="cuda")
+    k = c.k[c.table[0].long()[seen // page], seen % page, 0].double()
+    weight = torch.zeros(lens[0], dtype=torch.float64, device="cuda")
+    for t in range(n):
+        z = q[t].double() @ k.t() / math.sqrt(D)
+        z[:, seen > lens[0] - n + t] = -math.inf
+        p = torch.softmax(z, 1)
+        weight[seen] += p.sum(0)
+        tol = ref.BF16_STEP * (p @ k).abs() + (ref.BF16_STEP + 2.0 ** -12) * (p @ k.abs())
+        assert ((out[t].double() - p @ k).abs() <= tol).all()
+    acc = torch.zeros(2, lens[0], device="cuda")
+    b = m.paged_weights_args(q, lse, c.k, c.table, i32(cu), c.kv_len, acc, max_q=n)
+    ws = ws_for(m.dsv4_paged_attn_weights_workspace_size(b))
+    m.dsv4_paged_attn_weights(b, ws)
+    assert m.dsv4_read_error_word(ws)[1] == m.DSV4_EWORD_BAD_INDEX
+    assert (acc[1] == 0).all() and (acc[0, page:2 * page] == 0).all()
+    assert ((acc[0].double() - weight).abs() <= 2.0 ** -12 * weight).all()
+
+
+@pytest.mark.parametrize("page", [16, 128, 384])
+@pytest.mark.parametrize("place", ["in", "out"])
+def test_evict_with_large_pages_and_bad_pages_and_lengths(page, place):
+    """A row whose old or new page lies outside the pool does not move, everything else does; lengths are clamped to the
+    rows that tables and acc hold; each is reported, and no other row of the pool changes."""
+    m = lib()
+    g = gen(page)
+    D, budget, recent, rows = 128, 150, 30, 900
+    lens = [700, 900, 40, 500]
+    c = Cache(g, lens, page, 2, D, False, spare=2 + 4 * (-(-budget // page)), poison=False)
+    per = -(-budget // page)
+    free = sorted(set(range(c.k.shape[0])) - set(c.table.flatten().tolist()))
+    if place == "in":
+        wide = torch.zeros(4, max(c.table.shape[1], per), dtype=torch.int32, device="cuda")
+        wide[:, :c.table.shape[1]] = c.table
+        out_table = c.table = wide
+    else:
+        out_table = i32(free[:4 * per]).view(4, per)
+    acc = (normal(g, 4, rows, dtype=torch.float32).abs() * 64).round() / 64
+    full = c.table.shape[1] * page
+    for bad in ("none", "page in", "page out", "lengths", "acc rows"):
+        k, v, table, to = c.k.clone(), c.v.clone(), c.table.clone(), out_table.clone()
+        if place == "in":
+            to = table
+        n, weight = c.kv_len.clone(), acc.clone()
+        if bad == "page in":
+            table[0, -(-700 // page) - 1] = k.shape[0]   # (of the recent rows, which are kept)
+        if bad == "page out" and place == "out":
+            to[1, 0] = -1
+        if bad == "lengths":
+            n.copy_(i32([-3, 1 << 30, 40, 500]))
+        if bad == "acc rows":
+            weight = acc[:, :450].contiguous()
+        cap = min(full, weight.shape[1])
+        now = [min(max(x, 0), cap) for x in n.tolist()]
+        kept = ref.evict(now, weight.cpu(), budget, recent)
+        pool, tab, dest = k.shape[0], table.tolist(), to.tolist()
+        want_k, want_v = k.clone(), v.clone()
+        broken = False
+        for s, r in enumerate(kept):
+            for i, j in enumerate(r):
+                a, b = tab[s][j // page], dest[s][i // page]
+                if place == "in" and i == j:
+                    continue
+                if not (0 <= a < pool and 0 <= b < pool):
+                    broken = True
+                    continue
+                want_k[b, i % page] = k[a, j % page]
+                want_v[b, i % page] = v[a, j % page]
+        keep = torch.full((4, budget), -5, dtype=torch.int32, device="cuda")
+        len_out = torch.full((4,), -9, dtype=torch.int32, device="cuda")
+        got = torch.full_like(weight, -9.0)
+        a = m.paged_evict_args(k, table, n, weight, keep, budget=budget, recent=recent, v_pages=v, out_table=to, kv_len_out=len_out,
+                               acc_out=got)
+        ws = ws_for(m.dsv4_paged_evict_workspace_size(a))
+        m.dsv4_paged_evict(a, ws)
+        flagged = broken or now != n.tolist()
+        assert flagged == (bad != "none" and not (bad == "page out" and place == "in"))
+        assert m.dsv4_read_error_word(ws)[1] == (m.DSV4_EWORD_BAD_INDEX if flagged else 0), bad
+        assert len_out.tolist() == [len(r) for r in kept]
+        assert torch.equal(k, want_k) and torch.equal(v, want_v), bad
+        for s, r in enumerate(kept):
+            assert keep[s].tolist() == r + [-1] * (budget - len(r))
+            assert torch.equal(got[s, :len(r)], weight[s, r]) and (got[s, len(r):] == -9).all()
+
+
+@pytest.mark.parametrize("longest", [700, 40000])
+def test_a_graph_of_a_whole_step(longest):
+    """Append, attention, weights and eviction in place, captured as one graph: each replay gives the bits of the eager step."""
+    m = lib()
+    g = gen(longest)
+    B, H, D, page, budget = 3, 8, 128, 64, 500
+    lens = [longest, longest // 2, 90]
+    c = Cache(g, lens, page, 1, D, poison=False)
+    x = normal(g, B, H + 1, D, std=1.5)
+    pos = i32(lens).long()
+    slots = torch.stack([c.table[s, (n - 1) // page].long() * page + (n - 1) % page for s, n in enumerate(lens)])
+    cu = i32([0, 1, 2, 3])
+    q, out = torch.empty(B, H, D, dtype=BF, device="cuda"), torch.empty(B, H, D, dtype=BF, device="cuda")
+    lse = torch.empty(B, H, device="cuda")
+    acc = (torch.rand(B, c.table.shape[1] * page, generator=g, device="cuda") * 64).round() / 64
+    keep = torch.empty(B, budget, dtype=torch.int32, device="cuda")
+    state = [c.k, c.kv_len, acc]
+    start = [t.clone() for t in state]
+    n = m.norm_rope_args(x[:, :H], q, pos, k=x[:, H:], k_pages=c.k, slots=slots)
+    a = m.paged_attn_args(q, out, c.k, c.table, cu, c.kv_len, max_q=1, lse=lse, out_rope_pos=pos)
+    w = m.paged_weights_args(q, lse, c.k, c.table, cu, c.kv_len, acc, acc_in=acc, max_q=1)
+    e = m.paged_evict_args(c.k, c.table, c.kv_len, acc, keep, budget=budget, recent=64)
+    sizes = (m.dsv4_paged_attn_workspace_size(a), m.dsv4_paged_attn_weights_workspace_size(w), m.dsv4_paged_evict_workspace_size(e))
+    spaces = [ws_for(s) for s in sizes]
+
+    def step():
+        m.dsv4_norm_rope_append(n)
+        m.dsv4_paged_attn(a, spaces[0])
+        m.dsv4_paged_attn_weights(w, spaces[1])
+        m.dsv4_paged_evict(e, spaces[2])
+
+    def results():
+        assert all(m.dsv4_read_error_word(s) == (0, 0) for s in spaces)
+        return [t.clone() for t in (q, out, lse, keep, *state)]
+
+    step()
+    want = results()
+    assert want[5].tolist() == [min(x, budget) for x in lens]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(2):
+        for t, s in zip(state, start):
+            t.copy_(s)
+        keep.fill_(-5)
+        for s in spaces:
+            s.fill_(0x5A)
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip(results(), want))
