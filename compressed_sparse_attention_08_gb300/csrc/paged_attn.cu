@@ -549,7 +549,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         const float mo = -s_nm[st];
                         float f = 1.f;
                         if (cm > mo) {
-                            f = ex2(mo - cm);                        // (0 from kUnset)
+                            f = mo == kUnset ? 0.f : ex2(mo - cm);
                             s_nm[st] = -cm;
                             rescale = k > sg.kb;
                         }
