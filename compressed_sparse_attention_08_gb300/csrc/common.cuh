@@ -301,10 +301,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 
 // 32 registers per thread -> 32 lanes x 32 consecutive 32-bit TMEM columns (the inverse of
 // the x32 load); tcgen05.wait::st orders the stores before a later tcgen05 operation reads them.
-#define DSV4_TMEM_ST_32x32b_X8(taddr, r)                                                      \
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"      \
-                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),          \
-                    "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory")
 #define DSV4_TMEM_ST_32x32b_X32(taddr, r)                                                     \
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "                               \
                  "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"                     \
@@ -315,6 +311,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
                     "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),     \
                     "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),     \
                     "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory")
+// The same for 8 columns.
+#define DSV4_TMEM_ST_32x32b_X8(taddr, r)                                                      \
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"      \
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),          \
+                    "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory")
 #define DSV4_TMEM_WAIT_ST() asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory")
 
 // 32 lanes x 64 consecutive 32-bit TMEM columns -> 64 registers per thread.

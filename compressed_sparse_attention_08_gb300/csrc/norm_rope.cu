@@ -7,7 +7,7 @@
 // "nvfp4-megamoe-kernel: compare v0.1-e2e-working...v-c1-c2-c3-20260602", compressor_reduce.cu
 // apply_kv_norm_kernel.
 //
-// HBM bound: every element is read and written once. One launch serves query heads, keys and
+// Every element is read and written once (the floor is HBM). One launch serves query heads, keys and
 // values, so a fused projection's output is read where it lies. A CTA takes one token (or, with
 // few tokens, a share of one token's heads): the token's angles are formed once (fp64, Cody-
 // Waite reduced) into shared memory while its rows are already on their way; a row lies in 16 or
@@ -16,8 +16,9 @@
 // weight, cosine and sine become four factors per pair, held in registers for all rows, and a
 // pair costs three paired operations (with each row working out its own, the kernel issued 205
 // instructions per 16 bytes and was bound by that).
-// Measured: 2,039 tokens of 64 + 8 + 8 heads x 128 19.5 us, 4.3 TB/s; 16 tokens of 64 + 1 x 512
-// 3.7 us, a launch and one chain of latencies.
+// Measured: 2,039 tokens of 64 + 8 + 8 heads x 128 19.5 us, 4.3 TB/s: latency of loads, shuffles and
+// barriers at eight CTAs per SM (64 registers a thread) in 1.7 waves, with 28 % of the issue slots
+// used; 16 tokens of 64 + 1 x 512 3.7 us, a launch and one chain of latencies.
 #include <cmath>
 
 #include "internal.h"

@@ -6,7 +6,7 @@
 // the sequence stands at row p = kv_len[s] - n_s + t and sees the rows [max(0, p + 1 - window),
 // p + 1) (window 0: from row 0).
 //
-// Work is cut into units of `unit` (128 or 64) cache rows x one row tile: a row tile is `tpt` tokens times
+// Work is cut into units of kUnit = 128 cache rows x one row tile: a row tile is `tpt` tokens times
 // `hb` query heads of one KV head (at most N rows, the tensor-core tile). All units of a call
 // form one line, in the order (sequence, token tile, KV head and head block, rows), and CTA c
 // of g takes the units [T c / g, T (c + 1) / g): every CTA has the same amount of work whatever
@@ -86,7 +86,7 @@ __device__ __forceinline__ int paged_lo(const PagedGeom& g, const PagedSeq& q, i
     return g.window > 0 ? max(q.L - q.n + t + 1 - g.window, 0) : 0;
 }
 
-// Units of token tile tt: the blocks of `unit` rows that some token of it sees (at least one, so that
+// Units of token tile tt: the blocks of kUnit rows that some token of it sees (at least one, so that
 // tokens that see nothing are still answered).
 __device__ __forceinline__ int paged_tile_units(const PagedGeom& g, const PagedSeq& q, int tt) {
     const int t0 = tt * g.tpt, t1 = min(t0 + g.tpt, q.n) - 1;
@@ -224,7 +224,7 @@ struct PagedSeg {
     int kvh, head0, hv;                  // KV head, first query head, query heads
     int lo_u, hi_u;                      // rows that some token sees
     int lo_max, hi_min;                  // rows that every token sees
-    int row0;                            // first row of unit 0 (a multiple of `unit`)
+    int row0;                            // first row of unit 0 (a multiple of kUnit)
     int n, kb, ke;                       // the tile's units, this CTA's [kb, ke)
 };
 
@@ -269,7 +269,7 @@ struct PagedWalk {
     }
 };
 
-// One tile of `unit` cache rows as boxes of `br` rows: lanes 2i and 2i + 1 answer for box i (the
+// One tile of kUnit cache rows as boxes of `br` rows: lanes 2i and 2i + 1 answer for box i (the
 // two 64-channel halves of a slot). The page is only looked up here; paged_boxes uses it.
 struct PagedLook { int page, slot; bool need; };
 __device__ __forceinline__ PagedLook paged_look(const PagedGeom& g, const PagedSeg& sg, int row, int lane) {

@@ -499,7 +499,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     }
                     if (masked) hide();
                 };
-                // P = 2^(s - m) in bf16 (rounded: the tensor core takes bf16; the sum stays in fp32),
+                // P = 2^(s - m) in bf16 (rounded: the tensor core takes bf16 beside bf16 V; the sum stays in
+                // fp32. The outputs' error against 64 bits, relative to their size, is 0.0019 to 0.0023
+                // with it and 0.0017, their own rounding, without),
                 // the MN-major operand: a cache row's 64 queries are one 128-byte line
                 uint8_t* pbuf = sP + (u % C::PN) * C::PB;
                 auto put = [&] {

@@ -12,8 +12,10 @@
 // a row that was overwritten; a CTA therefore takes a slice of every row's channels (their
 // copies are independent) and walks all rows. Into other pages there is no such order, and
 // the rows are spread over CTAs too.
-// Measured: 4 sequences of up to 64K rows x 512 cut to 32K in 70 us (the move 50 us, 5.4 TB/s);
-// 3 of up to 1.5K rows 12 us, three dependent launches.
+// Measured, into other pages: 4 sequences of up to 64K rows x 512 cut to 32K in 70 us (the move 50
+// us, 5.4 TB/s); 3 of up to 1.5K rows 12 us, three dependent launches. In place: 4 sequences of 64K
+// rows 366 us (slices of 16 bytes, half a sector each), 16 of 16K rows cut to 8K 130 us (slices of
+// 64 bytes), 3 of 1.5K 20 us: the walk over all rows is serial in each CTA.
 #include "internal.h"
 #include "paged.cuh"
 
@@ -227,7 +229,7 @@ int launch_paged_evict(const dsv4_paged_evict_args& a, uint8_t* ws, uint32_t* ew
     p.row16 = a.kv_heads * a.dim / 8;
     const int sms = sm_count() > 0 ? sm_count() : 152;
     if (in_place) {
-        // slices of 64 bytes; thinner ones while that leaves SMs without work
+        // slices of 64 bytes; thinner ones, down to 16 bytes, while that leaves SMs without work
         p.slice = 4;
         while (p.slice > 1 && static_cast<long long>(a.batch) * pools * (p.row16 / p.slice) < sms) p.slice /= 2;
         p.rows_cta = a.budget;

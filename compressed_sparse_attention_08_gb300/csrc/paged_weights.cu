@@ -52,11 +52,15 @@ struct WCfg {
     static constexpr int D = D_, NB = D / 64;
     static constexpr int BOX = kPT * 128;                    // 128 rows (or queries) x 64 channels
     static constexpr int RES = NB * BOX;                     // the operand that stays
-    static constexpr int RB = D <= 256 ? 2 : 1;              // and how many (several KV heads: it changes every unit)
+    // and how many: with several KV heads it changes every unit, and the next one comes while this one
+    // is used (16 single tokens over 8,192 rows each, 32 heads over 8, pages of 16: D = 128 127 -> 82 us,
+    // D = 256 156 -> 116; a 300-token chunk alike with one or two, 59 and 63 us). At 512 two do not fit.
+    static constexpr int RB = D <= 256 ? 2 : 1;
     static constexpr int RS = D == 128 ? 8 : 5;              // ring boxes
     // The tensor core's running fp32 sum is cut, not rounded, at every step, which pulls scores
-    // towards 0: by 1.1e-6 on average at scores of 3 with 512 channels in one sum (measured), which
-    // the weights show in full. Two sums of 256 channels, added in fp32, leave half of it.
+    // towards 0. At scores of about 3 a weight is then off by 1.1e-6 on average (relative) with 512
+    // channels in one sum, and by 5.0e-7 with two sums of 256 that are added in fp32 (one sum of 256:
+    // 5.1e-7, of 128: 2.9e-7).
     static constexpr int SUMS = D == 512 ? 2 : 1;
     static constexpr int SB = kSB / SUMS;                    // score buffers
     static constexpr int OFF_R = RB * RES, OFF_S = OFF_R + RS * BOX;

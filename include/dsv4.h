@@ -421,8 +421,9 @@ int dsv4_paged_attn(const dsv4_paged_attn_args* args, void* ws, size_t ws_bytes,
 /* The attention weight that each cached row received from the call's tokens, over all heads:
  *   acc[s, j] = acc_in[s, j] + sum_{t, h: t sees j} exp(scale * q[t, h] . k_j - lse[t, h])
  * for j < kv_len[s] (the rest of acc is left as it was), with lse as dsv4_paged_attn wrote it
- * for the same q, rows, window and scale. acc_in NULL: 0; acc_in may be acc. The order of the
- * sum is fixed by the arguments and the lengths. fp32 accumulation. */
+ * for the same q, rows, window and scale. A query whose lse is -inf saw nothing and adds nothing; one
+ * whose lse is NaN makes the acc of the rows it sees NaN. acc_in NULL: 0; acc_in may be acc. The order
+ * of the sum is fixed by the arguments and the lengths. fp32 accumulation. */
 typedef struct dsv4_paged_weights_args {
     const void* q;            /* bf16 [total_q, heads, dim]                                   */
     const float* lse;         /* fp32 [total_q, heads]                                        */
