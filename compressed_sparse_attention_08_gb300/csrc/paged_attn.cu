@@ -29,8 +29,8 @@
 // and two CTAs with 256 channels each that exchange scores and P through distributed shared memory
 // (which moved about 12 bytes a cycle).
 //
-// Measured (64 heads x 512, K = V): 2,048 tokens behind 14K rows 3.96 ms, 1,040 TFLOP/s, bound by
-// shared memory; 16 single tokens over up to 8K rows 46 us (15 us of it HBM, the rest the start of cold
+// Measured (64 heads x 512, K = V): 2,048 tokens behind 14K rows 3.98 ms, 1,030 TFLOP/s, bound by
+// shared memory; 16 single tokens over up to 8K rows 47 us (15 us of it HBM, the rest the start of cold
 // CTAs and the merge); 4 over up to 256K rows 176 us, 5.05 TB/s. 32 heads over 8 of 128, tokens and
 // chunks mixed: 228 us, 565 TFLOP/s, bound by a unit's chain of softmax steps.
 #include <cmath>
