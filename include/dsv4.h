@@ -351,7 +351,8 @@ int dsv4_quantize_rows_fp8(const void* x, int rows, int dim, void* q, float* sca
  * arrays for them (the weights of a call without tokens are acc_in). batch: 0..2048; max_pages *
  * page_size: at most 2^29 (times batch: below 2^37). Lengths, tables, positions, lse, sink and acc need
  * the alignment of their type only (a table may be a slice of a larger one). The workspace sizes
- * look at counts only, no array, and are 0 for counts that the call refuses.
+ * look at no array, and are 0 where a count they look at (batch, heads, dim, max_q; batch, acc_rows,
+ * budget, recent for the eviction) is one that the call refuses.
  */
 
 /* RMSNorm of queries and keys per head, RoPE in the same pass, rows appended to the pages.
