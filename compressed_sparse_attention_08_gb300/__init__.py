@@ -21,5 +21,6 @@ from ._abi import (  # noqa: F401
     norm_rope_args, dsv4_norm_rope_append, paged_attn_args, dsv4_paged_attn,
     dsv4_paged_attn_workspace_size, paged_weights_args, dsv4_paged_attn_weights,
     dsv4_paged_attn_weights_workspace_size, paged_evict_args, dsv4_paged_evict,
-    dsv4_paged_evict_workspace_size,
+    dsv4_paged_evict_workspace_size, paged_plan_args, dsv4_paged_plan, dsv4_paged_plan_workspace_size,
+    rope_args, dsv4_rope, DSV4_ERR_NO_PAGES, DSV4_EWORD_NO_PAGES,
 )

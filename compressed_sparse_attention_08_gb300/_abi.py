@@ -18,8 +18,10 @@ DSV4_ERR_LAUNCH = 2
 DSV4_ERR_BAD_INDEX = 3
 DSV4_ERR_TIMEOUT = 4
 DSV4_ERR_UNSUPPORTED = 5
+DSV4_ERR_NO_PAGES = 6
 DSV4_EWORD_BAD_INDEX = 0x1
 DSV4_EWORD_TIMEOUT = 0x2
+DSV4_EWORD_NO_PAGES = 0x4
 DSV4_WAIT_FAULT_NONE = 0
 DSV4_WAIT_FAULT_SCORER_STAGE = 1
 DSV4_WAIT_FAULT_ATTN_QUERY = 2
@@ -37,6 +39,7 @@ EXPORTED_SYMBOLS = (
     "dsv4_norm_rope_append", "dsv4_paged_attn_workspace_size", "dsv4_paged_attn",
     "dsv4_paged_attn_weights_workspace_size", "dsv4_paged_attn_weights",
     "dsv4_paged_evict_workspace_size", "dsv4_paged_evict",
+    "dsv4_paged_plan_workspace_size", "dsv4_paged_plan", "dsv4_rope",
 )
 
 P = ctypes.c_void_p
@@ -113,6 +116,25 @@ class PagedEvictArgs(ctypes.Structure):
                 ("max_pages", I), ("out_pages", I), ("acc_rows", I), ("budget", I), ("recent", I)]
 
 
+class PagedPlanArgs(ctypes.Structure):
+    _fields_ = [("new_len", P), ("kv_len", P), ("held", P), ("shared", P), ("next_pos", P),
+                ("block_table", P), ("free_pages", P), ("free_count", P), ("cu_q", P),
+                ("kv_len_out", P), ("held_out", P), ("next_pos_out", P), ("free_count_out", P),
+                ("slots", P), ("pos", P), ("seq", P), ("batch", I), ("total_q", I),
+                ("page_size", I), ("num_pages", I), ("max_pages", I), ("free_cap", I)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("k", P), ("v", P), ("q_out", P), ("k_out", P), ("v_out", P),
+                ("slots", P), ("pos", P), ("q_stride", L), ("k_stride", L), ("v_stride", L),
+                ("q_out_stride", L), ("k_out_stride", L), ("tokens", I), ("heads", I),
+                ("kv_heads", I), ("dim", I), ("page_size", I), ("num_pages", I), ("dtype", I),
+                ("rope_dim", I), ("first", I), ("layout", I), ("inverse", I), ("scaling", I),
+                ("rope_theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
 class CsaArgs(ctypes.Structure):
     _fields_ = [("compress_kv", ctypes.POINTER(CompressArgs)),
                 ("compress_keys", ctypes.POINTER(CompressArgs)),
@@ -173,8 +195,10 @@ def library():
         lib.dsv4_copy_async.restype = I
         lib.dsv4_norm_rope_append.argtypes = [ctypes.POINTER(NormRopeArgs), P]
         lib.dsv4_norm_rope_append.restype = I
+        lib.dsv4_rope.argtypes = [ctypes.POINTER(RopeArgs), P]
+        lib.dsv4_rope.restype = I
         for name, st in (("dsv4_paged_attn", PagedAttnArgs), ("dsv4_paged_attn_weights", PagedWeightsArgs),
-                         ("dsv4_paged_evict", PagedEvictArgs)):
+                         ("dsv4_paged_evict", PagedEvictArgs), ("dsv4_paged_plan", PagedPlanArgs)):
             size = getattr(lib, name + "_workspace_size")
             size.argtypes = [ctypes.POINTER(st)]
             size.restype = ctypes.c_size_t
@@ -491,9 +515,9 @@ def dsv4_test_wait_fault(which, wait_limit_us=0):
 # Prepared argument structs, as for dsv4_csa_decode: a serving loop builds them once over its
 # buffers and issues the same call every step. A struct holds its tensors, and the call runs on
 # the device they are on.
-def _heads_ptr(t, name, optional=False):
-    """bf16 [tokens, heads, dim] whose tokens may be further apart than their heads (a part of a
-    fused projection): (pointer, token stride in elements)."""
+def _heads_ptr(t, name, optional=False, dtype=None):
+    """[tokens, heads, dim] in bf16 (or dtype) whose tokens may be further apart than their heads (a
+    part of a fused projection): (pointer, token stride in elements)."""
     if t is None:
         if optional:
             return None, 0
@@ -503,8 +527,8 @@ def _heads_ptr(t, name, optional=False):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dtype != (dtype or torch.bfloat16):
+        raise TypeError(f"{name} must be {dtype or torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim]")
     n, h, d = t.shape
@@ -707,3 +731,114 @@ def dsv4_paged_evict_workspace_size(args):
 def dsv4_paged_evict(args, ws, *, stream=None):
     """Eviction by accumulated weight, from a paged_evict_args struct."""
     _call(library().dsv4_paged_evict, args, stream, "dsv4_paged_evict", ws)
+
+
+def paged_plan_args(new_len, kv_len, held, block_table, free_pages, free_count, cu_q, slots, *, page_size,
+                    num_pages, shared=None, pos=None, seq=None, next_pos=None, kv_len_out=None, held_out=None,
+                    free_count_out=None, next_pos_out=None):
+    """A step's offsets, slots and pages from its lengths: new_len (or None: pages are only given back), kv_len, held
+    (and shared) int32 [B], block_table int32 [B, max_pages], free_pages int32 [capacity] with free_count int32 [1] of
+    them in use -> cu_q int32 [B + 1], slots int64 [T], and, where given, pos int64 [T] (from next_pos int64 [B], else
+    kv_len) and seq int32 [T]. kv_len_out, held_out, free_count_out and next_pos_out default to the arrays they follow
+    (in place)."""
+    bf16, f32, i32, i64 = _dt()
+    B = kv_len.shape[0]
+    kv_len_out = kv_len if kv_len_out is None else kv_len_out
+    held_out = held if held_out is None else held_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    if next_pos is None and next_pos_out is not None:
+        raise ValueError("next_pos_out needs next_pos")
+    next_pos_out = next_pos if next_pos_out is None else next_pos_out
+    for t, name in ((new_len, "new_len"), (kv_len, "kv_len"), (held, "held"), (shared, "shared"), (next_pos, "next_pos"),
+                    (kv_len_out, "kv_len_out"), (held_out, "held_out"), (next_pos_out, "next_pos_out")):
+        _shape(t, (B,), name)
+    _shape(block_table, (B, block_table.shape[-1]), "block_table")
+    _shape(free_pages, (free_pages.shape[0],), "free_pages")
+    _shape(free_count, (1,), "free_count")
+    _shape(free_count_out, (1,), "free_count_out")
+    _shape(cu_q, (B + 1,), "cu_q")
+    T = slots.shape[0]
+    _shape(slots, (T,), "slots")
+    _shape(pos, (T,), "pos")
+    _shape(seq, (T,), "seq")
+    a = _struct(PagedPlanArgs, _ptr(new_len, i32, "new_len", True), _ptr(kv_len, i32, "kv_len"), _ptr(held, i32, "held"),
+                _ptr(shared, i32, "shared", True), _ptr(next_pos, i64, "next_pos", True), _ptr(block_table, i32, "block_table"),
+                _ptr(free_pages, i32, "free_pages"), _ptr(free_count, i32, "free_count"), _ptr(cu_q, i32, "cu_q"),
+                _ptr(kv_len_out, i32, "kv_len_out"), _ptr(held_out, i32, "held_out"),
+                _ptr(next_pos_out, i64, "next_pos_out", True), _ptr(free_count_out, i32, "free_count_out"),
+                _ptr(slots, i64, "slots"), _ptr(pos, i64, "pos", True), _ptr(seq, i32, "seq", True), B, T, page_size,
+                num_pages, block_table.shape[1], free_pages.shape[0])
+    return _held(a, new_len, kv_len, held, shared, next_pos, block_table, free_pages, free_count, cu_q, kv_len_out, held_out,
+                 next_pos_out, free_count_out, slots, pos, seq)
+
+
+def dsv4_paged_plan_workspace_size(args):
+    return int(library().dsv4_paged_plan_workspace_size(ctypes.byref(args)))
+
+
+def dsv4_paged_plan(args, ws, *, stream=None):
+    """The bookkeeping of a step, from a paged_plan_args struct."""
+    _call(library().dsv4_paged_plan, args, stream, "dsv4_paged_plan", ws)
+
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "turns": 2, "index": 3}
+
+
+def rope_args(q, q_out, pos, *, k=None, k_out=None, v=None, v_out=None, slots=None, rope_dim, first=None,
+              layout="interleaved", inverse=False, rope_theta=10000.0, scaling="none", factor=1.0, original_len=0,
+              beta_fast=32.0, beta_slow=1.0, magnitude=1.0):
+    """Rotate q [T, H, D] -> q_out and k [T, KV, D] -> k_out [T, KV, D], all bf16, fp16 or fp32, or, with slots int64 [T],
+    to rows of a pool k_out [pages, page_size, KV, D] (v beside it, unchanged). pos int64 [T]. The channels first ..
+    first + rope_dim (default: the last) turn; layout: "interleaved" (2j, 2j + 1) or "half" (j, j + rope_dim / 2);
+    scaling: "none", "linear", "turns" or "index". inverse=True turns back (and is the backward pass). q or k may be
+    None; in place: q_out is q, k_out is k."""
+    import torch
+    bf16, f32, i32, i64 = _dt()
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q or k is required")
+    types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    if some.dtype not in types:
+        raise TypeError(f"q and k must be bf16, fp16 or fp32, got {some.dtype}")
+    if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+        raise ValueError(f"layout is one of {list(ROPE_LAYOUTS)}, scaling one of {list(ROPE_SCALINGS)}")
+    dt = some.dtype
+    T, _, D = some.shape
+    H = 0 if q is None else q.shape[1]
+    KV = 0 if k is None else k.shape[1]
+    _shape(q, (T, H, D), "q")
+    _shape(q_out, (T, H, D), "q_out")
+    _shape(k, (T, KV, D), "k")
+    _shape(v, (T, KV, D), "v")
+    _shape(pos, (T,), "pos")
+    _shape(slots, (T,), "slots")
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (v is None) != (v_out is None):
+        raise ValueError("q, k and v need their outputs")
+    if v is not None and slots is None:
+        raise ValueError("v is only stored by slots")
+    pages = page_size = 0
+    if slots is not None:
+        if k is None or k_out.dim() != 4:
+            raise ValueError("slots need k and a pool k_out [num_pages, page_size, kv_heads, dim]")
+        pages, page_size = k_out.shape[:2]
+        _shape(k_out, (pages, page_size, KV, D), "k_out")
+        _shape(v_out, k_out.shape, "v_out")
+        kop, kos = _ptr(k_out, dt, "k_out"), 0
+    else:
+        _shape(k_out, (T, KV, D), "k_out")
+        kop, kos = _heads_ptr(k_out, "k_out", True, dt)
+    qp, qs = _heads_ptr(q, "q", True, dt)
+    op, os_ = _heads_ptr(q_out, "q_out", True, dt)
+    kp, ks = _heads_ptr(k, "k", True, dt)
+    vp, vs = _heads_ptr(v, "v", True, dt)
+    a = _struct(RopeArgs, qp, kp, vp, op, kop, _ptr(v_out, dt, "v_out", True), _ptr(slots, i64, "slots", True),
+                _ptr(pos, i64, "pos"), qs, ks, vs, os_, kos, T, H, KV, D, page_size, pages, types[dt], rope_dim,
+                D - rope_dim if first is None else first, ROPE_LAYOUTS[layout], int(bool(inverse)), ROPE_SCALINGS[scaling],
+                rope_theta, factor, original_len, beta_fast, beta_slow, magnitude)
+    return _held(a, q, q_out, pos, k, k_out, v, v_out, slots)
+
+
+def dsv4_rope(args, *, stream=None):
+    """Rotary positions (and the append to the pages), from a rope_args struct."""
+    _call(library().dsv4_rope, args, stream, "dsv4_rope")

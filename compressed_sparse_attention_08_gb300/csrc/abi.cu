@@ -229,6 +229,62 @@ bool paged_evict_ok(const dsv4_paged_evict_args* a) {
     return true;
 }
 
+bool paged_plan_sizes_ok(const dsv4_paged_plan_args* a) { return a->batch >= 0 && a->batch <= kPagedMaxBatch; }
+
+bool paged_plan_ok(const dsv4_paged_plan_args* a) {
+    if (!a || !paged_ok(a->batch, 1, 128, a->page_size, a->num_pages, a->max_pages)) return false;
+    if (a->total_q < 0 || a->total_q > (1 << 24) || a->free_cap < 0 || a->free_cap > (1 << 30)) return false;
+    if (!num_ok(a->free_count, 4) || !num_ok(a->free_count_out, 4) || !num_ok(a->cu_q, 4)) return false;
+    if (a->free_cap > 0 && !num_ok(a->free_pages, 4)) return false;
+    if ((a->total_q > 0 && !num_ok(a->slots, 8)) || !opt_num_ok(a->pos, 8) || !opt_num_ok(a->seq, 4)) return false;
+    if ((a->next_pos == nullptr) != (a->next_pos_out == nullptr)) return false;
+    if (a->batch == 0) return true;                  // no sequence: no array of theirs is looked at
+    return opt_num_ok(a->new_len, 4) && num_ok(a->kv_len, 4) && num_ok(a->held, 4) && opt_num_ok(a->shared, 4) &&
+           opt_num_ok(a->next_pos, 8) && opt_num_ok(a->next_pos_out, 8) && num_ok(a->block_table, 4) && num_ok(a->kv_len_out, 4) &&
+           num_ok(a->held_out, 4);
+}
+
+bool rope_ok(const dsv4_rope_args* a) {
+    if (!a || a->tokens < 0 || a->tokens > (1 << 24) || a->heads < 0 || a->heads > 1024 || a->kv_heads < 0 || a->kv_heads > 1024)
+        return false;
+    if (a->dim < 8 || a->dim > 1024 || a->dim % 8 || a->dtype < DSV4_BF16 || a->dtype > DSV4_FP32) return false;
+    if (a->rope_dim < 2 || a->rope_dim > a->dim || a->rope_dim > 512 || (a->rope_dim & 1)) return false;
+    if (a->layout < 0 || a->layout > 1 || a->inverse < 0 || a->inverse > 1) return false;
+    if (a->first < 0 || a->first > a->dim - a->rope_dim || (a->layout == 0 && (a->first & 1))) return false;
+    if (!std::isfinite(a->rope_theta) || a->rope_theta <= 0.0 || !std::isfinite(a->magnitude)) return false;
+    if (a->scaling < DSV4_ROPE_PLAIN || a->scaling > DSV4_ROPE_BY_INDEX) return false;
+    if (a->scaling != DSV4_ROPE_PLAIN && !(a->factor > 0.0 && std::isfinite(a->factor))) return false;
+    if (a->scaling >= DSV4_ROPE_BY_TURNS &&
+        !(a->original_len > 0.0 && std::isfinite(a->original_len) && a->beta_slow > 0.0 && a->beta_fast > a->beta_slow &&
+          std::isfinite(a->beta_fast)))
+        return false;
+    if (a->scaling == DSV4_ROPE_BY_INDEX && a->rope_theta <= 1.0) return false;
+    if (a->tokens == 0) return true;                 // nothing to do: no array is looked at
+    if (!num_ok(a->pos, 8) || !opt_num_ok(a->slots, 8)) return false;
+    if (a->heads) {
+        if (!dev_ptr_ok(a->q) || !dev_ptr_ok(a->q_out) || !stride_ok(a->q_stride, a->heads, a->dim) ||
+            !stride_ok(a->q_out_stride, a->heads, a->dim))
+            return false;
+        if (a->q == a->q_out && a->q_stride != a->q_out_stride) return false;
+    } else if (a->q || a->q_out) {
+        return false;
+    }
+    if (a->kv_heads) {
+        if (!dev_ptr_ok(a->k) || !dev_ptr_ok(a->k_out) || !stride_ok(a->k_stride, a->kv_heads, a->dim)) return false;
+        if ((a->v == nullptr) != (a->v_out == nullptr) || (a->v && !a->slots)) return false;
+        if (a->v && (!dev_ptr_ok(a->v) || !dev_ptr_ok(a->v_out) || !stride_ok(a->v_stride, a->kv_heads, a->dim))) return false;
+        if (a->slots) {
+            if (a->page_size < 1 || a->page_size > 65536 || a->num_pages < 1 || a->k == a->k_out) return false;
+        } else {
+            if (!stride_ok(a->k_out_stride, a->kv_heads, a->dim)) return false;
+            if (a->k == a->k_out && a->k_stride != a->k_out_stride) return false;
+        }
+    } else if (a->k || a->v || a->k_out || a->v_out || a->slots) {
+        return false;
+    }
+    return true;
+}
+
 uint32_t* eword_of(void* ws) { return static_cast<uint32_t*>(ws); }
 uint8_t* body_of(void* ws) { return static_cast<uint8_t*>(ws) + kWsHeader; }
 
@@ -318,6 +374,7 @@ const char* dsv4_status_string(int status) {
         case DSV4_ERR_BAD_INDEX: return "an index outside the visible range was masked";
         case DSV4_ERR_TIMEOUT: return "a bounded device wait ran out";
         case DSV4_ERR_UNSUPPORTED: return "unsupported device (the library is built for sm_103 only)";
+        case DSV4_ERR_NO_PAGES: return "too few free pages for a sequence";
         default: return "unknown status";
     }
 }
@@ -554,6 +611,22 @@ int dsv4_paged_evict(const dsv4_paged_evict_args* a, void* ws, size_t ws_bytes, 
     return launch_paged_evict(*a, body_of(ws), eword_of(ws), reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t dsv4_paged_plan_workspace_size(const dsv4_paged_plan_args* a) { return a && paged_plan_sizes_ok(a) ? kWsHeader : 0; }
+
+int dsv4_paged_plan(const dsv4_paged_plan_args* a, void* ws, size_t ws_bytes, dsv4_stream_t stream) {
+    LaunchScope scope;
+    if (!paged_plan_ok(a) || !dev_ptr_ok(ws) || ws_bytes < dsv4_paged_plan_workspace_size(a)) return DSV4_ERR_INVALID_ARG;
+    if (int rc = device_check()) return rc;
+    return launch_paged_plan(*a, eword_of(ws), reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dsv4_rope(const dsv4_rope_args* a, dsv4_stream_t stream) {
+    LaunchScope scope;
+    if (!rope_ok(a)) return DSV4_ERR_INVALID_ARG;
+    if (int rc = device_check()) return rc;
+    return launch_rope(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int dsv4_read_error_word(void* ws, dsv4_stream_t stream, uint32_t* out) {
     if (!dev_ptr_ok(ws) || !out) return DSV4_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -565,6 +638,7 @@ int dsv4_read_error_word(void* ws, dsv4_stream_t stream, uint32_t* out) {
     *out = v;
     if (v & DSV4_EWORD_TIMEOUT) return DSV4_ERR_TIMEOUT;
     if (v & DSV4_EWORD_BAD_INDEX) return DSV4_ERR_BAD_INDEX;
+    if (v & DSV4_EWORD_NO_PAGES) return DSV4_ERR_NO_PAGES;
     return DSV4_OK;
 }
 

@@ -50,12 +50,14 @@ enum {
     DSV4_ERR_LAUNCH = 2,      /* a kernel launch failed */
     DSV4_ERR_BAD_INDEX = 3,   /* device: an index outside [0, visible) was masked */
     DSV4_ERR_TIMEOUT = 4,     /* device: a bounded wait ran out; the kernel returned early */
-    DSV4_ERR_UNSUPPORTED = 5  /* the device is not sm_103 (the only code the library holds) */
+    DSV4_ERR_UNSUPPORTED = 5, /* the device is not sm_103 (the only code the library holds) */
+    DSV4_ERR_NO_PAGES = 6     /* device: a sequence of dsv4_paged_plan found too few free pages */
 };
 
 /* Device error word bits (dsv4_read_error_word). */
 #define DSV4_EWORD_BAD_INDEX 0x1u
 #define DSV4_EWORD_TIMEOUT   0x2u
+#define DSV4_EWORD_NO_PAGES  0x4u
 
 /* ---------------------------------------------------------------------------------------
  * Stage 1. Block compressor + RMSNorm + partial RoPE.
@@ -326,11 +328,13 @@ int dsv4_quantize_rows_fp8(const void* x, int rows, int dim, void* q, float* sca
 /* ---------------------------------------------------------------------------------------
  * The paged cache. A pool of pages [num_pages, page_size, kv_heads, dim] holds the rows of many
  * sequences; row r of sequence s is page block_table[s, r / page_size], slot r % page_size, and
- * kv_len[s] rows are valid. Four calls work on it:
+ * kv_len[s] rows are valid. These calls work on it:
  *   dsv4_norm_rope_append     norm and rotate a step's queries and keys, append the rows
  *   dsv4_paged_attn           attention of each sequence's newest tokens over its rows
  *   dsv4_paged_attn_weights   the attention weight each row received, accumulated
  *   dsv4_paged_evict          keep the rows of most weight, compact the rest away
+ *   dsv4_paged_plan           a step's offsets, positions, slots and new pages from its lengths
+ *   dsv4_rope                 rotate a step's queries and keys, append the rows
  * Values are the key rows themselves (v_pages NULL: shared-KV attention, as in stage 4), or a
  * second pool of the same shape. The pages have dense per-sequence buffers ([A]
  * PERFORMANCE_AUDIT.md, the sliding-window cache; ARCHITECTURE_AND_MEMORY_AUDIT.md PART 2);
@@ -469,6 +473,96 @@ typedef struct dsv4_paged_evict_args {
 
 size_t dsv4_paged_evict_workspace_size(const dsv4_paged_evict_args* args);
 int dsv4_paged_evict(const dsv4_paged_evict_args* args, void* ws, size_t ws_bytes, dsv4_stream_t stream);
+
+/* The bookkeeping of a step, formed on the device from the requests' lengths: cumulative offsets,
+ * positions and slots of the new tokens, the block tables' new entries, and the stack of free
+ * pages. Sequence s has kv_len[s] rows in its first held[s] table entries and gets new_len[s] more;
+ * afterwards it holds want = ceil((kv_len + new_len) / page_size) pages:
+ *   held > want (rows were evicted, a request ended): the entries from max(want, shared[s]) on go
+ *     back to the stack, in order of sequence and entry (they stay in the table, where nothing
+ *     reads them). The first shared[s] entries belong to a prefix of several sequences and never go back.
+ *   held < want: the missing pages are taken from the top of the stack (the last entry first, the
+ *     pages just given back included), in order of sequence and row.
+ * A sequence for which the stack holds too few pages, counting all pages that sequences before it
+ * asked for, is not served: it keeps its rows and pages, its tokens get slot -1, and
+ * DSV4_EWORD_NO_PAGES is set. Sequences that need no page are always served.
+ * Token t of sequence s (tokens lie one sequence after the other) gets seq s, position next_pos[s] +
+ * t (next_pos NULL: kv_len[s] + t) and the slot page * page_size + slot in the page of row
+ * kv_len[s] + t, as dsv4_norm_rope_append and dsv4_rope take it; tokens past the last sequence's get
+ * slot -1, position 0 and seq -1, up to total_q. cu_q and kv_len_out are what dsv4_paged_attn takes.
+ * The *_out arrays may be the arrays they follow. Negative lengths and counts out of their arrays
+ * are clamped, a sequence whose tokens or pages do not fit total_q or max_pages is not served, a page
+ * number outside the pool gives slot -1; these set DSV4_EWORD_BAD_INDEX. batch: 0..2048. */
+typedef struct dsv4_paged_plan_args {
+    const int32_t* new_len;   /* int32 [batch] tokens of this step, or NULL: 0 (pages are only given back) */
+    const int32_t* kv_len;    /* int32 [batch] rows before the step                           */
+    const int32_t* held;      /* int32 [batch] table entries in use                           */
+    const int32_t* shared;    /* int32 [batch] entries that never go back, or NULL: 0         */
+    const int64_t* next_pos;  /* int64 [batch] position of the next token, or NULL            */
+    int32_t* block_table;     /* int32 [batch, max_pages]: taken pages are entered            */
+    int32_t* free_pages;      /* int32 [free_cap] the stack                                   */
+    const int32_t* free_count;/* int32 [1] its height                                         */
+    int32_t* cu_q;            /* int32 [batch + 1]                                            */
+    int32_t* kv_len_out;      /* int32 [batch]                                                */
+    int32_t* held_out;        /* int32 [batch]                                                */
+    int64_t* next_pos_out;    /* int64 [batch], or NULL when next_pos is                      */
+    int32_t* free_count_out;  /* int32 [1]                                                    */
+    int64_t* slots;           /* int64 [total_q]                                              */
+    int64_t* pos;             /* int64 [total_q], or NULL                                     */
+    int32_t* seq;             /* int32 [total_q], or NULL                                     */
+    int batch, total_q, page_size, num_pages, max_pages, free_cap;
+} dsv4_paged_plan_args;
+
+size_t dsv4_paged_plan_workspace_size(const dsv4_paged_plan_args* args);
+int dsv4_paged_plan(const dsv4_paged_plan_args* args, void* ws, size_t ws_bytes, dsv4_stream_t stream);
+
+/* Rotary positions alone, for queries and keys in one pass: pair j of the channels [first, first +
+ * rope_dim) of every head, (a, b) = channels first + (2j, 2j + 1) (layout 0) or first + (j, j +
+ * rope_dim / 2) (layout 1), becomes
+ *   (magnitude * (a cos t - b sin t), magnitude * (a sin t + b cos t)),  t = pos[token] * f_j
+ * (inverse = 1: -t, which is also the backward pass: the rotation's transpose); the other channels
+ * are copied. With f = rope_theta^(-2j / rope_dim), f_j is by `scaling`
+ *   DSV4_ROPE_PLAIN     f
+ *   DSV4_ROPE_LINEAR    f / factor
+ *   DSV4_ROPE_BY_TURNS  w f + (1 - w) f / factor, w = clamp((original_len f / 2 pi - beta_slow) /
+ *                       (beta_fast - beta_slow), 0, 1): channels that turn often in the original
+ *                       context keep their frequency
+ *   DSV4_ROPE_BY_INDEX  the same with w = 1 - clamp((j - lo) / (hi - lo), 0, 1), lo (hi) the index,
+ *                       rounded down (up) and cut to 0 .. rope_dim - 1, that makes beta_fast
+ *                       (beta_slow) turns: rope_dim ln(original_len / (2 pi beta)) / (2 ln theta);
+ *                       hi - lo is 0.001 where it would not be positive
+ * (B. Peng, J. Quesnelle, H. Fan, E. Shippole, "YaRN: Efficient Context Window Extension of Large
+ * Language Models", 2023.) Rotated keys go to k_out, token by token, or, with slots, to row slots[t]
+ * of a pool [num_pages, page_size, kv_heads, dim] as in dsv4_norm_rope_append, v beside them
+ * unchanged (a token whose slot is negative or past the pool stores nothing). q_out may be q and
+ * k_out, without slots, k. Two tokens must not name the same slot.
+ * Arithmetic: fp32 (angles in fp64), one rounding to the type. */
+enum { DSV4_ROPE_PLAIN = 0, DSV4_ROPE_LINEAR = 1, DSV4_ROPE_BY_TURNS = 2, DSV4_ROPE_BY_INDEX = 3 };
+enum { DSV4_BF16 = 0, DSV4_FP16 = 1, DSV4_FP32 = 2 };
+typedef struct dsv4_rope_args {
+    const void* q;            /* [tokens, heads, dim], or NULL with heads = 0                 */
+    const void* k;            /* [tokens, kv_heads, dim], or NULL with kv_heads = 0           */
+    const void* v;            /* [tokens, kv_heads, dim], or NULL; only with slots            */
+    void* q_out;              /* [tokens, heads, dim]                                         */
+    void* k_out;              /* [tokens, kv_heads, dim], or the pool with slots              */
+    void* v_out;              /* a pool like k_out, or NULL when v is                         */
+    const int64_t* slots;     /* int64 [tokens], or NULL                                      */
+    const int64_t* pos;       /* int64 [tokens]                                               */
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+                              /* elements from token to token: multiples of 8, >= heads * dim (k_out_stride: without slots) */
+    int tokens, heads, kv_heads;
+    int dim;                  /* a multiple of 8, 8..1024                                     */
+    int page_size, num_pages; /* with slots                                                   */
+    int dtype;                /* DSV4_BF16, DSV4_FP16 or DSV4_FP32, of q, k, v and the outputs */
+    int rope_dim;             /* even, 2..min(dim, 512)                                       */
+    int first;                /* 0..dim - rope_dim; even in layout 0                          */
+    int layout, inverse;
+    int scaling;              /* DSV4_ROPE_*                                                  */
+    double rope_theta, factor, original_len, beta_fast, beta_slow;
+    double magnitude;         /* 1 without                                                    */
+} dsv4_rope_args;
+
+int dsv4_rope(const dsv4_rope_args* args, dsv4_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
  * Test support: running the bounded-wait path on purpose. Not for a serving path.
