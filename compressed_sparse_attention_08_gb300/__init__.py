@@ -22,5 +22,6 @@ from ._abi import (  # noqa: F401
     dsv4_paged_attn_workspace_size, paged_weights_args, dsv4_paged_attn_weights,
     dsv4_paged_attn_weights_workspace_size, paged_evict_args, dsv4_paged_evict,
     dsv4_paged_evict_workspace_size, paged_plan_args, dsv4_paged_plan, dsv4_paged_plan_workspace_size,
-    rope_args, dsv4_rope, DSV4_ERR_NO_PAGES, DSV4_EWORD_NO_PAGES,
+    rope_args, dsv4_rope, DSV4_ERR_NO_PAGES, DSV4_EWORD_NO_PAGES, paged_prefix_args, dsv4_paged_prefix_attn,
+    dsv4_paged_prefix_attn_workspace_size, DSV4_WAIT_FAULT_PAGED_PREFIX,
 )

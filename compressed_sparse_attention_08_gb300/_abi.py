@@ -27,6 +27,7 @@ DSV4_WAIT_FAULT_SCORER_STAGE = 1
 DSV4_WAIT_FAULT_ATTN_QUERY = 2
 DSV4_WAIT_FAULT_PAGED_ATTN = 4
 DSV4_WAIT_FAULT_PAGED_WEIGHTS = 8
+DSV4_WAIT_FAULT_PAGED_PREFIX = 32
 
 EXPORTED_SYMBOLS = (
     "dsv4_compress", "dsv4_compress_step", "dsv4_quantize_rows_fp8", "dsv4_indexer_topk_workspace_size",
@@ -40,6 +41,7 @@ EXPORTED_SYMBOLS = (
     "dsv4_paged_attn_weights_workspace_size", "dsv4_paged_attn_weights",
     "dsv4_paged_evict_workspace_size", "dsv4_paged_evict",
     "dsv4_paged_plan_workspace_size", "dsv4_paged_plan", "dsv4_rope",
+    "dsv4_paged_prefix_attn_workspace_size", "dsv4_paged_prefix_attn",
 )
 
 P = ctypes.c_void_p
@@ -135,6 +137,15 @@ class RopeArgs(ctypes.Structure):
                 ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double)]
 
 
+class PagedPrefixArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("k_pages", P), ("v_pages", P), ("block_table", P), ("cu_q", P),
+                ("kv_len", P), ("prefix_len", P), ("group_start", P), ("sink", P), ("out", P),
+                ("lse", P), ("out_rope_pos", P), ("q_stride", L), ("batch", I), ("groups", I),
+                ("total_q", I), ("heads", I), ("kv_heads", I), ("dim", I), ("page_size", I),
+                ("num_pages", I), ("max_pages", I), ("scale", ctypes.c_float),
+                ("out_rope_dim", I), ("out_rope_theta", ctypes.c_double)]
+
+
 class CsaArgs(ctypes.Structure):
     _fields_ = [("compress_kv", ctypes.POINTER(CompressArgs)),
                 ("compress_keys", ctypes.POINTER(CompressArgs)),
@@ -198,7 +209,8 @@ def library():
         lib.dsv4_rope.argtypes = [ctypes.POINTER(RopeArgs), P]
         lib.dsv4_rope.restype = I
         for name, st in (("dsv4_paged_attn", PagedAttnArgs), ("dsv4_paged_attn_weights", PagedWeightsArgs),
-                         ("dsv4_paged_evict", PagedEvictArgs), ("dsv4_paged_plan", PagedPlanArgs)):
+                         ("dsv4_paged_evict", PagedEvictArgs), ("dsv4_paged_plan", PagedPlanArgs),
+                         ("dsv4_paged_prefix_attn", PagedPrefixArgs)):
             size = getattr(lib, name + "_workspace_size")
             size.argtypes = [ctypes.POINTER(st)]
             size.restype = ctypes.c_size_t
@@ -842,3 +854,37 @@ def rope_args(q, q_out, pos, *, k=None, k_out=None, v=None, v_out=None, slots=No
 def dsv4_rope(args, *, stream=None):
     """Rotary positions (and the append to the pages), from a rope_args struct."""
     _call(library().dsv4_rope, args, stream, "dsv4_rope")
+
+
+def paged_prefix_args(q, out, k_pages, block_table, cu_q, kv_len, prefix_len, *, group_start=None, v_pages=None,
+                      sink=None, lse=None, scale=None, out_rope_pos=None, out_rope_dim=64, out_rope_theta=10000.0):
+    """q, out, pages, table, lengths and options as paged_attn_args; prefix_len int32 [groups]: the rows that the
+    sequences group_start[g] .. group_start[g + 1] - 1 (int32 [groups + 1]; None: one group of all) share."""
+    bf16, f32, i32, i64 = _dt()
+    qp, qs, T, H, D, B, n, ps, KV, mp = _paged(q, k_pages, block_table, cu_q, kv_len)
+    _shape(out, (T, H, D), "out")
+    _shape(v_pages, k_pages.shape, "v_pages")
+    _shape(sink, (H,), "sink")
+    _shape(lse, (T, H), "lse")
+    _shape(out_rope_pos, (T,), "out_rope_pos")
+    G = prefix_len.shape[0]
+    _shape(prefix_len, (G,), "prefix_len")
+    _shape(group_start, (G + 1,), "group_start")
+    if group_start is None and G != 1:
+        raise ValueError("several groups need group_start")
+    a = _struct(PagedPrefixArgs, qp, _ptr(k_pages, bf16, "k_pages"), _ptr(v_pages, bf16, "v_pages", True),
+                _ptr(block_table, i32, "block_table"), _ptr(cu_q, i32, "cu_q"), _ptr(kv_len, i32, "kv_len"),
+                _ptr(prefix_len, i32, "prefix_len"), _ptr(group_start, i32, "group_start", True), _ptr(sink, f32, "sink", True),
+                _ptr(out, bf16, "out"), _ptr(lse, f32, "lse", True), _ptr(out_rope_pos, i64, "out_rope_pos", True), qs, B, G, T,
+                H, KV, D, ps, n, mp, 1.0 / math.sqrt(D) if scale is None else scale,
+                out_rope_dim if out_rope_pos is not None else 0, out_rope_theta)
+    return _held(a, q, out, k_pages, v_pages, block_table, cu_q, kv_len, prefix_len, group_start, sink, lse, out_rope_pos)
+
+
+def dsv4_paged_prefix_attn_workspace_size(args):
+    return int(library().dsv4_paged_prefix_attn_workspace_size(ctypes.byref(args)))
+
+
+def dsv4_paged_prefix_attn(args, ws, *, stream=None):
+    """Attention of the new tokens where groups of sequences share their first rows, from a paged_prefix_args struct."""
+    _call(library().dsv4_paged_prefix_attn, args, stream, "dsv4_paged_prefix_attn", ws)

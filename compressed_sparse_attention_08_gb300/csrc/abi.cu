@@ -244,6 +244,27 @@ bool paged_plan_ok(const dsv4_paged_plan_args* a) {
            num_ok(a->held_out, 4);
 }
 
+bool paged_prefix_sizes_ok(const dsv4_paged_prefix_args* a) {
+    return a->batch >= 0 && a->batch <= kPagedMaxBatch && a->groups >= 1 && a->groups <= kPagedMaxBatch && heads_ok(a->heads, a->kv_heads) &&
+           paged_dim_ok(a->dim) && a->total_q >= 0 && a->total_q <= (1 << 24);
+}
+
+bool paged_prefix_ok(const dsv4_paged_prefix_args* a) {
+    if (!a || !paged_prefix_sizes_ok(a) || !paged_ok(a->batch, a->kv_heads, a->dim, a->page_size, a->num_pages, a->max_pages)) return false;
+    if (!stride_ok(a->q_stride, a->heads, a->dim) || !std::isfinite(a->scale)) return false;
+    if (a->batch == 0 || a->total_q == 0) return true;   // nothing to do: no array is looked at
+    if (!dev_ptr_ok(a->q) || !dev_ptr_ok(a->k_pages) || !opt_ptr_ok(a->v_pages) || !num_ok(a->block_table, 4) ||
+        !num_ok(a->cu_q, 4) || !num_ok(a->kv_len, 4) || !num_ok(a->prefix_len, 4) || !opt_num_ok(a->group_start, 4) ||
+        !opt_num_ok(a->sink, 4) || !dev_ptr_ok(a->out) || !opt_num_ok(a->lse, 4) || !opt_num_ok(a->out_rope_pos, 8))
+        return false;
+    if (!a->group_start && a->groups != 1) return false;
+    if (a->out_rope_pos &&
+        (a->out_rope_dim < 2 || (a->out_rope_dim & 1) || a->out_rope_dim > a->dim || a->out_rope_dim > 128 ||
+         !std::isfinite(a->out_rope_theta) || a->out_rope_theta <= 0.0))
+        return false;
+    return true;
+}
+
 bool rope_ok(const dsv4_rope_args* a) {
     if (!a || a->tokens < 0 || a->tokens > (1 << 24) || a->heads < 0 || a->heads > 1024 || a->kv_heads < 0 || a->kv_heads > 1024)
         return false;
@@ -384,7 +405,7 @@ int dsv4_last_launch_count(void) { return g_last_launches; }
 int dsv4_test_wait_fault(int which, uint32_t wait_limit_us) {
     const bool known = which == DSV4_WAIT_FAULT_NONE || which == DSV4_WAIT_FAULT_SCORER_STAGE ||
                        which == DSV4_WAIT_FAULT_ATTN_QUERY || which == DSV4_WAIT_FAULT_PAGED_ATTN ||
-                       which == DSV4_WAIT_FAULT_PAGED_WEIGHTS;
+                       which == DSV4_WAIT_FAULT_PAGED_WEIGHTS || which == DSV4_WAIT_FAULT_PAGED_PREFIX;
     if (!known || wait_limit_us > 2000000u) return DSV4_ERR_INVALID_ARG;
     g_wait_limit_us.store(wait_limit_us);
     g_wait_fault.store(which);
@@ -618,6 +639,18 @@ int dsv4_paged_plan(const dsv4_paged_plan_args* a, void* ws, size_t ws_bytes, ds
     if (!paged_plan_ok(a) || !dev_ptr_ok(ws) || ws_bytes < dsv4_paged_plan_workspace_size(a)) return DSV4_ERR_INVALID_ARG;
     if (int rc = device_check()) return rc;
     return launch_paged_plan(*a, eword_of(ws), reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dsv4_paged_prefix_attn_workspace_size(const dsv4_paged_prefix_args* a) {
+    if (!a || !paged_prefix_sizes_ok(a)) return 0;
+    return kWsHeader + paged_prefix_ws_bytes(*a);
+}
+
+int dsv4_paged_prefix_attn(const dsv4_paged_prefix_args* a, void* ws, size_t ws_bytes, dsv4_stream_t stream) {
+    LaunchScope scope;
+    if (!paged_prefix_ok(a) || !dev_ptr_ok(ws) || ws_bytes < dsv4_paged_prefix_attn_workspace_size(a)) return DSV4_ERR_INVALID_ARG;
+    if (int rc = device_check()) return rc;
+    return launch_paged_prefix(*a, body_of(ws), eword_of(ws), reinterpret_cast<cudaStream_t>(stream));
 }
 
 int dsv4_rope(const dsv4_rope_args* a, dsv4_stream_t stream) {

@@ -83,7 +83,8 @@ size_t attn_ws_bytes(const dsv4_attn_args& a);
 int launch_attn(const dsv4_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
 
 
-// The paged cache (norm_rope.cu, paged_attn.cu, paged_weights.cu, paged_evict.cu, paged_plan.cu, rope.cu).
+// The paged cache (norm_rope.cu, paged_attn.cu, paged_weights.cu, paged_evict.cu, paged_plan.cu, rope.cu,
+// paged_prefix.cu).
 int launch_norm_rope(const dsv4_norm_rope_args& a, cudaStream_t stream);
 size_t paged_attn_ws_bytes(const dsv4_paged_attn_args& a);
 int launch_paged_attn(const dsv4_paged_attn_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
@@ -93,6 +94,8 @@ size_t paged_evict_ws_bytes(const dsv4_paged_evict_args& a);
 int launch_paged_evict(const dsv4_paged_evict_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
 int launch_paged_plan(const dsv4_paged_plan_args& a, uint32_t* eword, cudaStream_t stream);
 int launch_rope(const dsv4_rope_args& a, cudaStream_t stream);
+size_t paged_prefix_ws_bytes(const dsv4_paged_prefix_args& a);
+int launch_paged_prefix(const dsv4_paged_prefix_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
 struct PagedGeom;
 PagedGeom paged_geom(const int32_t* table, const int32_t* cu_q, const int32_t* kv_len, int batch, int total_q, int max_pages,
                      int page_size, int num_pages, int heads, int kv_heads, int window);

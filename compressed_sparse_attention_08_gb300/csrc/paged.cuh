@@ -33,7 +33,10 @@ __device__ __forceinline__ float key_to_float(uint32_t k) {
 
 constexpr int kUnit = 128;               // cache rows per unit
 
+struct PagedSeq { int q0, n, L; };       // first token, tokens, cache rows
+
 struct PagedGeom {
+    using Seq = PagedSeq;
     const int32_t* table;                // [batch, max_pages]
     const int32_t* cu_q;                 // [batch + 1]
     const int32_t* kv_len;               // [batch]
@@ -66,8 +69,6 @@ inline int paged_box_rows(int page_size) {
     return low < kUnit ? low : kUnit;
 }
 
-struct PagedSeq { int q0, n, L; };       // first token, tokens, cache rows
-
 // Counts outside their arrays are clamped, and `bad` is set.
 __device__ __forceinline__ PagedSeq paged_seq(const PagedGeom& g, int s, bool& bad) {
     const int a = g.cu_q[s], b = g.cu_q[s + 1], len = g.kv_len[s];
@@ -93,36 +94,49 @@ __device__ __forceinline__ int paged_tile_units(const PagedGeom& g, const PagedS
     return max((paged_hi(q, t1) + kUnit - 1) / kUnit - paged_lo(g, q, t0) / kUnit, 1);
 }
 
-struct PagedSched {
+// What the schedule asks of a line's geometry: how many sequences it has, tokens per tile, the tiles side by
+// side over the same tokens, and the lane exchange of what the units depend on.
+__device__ __forceinline__ int paged_count(const PagedGeom& g) { return g.batch; }
+__device__ __forceinline__ int paged_tokens(const PagedGeom& g) { return g.tpt; }
+__device__ __forceinline__ int paged_mult(const PagedGeom& g) { return g.KV * g.nhb; }
+__device__ __forceinline__ PagedSeq paged_shfl(const PagedSeq& q, int src) {
+    return PagedSeq{0, __shfl_sync(~0u, q.n, src), __shfl_sync(~0u, q.L, src)};
+}
+
+template <class Geom>
+struct PagedSchedOf {
     long long total, u0, u1;             // all units, this CTA's [u0, u1)
     int ge;                              // CTAs with work
     int s, tt, inner, k;                 // where u0 lies
-    PagedSeq q;                          // sequence s
+    typename Geom::Seq q;                // sequence s
 };
+using PagedSched = PagedSchedOf<PagedGeom>;
 
-// The share of worker `self` of `count`. Whole block of NT threads; `pref` is scratch for `batch` counts in shared memory. At least
+// The share of worker `self` of `count`. Whole block of NT threads; `pref` is scratch for a count per sequence in shared memory. At least
 // `min_units` units go to each worker with work. Returns with the result visible to the block.
-template <int NT>
-__device__ void paged_schedule(const PagedGeom& g, int self, int count, int min_units, long long* pref, PagedSched* out,
+template <int NT, class Geom>
+__device__ void paged_schedule(const Geom& g, int self, int count, int min_units, long long* pref, PagedSchedOf<Geom>* out,
                                uint32_t* err) {
+    using Seq = typename Geom::Seq;
+    const int batch = paged_count(g), tpt = paged_tokens(g);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int mult = g.KV * g.nhb;
+    const int mult = paged_mult(g);
     bool bad = false;
     // (up to 32 sequences per warp at a time, a lane each; the whole warp goes over a long one's tiles)
-    const int step = min((g.batch + NT / 32 - 1) / (NT / 32), 32);
-    for (int s0 = warp * step; s0 < g.batch; s0 += NT / 32 * step) {
+    const int step = min((batch + NT / 32 - 1) / (NT / 32), 32);
+    for (int s0 = warp * step; s0 < batch; s0 += NT / 32 * step) {
         const int s = s0 + lane;
-        const bool here = lane < step && s < g.batch;
-        PagedSeq q{0, 0, 0};
+        const bool here = lane < step && s < batch;
+        Seq q{};
         if (here) q = paged_seq(g, s, bad);
-        const int nt = (q.n + g.tpt - 1) / g.tpt;
+        const int nt = (q.n + tpt - 1) / tpt;
         long long units = 0;
         if (nt <= 4)
             for (int tt = 0; tt < nt; ++tt) units += paged_tile_units(g, q, tt);
         for (unsigned big = __ballot_sync(~0u, nt > 4); big; big &= big - 1) {
             const int src = __ffs(big) - 1;
-            const PagedSeq b{0, __shfl_sync(~0u, q.n, src), __shfl_sync(~0u, q.L, src)};
-            const int bnt = (b.n + g.tpt - 1) / g.tpt;
+            const Seq b = paged_shfl(q, src);
+            const int bnt = (b.n + tpt - 1) / tpt;
             long long u = 0;
             for (int tt = lane; tt < bnt; tt += 32) u += paged_tile_units(g, b, tt);
 #pragma unroll
@@ -135,16 +149,16 @@ __device__ void paged_schedule(const PagedGeom& g, int self, int count, int min_
     __syncthreads();
     if (warp == 0) {
         long long carry = 0;
-        for (int s0 = 0; s0 < g.batch; s0 += 32) {
+        for (int s0 = 0; s0 < batch; s0 += 32) {
             const int s = s0 + lane;
-            long long v = s < g.batch ? pref[s] : 0;
+            long long v = s < batch ? pref[s] : 0;
 #pragma unroll
             for (int w = 1; w < 32; w <<= 1) {
                 const long long o = __shfl_up_sync(~0u, v, w);
                 if (lane >= w) v += o;
             }
             v += carry;
-            if (s < g.batch) pref[s] = v;
+            if (s < batch) pref[s] = v;
             carry = __shfl_sync(~0u, v, 31);
         }
     }
@@ -153,25 +167,25 @@ __device__ void paged_schedule(const PagedGeom& g, int self, int count, int min_
     // tile of few units moves to the tile's end: a partial result costs about a unit's time on
     // either side, more than the imbalance of at most 2 units or 1/32 of a share.
     if (warp < 2) {
-        const long long T = g.batch > 0 ? pref[g.batch - 1] : 0;
+        const long long T = batch > 0 ? pref[batch - 1] : 0;
         const long long most = T / min_units < 1 ? 1 : T / min_units;
         const int ge = most < count ? static_cast<int>(most) : count;
         const long long share32 = T / ge / 32, small = share32 > 2 ? share32 : 2;
         const int c = self + warp;
         long long u = c < ge ? T * c / ge : T;
         int s = 0, tt = 0, inner = 0, k = 0;
-        PagedSeq q{0, 0, 0};
+        Seq q{};
         bool dummy = false;
         if (u == 0 && T > 0) q = paged_seq(g, 0, dummy);
         if (u < T && u > 0) {
-            int hi = g.batch - 1;                    // the first sequence whose units end past u
+            int hi = batch - 1;                    // the first sequence whose units end past u
             while (s < hi) {
                 const int mid = (s + hi) >> 1;
                 if (pref[mid] > u) hi = mid; else s = mid + 1;
             }
             const long long rem = u - (s ? pref[s - 1] : 0);
             q = paged_seq(g, s, dummy);
-            const int nt = (q.n + g.tpt - 1) / g.tpt;
+            const int nt = (q.n + tpt - 1) / tpt;
             long long cum = 0;
             for (int tt0 = 0; tt0 < nt; tt0 += 32) {
                 const int n = tt0 + lane < nt ? paged_tile_units(g, q, tt0 + lane) : 0;

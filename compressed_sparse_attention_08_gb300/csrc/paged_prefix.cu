@@ -1,0 +1,963 @@
+// Attention over a paged cache for groups of sequences that share their first rows.
+//
+//   s_j = scale q . k_j over the rows j the token sees,   m = max_j s_j (and the sink)
+//   o = sum_j e^(s_j - m) v_j / (sum_j e^(s_j - m) + e^(sink - m)),   lse = m + log(that sum)
+// as paged_attn.cu, whose sources hold here too; sharing a prefix is this library's own. The softmax
+// splits over any partition of the rows: with (m, l, o) of each part, l = sum e^(s - m) and o = sum e^(s - m) v,
+// the whole is sum_p e^(m_p - M) o_p / sum_p e^(m_p - M) l_p. So the prefix's rows meet all the group's tokens
+// together (the tokens of 32 sequences with 4 heads per KV head fill a tile of the tensor core, of which one
+// sequence's fill 4 rows of 128), each sequence's own rows meet its own tokens, and a merge joins them.
+//
+// The work is the line of units of paged.cuh over `groups + batch` sequences: first the groups' prefixes (rows
+// [0, P), all visible), then the sequences' own rows [P, ..). Every CTA takes an equal piece of the line.
+// A row of the tensor core's 128 lanes is a query (a token's head), its columns are cache rows:
+// S = Q K^T (128 queries x 128 rows, one step), O += P V with P in tensor memory, so a thread has one whole
+// row of scores: its maximum and sum need no other thread. Two steps are in flight, each with a buffer of
+// scores and a group of four softmax warps: while one group works on its scores, the tensor core does
+// the other's products. At 128 channels the steps are two tiles of queries over the same unit (when there
+// are that many queries), else two units; then both groups add to one O and hand each other the reference maximum.
+// Of 512 channels tensor memory holds 256 beside the scores, so a tile is taken twice, each time
+// with the scores over all channels and the product with half of V's (1.5 times the products' time).
+// Roles: warps 0, 2 and 3 move pages by TMA into a ring of slots of 128 rows x 128 channels, warp 1 issues
+// tcgen05.mma, warps 4-11 do the softmax and write the parts.
+#include <cmath>
+
+#include "internal.h"
+#include "paged.cuh"
+
+namespace dsv4 {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// A query's reference maximum moves only when a score exceeds it by more than kSpan (base-2 units): P =
+// 2^(s - m) then stays far inside the fp32 and bf16 range, and o does not depend on which m was used.
+constexpr float kSpan = 24.f;
+// The reference of a query that has seen nothing yet: finite, so that a score of -inf gives P = 0 beside it.
+constexpr float kUnset = -3.0e38f;
+
+// Sequence v of the line: the prefix of group v, or the rows of sequence v - groups behind its prefix.
+struct PrefixSeq {
+    int q0, n, L, lo;                    // first token, tokens, rows [lo, L)
+    int row;                             // of the block table
+    int own;                             // 1: a sequence's own rows (token t sees those below L - n + t + 1)
+};
+
+struct PrefixGeom {
+    PagedGeom p;
+    const int32_t* prefix_len;           // [groups]
+    const int32_t* group_start;          // [groups + 1] or null: one group of all
+    int groups, tiles, halves;           // tiles of queries per segment, passes over V's channels
+};
+
+// The geometry with the prefix lengths as they are used (by this CTA: each forms its own copy).
+struct PrefixLine {
+    using Seq = PrefixSeq;
+    const PrefixGeom& g;
+    const int32_t* plen;
+};
+
+__device__ __forceinline__ int group_first(const PrefixGeom& g, int i) {
+    const int b = g.group_start ? g.group_start[i] : (i ? g.p.batch : 0);
+    return min(max(b, 0), g.p.batch);
+}
+// The group of sequence s, or -1.
+__device__ __forceinline__ int group_of(const PrefixGeom& g, int s) {
+    if (!g.group_start) return 0;
+    int lo = 0, hi = g.groups;           // the last group that starts at or before s
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (g.group_start[mid] <= s) lo = mid; else hi = mid;
+    }
+    return group_first(g, lo) <= s && s < group_first(g, lo + 1) ? lo : -1;
+}
+
+__device__ __forceinline__ PrefixSeq paged_seq(const PrefixLine& l, int v, bool& bad) {
+    const PrefixGeom& g = l.g;
+    PrefixSeq q;
+    if (v < g.groups) {
+        const int a = group_first(g, v), b = group_first(g, v + 1), P = l.plen[v];
+        q.q0 = min(max(g.p.cu_q[a], 0), g.p.total_q);
+        q.n = P > 0 ? max(min(max(g.p.cu_q[b], 0), g.p.total_q) - q.q0, 0) : 0;
+        q.L = P;
+        q.lo = 0;
+        q.row = a;
+        q.own = 0;
+        return q;
+    }
+    const int s = v - g.groups;
+    const PagedSeq o = paged_seq(g.p, s, bad);
+    const int grp = group_of(g, s);
+    q.q0 = o.q0;
+    q.n = o.n;
+    q.L = o.L;
+    q.lo = grp >= 0 && o.n > 0 ? l.plen[grp] : 0;
+    q.row = s;
+    q.own = 1;
+    return q;
+}
+__device__ __forceinline__ int paged_count(const PrefixLine& l) { return l.g.groups + l.g.p.batch; }
+__device__ __forceinline__ int paged_tokens(const PrefixLine& l) { return l.g.p.tpt * l.g.tiles; }
+__device__ __forceinline__ int paged_mult(const PrefixLine& l) { return l.g.p.KV * l.g.p.nhb * l.g.halves; }
+__device__ __forceinline__ PrefixSeq paged_shfl(const PrefixSeq& q, int src) {
+    return PrefixSeq{0, __shfl_sync(~0u, q.n, src), __shfl_sync(~0u, q.L, src), __shfl_sync(~0u, q.lo, src), 0,
+                     __shfl_sync(~0u, q.own, src)};
+}
+__device__ __forceinline__ int seen(const PrefixSeq& q, int t) { return q.own ? max(q.L - q.n + t + 1, 0) : q.L; }
+__device__ __forceinline__ int unit_row0(const PrefixGeom& g, const PrefixSeq& q) { return q.lo & ~(g.p.br - 1); }
+__device__ __forceinline__ int segment_units(const PrefixGeom& g, const PrefixSeq& q, int t_last) {
+    return max((seen(q, t_last) - unit_row0(g, q) + kUnit - 1) / kUnit, 1);
+}
+__device__ __forceinline__ int paged_tile_units(const PrefixLine& l, const PrefixSeq& q, int tt) {
+    return segment_units(l.g, q, min((tt + 1) * paged_tokens(l), q.n) - 1);
+}
+
+// A segment of the line: up to `tiles` tiles of queries of one KV head, and this CTA's part of their units.
+struct PrefixSeg {
+    PrefixSeq q;
+    int t0, tok0, tn, nt;                // first token in the sequence and in the batch, tokens, tiles
+    int kvh, head0, hv, half;            // KV head, first query head, query heads, half of V's channels
+    int hi_u, hi_min;                    // rows below which some token sees, and every token
+    int row0, n, kb, ke;                 // first row of unit 0, the segment's units, this CTA's [kb, ke)
+};
+
+struct PrefixWalk {
+    const PrefixLine& l;
+    int s, tt, inner, k;
+    long long left;
+    PrefixSeq q;
+    __device__ PrefixWalk(const PrefixLine& line, const PagedSchedOf<PrefixLine>& sc)
+        : l(line), s(sc.s), tt(sc.tt), inner(sc.inner), k(sc.k), left(sc.u1 - sc.u0), q(sc.q) {}
+    __device__ bool next(PrefixSeg& o) {
+        if (left <= 0) return false;
+        const PrefixGeom& g = l.g;
+        const int tps = paged_tokens(l);
+        while (tt * tps >= q.n) {        // the next sequence with tokens
+            if (++s >= paged_count(l)) return false;
+            tt = 0;
+            bool dummy = false;
+            q = paged_seq(l, s, dummy);
+        }
+        o.q = q;
+        o.t0 = tt * tps;
+        o.tok0 = q.q0 + o.t0;
+        o.tn = min(tps, q.n - o.t0);
+        o.nt = o.tn > g.p.tpt ? 2 : 1;
+        const int hb = inner / g.halves;
+        o.half = inner - hb * g.halves;
+        o.kvh = hb / g.p.nhb;
+        const int blk = hb - o.kvh * g.p.nhb;
+        o.head0 = o.kvh * g.p.G + blk * g.p.hb;
+        o.hv = min(g.p.hb, g.p.G - blk * g.p.hb);
+        o.hi_u = seen(q, o.t0 + o.tn - 1);
+        o.hi_min = seen(q, o.t0);
+        o.row0 = unit_row0(g, q);
+        o.n = segment_units(g, q, o.t0 + o.tn - 1);
+        o.kb = k;
+        const long long take = left < o.n - k ? left : o.n - k;
+        o.ke = k + static_cast<int>(take);
+        left -= take;
+        k = 0;
+        if (++inner == paged_mult(l)) { inner = 0; ++tt; }
+        return true;
+    }
+};
+
+struct PrefixParams {
+    PrefixGeom g;
+    const float* sink;                   // [H] or null
+    __nv_bfloat16* out;                  // [total_q, H, D]
+    float* lse;                          // [total_q, H] or null
+    // Parts: of a segment's first units, by kind (0 prefix, 1 own rows), token and head; of a
+    // segment that goes on from another CTA, by CTA (each has one at most).
+    float4* home_ml;                     // [2][halves][total_q][H]: m, l, (CTA | CTAs << 8 | row << 16), whether there is a prefix
+    float2* cont_ml;                     // [CTAs][tiles * 128]
+    float* home_o;                       // [2][total_q][H][D]
+    float* cont_o;                       // [CTAs][tiles * 128][DV]
+    int32_t* plen;                       // [CTAs][groups]
+    uint32_t* err;                       // [CTAs]
+    float scale2;                        // scale * log2(e)
+    const int64_t* orp;                  // [total_q] or null
+    int or_pairs;
+    int shared, min_units;
+    int fault;                           // test control: a CTA's first query tile is never copied
+    unsigned long long wait_ns;
+    double or_freq[64];                  // theta^(-2j / out_rope_dim)
+};
+
+constexpr int kMaxSlots = 8, kSegs = 4;  // (the loads run at most two segments ahead of the outputs)
+struct PrefixCtl {
+    uint64_t q_full, q_empty, full[kMaxSlots], empty[kMaxSlots];
+    uint64_t seg_full[kSegs], s_full[2], p_full[2], pv_done[2], ref_done[2][4], l_ready[2][4], o_empty;
+    uint64_t drained;                    // products in flight when a wait ran out
+    uint32_t ring_end[kLoadWarps], seg_end[kLoadWarps];
+    PagedSchedOf<PrefixLine> sched;
+    PrefixSeg segs[kSegs];               // written by a load warp for the softmax
+    float ref[128];                      // reference maxima (base-2 units), where two groups share a tile
+    float l[2][128];
+    unsigned bad[8];
+    uint32_t tmem, err;
+    int abort;
+};
+
+template <int D_>
+struct XCfg {
+    static constexpr int D = D_;
+    static constexpr int TILES = D == 128 ? 2 : 1, HALVES = D == 512 ? 2 : 1;
+    static constexpr int DV = D == 512 ? 256 : D;            // V's channels of a pass
+    static constexpr int KS = D / 128, VS = DV / 128;        // slots of a K and a V tile
+    static constexpr int BOX = kUnit * 128, SLOT = 2 * BOX;  // 128 rows x 64 channels; x 128
+    static constexpr int QBOX = 128 * 128, QTILE = 2 * KS * QBOX, QB = TILES * QTILE;
+    static constexpr int ST_FIT = (232448 - static_cast<int>(sizeof(PrefixCtl)) - QB) / SLOT;
+    static constexpr int ST = ST_FIT > kMaxSlots ? kMaxSlots : ST_FIT;
+    static constexpr int OFF_Q = ST * SLOT, OFF_C = OFF_Q + QB, SMEM = OFF_C + static_cast<int>(sizeof(PrefixCtl));
+    static constexpr bool KEEP = HALVES == 1;                // a shared K/V tile stays for both products
+    static constexpr int OCOL = 256;                         // scores: columns 0 and 128; P over their first 64
+    static_assert(SMEM <= 232448 && ST >= 3 && (!KEEP || ST > 2 * KS) && OCOL + TILES * DV <= 512, "fits");
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16 (bf16 inputs, fp32 accumulate): A's rows are lanes, a column holds two k.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __noinline__ float2 out_rope_angle(double a) {
+    float sn, cs;
+    sincosf(reduced_angle(a), &sn, &cs);
+    return make_float2(cs, sn);
+}
+
+// The pages of a tile of kUnit rows, as paged_look.
+__device__ __forceinline__ PagedLook prefix_look(const PagedGeom& g, const PrefixSeg& sg, int row, int lane) {
+    PagedLook t{0, 0, false};
+    const int i = lane >> 1, r = row + i * g.br;
+    t.need = i < (kUnit >> g.br_log2) && r < sg.hi_u && r + g.br > sg.q.lo;
+    if (t.need) {
+        const int pg = r / g.page_size;
+        t.slot = r - pg * g.page_size;
+        t.page = g.table[static_cast<size_t>(sg.q.row) * g.max_pages + pg];
+    }
+    return t;
+}
+
+// The prefix lengths that the groups use: no row that some token of the group does not see. `s_len`: scratch.
+__device__ void prefix_lengths(const PrefixGeom& g, int* s_len, int32_t* out, uint32_t* err) {
+    bool bad = false;
+    const int cap = g.p.max_pages * g.p.page_size;
+    for (int i = threadIdx.x; i < g.groups; i += kThreads) {
+        const int x = g.prefix_len[i];
+        s_len[i] = min(max(x, 0), cap);
+        bad |= x != s_len[i];
+        if (g.group_start) {
+            const int a = g.group_start[i], b = g.group_start[i + 1];
+            bad |= a < 0 || b < a || b > g.p.batch;
+        }
+    }
+    __syncthreads();
+    for (int s = threadIdx.x; s < g.p.batch; s += kThreads) {
+        const PagedSeq q = paged_seq(g.p, s, bad);
+        const int grp = group_of(g, s);
+        if (grp >= 0 && q.n > 0 && q.L - q.n < s_len[grp]) atomicMin(&s_len[grp], max(q.L - q.n, 0));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < g.groups; i += kThreads) out[i] = s_len[i];
+    if (bad) atomicOr(err, DSV4_EWORD_BAD_INDEX);
+    __syncthreads();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PrefixParams p) {
+    using C = XCfg<D>;
+    constexpr int ST = C::ST, KS = C::KS, VS = C::VS;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    PrefixCtl& ctl = *reinterpret_cast<PrefixCtl*>(sm + C::OFF_C);
+    uint8_t* sQ = sm + C::OFF_Q;
+    volatile int* abort_flag = &ctl.abort;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int worker = blockIdx.x, workers = gridDim.x;
+    if (tid == 0) {
+        tma_prefetch_desc(&qmap);
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+        mbar_init(&ctl.q_full, kLoadWarps);
+        mbar_init(&ctl.q_empty, 1);
+        for (int i = 0; i < ST; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.s_full[i], 1);
+            mbar_init(&ctl.p_full[i], 4);
+            mbar_init(&ctl.pv_done[i], 1);
+            for (int j = 0; j < 4; ++j) { mbar_init(&ctl.ref_done[i][j], 1); mbar_init(&ctl.l_ready[i][j], 1); }
+        }
+        for (int i = 0; i < kSegs; ++i) mbar_init(&ctl.seg_full[i], 1);
+        mbar_init(&ctl.o_empty, 8);
+        mbar_init(&ctl.drained, 1);
+        ctl.abort = 0;
+        ctl.err = 0;
+        fence_barrier_init();
+    }
+    if (warp == 2) tmem_alloc(&ctl.tmem, 512);
+    pdl_trigger();
+    pdl_wait();                          // lengths, queries and rows may come from the kernel before
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    int32_t* plen = p.plen + static_cast<size_t>(worker) * p.g.groups;
+    prefix_lengths(p.g, reinterpret_cast<int*>(sm), plen, &ctl.err);
+    const PrefixLine line{p.g, plen};
+    paged_schedule<kThreads>(line, worker, workers, p.min_units, reinterpret_cast<long long*>(sm), &ctl.sched, &ctl.err);
+    // the schedule's scratch is overwritten by TMA next
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+
+    const PagedGeom& g = p.g.p;
+    const PagedSchedOf<PrefixLine>& sched = ctl.sched;
+    const bool keep = C::KEEP && p.shared;               // K rows stay in place as V
+    const uint32_t units = static_cast<uint32_t>(sched.u1 - sched.u0);
+    if (warp == 0 || warp == 2 || warp == 3) {
+        // ---------------------------------------------------------------- pages and queries
+        // Three warps walk the same slots and take them in turn. Order: as the products need them, K0 V0 K1
+        // V1 .. with two tiles of queries, K0 K1 V0 K2 V1 .. with one, K0 K1 .. where a tile is both.
+        const int mine = warp == 0 ? 0 : warp - 1;
+        PrefixWalk w(line, sched);
+        PrefixSeg sg;
+        const uint32_t qtile = static_cast<uint32_t>(g.hb) * g.tpt * D * 2;
+        const int piece = lane >> 1, box = lane & 1;
+        uint32_t ring = 0, seg = 0;
+        bool dead = false, more = w.next(sg);
+        PagedLook cur{0, 0, false}, prev{0, 0, false};
+        if (more) cur = prefix_look(g, sg, sg.row0 + sg.kb * kUnit, lane);
+        int k = more ? sg.kb : 0;
+        auto load = [&](const CUtensorMap* map, const PagedLook& t, int slots, int ch0, int kvh, int unit) {
+            const PagedBoxes bx = paged_boxes(g, t);
+            const uint32_t bytes = static_cast<uint32_t>(__popc(bx.ok)) * g.br * 128;
+#pragma unroll 1
+            for (int mt = 0; mt < slots; ++mt, ++ring) {
+                if (ring % kLoadWarps != static_cast<uint32_t>(mine)) continue;
+                const uint32_t slot = ring % ST;
+                if (ring >= ST)
+                    dead = __any_sync(~0u, !mbar_wait(&ctl.empty[slot], (ring / ST - 1) & 1, abort_flag, p.wait_ns));
+                if (dead) return;
+                if (lane == 0) {
+                    if (mt == 0 && unit >= 0) {
+                        ctl.bad[unit & 7] = bx.bad;
+                        if (bx.bad) atomicOr(&ctl.err, DSV4_EWORD_BAD_INDEX);
+                    }
+                    if (bytes) mbar_arrive_expect_tx(&ctl.full[slot], bytes);
+                    else mbar_arrive(&ctl.full[slot]);
+                }
+                __syncwarp();
+                if ((bx.ok >> lane) & 1)
+                    tma_load_4d(sm + slot * C::SLOT + box * C::BOX + piece * g.br * 128, map, &ctl.full[slot],
+                                ch0 + mt * 128 + box * 64, kvh, t.slot, t.page);
+            }
+        };
+        for (int u = 0; !dead && more; ++u) {
+            if (k == sg.kb) {                        // a new segment
+                if (seg > 0) dead = __any_sync(~0u, !mbar_wait(&ctl.q_empty, (seg - 1) & 1, abort_flag, p.wait_ns));
+                if (dead) break;
+                if (lane == 0) {
+                    if (mine == 0) {
+                        ctl.segs[seg % kSegs] = sg;
+                        mbar_arrive(&ctl.seg_full[seg % kSegs]);
+                    }
+                    const bool skip = p.fault && seg == 0;
+                    if (!skip && mine == 0) mbar_arrive_expect_tx(&ctl.q_full, qtile * sg.nt);
+                    else if (!skip) mbar_arrive(&ctl.q_full);
+#pragma unroll 1
+                    for (int b = skip ? 4 * KS : mine; b < 2 * KS * sg.nt; b += kLoadWarps) {
+                        const int tile = b >= 2 * KS ? 1 : 0, c = b - tile * 2 * KS;
+                        tma_load_3d(sQ + b * C::QBOX, &qmap, &ctl.q_full, c * 64, sg.head0, sg.tok0 + tile * g.tpt);
+                    }
+                }
+                ++seg;
+            }
+            // the pages of the next unit are looked up while this one's copies wait
+            const int kvh = sg.kvh, v0 = sg.half * 256;
+            const bool first = k == sg.kb, last = k + 1 == sg.ke, two = sg.nt == 2;
+            PagedLook next{0, 0, false};
+            if (++k >= sg.ke) {
+                more = w.next(sg);
+                k = more ? sg.kb : 0;
+            }
+            if (more) next = prefix_look(g, sg, sg.row0 + k * kUnit, lane);
+            load(&kmap, cur, KS, 0, kvh, u);
+            if (!keep) {
+                if (two) {
+                    if (!dead) load(&vmap, cur, VS, v0, kvh, -1);
+                } else {
+                    if (!dead && !first) load(&vmap, prev, VS, v0, kvh, -1);
+                    if (!dead && last) load(&vmap, cur, VS, v0, kvh, -1);
+                }
+            }
+            prev = cur;
+            cur = next;
+        }
+        if (lane == 0) {
+            ctl.ring_end[mine] = ring;
+            ctl.seg_end[mine] = seg;
+            if (dead) {
+                atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
+                ctl.abort = 1;
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- tensor core
+        // Steps (unit, tile) in order; the product with V of step j - 2 comes before the scores of step j, whose
+        // buffer holds that step's P (the tensor core does a thread's products in the order of their issue).
+        PrefixWalk w(line, sched);
+        PrefixSeg sg;
+        uint32_t u = 0, seg = 0, ring0 = 0, step0 = 0;   // units, segments, slots and steps before this segment
+        bool dead = false;
+        const bool one = elect_one();
+        // (the warp stays together: a wait that runs out does so for all lanes)
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return !__any_sync(~0u, !mbar_wait(bar, parity & 1, abort_flag, p.wait_ns)); };
+        const uint32_t q0 = smem_u32(sQ), t0 = smem_u32(sm);
+        const uint32_t idS = idesc_bf16_f32(128, kUnit), idO = idesc_bf16_f32(128, 128) | (1u << 16);
+        while (!dead && w.next(sg)) {
+            dead = !wait(&ctl.q_full, seg);
+            const uint32_t n = sg.ke - sg.kb, nt = sg.nt, steps = n * nt;
+            auto k_slot = [&](uint32_t x) {
+                return ring0 + (keep ? x * KS : nt == 2 ? x * (KS + VS) : x * KS + (x > 0 ? x - 1 : 0) * VS);
+            };
+            auto v_slot = [&](uint32_t x) {
+                return ring0 + (keep ? x * KS : nt == 2 ? x * (KS + VS) + KS : min(x + 2, n) * KS + x * VS);
+            };
+            for (uint32_t j = 0; j < steps + 2 && !dead; ++j) {
+                if (j >= 2) {                        // O += P V
+                    const uint32_t i = step0 + j - 2, x = nt == 2 ? (j - 2) >> 1 : j - 2, tile = nt == 2 ? j & 1 : 0;
+                    const bool last_use = tile + 1 == nt;
+                    if (j < 2 + nt && tile == 0 && seg > 0) dead = !wait(&ctl.o_empty, seg - 1);
+                    dead = dead || !wait(&ctl.p_full[i & 1], i >> 1);
+                    if (dead) break;
+                    uint32_t r = v_slot(x);
+                    const int j0 = sg.row0 + (sg.kb + static_cast<int>(x)) * kUnit;
+                    const unsigned bad = *reinterpret_cast<volatile unsigned*>(&ctl.bad[(u + x) & 7]);
+                    if (tile == 0 && (j0 < sg.q.lo || j0 + kUnit > sg.hi_u || bad)) {
+                        // Rows that no token sees hold anything: as V they must not meet P = 0.
+                        for (int s = 0; s < VS && !dead; ++s) dead = !wait(&ctl.full[(r + s) % ST], (r + s) / ST);
+                        if (dead) break;
+                        const int z0 = max(sg.q.lo - j0, 0), z1 = max(sg.hi_u - j0, 0);
+                        for (int row = 0; row < kUnit; ++row) {
+                            if (row >= z0 && row < z1 && !paged_bad_row(g, bad, row)) continue;
+                            for (int c = lane; c < VS * 16; c += 32) {
+                                const uint32_t slot = (r + (c >> 4)) % ST;
+                                *reinterpret_cast<uint4*>(sm + slot * C::SLOT + ((c >> 3) & 1) * C::BOX + row * 128 + (c & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int s = 0; s < VS; ++s, ++r) {
+                        const uint32_t slot = r % ST;
+                        dead = !wait(&ctl.full[slot], r / ST);
+                        if (dead) break;
+                        tc_fence_after();
+                        const uint64_t b = sdesc_mnmajor_sw128(t0 + slot * C::SLOT, C::BOX, 1024u);
+                        const uint32_t d = tmem + C::OCOL + tile * C::DV + s * 128, a = tmem + (i & 1) * 128;
+                        if (one) {
+#pragma unroll
+                            for (int kk = 0; kk < kUnit / 16; ++kk)
+                                umma_bf16_ts(d, a + kk * 8, b + kk * 128, idO, kk > 0 || x > 0 ? 1u : 0u);
+                            if (last_use) umma_commit(&ctl.empty[slot]);
+                        }
+                        __syncwarp();
+                    }
+                    if (dead) break;
+                    if (one) umma_commit(&ctl.pv_done[i & 1]);
+                    __syncwarp();
+                }
+                if (j < steps) {                     // S = Q K^T
+                    const uint32_t i = step0 + j, x = nt == 2 ? j >> 1 : j, tile = nt == 2 ? j & 1 : 0;
+                    const bool last_use = tile + 1 == nt;
+                    uint32_t r = k_slot(x);
+                    const uint32_t d = tmem + (i & 1) * 128;
+#pragma unroll
+                    for (int s = 0; s < KS; ++s, ++r) {
+                        const uint32_t slot = r % ST;
+                        dead = !wait(&ctl.full[slot], r / ST);
+                        if (dead) break;
+                        tc_fence_after();
+                        const uint64_t b = sdesc_kmajor_sw128(t0 + slot * C::SLOT);
+                        const uint64_t a = sdesc_kmajor_sw128(q0 + tile * C::QTILE + s * 2 * C::QBOX);
+                        if (one) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                umma_bf16(d, a + (kk >> 2) * (C::QBOX / 16) + (kk & 3) * 2, b + (kk >> 2) * (C::BOX / 16) + (kk & 3) * 2,
+                                          idS, s > 0 || kk > 0 ? 1u : 0u);
+                            if (!keep && last_use) umma_commit(&ctl.empty[slot]);
+                        }
+                        __syncwarp();
+                    }
+                    if (dead) break;
+                    if (one) {
+                        umma_commit(&ctl.s_full[i & 1]);
+                        if (j + 1 == steps) umma_commit(&ctl.q_empty);
+                    }
+                    __syncwarp();
+                }
+            }
+            ++seg;
+            u += n;
+            step0 += steps;
+            ring0 += keep ? n * KS : n * (KS + VS);
+        }
+        if (dead && lane == 0) {
+            atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
+            ctl.abort = 1;
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax and parts
+        const int q4 = warp & 3, grp = (warp - 4) >> 2;
+        const int row = q4 * 32 + lane;                              // of a tile
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+        const uint32_t sbuf = lane_base + grp * 128;
+        const uint64_t scale22 = pack_f32x2(p.scale2, p.scale2);
+        const int rt = row / g.hb, rh = row - rt * g.hb;             // this row's token in a tile, and head
+        // Every wait here is for a phase that cannot be followed by the next before this warp has seen it: the warps
+        // wait for one another through barriers only, and all of those end by themselves.
+        uint32_t u = 0, i0 = 0, shared_segs = 0;
+        bool dead = false;
+        for (uint32_t seg = 0; u < units; ++seg) {
+            dead = !mbar_wait(&ctl.seg_full[seg % kSegs], (seg / kSegs) & 1, abort_flag, p.wait_ns);
+            dead = __any_sync(~0u, dead);
+            if (dead) break;
+            const PrefixSeg& sg = ctl.segs[seg % kSegs];
+            const uint32_t nt = sg.nt, n = sg.ke - sg.kb, steps = n * nt;
+            const uint32_t tile = nt == 2 ? (grp ^ i0) & 1 : 0;
+            const int tok = static_cast<int>(tile) * g.tpt + rt;     // in the segment
+            const bool valid = rt < g.tpt && tok < sg.tn && rh < sg.hv;
+            const int lo = sg.q.lo, hi = valid ? seen(sg.q, sg.t0 + tok) : 0;
+            const bool any = __any_sync(~0u, valid);
+            const uint32_t ocol = lane_base + C::OCOL + tile * C::DV;
+            float ref = kUnset, l = 0.f;
+            for (uint32_t j = (grp ^ i0) & 1; j < steps; j += 2) {
+                const uint32_t i = i0 + j, x = nt == 2 ? j >> 1 : j;
+                if (!dead) dead = !mbar_wait(&ctl.s_full[grp], (i >> 1) & 1, abort_flag, p.wait_ns);
+                if (nt == 1 && j > 0) {                              // the other group's reference
+                    if (!dead) dead = !mbar_wait(&ctl.ref_done[grp ^ 1][q4], ((i - 1) >> 1) & 1, abort_flag, p.wait_ns);
+                    const float r = ctl.ref[row];
+                    if (r != ref) {
+                        l *= ex2(ref - r);
+                        ref = r;
+                    }
+                }
+                dead = __any_sync(~0u, dead);
+                if (dead) break;
+                tc_fence_after();
+                if (!any) {                                          // (P of rows without a query: their outputs are not written)
+                    if (lane == 0) {
+                        mbar_arrive(&ctl.ref_done[grp][q4]);
+                        mbar_arrive(&ctl.p_full[grp]);
+                    }
+                    __syncwarp();
+                    continue;
+                }
+                const int j0 = sg.row0 + (sg.kb + static_cast<int>(x)) * kUnit;
+                const unsigned bad = *reinterpret_cast<volatile unsigned*>(&ctl.bad[(u + x) & 7]);
+                uint32_t v[128];
+                DSV4_TMEM_LD_32x32b_X32(sbuf, v);
+                DSV4_TMEM_LD_32x32b_X32(sbuf + 32, (v + 32));
+                DSV4_TMEM_LD_32x32b_X32(sbuf + 64, (v + 64));
+                DSV4_TMEM_LD_32x32b_X32(sbuf + 96, (v + 96));
+                tmem_wait_ld();
+                // base-2 scores relative to the reference (none yet: to 0)
+                const bool unset = ref == kUnset;
+                const float nref = unset ? 0.f : -ref;
+                const uint64_t nref2 = pack_f32x2(nref, nref);
+#pragma unroll
+                for (int c = 0; c < 128; c += 2) {
+                    uint64_t y = nref2;
+                    fma_f32x2(y, pack_f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), scale22);
+                    float a, b;
+                    unpack_f32x2(y, a, b);
+                    v[c] = __float_as_uint(a);
+                    v[c + 1] = __float_as_uint(b);
+                }
+                if (j0 < lo || j0 + kUnit > sg.hi_min || bad) {
+                    const int a = lo - j0, b = hi - j0;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c < a || c >= b) v[c] = 0xFF800000u;
+                    if (bad) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            if (paged_bad_row(g, bad, c)) v[c] = 0xFF800000u;
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 128; c += 2)
+                    mx[(c >> 1) & 3] = fmaxf(fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), mx[(c >> 1) & 3]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // A row that outruns its reference moves it (its first scores always do).
+                const bool move = valid && (unset ? top > -INFINITY : top > kSpan);
+                if (__any_sync(~0u, move)) {
+                    const float f = move && !unset ? ex2(-top) : 1.f;
+                    const uint64_t d2 = move ? pack_f32x2(-top, -top) : 0ull;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 2) {
+                        uint64_t y = pack_f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                        add_f32x2(y, d2);
+                        float a, b;
+                        unpack_f32x2(y, a, b);
+                        v[c] = __float_as_uint(a);
+                        v[c + 1] = __float_as_uint(b);
+                    }
+                    if (move) ref = unset ? top : ref + top;
+                    l *= f;
+                    if (x > 0 && __any_sync(~0u, f != 1.f)) {        // O by the factors, once the product before is done
+                        const uint32_t ip = i - (nt == 2 ? 2 : 1);
+                        if (!dead) dead = !mbar_wait(&ctl.pv_done[ip & 1], (ip >> 1) & 1, abort_flag, p.wait_ns);
+                        dead = __any_sync(~0u, dead);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < C::DV; c += 8) {
+                            uint32_t r[8];
+                            DSV4_TMEM_LD_32x32b_X8(ocol + c, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int b = 0; b < 8; ++b) r[b] = __float_as_uint(__uint_as_float(r[b]) * f);
+                            DSV4_TMEM_ST_32x32b_X8(ocol + c, r);
+                        }
+                        DSV4_TMEM_WAIT_ST();
+                    }
+                }
+                if (nt == 1) ctl.ref[row] = ref;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.ref_done[grp][q4]);
+                // P = 2^(s - m) in bf16, over the scores (rounded: the tensor core takes bf16 beside bf16 V; the sum stays
+                // in fp32)
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int c = 0; c < 128; c += 2) {
+                    const float a = ex2(__uint_as_float(v[c])), b = ex2(__uint_as_float(v[c + 1]));
+                    add_f32x2(sum[(c >> 1) & 1], pack_f32x2(a, b));
+                    v[c >> 1] = pack2(a, b);
+                }
+                DSV4_TMEM_ST_32x32b_X32(sbuf, v);
+                DSV4_TMEM_ST_32x32b_X32(sbuf + 32, (v + 32));
+                add_f32x2(sum[0], sum[1]);
+                float sa, sb;
+                unpack_f32x2(sum[0], sa, sb);
+                l += sa + sb;
+                DSV4_TMEM_WAIT_ST();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.p_full[grp]);
+            }
+            dead = __any_sync(~0u, dead);
+            if (dead) break;
+            // ---------------------------------------------------------------- the segment's part
+            // (the product's end is waited for first: it says that all warps are done with the segment before)
+            const uint32_t il = i0 + steps - 1 - (nt == 2 ? 1 - tile : 0);
+            dead = !mbar_wait(&ctl.pv_done[il & 1], (il >> 1) & 1, abort_flag, p.wait_ns);
+            int ch0 = 0, chn = C::DV;                                // this warp's channels
+            if (nt == 1) {
+                // the other group's warp of the same rows: the last reference, both sums
+                if (!dead && (il & 1) != static_cast<uint32_t>(grp))
+                    dead = !mbar_wait(&ctl.ref_done[grp ^ 1][q4], (il >> 1) & 1, abort_flag, p.wait_ns);
+                const float r = ctl.ref[row];
+                ctl.l[grp][row] = r == ref ? l : l * ex2(ref - r);
+                ref = r;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.l_ready[grp][q4]);
+                if (!dead) dead = !mbar_wait(&ctl.l_ready[grp ^ 1][q4], shared_segs & 1, abort_flag, p.wait_ns);
+                ++shared_segs;
+                l = ctl.l[0][row] + ctl.l[1][row];
+                ch0 = grp * (C::DV / 2);
+                chn = C::DV / 2;
+            }
+            dead = __any_sync(~0u, dead);
+            if (dead) break;
+            tc_fence_after();
+            const bool home = sg.kb == 0;
+            const size_t at = (static_cast<size_t>(sg.tok0 + (valid ? tok : 0)) * g.H + sg.head0 + (valid ? rh : 0));
+            const int crow = static_cast<int>(tile) * 128 + row;
+            float* dst;
+            if (home) dst = p.home_o + (static_cast<size_t>(sg.q.own) * g.total_q * g.H + at) * D + sg.half * 256 + ch0;
+            else dst = p.cont_o + (static_cast<size_t>(worker) * C::TILES * 128 + crow) * C::DV + ch0;
+            if (any) {
+#pragma unroll 1
+                for (int c = 0; c < chn; c += 32) {
+                    uint32_t r[32];
+                    DSV4_TMEM_LD_32x32b_X32(ocol + ch0 + c, r);
+                    tmem_wait_ld();
+                    if (valid) {
+#pragma unroll
+                        for (int b = 0; b < 32; b += 4)
+                            *reinterpret_cast<uint4*>(dst + c + b) = make_uint4(r[b], r[b + 1], r[b + 2], r[b + 3]);
+                    }
+                }
+                if (valid && (nt == 2 || grp == 0)) {
+                    // No row of this part is the query's, by its bounds or because their pages are not in the pool (then the
+                    // sum is 0).
+                    const bool none = min(hi, sg.row0 + sg.ke * kUnit) <= max(lo, sg.row0 + sg.kb * kUnit) ||
+                                      (l == 0.f && (*reinterpret_cast<volatile uint32_t*>(&ctl.err) & DSV4_EWORD_BAD_INDEX));
+                    const float m = none ? -INFINITY : ref;
+                    if (home) {
+                        int np = 1;
+                        if (sg.ke < sg.n) {                          // the CTAs that go on with the segment
+                            const long long end = sched.u0 + u + n - sg.ke + sg.n, T = sched.total;
+                            int last = static_cast<int>((end * sched.ge - 1) / T);
+                            while (last + 1 < sched.ge && T * (last + 1) / sched.ge < end) ++last;
+                            while (T * last / sched.ge >= end) --last;
+                            np = last - worker + 1;
+                        }
+                        const int info = worker | np << 8 | crow << 16;
+                        p.home_ml[static_cast<size_t>(sg.q.own * C::HALVES + sg.half) * g.total_q * g.H + at] =
+                            make_float4(m, l, __int_as_float(info), __int_as_float(sg.q.own && lo > 0 ? 1 : 0));
+                    } else {
+                        p.cont_ml[static_cast<size_t>(worker) * C::TILES * 128 + crow] = make_float2(m, l);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.o_empty);
+            u += n;
+            i0 += steps;
+        }
+        dead = __any_sync(~0u, dead);
+        if (dead && lane == 0) {
+            atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
+            ctl.abort = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (ctl.abort) {
+        // A wait ran out in some role, and the others may have finished before it: the copies and
+        // products still in flight end (each wait bounded) before memory is given up.
+        if (warp == 1) {
+            if (elect_one()) umma_commit(&ctl.drained);
+            __syncwarp();
+            mbar_wait(&ctl.drained, 0, nullptr, kDrainNs);
+        }
+        if (tid == 0) {
+            const uint32_t seg = max(max(ctl.seg_end[0], ctl.seg_end[1]), ctl.seg_end[2]);
+            if (seg && !p.fault) mbar_wait(&ctl.q_full, (seg - 1) & 1, nullptr, kDrainNs);
+            ring_drain<ST>(ctl.full, ctl.ring_end);
+        }
+        __syncthreads();
+    }
+    if (warp == 2) tmem_dealloc(tmem, 512);
+    if (tid == 0) p.err[blockIdx.x] = ctl.err;
+}
+
+// Joins each query's parts, and gathers the error bits. An item is 128 channels of one query: one warp, four
+// channels per lane.
+constexpr int kMergeThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads)
+prefix_merge_kernel(const __grid_constant__ PrefixParams p, int ctas, uint32_t* eword) {
+    using C = XCfg<D>;
+    constexpr int CH = D / 128, PL = 5;  // chunks of a query; parts of a segment per lane (at most 160)
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    if (blockIdx.x == 0 && warp == 0) {
+        uint32_t err = 0;
+        for (int c = lane; c < ctas; c += 32) err |= p.err[c];
+        err = __reduce_or_sync(~0u, err);
+        if (lane == 0) *eword = err;
+    }
+    const PagedGeom& g = p.g.p;
+    const int first = min(max(g.cu_q[0], 0), g.total_q), end = min(max(g.cu_q[g.batch], 0), g.total_q);
+    constexpr int WB = kMergeThreads / 32;
+    const long long items = static_cast<long long>(max(end - first, 0)) * g.H * CH;
+    for (long long it = static_cast<long long>(blockIdx.x) * WB + warp; it < items; it += static_cast<long long>(gridDim.x) * WB) {
+        const long long qh = it / CH;
+        const int chunk = static_cast<int>(it - qh * CH), half = C::HALVES == 2 ? chunk >> 1 : 0, ch = chunk * 128 + lane * 4;
+        const size_t at = static_cast<size_t>(first) * g.H + qh;
+        const int tok = static_cast<int>(at / g.H), h = static_cast<int>(at - static_cast<size_t>(tok) * g.H);
+        const size_t kind = static_cast<size_t>(g.total_q) * g.H;
+        const float4 own = p.home_ml[(C::HALVES + half) * kind + at];
+        float4 pre = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        const bool two = __float_as_int(own.w) == 1;
+        if (two) pre = p.home_ml[half * kind + at];
+        const float snk = p.sink ? p.sink[h] * kLog2e : -INFINITY;
+        float w[2][PL], l[2][PL], M = -INFINITY;
+        int c0[2], np[2], row[2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const float4 ml = a ? own : pre;
+            const int info = __float_as_int(ml.z);
+            c0[a] = info & 255;
+            row[a] = min((info >> 16) & 0x7FFF, C::TILES * 128 - 1);
+            np[a] = a || two ? min((info >> 8) & 255, ctas - c0[a]) : 0;
+#pragma unroll
+            for (int k = 0; k < PL; ++k) {
+                const int i = lane + 32 * k;
+                float2 x = make_float2(-INFINITY, 0.f);
+                if (i == 0 && np[a] > 0) x = make_float2(ml.x, ml.y);
+                else if (i < np[a]) x = p.cont_ml[static_cast<size_t>(c0[a] + i) * C::TILES * 128 + row[a]];
+                w[a][k] = x.x;
+                l[a][k] = x.y;
+                M = fmaxf(M, x.x);
+            }
+        }
+#pragma unroll
+        for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
+        const float top = fmaxf(M, snk);
+        float sum = 0.f;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int k = 0; k < PL; ++k) {
+                w[a][k] = w[a][k] == -INFINITY ? 0.f : exp2f(w[a][k] - top);
+                // (a part whose pages were all hidden holds no sum; one that holds NaN keeps it, also beside a weight of 0)
+                sum += l[a][k] * w[a][k];
+            }
+#pragma unroll
+        for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
+        const float den = sum + (snk == -INFINITY ? 0.f : exp2f(snk - top));
+        if (chunk == 0 && lane == 0 && p.lse)
+            p.lse[at] = M == -INFINITY ? (p.sink ? p.sink[h] : -INFINITY) : top * kLn2 + logf(den);
+        const float f = M == -INFINITY ? 0.f : 1.f / den;            // (-inf: no part had a row of the query's)
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const float* home = p.home_o + (a * kind + at) * D + ch;
+            const float* cont = p.cont_o + (static_cast<size_t>(c0[a]) * C::TILES * 128 + row[a]) * C::DV + (ch - half * 256);
+            for (int i0 = 0; i0 < np[a]; i0 += 8) {
+                float wk = w[a][0];
+#pragma unroll
+                for (int k = 1; k < PL; ++k)
+                    if (i0 >= 32 * k) wk = w[a][k];
+                float4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i0 + i < np[a])
+                        v[i] = *reinterpret_cast<const float4*>(i0 + i ? cont + static_cast<size_t>(i0 + i) * C::TILES * 128 * C::DV : home);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float e = __shfl_sync(~0u, wk, (i0 + i) & 31);
+                    if (i0 + i < np[a] && e != 0.f) {                // (a part that saw nothing may hold anything)
+                        o[0] = fmaf(e, v[i].x, o[0]); o[1] = fmaf(e, v[i].y, o[1]);
+                        o[2] = fmaf(e, v[i].z, o[2]); o[3] = fmaf(e, v[i].w, o[3]);
+                    }
+                }
+            }
+        }
+        const int r0 = D - 2 * p.or_pairs;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = f == 0.f ? 0.f : o[i] * f;
+        if (p.orp && ch + 3 >= r0) {
+#pragma unroll 1
+            for (int i = 0; i < 4; i += 2) {
+                if (ch + i < r0) continue;
+                const float2 cs = out_rope_angle(static_cast<double>(p.orp[tok]) * p.or_freq[(ch + i - r0) >> 1]);
+                const float e = i ? o[2] : o[0], b = i ? o[3] : o[1];
+                const float e1 = e * cs.x + b * cs.y, b1 = -e * cs.y + b * cs.x;
+                if (i) { o[2] = e1; o[3] = b1; } else { o[0] = e1; o[1] = b1; }
+            }
+        }
+        *reinterpret_cast<uint2*>(p.out + at * D + ch) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+    }
+}
+
+int prefix_ctas() {
+    const int n = sm_count();
+    return n > 0 && n <= 160 ? n : 160;
+}
+
+struct PrefixWs {
+    size_t home_ml, cont_ml, home_o, cont_o, plen, err, total;
+};
+PrefixWs prefix_ws(const dsv4_paged_prefix_args& a) {
+    const size_t ctas = prefix_ctas(), th = static_cast<size_t>(a.total_q) * a.heads;
+    const int tiles = a.dim == 128 ? 2 : 1, halves = a.dim == 512 ? 2 : 1, dv = a.dim == 512 ? 256 : a.dim;
+    PrefixWs w{};
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t r = at; at += align_up(bytes, 256); return r; };
+    w.home_ml = take(2 * halves * th * 16);
+    w.cont_ml = take(ctas * tiles * 128 * 8);
+    w.home_o = take(2 * th * a.dim * 4);
+    w.cont_o = take(ctas * tiles * 128 * dv * 4);
+    w.plen = take(ctas * a.groups * 4);
+    w.err = take(ctas * 4);
+    w.total = at;
+    return w;
+}
+
+template <int D>
+int run(const dsv4_paged_prefix_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t st) {
+    using C = XCfg<D>;
+    PrefixParams p{};
+    p.g.p = paged_geom(a.block_table, a.cu_q, a.kv_len, a.batch, a.total_q, a.max_pages, a.page_size, a.num_pages, a.heads,
+                       a.kv_heads, 0);
+    paged_tile(p.g.p, 128);
+    p.g.prefix_len = a.prefix_len;
+    p.g.group_start = a.group_start;
+    p.g.groups = a.groups;
+    p.g.tiles = C::TILES;
+    p.g.halves = C::HALVES;
+    CUtensorMap qmap, kmap, vmap;
+    if (!paged_query_map(&qmap, a.q, D, a.heads, a.total_q, a.q_stride, p.g.p.hb, p.g.p.tpt) ||
+        !paged_pool_map(&kmap, a.k_pages, D, a.kv_heads, a.page_size, a.num_pages, p.g.p.br))
+        return DSV4_ERR_LAUNCH;
+    if (!a.v_pages) vmap = kmap;
+    else if (!paged_pool_map(&vmap, a.v_pages, D, a.kv_heads, a.page_size, a.num_pages, p.g.p.br)) return DSV4_ERR_LAUNCH;
+    auto kern = paged_prefix_kernel<D>;
+    if (once_per_device(reinterpret_cast<const void*>(kern), kAttrLaunch, [kern] {
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        }) != cudaSuccess)
+        return DSV4_ERR_LAUNCH;
+    const int ctas = prefix_ctas();
+    const PrefixWs w = prefix_ws(a);
+    p.home_ml = reinterpret_cast<float4*>(ws + w.home_ml);
+    p.cont_ml = reinterpret_cast<float2*>(ws + w.cont_ml);
+    p.home_o = reinterpret_cast<float*>(ws + w.home_o);
+    p.cont_o = reinterpret_cast<float*>(ws + w.cont_o);
+    p.plen = reinterpret_cast<int32_t*>(ws + w.plen);
+    p.err = reinterpret_cast<uint32_t*>(ws + w.err);
+    p.sink = a.sink;
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    p.lse = a.lse;
+    p.scale2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    p.orp = a.out_rope_pos;
+    p.or_pairs = a.out_rope_pos ? a.out_rope_dim / 2 : 0;
+    for (int j = 0; j < p.or_pairs; ++j) p.or_freq[j] = std::pow(a.out_rope_theta, -2.0 * j / a.out_rope_dim);
+    p.shared = a.v_pages == nullptr;
+    p.min_units = 2;
+    const WaitCtl wc = wait_ctl(DSV4_WAIT_FAULT_PAGED_PREFIX);
+    p.fault = wc.fault;
+    p.wait_ns = wc.wait_ns;
+    count_launch();
+    if (launch_k(kern, dim3(ctas), dim3(kThreads), C::SMEM, st, true, qmap, kmap, vmap, p) != cudaSuccess) return DSV4_ERR_LAUNCH;
+    const long long warps = static_cast<long long>(a.total_q) * a.heads * (D / 128), most = ctas * 8;
+    const long long blocks = (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+    count_launch();
+    if (launch_k(prefix_merge_kernel<D>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(kMergeThreads), 0, st, true, p,
+                 ctas, eword) != cudaSuccess)
+        return DSV4_ERR_LAUNCH;
+    return DSV4_OK;
+}
+
+}  // namespace
+
+size_t paged_prefix_ws_bytes(const dsv4_paged_prefix_args& a) { return prefix_ws(a).total; }
+
+int launch_paged_prefix(const dsv4_paged_prefix_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t st) {
+    if (a.batch == 0 || a.total_q == 0) return cudaMemsetAsync(eword, 0, 4, st) == cudaSuccess ? DSV4_OK : DSV4_ERR_LAUNCH;
+    if (a.dim == 512) return run<512>(a, ws, eword, st);
+    if (a.dim == 256) return run<256>(a, ws, eword, st);
+    return run<128>(a, ws, eword, st);
+}
+
+}  // namespace dsv4

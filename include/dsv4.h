@@ -335,6 +335,7 @@ int dsv4_quantize_rows_fp8(const void* x, int rows, int dim, void* q, float* sca
  *   dsv4_paged_evict          keep the rows of most weight, compact the rest away
  *   dsv4_paged_plan           a step's offsets, positions, slots and new pages from its lengths
  *   dsv4_rope                 rotate a step's queries and keys, append the rows
+ *   dsv4_paged_prefix_attn    dsv4_paged_attn where groups of sequences share their first rows
  * Values are the key rows themselves (v_pages NULL: shared-KV attention, as in stage 4), or a
  * second pool of the same shape. The pages have dense per-sequence buffers ([A]
  * PERFORMANCE_AUDIT.md, the sliding-window cache; ARCHITECTURE_AND_MEMORY_AUDIT.md PART 2);
@@ -564,6 +565,39 @@ typedef struct dsv4_rope_args {
 
 int dsv4_rope(const dsv4_rope_args* args, dsv4_stream_t stream);
 
+/* dsv4_paged_attn for a batch in which groups of sequences share the first rows of their caches (a
+ * system prompt, one document under many questions). Group g is the sequences group_start[g] ..
+ * group_start[g+1] - 1 (NULL: one group, of all), whose first prefix_len[g] rows are the same: they are
+ * read through the block table of the group's first sequence and meet all the group's tokens
+ * together, the rows behind them are read through each sequence's own. The result is dsv4_paged_attn's
+ * with window 0. Where a sequence of the group has a token that stands inside the prefix, the
+ * group's prefix ends before that token; sequences outside every group have none. (Each sequence's table
+ * names pages for all its rows. For the shared ones they need not be the same pages.)
+ * Without a prefix the call is right but slower than dsv4_paged_attn. */
+typedef struct dsv4_paged_prefix_args {
+    const void* q;            /* bf16 [total_q, heads, dim]                                   */
+    const void* k_pages;      /* bf16 [num_pages, page_size, kv_heads, dim]                   */
+    const void* v_pages;      /* the same, or NULL: the key rows are the values               */
+    const int32_t* block_table; /* int32 [batch, max_pages]                                   */
+    const int32_t* cu_q;      /* int32 [batch + 1]                                            */
+    const int32_t* kv_len;    /* int32 [batch], prefix and the new tokens' rows included      */
+    const int32_t* prefix_len;  /* int32 [groups]                                             */
+    const int32_t* group_start; /* int32 [groups + 1], not decreasing, or NULL with groups = 1 */
+    const float* sink;        /* fp32 [heads], or NULL                                        */
+    void* out;                /* bf16 [total_q, heads, dim]                                   */
+    float* lse;               /* fp32 [total_q, heads], or NULL                               */
+    const int64_t* out_rope_pos; /* int64 [total_q], or NULL                                  */
+    long long q_stride;       /* elements from token to token: a multiple of 8, >= heads * dim */
+    int batch, groups, total_q, heads, kv_heads, dim, page_size, num_pages, max_pages;
+    float scale;              /* 1/sqrt(dim) on the pages                                     */
+    int out_rope_dim;         /* even, 2..min(dim, 128) when out_rope_pos is given            */
+    double out_rope_theta;
+} dsv4_paged_prefix_args;
+
+/* The workspace holds fp32 partial outputs: 2 * total_q * heads * (dim + 8) numbers at most, and one tile per SM. */
+size_t dsv4_paged_prefix_attn_workspace_size(const dsv4_paged_prefix_args* args);
+int dsv4_paged_prefix_attn(const dsv4_paged_prefix_args* args, void* ws, size_t ws_bytes, dsv4_stream_t stream);
+
 /* ---------------------------------------------------------------------------------------
  * Test support: running the bounded-wait path on purpose. Not for a serving path.
  *
@@ -587,6 +621,8 @@ int dsv4_rope(const dsv4_rope_args* args, dsv4_stream_t stream);
  *     tensor-core warp's wait for it runs out, then those of the softmax and of the page loads.
  *   DSV4_WAIT_FAULT_PAGED_WEIGHTS: dsv4_paged_attn_weights issues no copy of the first operand
  *     that stays in shared memory; the same waits run out. (acc then holds no meaningful sums.)
+ *   DSV4_WAIT_FAULT_PAGED_PREFIX: dsv4_paged_prefix_attn issues no copy of a CTA's first query tile,
+ *     as dsv4_paged_attn.
  * [A] fmha_multitile_capi.cu (errors of the device path returned through C-ABI status codes,
  * never by trapping the process).
  */
@@ -595,7 +631,8 @@ enum {
     DSV4_WAIT_FAULT_SCORER_STAGE = 1,
     DSV4_WAIT_FAULT_ATTN_QUERY = 2,
     DSV4_WAIT_FAULT_PAGED_ATTN = 4,
-    DSV4_WAIT_FAULT_PAGED_WEIGHTS = 8
+    DSV4_WAIT_FAULT_PAGED_WEIGHTS = 8,
+    DSV4_WAIT_FAULT_PAGED_PREFIX = 32
 };
 int dsv4_test_wait_fault(int which, uint32_t wait_limit_us);
 

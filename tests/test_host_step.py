@@ -39,6 +39,41 @@ def _rope(**over):
     return RopeArgs(**a)
 
 
+def _prefix(**over):
+    from compressed_sparse_attention_08_gb300._abi import PagedPrefixArgs
+    a = dict(q=_p(1), k_pages=_p(2), v_pages=None, block_table=_p(3), cu_q=_p(4), kv_len=_p(5), prefix_len=_p(6), group_start=_p(7),
+             sink=_p(8), out=_p(9), lse=_p(10), out_rope_pos=_p(11), q_stride=512 * 64, batch=4, groups=2, total_q=4, heads=64,
+             kv_heads=1, dim=512, page_size=64, num_pages=100, max_pages=16, scale=0.04, out_rope_dim=64, out_rope_theta=1e4)
+    a.update(over)
+    return PagedPrefixArgs(**a)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(batch=-1), dict(batch=2049), dict(groups=0), dict(groups=2049), dict(total_q=-1), dict(total_q=(1 << 24) + 1), dict(heads=0),
+    dict(heads=1025), dict(heads=6, kv_heads=4), dict(kv_heads=0), dict(dim=64), dict(dim=384), dict(page_size=12), dict(page_size=0),
+    dict(num_pages=0), dict(max_pages=0), dict(max_pages=1 << 25), dict(q_stride=8), dict(q_stride=512 * 64 + 4), dict(scale=float("nan")),
+    dict(q=None), dict(q=_p(1, 8)), dict(k_pages=_p(2, 8)), dict(v_pages=_p(12, 8)), dict(block_table=None), dict(cu_q=None),
+    dict(kv_len=None), dict(prefix_len=None), dict(prefix_len=_p(6, 2)), dict(group_start=None), dict(group_start=_p(7, 1)),
+    dict(sink=_p(8, 2)), dict(out=None), dict(lse=_p(10, 2)), dict(out_rope_pos=_p(11, 4)), dict(out_rope_dim=0), dict(out_rope_dim=65),
+    dict(out_rope_dim=130), dict(out_rope_theta=-1.0)])
+def test_prefix_rejects_on_host(lib, bad):
+    assert lib.dsv4_paged_prefix_attn(ctypes.byref(_prefix(**bad)), _p(20), 1 << 40, None) == 1, bad
+
+
+def test_prefix_workspace(lib):
+    size = lib.dsv4_paged_prefix_attn_workspace_size
+    need = size(ctypes.byref(_prefix()))
+    assert need > 256 and size(None) == 0 and size(ctypes.byref(_prefix(max_pages=1024))) == need
+    more = size(ctypes.byref(_prefix(total_q=1004)))
+    assert 2 * 1000 * 64 * 512 * 4 <= more - need <= 2 * 1000 * 64 * 520 * 4 + 4096
+    assert size(ctypes.byref(_prefix(total_q=1 << 24, heads=1024, kv_heads=1024))) > 1 << 45       # (not wrapped)
+    for bad in (dict(batch=-1), dict(groups=0), dict(kv_heads=0), dict(heads=6, kv_heads=4), dict(dim=0), dict(total_q=-1)):
+        assert size(ctypes.byref(_prefix(**bad))) == 0, bad
+    for ws, n in ((_p(20), need - 1), (None, need), (_p(20, 8), need)):
+        assert lib.dsv4_paged_prefix_attn(ctypes.byref(_prefix()), ws, n, None) == 1
+    assert lib.dsv4_paged_prefix_attn(None, _p(20), need, None) == 1
+
+
 @pytest.mark.parametrize("bad", [
     dict(batch=-1), dict(batch=2049), dict(total_q=-1), dict(total_q=(1 << 24) + 1), dict(page_size=0), dict(page_size=12),
     dict(page_size=65544), dict(num_pages=0), dict(max_pages=0), dict(max_pages=1 << 26), dict(free_cap=-1), dict(kv_len=None),
@@ -99,6 +134,9 @@ def test_binding_refuses_shapes_and_types():
         m.paged_plan_args(n, n, n, t, n, n[:1], n, pos, page_size=16, num_pages=4)
     with pytest.raises(ValueError, match="held"):
         m.paged_plan_args(n, n, n[:1], t, n, n[:1], torch.zeros(3), pos, page_size=16, num_pages=4)
+    pages = torch.zeros(4, 16, 1, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        m.paged_prefix_args(q, q, pages, t, torch.zeros(3, dtype=torch.int32), n, n[:1])
     with pytest.raises(ValueError, match="next_pos"):
         m.paged_plan_args(n, n, n, t, n, n[:1], torch.zeros(3), pos, page_size=16, num_pages=4, next_pos_out=pos)
 
