@@ -311,7 +311,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
                     "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),     \
                     "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),     \
                     "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory")
-// The same for 8 columns.
+// The same for 16 and for 8 columns.
+#define DSV4_TMEM_ST_32x32b_X16(taddr, r)                                                     \
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "                               \
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"                    \
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),          \
+                    "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),          \
+                    "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory")
 #define DSV4_TMEM_ST_32x32b_X8(taddr, r)                                                      \
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"      \
                  :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),          \

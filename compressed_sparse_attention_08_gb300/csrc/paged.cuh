@@ -99,6 +99,9 @@ __device__ __forceinline__ int paged_tile_units(const PagedGeom& g, const PagedS
 __device__ __forceinline__ int paged_count(const PagedGeom& g) { return g.batch; }
 __device__ __forceinline__ int paged_tokens(const PagedGeom& g) { return g.tpt; }
 __device__ __forceinline__ int paged_mult(const PagedGeom& g) { return g.KV * g.nhb; }
+// (the line may count more than units: a unit's weight, and what a tile has beside its units, at its end)
+__device__ __forceinline__ int paged_weight(const PagedGeom&, const PagedSeq&, int) { return 1; }
+__device__ __forceinline__ int paged_over(const PagedGeom&, const PagedSeq&, int) { return 0; }
 __device__ __forceinline__ PagedSeq paged_shfl(const PagedSeq& q, int src) {
     return PagedSeq{0, __shfl_sync(~0u, q.n, src), __shfl_sync(~0u, q.L, src)};
 }
@@ -203,7 +206,10 @@ __device__ void paged_schedule(const Geom& g, int self, int count, int min_units
                     tt = tt0 + f;
                     inner = static_cast<int>(r / nf);
                     k = static_cast<int>(r - static_cast<long long>(inner) * nf);
-                    if (k > 0 && nf <= small) {      // the next tile's start
+                    const int part = k % paged_weight(g, q, tt);
+                    u -= part;
+                    k -= part;
+                    if (k > 0 && (nf <= small || k >= nf - paged_over(g, q, tt))) {   // the next tile's start
                         u += nf - k;
                         k = 0;
                         if (++inner == mult) { inner = 0; ++tt; }

@@ -20,7 +20,9 @@
 // with the scores over all channels and the product with half of V's (1.5 times the products' time).
 // Roles: warps 0, 2 and 3 move pages by TMA into a ring of slots of 128 rows x 128 channels, warp 1 issues
 // tcgen05.mma, warps 4-11 do the softmax and write the parts.
+#include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged.cuh"
@@ -49,6 +51,9 @@ struct PrefixGeom {
     const int32_t* group_start;          // [groups + 1] or null: one group of all
     int groups, tiles, halves;           // tiles of queries per segment, passes over V's channels
 };
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 // The geometry with the prefix lengths as they are used (by this CTA: each forms its own copy).
 struct PrefixLine {
@@ -108,8 +113,17 @@ __device__ __forceinline__ int unit_row0(const PrefixGeom& g, const PrefixSeq& q
 __device__ __forceinline__ int segment_units(const PrefixGeom& g, const PrefixSeq& q, int t_last) {
     return max((seen(q, t_last) - unit_row0(g, q) + kUnit - 1) / kUnit, 1);
 }
+// The line counts time, in 600 cycles or so: a unit of two tiles takes 5, of one tile 3 (at 256 and 512 channels all
+// have one, and take longer: only ratios count), a segment's start and end 21 and 11 (6 of longer units).
+__device__ __forceinline__ bool two_tiles(const PrefixLine& l, const PrefixSeq& q, int tt) {
+    return l.g.tiles == 2 && q.n - tt * paged_tokens(l) > l.g.p.tpt;
+}
+__device__ __forceinline__ int paged_weight(const PrefixLine& l, const PrefixSeq& q, int tt) { return two_tiles(l, q, tt) ? 5 : 3; }
+__device__ __forceinline__ int paged_over(const PrefixLine& l, const PrefixSeq& q, int tt) {
+    return l.g.tiles == 1 ? 6 : two_tiles(l, q, tt) ? 21 : 11;
+}
 __device__ __forceinline__ int paged_tile_units(const PrefixLine& l, const PrefixSeq& q, int tt) {
-    return segment_units(l.g, q, min((tt + 1) * paged_tokens(l), q.n) - 1);
+    return segment_units(l.g, q, min((tt + 1) * paged_tokens(l), q.n) - 1) * paged_weight(l, q, tt) + paged_over(l, q, tt);
 }
 
 // A segment of the line: up to `tiles` tiles of queries of one KV head, and this CTA's part of their units.
@@ -119,6 +133,7 @@ struct PrefixSeg {
     int kvh, head0, hv, half;            // KV head, first query head, query heads, half of V's channels
     int hi_u, hi_min;                    // rows below which some token sees, and every token
     int row0, n, kb, ke;                 // first row of unit 0, the segment's units, this CTA's [kb, ke)
+    int weight, cost;                    // of a unit, and of this CTA's part, on the line
 };
 
 struct PrefixWalk {
@@ -153,10 +168,12 @@ struct PrefixWalk {
         o.hi_min = seen(q, o.t0);
         o.row0 = unit_row0(g, q);
         o.n = segment_units(g, q, o.t0 + o.tn - 1);
-        o.kb = k;
-        const long long take = left < o.n - k ? left : o.n - k;
-        o.ke = k + static_cast<int>(take);
-        left -= take;
+        o.weight = paged_weight(l, q, tt);
+        o.kb = k / o.weight;
+        const long long rest = left / o.weight;
+        o.ke = rest < o.n - o.kb ? o.kb + static_cast<int>(rest) : o.n;
+        o.cost = (o.ke - o.kb) * o.weight + (o.ke == o.n ? paged_over(l, q, tt) : 0);
+        left -= o.cost;
         k = 0;
         if (++inner == paged_mult(l)) { inner = 0; ++tt; }
         return true;
@@ -180,6 +197,7 @@ struct PrefixParams {
     const int64_t* orp;                  // [total_q] or null
     int or_pairs;
     int shared, min_units;
+    int negate;                          // a negative scale: Q is negated (bit 13 of the products' descriptor)
     int fault;                           // test control: a CTA's first query tile is never copied
     unsigned long long wait_ns;
     double or_freq[64];                  // theta^(-2j / out_rope_dim)
@@ -187,10 +205,13 @@ struct PrefixParams {
 
 constexpr int kMaxSlots = 8, kSegs = 4;  // (the loads run at most two segments ahead of the outputs)
 struct PrefixCtl {
-    uint64_t q_full, q_empty, full[kMaxSlots], empty[kMaxSlots];
-    uint64_t seg_full[kSegs], s_full[2], p_full[2], pv_done[2], ref_done[2][4], l_ready[2][4], o_empty;
+    uint64_t q_full, q_empty, empty[kMaxSlots];
+    // A slot's copies, counted apart for K (and tiles that are both) and for V.
+    uint64_t full[2][kMaxSlots];
+    uint8_t last[kMaxSlots];             // a slot's last copy: 4 | parity << 1 | V
+    uint64_t seg_full[kSegs], s_full[2], p_full[2], pv_done[2], o_done[2], ref_done[2][4], l_ready[2][4], o_empty;
     uint64_t drained;                    // products in flight when a wait ran out
-    uint32_t ring_end[kLoadWarps], seg_end[kLoadWarps];
+    uint32_t seg_end[kLoadWarps];
     PagedSchedOf<PrefixLine> sched;
     PrefixSeg segs[kSegs];               // written by a load warp for the softmax
     float ref[128];                      // reference maxima (base-2 units), where two groups share a tile
@@ -230,11 +251,48 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
+// The largest of three (a NaN loses), in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 32 bytes, a sector of its own for every lane.
+__device__ __forceinline__ void store32(float* p, const uint32_t* r) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
+                 "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+
 __device__ __noinline__ float2 out_rope_angle(double a) {
     float sn, cs;
     sincosf(reduced_angle(a), &sn, &cs);
     return make_float2(cs, sn);
 }
+
+// A bounded wait whose first look is all that stands in the way of a barrier that is there already.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, const volatile int* abort, unsigned long long ns) {
+    return mbar_wait(bar, parity, abort, ns);
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int* abort, unsigned long long ns) {
+    return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, ns);
+}
+
+// A reader's place in the ring of ST slots, and for each slot the parity of its next copy for this reader.
+template <uint32_t ST>
+struct RingAt {
+    uint32_t slot, turns;
+    template <uint32_t N>
+    __device__ __forceinline__ void skip() {
+        slot += N % ST;
+        if (slot >= ST) slot -= ST;
+    }
+    __device__ __forceinline__ uint32_t parity() const { return turns >> slot & 1; }
+    __device__ __forceinline__ void next() {             // this slot's copy is used
+        turns ^= 1u << slot;
+        skip<1>();
+    }
+};
 
 // The pages of a tile of kUnit rows, as paged_look.
 __device__ __forceinline__ PagedLook prefix_look(const PagedGeom& g, const PrefixSeg& sg, int row, int lane) {
@@ -293,11 +351,17 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         tma_prefetch_desc(&vmap);
         mbar_init(&ctl.q_full, kLoadWarps);
         mbar_init(&ctl.q_empty, 1);
-        for (int i = 0; i < ST; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&ctl.full[0][i], 1);
+            mbar_init(&ctl.full[1][i], 1);
+            mbar_init(&ctl.empty[i], 1);
+            ctl.last[i] = 0;
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.s_full[i], 1);
             mbar_init(&ctl.p_full[i], 4);
             mbar_init(&ctl.pv_done[i], 1);
+            mbar_init(&ctl.o_done[i], 1);
             for (int j = 0; j < 4; ++j) { mbar_init(&ctl.ref_done[i][j], 1); mbar_init(&ctl.l_ready[i][j], 1); }
         }
         for (int i = 0; i < kSegs; ++i) mbar_init(&ctl.seg_full[i], 1);
@@ -325,7 +389,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     const PagedGeom& g = p.g.p;
     const PagedSchedOf<PrefixLine>& sched = ctl.sched;
     const bool keep = C::KEEP && p.shared;               // K rows stay in place as V
-    const uint32_t units = static_cast<uint32_t>(sched.u1 - sched.u0);
+    const uint32_t share = static_cast<uint32_t>(sched.u1 - sched.u0);
     if (warp == 0 || warp == 2 || warp == 3) {
         // ---------------------------------------------------------------- pages and queries
         // Three warps walk the same slots and take them in turn. Order: as the products need them, K0 V0 K1
@@ -335,38 +399,41 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         PrefixSeg sg;
         const uint32_t qtile = static_cast<uint32_t>(g.hb) * g.tpt * D * 2;
         const int piece = lane >> 1, box = lane & 1;
-        uint32_t ring = 0, seg = 0;
+        uint32_t ring = 0, seg = 0, turn[2] = {0, 0};    // (a bit per slot: the parity of its next copy)
         bool dead = false, more = w.next(sg);
         PagedLook cur{0, 0, false}, prev{0, 0, false};
         if (more) cur = prefix_look(g, sg, sg.row0 + sg.kb * kUnit, lane);
         int k = more ? sg.kb : 0;
         auto load = [&](const CUtensorMap* map, const PagedLook& t, int slots, int ch0, int kvh, int unit) {
+            const int kind = unit < 0;                   // K (with its unit), or V
             const PagedBoxes bx = paged_boxes(g, t);
             const uint32_t bytes = static_cast<uint32_t>(__popc(bx.ok)) * g.br * 128;
 #pragma unroll 1
             for (int mt = 0; mt < slots; ++mt, ++ring) {
+                const uint32_t slot = ring % ST, parity = turn[kind] >> slot & 1;
+                turn[kind] ^= 1u << slot;
                 if (ring % kLoadWarps != static_cast<uint32_t>(mine)) continue;
-                const uint32_t slot = ring % ST;
                 if (ring >= ST)
-                    dead = __any_sync(~0u, !mbar_wait(&ctl.empty[slot], (ring / ST - 1) & 1, abort_flag, p.wait_ns));
+                    dead = __any_sync(~0u, !wait_for(&ctl.empty[slot], (ring / ST - 1) & 1, abort_flag, p.wait_ns));
                 if (dead) return;
                 if (lane == 0) {
                     if (mt == 0 && unit >= 0) {
                         ctl.bad[unit & 7] = bx.bad;
                         if (bx.bad) atomicOr(&ctl.err, DSV4_EWORD_BAD_INDEX);
                     }
-                    if (bytes) mbar_arrive_expect_tx(&ctl.full[slot], bytes);
-                    else mbar_arrive(&ctl.full[slot]);
+                    ctl.last[slot] = static_cast<uint8_t>(4 | parity << 1 | kind);
+                    if (bytes) mbar_arrive_expect_tx(&ctl.full[kind][slot], bytes);
+                    else mbar_arrive(&ctl.full[kind][slot]);
                 }
                 __syncwarp();
                 if ((bx.ok >> lane) & 1)
-                    tma_load_4d(sm + slot * C::SLOT + box * C::BOX + piece * g.br * 128, map, &ctl.full[slot],
+                    tma_load_4d(sm + slot * C::SLOT + box * C::BOX + piece * g.br * 128, map, &ctl.full[kind][slot],
                                 ch0 + mt * 128 + box * 64, kvh, t.slot, t.page);
             }
         };
         for (int u = 0; !dead && more; ++u) {
             if (k == sg.kb) {                        // a new segment
-                if (seg > 0) dead = __any_sync(~0u, !mbar_wait(&ctl.q_empty, (seg - 1) & 1, abort_flag, p.wait_ns));
+                if (seg > 0) dead = __any_sync(~0u, !wait_for(&ctl.q_empty, (seg - 1) & 1, abort_flag, p.wait_ns));
                 if (dead) break;
                 if (lane == 0) {
                     if (mine == 0) {
@@ -406,7 +473,6 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             cur = next;
         }
         if (lane == 0) {
-            ctl.ring_end[mine] = ring;
             ctl.seg_end[mine] = seg;
             if (dead) {
                 atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
@@ -415,106 +481,213 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- tensor core
-        // Steps (unit, tile) in order; the product with V of step j - 2 comes before the scores of step j, whose
-        // buffer holds that step's P (the tensor core does a thread's products in the order of their issue).
+        // Steps (unit, tile) in order; the product with V of step i - 2 comes before the scores of step i, whose
+        // buffer holds that step's P (the tensor core does a thread's products in the order of their issue; a commit
+        // speaks for all before it, so scores that have come say that the product two steps before is done).
+        // A product takes the core 64 cycles and the warp 23; but anything else costs the warp about 10 cycles an
+        // instruction, 60 a commit and 100 to 150 a look at a barrier, and with a general loop over steps that was 1,400 a
+        // step, more than the products' 1,024. So the two forms of a segment have loops of their own with little in
+        // them, P, V and K are looked at together, a lane each, and what can wait is done behind issued products.
+        // (One warp for S and one for O: the two tiles' products mixed, both tiles' softmax ran at the same time, and then
+        // the core idled.) Votes and exchanges tell the compiler that the warp stays together.
+        // (Every wait of the kernel is for a phase whose predecessor the waiter has seen, itself or through what it waited for
+        // before, and whose successor cannot end before it goes on: parity tells no more.)
         PrefixWalk w(line, sched);
-        PrefixSeg sg;
-        uint32_t u = 0, seg = 0, ring0 = 0, step0 = 0;   // units, segments, slots and steps before this segment
+        PrefixSeg sg{};
+        uint32_t u = 0, seg = 0, i0 = 0, ends = 0;       // units, segments, steps, steps with pv_done before this segment
         bool dead = false;
         const bool one = elect_one();
-        // (the warp stays together: a wait that runs out does so for all lanes)
-        auto wait = [&](uint64_t* bar, uint32_t parity) { return !__any_sync(~0u, !mbar_wait(bar, parity & 1, abort_flag, p.wait_ns)); };
-        const uint32_t q0 = smem_u32(sQ), t0 = smem_u32(sm);
-        const uint32_t idS = idesc_bf16_f32(128, kUnit), idO = idesc_bf16_f32(128, 128) | (1u << 16);
-        while (!dead && w.next(sg)) {
-            dead = !wait(&ctl.q_full, seg);
-            const uint32_t n = sg.ke - sg.kb, nt = sg.nt, steps = n * nt;
-            auto k_slot = [&](uint32_t x) {
-                return ring0 + (keep ? x * KS : nt == 2 ? x * (KS + VS) : x * KS + (x > 0 ? x - 1 : 0) * VS);
-            };
-            auto v_slot = [&](uint32_t x) {
-                return ring0 + (keep ? x * KS : nt == 2 ? x * (KS + VS) + KS : min(x + 2, n) * KS + x * VS);
-            };
-            for (uint32_t j = 0; j < steps + 2 && !dead; ++j) {
-                if (j >= 2) {                        // O += P V
-                    const uint32_t i = step0 + j - 2, x = nt == 2 ? (j - 2) >> 1 : j - 2, tile = nt == 2 ? j & 1 : 0;
-                    const bool last_use = tile + 1 == nt;
-                    if (j < 2 + nt && tile == 0 && seg > 0) dead = !wait(&ctl.o_empty, seg - 1);
-                    dead = dead || !wait(&ctl.p_full[i & 1], i >> 1);
-                    if (dead) break;
-                    uint32_t r = v_slot(x);
-                    const int j0 = sg.row0 + (sg.kb + static_cast<int>(x)) * kUnit;
-                    const unsigned bad = *reinterpret_cast<volatile unsigned*>(&ctl.bad[(u + x) & 7]);
-                    if (tile == 0 && (j0 < sg.q.lo || j0 + kUnit > sg.hi_u || bad)) {
-                        // Rows that no token sees hold anything: as V they must not meet P = 0.
-                        for (int s = 0; s < VS && !dead; ++s) dead = !wait(&ctl.full[(r + s) % ST], (r + s) / ST);
-                        if (dead) break;
-                        const int z0 = max(sg.q.lo - j0, 0), z1 = max(sg.hi_u - j0, 0);
-                        for (int row = 0; row < kUnit; ++row) {
-                            if (row >= z0 && row < z1 && !paged_bad_row(g, bad, row)) continue;
-                            for (int c = lane; c < VS * 16; c += 32) {
-                                const uint32_t slot = (r + (c >> 4)) % ST;
-                                *reinterpret_cast<uint4*>(sm + slot * C::SLOT + ((c >> 3) & 1) * C::BOX + row * 128 + (c & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                            }
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                    }
+        // (a wait that runs out does so for all lanes)
+        auto look = [&](uint64_t* bar, uint32_t parity, bool on) {
+            return !__any_sync(~0u, on && !wait_for(bar, parity & 1, abort_flag, p.wait_ns));
+        };
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return look(bar, parity, true); };
+        RingAt<ST> kat{0, 0}, vat{0, 0};                 // the next K and V slots, in the order of the loads
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+        const uint32_t idS = idesc_bf16_f32(128, kUnit) | (p.negate ? 1u << 13 : 0u), idO = idesc_bf16_f32(128, 128) | (1u << 16);
+        const uint64_t qdesc = sdesc_kmajor_sw128(smem_u32(sQ)), kdesc = sdesc_kmajor_sw128(smem_u32(sm)),
+                       vdesc = sdesc_mnmajor_sw128(smem_u32(sm), C::BOX, 1024u);
+        // (one lane) S of buffer `buf` (+)= Q's channels 128 s .. of a tile x K's in a slot
+        auto mul_k = [&](uint32_t buf, uint32_t tile, int s, uint32_t slot) {
+            const uint64_t a = qdesc + tile * (C::QTILE / 16) + s * (2 * C::QBOX / 16), b = kdesc + slot * (C::SLOT / 16);
 #pragma unroll
-                    for (int s = 0; s < VS; ++s, ++r) {
-                        const uint32_t slot = r % ST;
-                        dead = !wait(&ctl.full[slot], r / ST);
-                        if (dead) break;
-                        tc_fence_after();
-                        const uint64_t b = sdesc_mnmajor_sw128(t0 + slot * C::SLOT, C::BOX, 1024u);
-                        const uint32_t d = tmem + C::OCOL + tile * C::DV + s * 128, a = tmem + (i & 1) * 128;
-                        if (one) {
+            for (int kk = 0; kk < 8; ++kk)
+                umma_bf16(tm + buf * 128, a + (kk >> 2) * (C::QBOX / 16) + (kk & 3) * 2, b + (kk >> 2) * (C::BOX / 16) + (kk & 3) * 2, idS,
+                          kk > 0 ? 1u : s);
+        };
+        // (one lane) O's columns at `d` (+)= P of buffer `buf` x V in a slot
+        auto mul_v = [&](uint32_t d, uint32_t buf, uint32_t slot, uint32_t more) {
+            const uint64_t b = vdesc + slot * (C::SLOT / 16);
 #pragma unroll
-                            for (int kk = 0; kk < kUnit / 16; ++kk)
-                                umma_bf16_ts(d, a + kk * 8, b + kk * 128, idO, kk > 0 || x > 0 ? 1u : 0u);
-                            if (last_use) umma_commit(&ctl.empty[slot]);
-                        }
-                        __syncwarp();
-                    }
-                    if (dead) break;
-                    if (one) umma_commit(&ctl.pv_done[i & 1]);
-                    __syncwarp();
+            for (int kk = 0; kk < kUnit / 16; ++kk)
+                umma_bf16_ts(tm + C::OCOL + d, tm + buf * 128 + kk * 8, b + kk * 128, idO, kk > 0 ? 1u : more);
+        };
+        // Whether unit x of the segment, whose K has come, holds rows that no token sees.
+        auto edge = [&](uint32_t x) {
+            const int j0 = sg.row0 + (sg.kb + static_cast<int>(x)) * kUnit;
+            const unsigned bad = *reinterpret_cast<volatile unsigned*>(&ctl.bad[(u + x) & 7]);
+            return __any_sync(~0u, j0 < sg.q.lo || j0 + kUnit > sg.hi_u || bad);
+        };
+        // Such rows hold anything: as V they must not meet P = 0.
+        auto clear_rows = [&](uint32_t x) {
+            const int j0 = sg.row0 + (sg.kb + static_cast<int>(x)) * kUnit;
+            const unsigned bad = *reinterpret_cast<volatile unsigned*>(&ctl.bad[(u + x) & 7]);
+            auto clear = [&](int row0, int rows) {
+                for (int c = lane; c < rows * (VS * 16); c += 32) {
+                    const int row = row0 + c / (VS * 16), x16 = c % (VS * 16);
+                    uint32_t slot = vat.slot + (x16 >> 4);
+                    if (slot >= ST) slot -= ST;
+                    *reinterpret_cast<uint4*>(sm + slot * C::SLOT + ((x16 >> 3) & 1) * C::BOX + row * 128 + (x16 & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
                 }
-                if (j < steps) {                     // S = Q K^T
-                    const uint32_t i = step0 + j, x = nt == 2 ? j >> 1 : j, tile = nt == 2 ? j & 1 : 0;
-                    const bool last_use = tile + 1 == nt;
-                    uint32_t r = k_slot(x);
-                    const uint32_t d = tmem + (i & 1) * 128;
-#pragma unroll
-                    for (int s = 0; s < KS; ++s, ++r) {
-                        const uint32_t slot = r % ST;
-                        dead = !wait(&ctl.full[slot], r / ST);
-                        if (dead) break;
-                        tc_fence_after();
-                        const uint64_t b = sdesc_kmajor_sw128(t0 + slot * C::SLOT);
-                        const uint64_t a = sdesc_kmajor_sw128(q0 + tile * C::QTILE + s * 2 * C::QBOX);
-                        if (one) {
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                umma_bf16(d, a + (kk >> 2) * (C::QBOX / 16) + (kk & 3) * 2, b + (kk >> 2) * (C::BOX / 16) + (kk & 3) * 2,
-                                          idS, s > 0 || kk > 0 ? 1u : 0u);
-                            if (!keep && last_use) umma_commit(&ctl.empty[slot]);
-                        }
-                        __syncwarp();
+            };
+            const int z0 = min(max(sg.q.lo - j0, 0), kUnit), z1 = min(max(sg.hi_u - j0, z0), kUnit);
+            clear(0, z0);
+            clear(z1, kUnit - z1);
+            for (int r = 0; bad && r < (kUnit >> g.br_log2); ++r)
+                if (bad >> (2 * r) & 1) clear(r << g.br_log2, g.br);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        };
+        // Two tiles: K0 V0 K1 V1 .. (one slot each), or K0 K1 ..
+        auto two_tiles = [&]() {
+            const uint32_t n = __shfl_sync(~0u, sg.ke - sg.kb, 0), b0 = i0 & 1, b1 = b0 ^ 1;
+            uint32_t pp0 = i0 >> 1, pp1 = (i0 + 1) >> 1; // phases of P
+            if (!keep) vat.template skip<1>();
+            if (!wait(&ctl.full[0][kat.slot], kat.parity())) return false;
+            tc_fence_after();
+            bool edgy = edge(0);
+            if (one) {
+                mul_k(b0, 0, 0, kat.slot);
+                umma_commit(&ctl.s_full[b0]);
+                mul_k(b1, 1, 0, kat.slot);
+                umma_commit(&ctl.s_full[b1]);
+                if (!keep) umma_commit(&ctl.empty[kat.slot]);
+                if (n == 1) umma_commit(&ctl.q_empty);
+            }
+            __syncwarp();
+            kat.next();
+            if (!keep) kat.template skip<1>();
+            for (uint32_t x = 0; x < n; ++x, ++pp0, ++pp1) {
+                const bool more = x + 1 < n;
+                // lane 0: the first tile's P; 1: the next K; others: V
+                if (!look(lane == 0 ? &ctl.p_full[b0] : lane == 1 ? &ctl.full[0][kat.slot] : &ctl.full[1][vat.slot],
+                          lane == 0 ? pp0 : lane == 1 ? kat.parity() : vat.parity(), lane == 0 || (lane == 1 ? more : !keep)))
+                    return false;
+                tc_fence_after();
+                if (edgy) clear_rows(x);
+                if (x == 0 && seg > 0 && !wait(&ctl.o_empty, seg - 1)) return false;
+                if (one) {
+                    mul_v(0, b0, vat.slot, x);
+                    if (more) {
+                        mul_k(b0, 0, 0, kat.slot);
+                        umma_commit(&ctl.s_full[b0]);
+                    } else {
+                        umma_commit(&ctl.o_done[b0]);
                     }
-                    if (dead) break;
-                    if (one) {
-                        umma_commit(&ctl.s_full[i & 1]);
-                        if (j + 1 == steps) umma_commit(&ctl.q_empty);
+                }
+                __syncwarp();
+                if (more) edgy = edge(x + 1);
+                if (!wait(&ctl.p_full[b1], pp1)) return false;
+                tc_fence_after();
+                if (one) {
+                    mul_v(C::DV, b1, vat.slot, x);
+                    if (more) {
+                        mul_k(b1, 1, 0, kat.slot);
+                        umma_commit(&ctl.s_full[b1]);
+                        if (!keep) umma_commit(&ctl.empty[kat.slot]);
+                        if (x + 2 == n) umma_commit(&ctl.q_empty);
+                    } else {
+                        umma_commit(&ctl.o_done[b1]);
                     }
-                    __syncwarp();
+                    umma_commit(&ctl.empty[vat.slot]);
+                }
+                __syncwarp();
+                vat.next();
+                if (more) {
+                    kat.next();
+                    if (!keep) {
+                        vat.template skip<1>();
+                        kat.template skip<1>();
+                    }
                 }
             }
-            ++seg;
-            u += n;
-            step0 += steps;
-            ring0 += keep ? n * KS : n * (KS + VS);
+            return true;
+        };
+        // One tile: K0 K1 V0 K2 V1 .., or K0 K1 ..
+        auto one_tile = [&]() {
+            const uint32_t n = __shfl_sync(~0u, sg.ke - sg.kb, 0);
+            uint32_t edges = 0;                          // a bit per unit, the newest lowest
+            auto scores = [&](uint32_t x) {
+                const uint32_t buf = (i0 + x) & 1;
+#pragma unroll 1
+                for (int s = 0; s < KS; ++s) {
+                    if (!wait(&ctl.full[0][kat.slot], kat.parity())) return false;
+                    tc_fence_after();
+                    if (one) {
+                        mul_k(buf, 0, s, kat.slot);
+                        if (!keep) umma_commit(&ctl.empty[kat.slot]);
+                        if (s + 1 == KS) {
+                            umma_commit(&ctl.s_full[buf]);
+                            if (x + 1 == n) umma_commit(&ctl.q_empty);
+                        }
+                    }
+                    __syncwarp();
+                    kat.next();
+                }
+                if (!keep && x > 0) kat.template skip<VS>();
+                edges = edges << 1 | (edge(x) ? 1u : 0u);
+                return true;
+            };
+            if (!keep) {
+                vat.template skip<KS>();
+                if (n > 1) vat.template skip<KS>();
+            }
+            if (!scores(0) || (n > 1 && !scores(1))) return false;
+            for (uint32_t x = 0; x < n; ++x) {
+                const uint32_t i = i0 + x, buf = i & 1;
+                RingAt<ST> v1 = vat;
+                if (VS == 2) v1.template skip<1>();
+                // lane 0: P; others: V
+                const bool odd = VS == 2 && (lane & 1);
+                if (!look(lane == 0 ? &ctl.p_full[buf] : &ctl.full[1][odd ? v1.slot : vat.slot],
+                          lane == 0 ? i >> 1 : odd ? v1.parity() : vat.parity(), lane == 0 || !keep))
+                    return false;
+                tc_fence_after();
+                if (edges >> (x + 1 < n ? 1 : 0) & 1) clear_rows(x);
+                if (x == 0 && seg > 0 && !wait(&ctl.o_empty, seg - 1)) return false;
+                if (one) {
+                    mul_v(0, buf, vat.slot, x);
+                    umma_commit(&ctl.empty[vat.slot]);
+                    if (VS == 2) {
+                        mul_v(128, buf, v1.slot, x);
+                        umma_commit(&ctl.empty[v1.slot]);
+                    }
+                    umma_commit(&ctl.pv_done[(ends + x) & 1]);
+                }
+                __syncwarp();
+                vat.next();
+                if (VS == 2) vat.next();
+                if (x + 2 < n) {
+                    if (!keep) vat.template skip<KS>();
+                    if (!scores(x + 2)) return false;
+                }
+            }
+            if (!keep) kat.template skip<VS>();          // (the segment's last V)
+            ends += n;
+            return true;
+        };
+        for (; __any_sync(~0u, w.next(sg)); ++seg) {
+            dead = !wait(&ctl.q_full, seg);
+            if (dead) break;
+            const bool two = C::TILES == 2 && __any_sync(~0u, sg.nt == 2);
+            if constexpr (C::TILES == 2) {
+                if (two) dead = !two_tiles();
+            }
+            if (!two) dead = !one_tile();
+            if (dead) break;
+            u += sg.ke - sg.kb;
+            i0 += (sg.ke - sg.kb) * sg.nt;
         }
         if (dead && lane == 0) {
             atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
@@ -528,12 +701,10 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         const uint32_t sbuf = lane_base + grp * 128;
         const uint64_t scale22 = pack_f32x2(p.scale2, p.scale2);
         const int rt = row / g.hb, rh = row - rt * g.hb;             // this row's token in a tile, and head
-        // Every wait here is for a phase that cannot be followed by the next before this warp has seen it: the warps
-        // wait for one another through barriers only, and all of those end by themselves.
-        uint32_t u = 0, i0 = 0, shared_segs = 0;
+        uint32_t at = 0, u = 0, i0 = 0, ends = 0, twos = 0;          // place on the line; units, steps, steps with pv_done, segments of two tiles
         bool dead = false;
-        for (uint32_t seg = 0; u < units; ++seg) {
-            dead = !mbar_wait(&ctl.seg_full[seg % kSegs], (seg / kSegs) & 1, abort_flag, p.wait_ns);
+        for (uint32_t seg = 0; at < share; ++seg) {
+            dead = !wait_for(&ctl.seg_full[seg % kSegs], (seg / kSegs) & 1, abort_flag, p.wait_ns);
             dead = __any_sync(~0u, dead);
             if (dead) break;
             const PrefixSeg& sg = ctl.segs[seg % kSegs];
@@ -547,9 +718,9 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             float ref = kUnset, l = 0.f;
             for (uint32_t j = (grp ^ i0) & 1; j < steps; j += 2) {
                 const uint32_t i = i0 + j, x = nt == 2 ? j >> 1 : j;
-                if (!dead) dead = !mbar_wait(&ctl.s_full[grp], (i >> 1) & 1, abort_flag, p.wait_ns);
+                if (!dead) dead = !wait_for(&ctl.s_full[grp], (i >> 1) & 1, abort_flag, p.wait_ns);
                 if (nt == 1 && j > 0) {                              // the other group's reference
-                    if (!dead) dead = !mbar_wait(&ctl.ref_done[grp ^ 1][q4], ((i - 1) >> 1) & 1, abort_flag, p.wait_ns);
+                    if (!dead) dead = !wait_for(&ctl.ref_done[grp ^ 1][q4], ((i - 1) >> 1) & 1, abort_flag, p.wait_ns);
                     const float r = ctl.ref[row];
                     if (r != ref) {
                         l *= ex2(ref - r);
@@ -569,60 +740,51 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 }
                 const int j0 = sg.row0 + (sg.kb + static_cast<int>(x)) * kUnit;
                 const unsigned bad = *reinterpret_cast<volatile unsigned*>(&ctl.bad[(u + x) & 7]);
-                uint32_t v[128];
-                DSV4_TMEM_LD_32x32b_X32(sbuf, v);
-                DSV4_TMEM_LD_32x32b_X32(sbuf + 32, (v + 32));
-                DSV4_TMEM_LD_32x32b_X32(sbuf + 64, (v + 64));
-                DSV4_TMEM_LD_32x32b_X32(sbuf + 96, (v + 96));
-                tmem_wait_ld();
-                // base-2 scores relative to the reference (none yet: to 0)
-                const bool unset = ref == kUnset;
-                const float nref = unset ? 0.f : -ref;
-                const uint64_t nref2 = pack_f32x2(nref, nref);
+                if (j0 < lo || j0 + kUnit > sg.hi_min || bad) {      // hidden scores become -inf in tensor memory
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 32) {
+                        const int a = lo - j0 - c, b = hi - j0 - c;  // columns [a, b) of these are seen
+                        uint32_t on = b <= 0 || a >= 32 ? 0u : (b >= 32 ? ~0u : (1u << b) - 1) & (a <= 0 ? ~0u : ~0u << a);
+                        for (int i = 0; bad && i < 32; i += 8)
+                            if (paged_bad_row(g, bad, c + i)) on &= ~(255u << i);
+                        if (__all_sync(~0u, on == ~0u || !valid)) continue;
+                        uint32_t v[32];
+                        DSV4_TMEM_LD_32x32b_X32(sbuf + c, v);
+                        tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 128; c += 2) {
-                    uint64_t y = nref2;
-                    fma_f32x2(y, pack_f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), scale22);
-                    float a, b;
-                    unpack_f32x2(y, a, b);
-                    v[c] = __float_as_uint(a);
-                    v[c + 1] = __float_as_uint(b);
-                }
-                if (j0 < lo || j0 + kUnit > sg.hi_min || bad) {
-                    const int a = lo - j0, b = hi - j0;
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c < a || c >= b) v[c] = 0xFF800000u;
-                    if (bad) {
-#pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (paged_bad_row(g, bad, c)) v[c] = 0xFF800000u;
+                        for (int i = 0; i < 32; ++i)
+                            if (!(on & 1u << i)) v[i] = 0xFF800000u;
+                        DSV4_TMEM_ST_32x32b_X32(sbuf + c, v);
                     }
+                    DSV4_TMEM_WAIT_ST();
                 }
+                // The row's largest score, then its exponentials: the scores are read twice (a row's 128 in registers
+                // throughout would leave none for the rest), the second time a quarter ahead of the exponentials.
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 128; c += 2)
-                    mx[(c >> 1) & 3] = fmaxf(fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), mx[(c >> 1) & 3]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                for (int h = 0; h < 128; h += 64) {
+                    uint32_t v[64];
+                    DSV4_TMEM_LD_32x32b_X64(sbuf + h, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2)
+                        mx[(c >> 1) & 3] = max3(__uint_as_float(v[c]), __uint_as_float(v[c + 1]), mx[(c >> 1) & 3]);
+                }
+                uint32_t v[2][32];
+                DSV4_TMEM_LD_32x32b_X32(sbuf, v[0]);
+                mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool unset = ref == kUnset;
+                const float top = fmaf(mx[0], p.scale2, unset ? 0.f : -ref);
                 // A row that outruns its reference moves it (its first scores always do).
                 const bool move = valid && (unset ? top > -INFINITY : top > kSpan);
                 if (__any_sync(~0u, move)) {
                     const float f = move && !unset ? ex2(-top) : 1.f;
-                    const uint64_t d2 = move ? pack_f32x2(-top, -top) : 0ull;
-#pragma unroll
-                    for (int c = 0; c < 128; c += 2) {
-                        uint64_t y = pack_f32x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-                        add_f32x2(y, d2);
-                        float a, b;
-                        unpack_f32x2(y, a, b);
-                        v[c] = __float_as_uint(a);
-                        v[c + 1] = __float_as_uint(b);
-                    }
                     if (move) ref = unset ? top : ref + top;
                     l *= f;
-                    if (x > 0 && __any_sync(~0u, f != 1.f)) {        // O by the factors, once the product before is done
-                        const uint32_t ip = i - (nt == 2 ? 2 : 1);
-                        if (!dead) dead = !mbar_wait(&ctl.pv_done[ip & 1], (ip >> 1) & 1, abort_flag, p.wait_ns);
+                    if (x > 0 && __any_sync(~0u, f != 1.f)) {
+                        // O by the factors, once the product before is done (of two tiles, this one's is: see above)
+                        const uint32_t e = ends + j - 1;
+                        if (!dead && nt == 1) dead = !wait_for(&ctl.pv_done[e & 1], (e >> 1) & 1, abort_flag, p.wait_ns);
                         dead = __any_sync(~0u, dead);
                         tc_fence_after();
 #pragma unroll 1
@@ -642,54 +804,75 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 if (lane == 0) mbar_arrive(&ctl.ref_done[grp][q4]);
                 // P = 2^(s - m) in bf16, over the scores (rounded: the tensor core takes bf16 beside bf16 V; the sum stays
                 // in fp32)
+                const float nref = ref == kUnset ? 0.f : -ref;
+                const uint64_t nref2 = pack_f32x2(nref, nref);
                 uint64_t sum[2] = {0ull, 0ull};
+                auto exps = [&](int h) {
+                    uint32_t o[16];
+                    uint32_t (&now)[32] = v[h & 1], (&next)[32] = v[~h & 1];
+                    tmem_wait_ld();
+                    if (h < 3) DSV4_TMEM_LD_32x32b_X32(sbuf + 32 * h + 32, next);
 #pragma unroll
-                for (int c = 0; c < 128; c += 2) {
-                    const float a = ex2(__uint_as_float(v[c])), b = ex2(__uint_as_float(v[c + 1]));
-                    add_f32x2(sum[(c >> 1) & 1], pack_f32x2(a, b));
-                    v[c >> 1] = pack2(a, b);
-                }
-                DSV4_TMEM_ST_32x32b_X32(sbuf, v);
-                DSV4_TMEM_ST_32x32b_X32(sbuf + 32, (v + 32));
-                add_f32x2(sum[0], sum[1]);
-                float sa, sb;
-                unpack_f32x2(sum[0], sa, sb);
-                l += sa + sb;
+                    for (int c = 0; c < 32; c += 2) {
+                        uint64_t y = nref2;
+                        fma_f32x2(y, pack_f32x2(__uint_as_float(now[c]), __uint_as_float(now[c + 1])), scale22);
+                        float a, b;
+                        unpack_f32x2(y, a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        add_f32x2(sum[(c >> 1) & 1], pack_f32x2(a, b));
+                        o[c >> 1] = pack2(a, b);
+                    }
+                    DSV4_TMEM_ST_32x32b_X16(sbuf + 16 * h, o);
+                };
+                exps(0);
+                exps(1);
+                exps(2);
+                exps(3);
                 DSV4_TMEM_WAIT_ST();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.p_full[grp]);
+                add_f32x2(sum[0], sum[1]);
+                float sa, sb;
+                unpack_f32x2(sum[0], sa, sb);
+                l += sa + sb;
             }
             dead = __any_sync(~0u, dead);
             if (dead) break;
             // ---------------------------------------------------------------- the segment's part
-            // (the product's end is waited for first: it says that all warps are done with the segment before)
+            // The end of the last product, once the last step is known to have come to its softmax (the phase before is over
+            // then). The warps of the same rows in both groups meet here: all that either waits for in the next segment comes
+            // after all of this one.
             const uint32_t il = i0 + steps - 1 - (nt == 2 ? 1 - tile : 0);
-            dead = !mbar_wait(&ctl.pv_done[il & 1], (il >> 1) & 1, abort_flag, p.wait_ns);
+            if ((il & 1) != static_cast<uint32_t>(grp))
+                dead = !wait_for(&ctl.ref_done[grp ^ 1][q4], (il >> 1) & 1, abort_flag, p.wait_ns);
+            const uint32_t e = ends + steps - 1;
+            if (!dead)
+                dead = nt == 2 ? !wait_for(&ctl.o_done[grp], twos & 1, abort_flag, p.wait_ns)
+                               : !wait_for(&ctl.pv_done[e & 1], (e >> 1) & 1, abort_flag, p.wait_ns);
+            if (nt == 2) ++twos;
+            else ends += steps;
             int ch0 = 0, chn = C::DV;                                // this warp's channels
-            if (nt == 1) {
-                // the other group's warp of the same rows: the last reference, both sums
-                if (!dead && (il & 1) != static_cast<uint32_t>(grp))
-                    dead = !mbar_wait(&ctl.ref_done[grp ^ 1][q4], (il >> 1) & 1, abort_flag, p.wait_ns);
+            if (nt == 1) {                                           // both have the same rows: the last reference, both sums
                 const float r = ctl.ref[row];
                 ctl.l[grp][row] = r == ref ? l : l * ex2(ref - r);
                 ref = r;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.l_ready[grp][q4]);
-                if (!dead) dead = !mbar_wait(&ctl.l_ready[grp ^ 1][q4], shared_segs & 1, abort_flag, p.wait_ns);
-                ++shared_segs;
-                l = ctl.l[0][row] + ctl.l[1][row];
                 ch0 = grp * (C::DV / 2);
                 chn = C::DV / 2;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.l_ready[grp][q4]);
+            if (!dead) dead = !wait_for(&ctl.l_ready[grp ^ 1][q4], seg & 1, abort_flag, p.wait_ns);
+            if (nt == 1) l = ctl.l[0][row] + ctl.l[1][row];
             dead = __any_sync(~0u, dead);
             if (dead) break;
             tc_fence_after();
             const bool home = sg.kb == 0;
-            const size_t at = (static_cast<size_t>(sg.tok0 + (valid ? tok : 0)) * g.H + sg.head0 + (valid ? rh : 0));
+            const size_t qh = (static_cast<size_t>(sg.tok0 + (valid ? tok : 0)) * g.H + sg.head0 + (valid ? rh : 0));
             const int crow = static_cast<int>(tile) * 128 + row;
             float* dst;
-            if (home) dst = p.home_o + (static_cast<size_t>(sg.q.own) * g.total_q * g.H + at) * D + sg.half * 256 + ch0;
+            if (home) dst = p.home_o + (static_cast<size_t>(sg.q.own) * g.total_q * g.H + qh) * D + sg.half * 256 + ch0;
             else dst = p.cont_o + (static_cast<size_t>(worker) * C::TILES * 128 + crow) * C::DV + ch0;
             if (any) {
 #pragma unroll 1
@@ -699,8 +882,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                     tmem_wait_ld();
                     if (valid) {
 #pragma unroll
-                        for (int b = 0; b < 32; b += 4)
-                            *reinterpret_cast<uint4*>(dst + c + b) = make_uint4(r[b], r[b + 1], r[b + 2], r[b + 3]);
+                        for (int b = 0; b < 32; b += 8) store32(dst + c + b, r + b);
                     }
                 }
                 if (valid && (nt == 2 || grp == 0)) {
@@ -712,14 +894,14 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                     if (home) {
                         int np = 1;
                         if (sg.ke < sg.n) {                          // the CTAs that go on with the segment
-                            const long long end = sched.u0 + u + n - sg.ke + sg.n, T = sched.total;
+                            const long long end = sched.u0 + at + static_cast<long long>(sg.n) * sg.weight, T = sched.total;   // (home: the segment starts here)
                             int last = static_cast<int>((end * sched.ge - 1) / T);
                             while (last + 1 < sched.ge && T * (last + 1) / sched.ge < end) ++last;
                             while (T * last / sched.ge >= end) --last;
                             np = last - worker + 1;
                         }
                         const int info = worker | np << 8 | crow << 16;
-                        p.home_ml[static_cast<size_t>(sg.q.own * C::HALVES + sg.half) * g.total_q * g.H + at] =
+                        p.home_ml[static_cast<size_t>(sg.q.own * C::HALVES + sg.half) * g.total_q * g.H + qh] =
                             make_float4(m, l, __int_as_float(info), __int_as_float(sg.q.own && lo > 0 ? 1 : 0));
                     } else {
                         p.cont_ml[static_cast<size_t>(worker) * C::TILES * 128 + crow] = make_float2(m, l);
@@ -729,6 +911,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.o_empty);
+            at += sg.cost;
             u += n;
             i0 += steps;
         }
@@ -752,7 +935,8 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         if (tid == 0) {
             const uint32_t seg = max(max(ctl.seg_end[0], ctl.seg_end[1]), ctl.seg_end[2]);
             if (seg && !p.fault) mbar_wait(&ctl.q_full, (seg - 1) & 1, nullptr, kDrainNs);
-            ring_drain<ST>(ctl.full, ctl.ring_end);
+            for (int i = 0; i < ST; ++i)
+                if (ctl.last[i]) mbar_wait(&ctl.full[ctl.last[i] & 1][i], ctl.last[i] >> 1 & 1, nullptr, kDrainNs);
         }
         __syncthreads();
     }
@@ -891,7 +1075,7 @@ PrefixWs prefix_ws(const dsv4_paged_prefix_args& a) {
     w.cont_o = take(ctas * tiles * 128 * dv * 4);
     w.plen = take(ctas * a.groups * 4);
     w.err = take(ctas * 4);
-    w.total = at;
+    w.total = at + 256;                  // (the parts start at a multiple of 256, wherever the workspace does)
     return w;
 }
 
@@ -920,6 +1104,7 @@ int run(const dsv4_paged_prefix_args& a, uint8_t* ws, uint32_t* eword, cudaStrea
         return DSV4_ERR_LAUNCH;
     const int ctas = prefix_ctas();
     const PrefixWs w = prefix_ws(a);
+    ws = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(ws), 256));
     p.home_ml = reinterpret_cast<float4*>(ws + w.home_ml);
     p.cont_ml = reinterpret_cast<float2*>(ws + w.cont_ml);
     p.home_o = reinterpret_cast<float*>(ws + w.home_o);
@@ -930,11 +1115,14 @@ int run(const dsv4_paged_prefix_args& a, uint8_t* ws, uint32_t* eword, cudaStrea
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.lse = a.lse;
     p.scale2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    p.negate = p.scale2 < 0.f;
+    p.scale2 = std::fabs(p.scale2);
+    if (p.scale2 == 0.f) p.scale2 = FLT_MIN;             // (a hidden row's -inf stays -inf, and any score is 0 beside a reference)
     p.orp = a.out_rope_pos;
     p.or_pairs = a.out_rope_pos ? a.out_rope_dim / 2 : 0;
     for (int j = 0; j < p.or_pairs; ++j) p.or_freq[j] = std::pow(a.out_rope_theta, -2.0 * j / a.out_rope_dim);
     p.shared = a.v_pages == nullptr;
-    p.min_units = 2;
+    p.min_units = 6;                     // two units of one tile
     const WaitCtl wc = wait_ctl(DSV4_WAIT_FAULT_PAGED_PREFIX);
     p.fault = wc.fault;
     p.wait_ns = wc.wait_ns;
