@@ -632,13 +632,15 @@ int dsv4_paged_evict(const dsv4_paged_evict_args* a, void* ws, size_t ws_bytes, 
     return launch_paged_evict(*a, body_of(ws), eword_of(ws), reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t dsv4_paged_plan_workspace_size(const dsv4_paged_plan_args* a) { return a && paged_plan_sizes_ok(a) ? kWsHeader : 0; }
+size_t dsv4_paged_plan_workspace_size(const dsv4_paged_plan_args* a) {
+    return a && paged_plan_sizes_ok(a) ? kWsHeader + paged_plan_ws_bytes() : 0;
+}
 
 int dsv4_paged_plan(const dsv4_paged_plan_args* a, void* ws, size_t ws_bytes, dsv4_stream_t stream) {
     LaunchScope scope;
     if (!paged_plan_ok(a) || !dev_ptr_ok(ws) || ws_bytes < dsv4_paged_plan_workspace_size(a)) return DSV4_ERR_INVALID_ARG;
     if (int rc = device_check()) return rc;
-    return launch_paged_plan(*a, eword_of(ws), reinterpret_cast<cudaStream_t>(stream));
+    return launch_paged_plan(*a, body_of(ws), eword_of(ws), reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t dsv4_paged_prefix_attn_workspace_size(const dsv4_paged_prefix_args* a) {

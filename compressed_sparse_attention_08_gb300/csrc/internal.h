@@ -92,7 +92,8 @@ size_t paged_weights_ws_bytes(const dsv4_paged_weights_args& a);
 int launch_paged_weights(const dsv4_paged_weights_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
 size_t paged_evict_ws_bytes(const dsv4_paged_evict_args& a);
 int launch_paged_evict(const dsv4_paged_evict_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
-int launch_paged_plan(const dsv4_paged_plan_args& a, uint32_t* eword, cudaStream_t stream);
+size_t paged_plan_ws_bytes();
+int launch_paged_plan(const dsv4_paged_plan_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);
 int launch_rope(const dsv4_rope_args& a, cudaStream_t stream);
 size_t paged_prefix_ws_bytes(const dsv4_paged_prefix_args& a);
 int launch_paged_prefix(const dsv4_paged_prefix_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t stream);

@@ -3,48 +3,55 @@
 // rules). The sources keep dense per-sequence buffers; the paged form is this library's own.
 //
 // All of it follows from three sums over the sequences: of tokens, of pages given back, of pages taken.
-// Each CTA forms the sums of the whole batch itself (at most 2,048 sequences, four per thread), so the
-// CTAs need nothing from one another, and then takes its share of three flat lists: tokens, pages
-// given back, pages taken. An entry finds its sequence by bisection in the sums. A page that is given back and
-// taken again is read where it stands in its table, so the lists need no order among them. The state
-// (lengths, pages held, the stack's height) may be updated in place: the CTAs form one cluster, and its
-// first writes the state after all have met at the cluster's barrier.
+// One CTA forms them for the whole batch (at most 2,048 sequences, four per thread) and writes the state (lengths,
+// pages held, the stack's height; in place too: it has read them all by then). What is left are three flat lists,
+// tokens, pages given back and pages taken, whose entries find their sequence by bisection in the sums. A page
+// that is given back and taken again is read where it stands in its table, so the lists need no order among
+// them. With few tokens the same CTA goes through them; with many a second launch does, from the sums in the
+// workspace, on the whole device.
+// Latency bounds both: a launch, the lengths' loads, three sums, then a token's search, its sequence's numbers, its page and its
+// slot, one after the other.
 #include "internal.h"
 #include "common.cuh"
 
 namespace dsv4 {
 namespace {
 
-constexpr int kT = 512, kPer = 4, kMaxBatch = kT * kPer, kCluster = 8;
+constexpr int kMaxBatch = 2048, kListT = 256;
 
-__device__ __forceinline__ void red_cluster_or(uint32_t addr, uint32_t v) {
-    asm volatile("red.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
+// What the lists need of a batch: sums (inclusive) and numbers per sequence.
+struct PlanSums {
+    int64_t next[kMaxBatch];             // position of the first new token
+    int tok[kMaxBatch], back[kMaxBatch], take[kMaxBatch];
+    int rows[kMaxBatch], held[kMaxBatch], from[kMaxBatch];   // before the step; the first page given back
+    uint32_t off[kMaxBatch / 32];        // sequences that are not served
+    int stack, count, taken, n_back;     // the stack's height with what is given back, and before; pages taken, given back
+};
 
-// Inclusive sum over the block of a thread's four numbers; v becomes the sums, the total is returned.
-__device__ __forceinline__ long long block_sum(long long (&v)[kPer], long long* part) {
+// Inclusive sum over the block of a thread's PER numbers; v becomes the sums, the total is returned.
+template <int T, int PER>
+__device__ __forceinline__ long long block_sum(long long (&v)[PER], long long* part) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int i = 1; i < kPer; ++i) v[i] += v[i - 1];
-    long long x = v[kPer - 1];
+    for (int i = 1; i < PER; ++i) v[i] += v[i - 1];
+    long long x = v[PER - 1];
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
         const long long o = __shfl_up_sync(~0u, x, w);
         if (lane >= w) x += o;
     }
-    __syncthreads();                                     // (part may still be read by the sum before)
     if (lane == 31) part[warp] = x;
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w < kT / 32; ++w) {
+    for (int w = 0; w < T / 32; ++w) {
         const long long p = part[w];
         before += w < warp ? p : 0;
         total += p;
     }
-    const long long base = before + x - v[kPer - 1];
+    const long long base = before + x - v[PER - 1];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] += base;
+    for (int i = 0; i < PER; ++i) v[i] += base;
     return total;
 }
 
@@ -58,124 +65,36 @@ __device__ __forceinline__ int find(const int* ends, int n, int x) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kT)
-paged_plan_kernel(const __grid_constant__ dsv4_paged_plan_args p, uint32_t* eword) {
-    __shared__ int s_tok[kMaxBatch], s_back[kMaxBatch], s_take[kMaxBatch];   // inclusive sums
-    __shared__ uint32_t s_off[kMaxBatch / 32];                               // sequences that are not served
-    __shared__ long long s_part[kT / 32];
-    __shared__ int s_taken;
-    __shared__ uint32_t s_err;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int rank = blockIdx.x, ctas = gridDim.x, B = p.batch;
-    pdl_trigger();
-    pdl_wait();
-    if (tid == 0) { s_err = 0; s_taken = 0; }
-    if (tid < kMaxBatch / 32) s_off[tid] = 0;
-    if (ctas > 1) cluster_arrive();
-    const int cap = p.free_cap;
-    uint32_t err = 0;
-    const int count0 = *p.free_count, count = min(max(count0, 0), cap);
-    if (count != count0) err |= DSV4_EWORD_BAD_INDEX;
-    // this thread's sequences
-    int n[kPer], L[kPer], h[kPer], keep[kPer], take[kPer];
-    long long sum[kPer];
-    bool off[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int s = tid * kPer + i;
-        n[i] = L[i] = h[i] = keep[i] = take[i] = 0;
-        off[i] = false;
-        if (s < B) {
-            const int n0 = p.new_len ? p.new_len[s] : 0, L0 = p.kv_len[s], h0 = p.held[s], sh = p.shared ? p.shared[s] : 0;
-            n[i] = max(n0, 0);
-            L[i] = min(max(L0, 0), p.max_pages * p.page_size);
-            h[i] = min(max(h0, 0), p.max_pages);
-            keep[i] = min(max(sh, 0), h[i]);
-            if (n0 < 0 || L[i] != L0 || h[i] != h0 || sh < 0) err |= DSV4_EWORD_BAD_INDEX;
-        }
-        sum[i] = n[i];
-    }
-    block_sum(sum, s_part);
-    long long back[kPer], want[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int s = tid * kPer + i;
-        want[i] = (static_cast<long long>(L[i]) + n[i] + p.page_size - 1) / p.page_size;
-        off[i] = (n[i] > 0 && sum[i] > p.total_q) || want[i] > p.max_pages;
-        if (off[i]) err |= DSV4_EWORD_BAD_INDEX;
-        keep[i] = off[i] ? h[i] : static_cast<int>(min(max(want[i], static_cast<long long>(keep[i])), static_cast<long long>(h[i])));
-        back[i] = h[i] - keep[i];
-        take[i] = off[i] ? 0 : static_cast<int>(max(want[i] - h[i], 0ll));
-        if (s < B) s_tok[s] = static_cast<int>(min(sum[i], static_cast<long long>(p.total_q)));
-    }
-    // (at most 2,048 x 2^26 pages: the sums of counts that cannot be are cut to the stack's size)
-    long long ends[kPer];
-    const long long all_back = block_sum(back, s_part);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) ends[i] = take[i];
-    block_sum(ends, s_part);
-    const int room = cap - count, n_back = static_cast<int>(min(all_back, static_cast<long long>(room)));
-    if (all_back > room) err |= DSV4_EWORD_BAD_INDEX;
-    const int stack = count + n_back;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int s = tid * kPer + i;
-        if (s >= B) continue;
-        if (take[i] > 0 && ends[i] > stack) {
-            off[i] = true;
-            err |= DSV4_EWORD_NO_PAGES;
-        }
-        s_back[s] = static_cast<int>(min(back[i], static_cast<long long>(n_back)));
-        s_take[s] = static_cast<int>(min(ends[i], static_cast<long long>(cap) + 1));
-        if (off[i]) atomicOr(&s_off[s >> 5], 1u << (s & 31));
-    }
-    // Pages taken in all: the sum at the last sequence that is served and takes some. (Behind the first that is not
-    // served no one takes any, and the sums of those before do not exceed the stack.)
-    int top = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (take[i] > 0 && !off[i]) top = static_cast<int>(ends[i]);
-    top = __reduce_max_sync(~0u, top);
-    if (lane == 0 && top) atomicMax(&s_taken, top);
-    __syncthreads();
-    const int taken = s_taken;
+// The three lists, by threads `self`, `self` + `step`, ..; returns error bits. The sums tok, back and take are passed apart.
+__device__ uint32_t plan_lists(const dsv4_paged_plan_args& p, const PlanSums& q, const int* tok, const int* back, const int* take, int self,
+                               int step) {
+    const int B = p.batch;
     const long long mp = p.max_pages;
-    const int g0 = rank * kT + tid, step = ctas * kT;
-    // Pages given back. (Where the stack has no room for all, the sums are cut and the first n_back are kept: from a
-    // sequence's first on, so its place is counted from what it keeps.)
-    auto back_page = [&](int i) {
-        const int s = find(s_back, B, i);
-        const int first = s ? s_back[s - 1] : 0;
-        const int hs = min(max(p.held[s], 0), p.max_pages);
-        const int sh = min(max(p.shared ? p.shared[s] : 0, 0), hs);
-        const int Ls = min(max(p.kv_len[s], 0), p.max_pages * p.page_size), ns = max(p.new_len ? p.new_len[s] : 0, 0);
-        const long long w = (static_cast<long long>(Ls) + ns + p.page_size - 1) / p.page_size;
-        const int from = static_cast<int>(max(w, static_cast<long long>(sh)));
-        return p.block_table[s * mp + from + (i - first)];
+    uint32_t err = 0;
+    auto given_page = [&](int i) {                       // the i-th page given back
+        const int s = find(back, B, i);
+        return p.block_table[s * mp + q.from[s] + (i - (s ? back[s - 1] : 0))];
     };
-    for (int i = g0; i < n_back; i += step) p.free_pages[count + i] = back_page(i);
     auto taken_page = [&](int k) {                       // the k-th page taken
-        const int x = stack - 1 - k;
-        return x < count ? p.free_pages[x] : back_page(x - count);
+        const int x = q.stack - 1 - k;
+        return x < q.count ? p.free_pages[x] : given_page(x - q.count);
     };
-    for (int k = g0; k < taken; k += step) {
-        const int s = find(s_take, B, k);
-        const int first = s ? s_take[s - 1] : 0;
-        p.block_table[s * mp + min(max(p.held[s], 0), p.max_pages) + (k - first)] = taken_page(k);
+    for (int i = self; i < q.n_back; i += step) p.free_pages[q.count + i] = given_page(i);
+    for (int k = self; k < q.taken; k += step) {
+        const int s = find(take, B, k);
+        p.block_table[s * mp + q.held[s] + (k - (s ? take[s - 1] : 0))] = taken_page(k);
     }
-    const int tokens = B > 0 ? s_tok[B - 1] : 0;
-    for (int t = g0; t < p.total_q; t += step) {
+    const int tokens = B > 0 ? tok[B - 1] : 0;
+    for (int t = self; t < p.total_q; t += step) {
         long long slot = -1, pos = 0;
         int s = -1;
         if (t < tokens) {
-            s = find(s_tok, B, t);
-            const int i = t - (s ? s_tok[s - 1] : 0);
-            const int Ls = min(max(p.kv_len[s], 0), p.max_pages * p.page_size);
-            pos = (p.next_pos ? p.next_pos[s] : Ls) + i;
-            if (!(s_off[s >> 5] >> (s & 31) & 1)) {
-                const int row = Ls + i, j = row / p.page_size;
-                const int hs = min(max(p.held[s], 0), p.max_pages);
-                const int page = j < hs ? p.block_table[s * mp + j] : taken_page((s ? s_take[s - 1] : 0) + j - hs);
+            s = find(tok, B, t);
+            const int i = t - (s ? tok[s - 1] : 0), row = q.rows[s] + i, held = q.held[s];
+            pos = q.next[s] + i;
+            if (!(q.off[s >> 5] >> (s & 31) & 1)) {
+                const int j = row / p.page_size;
+                const int page = j < held ? p.block_table[s * mp + j] : taken_page((s ? take[s - 1] : 0) + j - held);
                 if (page >= 0 && page < p.num_pages) slot = static_cast<long long>(page) * p.page_size + (row - j * p.page_size);
                 else err |= DSV4_EWORD_BAD_INDEX;
             }
@@ -184,30 +103,126 @@ paged_plan_kernel(const __grid_constant__ dsv4_paged_plan_args p, uint32_t* ewor
         if (p.pos) p.pos[t] = pos;
         if (p.seq) p.seq[t] = s;
     }
-    __syncwarp();
-    if (ctas > 1) cluster_wait();                        // (the first CTA's error bits are cleared)
-    err = __reduce_or_sync(~0u, err);
-    if (lane == 0 && err) {
-        if (ctas > 1) red_cluster_or(cluster_map(&s_err, 0), err);
-        else atomicOr(&s_err, err);
-    }
-    __syncwarp();
-    // the state, once every CTA has read it
-    if (ctas > 1) {
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
-    }
-    if (rank != 0) return;
+    return err;
+}
+
+// Sums and state; with `lists`, the lists too. q: in the workspace.
+template <int T, int PER>
+__global__ void __launch_bounds__(T)
+plan_kernel(const __grid_constant__ dsv4_paged_plan_args p, PlanSums* out, int lists, uint32_t* eword) {
+    constexpr int MOST = T * PER;
+    __shared__ int s_tok[MOST], s_back[MOST], s_take[MOST];
+    __shared__ long long s_part[3][T / 32];
+    __shared__ int s_taken;
+    __shared__ uint32_t s_err;
+    const int tid = threadIdx.x, lane = tid & 31, B = p.batch;
+    pdl_trigger();
+    pdl_wait();
+    PlanSums& q = *out;
+    if (tid == 0) { s_err = 0; s_taken = 0; }
+    const int cap = p.free_cap, count0 = *p.free_count, count = min(max(count0, 0), cap);
+    uint32_t err = count != count0 ? DSV4_EWORD_BAD_INDEX : 0;
+    // this thread's sequences
+    int n[PER], L[PER], h[PER], keep[PER], take[PER];
+    long long sum[PER], next[PER];
+    bool off[PER];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int s = tid * kPer + i;
+    for (int i = 0; i < PER; ++i) {
+        const int s = tid * PER + i;
+        n[i] = L[i] = h[i] = keep[i] = take[i] = 0;
+        off[i] = false;
+        next[i] = 0;
+        if (s < B) {
+            const int n0 = p.new_len ? p.new_len[s] : 0, L0 = p.kv_len[s], h0 = p.held[s], sh = p.shared ? p.shared[s] : 0;
+            n[i] = max(n0, 0);
+            L[i] = min(max(L0, 0), p.max_pages * p.page_size);
+            h[i] = min(max(h0, 0), p.max_pages);
+            keep[i] = min(max(sh, 0), h[i]);
+            next[i] = p.next_pos ? p.next_pos[s] : L[i];
+            if (n0 < 0 || L[i] != L0 || h[i] != h0 || sh < 0) err |= DSV4_EWORD_BAD_INDEX;
+        }
+        sum[i] = n[i];
+    }
+    block_sum<T, PER>(sum, s_part[0]);
+    long long back[PER], ends[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int s = tid * PER + i;
+        const long long want = (static_cast<long long>(L[i]) + n[i] + p.page_size - 1) / p.page_size;
+        off[i] = (n[i] > 0 && sum[i] > p.total_q) || want > p.max_pages;
+        if (off[i]) err |= DSV4_EWORD_BAD_INDEX;
+        keep[i] = off[i] ? h[i] : static_cast<int>(min(max(want, static_cast<long long>(keep[i])), static_cast<long long>(h[i])));
+        back[i] = h[i] - keep[i];
+        take[i] = off[i] ? 0 : static_cast<int>(max(want - h[i], 0ll));
+        ends[i] = take[i];
+        if (s < B) s_tok[s] = static_cast<int>(min(sum[i], static_cast<long long>(p.total_q)));
+    }
+    // (at most 2,048 x 2^26 pages: sums of counts that cannot be are cut to the stack's size)
+    const long long all_back = block_sum<T, PER>(back, s_part[1]);
+    block_sum<T, PER>(ends, s_part[2]);
+    const int room = cap - count, n_back = static_cast<int>(min(all_back, static_cast<long long>(room)));
+    if (all_back > room) err |= DSV4_EWORD_BAD_INDEX;
+    const int stack = count + n_back;
+    // Pages taken in all: the sum at the last sequence that is served and takes some. (Behind the first that is not
+    // served no one takes any, and the sums of those before do not exceed the stack.)
+    int top = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int s = tid * PER + i;
+        if (take[i] > 0 && ends[i] > stack) {
+            off[i] = true;
+            err |= DSV4_EWORD_NO_PAGES;
+        }
+        if (take[i] > 0 && !off[i]) top = static_cast<int>(ends[i]);
+        if (s >= B) continue;
+        s_back[s] = static_cast<int>(min(back[i], static_cast<long long>(n_back)));
+        s_take[s] = static_cast<int>(min(ends[i], static_cast<long long>(cap) + 1));
+        q.rows[s] = L[i];
+        q.held[s] = h[i];
+        q.from[s] = keep[i];
+        q.next[s] = next[i];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {                      // (bits of a word: 32 / PER neighbouring threads)
+        uint32_t bit = off[i] ? 1u << ((tid * PER + i) & 31) : 0;
+        if (i == 0) top = __reduce_max_sync(~0u, top);
+#pragma unroll
+        for (int w = 1; w < 32 / PER; w <<= 1) bit |= __shfl_xor_sync(~0u, bit, w);
+        n[i] = off[i] ? 0 : n[i];                        // what is added to the state
+        if (i == 0) sum[0] = bit;
+        else sum[0] |= bit;
+    }
+    if (tid % (32 / PER) == 0) q.off[tid * PER / 32] = static_cast<uint32_t>(sum[0]);
+    if (lane == 0 && top) atomicMax(&s_taken, top);
+    __syncthreads();
+    const int taken = s_taken;
+    if (tid == 0) {
+        q.stack = stack;
+        q.count = count;
+        q.taken = taken;
+        q.n_back = n_back;
+    }
+    if (lists) {
+        __syncthreads();                                 // (the numbers in the workspace)
+        err |= plan_lists(p, q, s_tok, s_back, s_take, tid, T);
+    }
+    err = __reduce_or_sync(~0u, err);
+    if (lane == 0 && err) atomicOr(&s_err, err);
+    __syncthreads();
+    // the state (every thread has read it)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int s = tid * PER + i;
         if (s >= B) continue;
         p.cu_q[s + 1] = s_tok[s];
-        p.kv_len_out[s] = off[i] ? L[i] : L[i] + n[i];
+        p.kv_len_out[s] = L[i] + n[i];
         p.held_out[s] = off[i] ? h[i] : keep[i] + take[i];
-        if (p.next_pos_out) p.next_pos_out[s] = p.next_pos[s] + (off[i] ? 0 : n[i]);
+        if (p.next_pos_out) p.next_pos_out[s] = next[i] + n[i];
+        if (!lists) {
+            q.tok[s] = s_tok[s];
+            q.back[s] = s_back[s];
+            q.take[s] = s_take[s];
+        }
     }
     if (tid == 0) {
         p.cu_q[0] = 0;
@@ -216,16 +231,40 @@ paged_plan_kernel(const __grid_constant__ dsv4_paged_plan_args p, uint32_t* ewor
     }
 }
 
+__global__ void __launch_bounds__(kListT)
+plan_lists_kernel(const __grid_constant__ dsv4_paged_plan_args p, const PlanSums* in, uint32_t* eword) {
+    __shared__ int s_tok[kMaxBatch], s_back[kMaxBatch], s_take[kMaxBatch];
+    const PlanSums& q = *in;
+    pdl_trigger();
+    pdl_wait();
+    for (int s = threadIdx.x; s < p.batch; s += kListT) {
+        s_tok[s] = q.tok[s];
+        s_back[s] = q.back[s];
+        s_take[s] = q.take[s];
+    }
+    __syncthreads();
+    uint32_t err = plan_lists(p, q, s_tok, s_back, s_take, blockIdx.x * kListT + threadIdx.x, gridDim.x * kListT);
+    err = __reduce_or_sync(~0u, err);
+    if ((threadIdx.x & 31) == 0 && err) atomicOr(eword, err);
+}
+
 }  // namespace
 
-int launch_paged_plan(const dsv4_paged_plan_args& a, uint32_t* eword, cudaStream_t st) {
-    // One CTA while its threads have a few tokens each; eight with more (the cluster's barriers cost
-    // about as much as the tokens of one CTA then).
-    const long long work = a.total_q;
-    const unsigned ctas = work <= 4 * kT ? 1 : kCluster;
+size_t paged_plan_ws_bytes() { return sizeof(PlanSums); }
+
+int launch_paged_plan(const dsv4_paged_plan_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t st) {
+    PlanSums* q = reinterpret_cast<PlanSums*>(ws);
+    // One launch while a thread has a few tokens; a second one for more costs less than they do then.
+    const int lists = a.total_q <= 2048;
     count_launch();
-    return launch_cluster_k(paged_plan_kernel, dim3(ctas), dim3(kT), 0, st, true, ctas, a, eword) == cudaSuccess ? DSV4_OK
-                                                                                                                  : DSV4_ERR_LAUNCH;
+    const cudaError_t e = a.batch <= 128 ? launch_k(plan_kernel<128, 1>, dim3(1), dim3(128), 0, st, true, a, q, lists, eword)
+                                         : launch_k(plan_kernel<512, 4>, dim3(1), dim3(512), 0, st, true, a, q, lists, eword);
+    if (e != cudaSuccess) return DSV4_ERR_LAUNCH;
+    if (lists) return DSV4_OK;
+    const int sms = sm_count() > 0 ? sm_count() : 152, most = 4 * sms, need = (a.total_q + kListT - 1) / kListT;
+    count_launch();
+    return launch_k(plan_lists_kernel, dim3(need < most ? need : most), dim3(kListT), 0, st, true, a, q, eword) == cudaSuccess
+               ? DSV4_OK : DSV4_ERR_LAUNCH;
 }
 
 }  // namespace dsv4

@@ -13,8 +13,15 @@
 // bytes half a part apart) and goes down the heads with it, so that the cosines and sines of its pairs
 // are read from shared memory once and stay in registers. They are formed once per CTA, in fp64 (Cody-
 // Waite reduced), while the first rows are already on their way.
+// What matters is how many such CTAs an SM holds (each waits for a position, then for its loads and angles): 128
+// threads held to 72 registers where a column is two vectors and to 48 where it is one. Measured: 2,039 tokens of 64 + 8 + 8
+// heads x 128 with the append 17.2 us, 4.8 TB/s (with 256 threads 19.2); 1,023 tokens of 64 + 1 x 512, 64 channels
+// turning, 28.2 us, 4.8 TB/s; 8,192 tokens of 32 + 8 x 128 in fp32 60.8 us, 5.5 TB/s of 6.8; 16 tokens 4.1 us. CTAs that walk
+// the tokens with the next one's loads in registers were slower (23, 37 and 83 us): fewer fit, and a barrier a token
+// ties their threads together.
 #include <cmath>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "internal.h"
 #include "common.cuh"
@@ -22,7 +29,8 @@
 namespace dsv4 {
 namespace {
 
-constexpr int kT = 256, kMaxPairs = 256;
+constexpr int kT = 128, kMaxPairs = 256;
+constexpr int kInFlight = 4;             // heads per thread whose loads are in flight together
 
 struct RopePart {                        // queries, keys or values
     const uint8_t* src;
@@ -108,11 +116,12 @@ struct Vec<float> {
 enum { kPairs = 0, kHalves = 1, kScalar = 2 };
 
 template <class E, int MODE>
-__global__ void __launch_bounds__(kT)
+__global__ void __launch_bounds__(kT, MODE == kHalves ? 7 : 10)
 rope_kernel(const __grid_constant__ RopeParams p) {
     using V = Vec<E>;
-    constexpr int N = V::N, U = 4;                       // heads whose loads are in flight together
+    constexpr int N = V::N, U = kInFlight;
     constexpr int NF = MODE == kPairs ? N / 2 : MODE == kHalves ? N : 1;
+    using Data = typename std::conditional<MODE == kScalar, E, uint4>::type;
     __shared__ float2 cs[kMaxPairs];
     const int tid = threadIdx.x;
     const int tok = blockIdx.x / p.split, part = blockIdx.x - tok * p.split;
@@ -120,86 +129,81 @@ rope_kernel(const __grid_constant__ RopeParams p) {
     pdl_wait();
     const int64_t pos = p.pos[tok];
     const long long slot = p.slots ? p.slots[tok] : tok;
-    const bool stored = !p.slots || (slot >= 0 && slot < p.n_slots);
-    for (int i = tid; i < p.pairs; i += kT) {
-        float sn, c;
-        sincosf(reduced_angle(static_cast<double>(pos) * p.freq[i]), &sn, &c);
-        cs[i] = make_float2(c * p.magnitude, sn * p.magnitude * p.sign);
-    }
-    __syncthreads();
-    const int heads = p.part[0].heads + (stored ? p.part[1].heads + p.part[2].heads : 0);
-    const int h0 = heads * part / p.split, h1 = heads * (part + 1) / p.split;
+    const int most = p.part[0].heads + p.part[1].heads + p.part[2].heads;
+    const int h0 = most * part / p.split, hn = most * (part + 1) / p.split;
     const int rp = p.cols < kT ? kT / p.cols : 1;        // heads per pass
-    for (int c0 = 0; c0 < p.cols; c0 += kT) {            // (more than kT columns only in single channels)
-        const int sub = tid / p.cols, col = c0 + tid - sub * p.cols;
-        if (sub >= rp || col >= p.cols) continue;
-        const bool rot = col >= p.rot0 && col < p.rot0 + p.rot;
-        // the column's place in a head, and its pairs
-        int at;
+    const int sub = tid / p.cols;
+    for (int c0 = 0; c0 < p.cols; c0 += kT) {            // (more than kT columns: in laps)
+        const int col = c0 + tid - sub * p.cols;
+        const bool here = sub < rp && col < p.cols;
+        const bool rot = here && col >= p.rot0 && col < p.rot0 + p.rot;
+        constexpr int width = MODE == kScalar ? static_cast<int>(sizeof(E)) : 16;
+        const int at = MODE == kPairs || col < p.rot0 + p.rot ? col * width : col * width + p.half;   // place in a head
+        // where a head's column comes from and goes to; nothing in place where it does not turn
+        auto place = [&](int h, const uint8_t*& src, uint8_t*& dst) {
+            int w = 0;
+            if (h >= p.part[0].heads) { h -= p.part[0].heads; w = 1; }
+            if (w && h >= p.part[1].heads) { h -= p.part[1].heads; w = 2; }
+            const RopePart& r = p.part[w];
+            src = r.src + tok * r.src_stride + static_cast<long long>(h) * p.row + at;
+            dst = r.dst + (w ? slot : tok) * r.dst_stride + static_cast<long long>(h) * p.row + at;
+            return rot && w < 2;
+        };
+        Data a[U], b[U];
+        auto load = [&](int base) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = base + u * rp;
+                if (!here || h >= hn) continue;
+                const uint8_t* src;
+                uint8_t* dst;
+                place(h, src, dst);
+                a[u] = *reinterpret_cast<const Data*>(src);
+                if (MODE != kPairs && rot) b[u] = *reinterpret_cast<const Data*>(src + p.half);
+            }
+        };
+        load(h0 + sub);                                  // (on their way while the angles are formed)
+        if (c0 == 0) {
+            for (int i = tid; i < p.pairs; i += kT) {
+                float sn, c;
+                sincosf(reduced_angle(static_cast<double>(pos) * p.freq[i]), &sn, &c);
+                cs[i] = make_float2(c * p.magnitude, sn * p.magnitude * p.sign);
+            }
+            __syncthreads();
+        }
+        if (!here) continue;
+        // a token without a slot stores no keys and values
+        const int h1 = p.slots && !(slot >= 0 && slot < p.n_slots) ? min(hn, p.part[0].heads) : hn;
         float2 f[NF];
         unsigned in = ~0u;                               // pairs of the column that belong to the part
         if constexpr (MODE == kPairs) {
-            at = col * 16;
             in = 0;
 #pragma unroll
             for (int i = 0; i < NF; ++i) {
                 const int j = (col * N - p.first) / 2 + i;
-                const bool here = j >= 0 && j < p.pairs;
-                in |= here ? 1u << i : 0u;
-                f[i] = here ? cs[j] : make_float2(1.f, 0.f);
+                const bool on = j >= 0 && j < p.pairs;
+                in |= on ? 1u << i : 0u;
+                f[i] = on ? cs[j] : make_float2(1.f, 0.f);
             }
         } else {
-            const int width = MODE == kHalves ? 16 : static_cast<int>(sizeof(E));
-            at = (col < p.rot0 + p.rot ? col * width : col * width + p.half);
 #pragma unroll
             for (int i = 0; i < NF; ++i) f[i] = rot ? cs[(col - p.rot0) * NF + i] : make_float2(1.f, 0.f);
         }
         for (int base = h0 + sub; base < h1; base += U * rp) {
-            const uint8_t* src[U];
-            uint8_t* dst[U];
-            bool turn[U], on[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                int h = base + u * rp, w = 0;
-                if (h >= p.part[0].heads) { h -= p.part[0].heads; w = 1; }
-                if (w && h >= p.part[1].heads) { h -= p.part[1].heads; w = 2; }
-                const RopePart& r = p.part[w];
-                src[u] = r.src + tok * r.src_stride + static_cast<long long>(h) * p.row + at;
-                dst[u] = r.dst + (w ? slot : tok) * r.dst_stride + static_cast<long long>(h) * p.row + at;
-                turn[u] = rot && w < 2;
-                on[u] = base + u * rp < h1 && (turn[u] || src[u] != dst[u]);   // (in place the copies are there)
-            }
-            if constexpr (MODE == kScalar) {
-                E a[U], b[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (!on[u]) continue;
-                    a[u] = *reinterpret_cast<const E*>(src[u]);
-                    if (rot) b[u] = *reinterpret_cast<const E*>(src[u] + p.half);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (!on[u]) continue;
-                    if (turn[u]) {
+                const int h = base + u * rp;
+                if (h >= h1) continue;
+                const uint8_t* src;
+                uint8_t* dst;
+                const bool turn = place(h, src, dst);
+                if (!turn && src == dst) continue;       // (in place: the copy is there)
+                if (turn) {
+                    if constexpr (MODE == kScalar) {
                         const float x = V::one(&a[u]), y = V::one(&b[u]);
                         V::one(&a[u], x * f[0].x - y * f[0].y);
                         V::one(&b[u], x * f[0].y + y * f[0].x);
-                    }
-                    *reinterpret_cast<E*>(dst[u]) = a[u];
-                    if (rot) *reinterpret_cast<E*>(dst[u] + p.half) = b[u];
-                }
-            } else {
-                uint4 a[U], b[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (!on[u]) continue;
-                    a[u] = *reinterpret_cast<const uint4*>(src[u]);
-                    if (MODE == kHalves && rot) b[u] = *reinterpret_cast<const uint4*>(src[u] + p.half);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (!on[u]) continue;
-                    if (turn[u]) {
+                    } else {
                         float x[N];
                         V::get(a[u], x);
                         if constexpr (MODE == kPairs) {
@@ -223,10 +227,11 @@ rope_kernel(const __grid_constant__ RopeParams p) {
                         }
                         a[u] = V::put(x);
                     }
-                    *reinterpret_cast<uint4*>(dst[u]) = a[u];
-                    if (MODE == kHalves && rot) *reinterpret_cast<uint4*>(dst[u] + p.half) = b[u];
                 }
+                *reinterpret_cast<Data*>(dst) = a[u];
+                if (MODE != kPairs && rot) *reinterpret_cast<Data*>(dst + p.half) = b[u];
             }
+            if (base + U * rp < h1) load(base + U * rp);
         }
     }
 }
@@ -254,11 +259,11 @@ int run(const dsv4_rope_args& a, RopeParams& p, cudaStream_t st) {
         p.rot0 = a.first / w;
         p.rot = hd / w;
     }
-    // With few tokens a token's heads are spread over CTAs of one pass each; with many, one CTA per token
-    // forms the angles once.
+    // With few tokens a token's heads are spread over CTAs of one pass each, with many over CTAs of at most eight passes: each
+    // forms the angles anew, but the tail is short.
     const int rp = p.cols < kT ? kT / p.cols : 1, heads = p.part[0].heads + p.part[1].heads + p.part[2].heads;
-    const int sms = sm_count() > 0 ? sm_count() : 152;
-    p.split = a.tokens < 4 * sms ? (heads + rp - 1) / rp : 1;
+    const int sms = sm_count() > 0 ? sm_count() : 152, each = a.tokens < 4 * sms ? rp : 2 * kInFlight * rp;
+    p.split = (heads + each - 1) / each;
     auto kern = mode == kPairs ? rope_kernel<E, kPairs> : mode == kHalves ? rope_kernel<E, kHalves> : rope_kernel<E, kScalar>;
     count_launch();
     return launch_k(kern, dim3(static_cast<unsigned>(a.tokens) * p.split), dim3(kT), 0, st, true, p) == cudaSuccess ? DSV4_OK
