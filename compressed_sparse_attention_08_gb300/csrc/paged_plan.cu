@@ -3,7 +3,7 @@
 // rules). The sources keep dense per-sequence buffers; the paged form is this library's own.
 //
 // All of it follows from three sums over the sequences: of tokens, of pages given back, of pages taken.
-// One CTA forms them for the whole batch (at most 2,048 sequences, four per thread) and writes the state (lengths,
+// One CTA forms them for the whole batch (at most 2,048 sequences, two per thread) and writes the state (lengths,
 // pages held, the stack's height; in place too: it has read them all by then). What is left are three flat lists,
 // tokens, pages given back and pages taken, whose entries find their sequence by bisection in the sums. A page
 // that is given back and taken again is read where it stands in its table, so the lists need no order among
@@ -28,31 +28,47 @@ struct PlanSums {
     int stack, count, taken, n_back;     // the stack's height with what is given back, and before; pages taken, given back
 };
 
-// Inclusive sum over the block of a thread's PER numbers; v becomes the sums, the total is returned.
+// Inclusive sums over a thread's numbers v[i] of places i * T + tid; v becomes the sums, the total is returned.
+// `part`: scratch for PER * T / 32 numbers, not in use by another sum.
 template <int T, int PER>
 __device__ __forceinline__ long long block_sum(long long (&v)[PER], long long* part) {
+    constexpr int W = T / 32, NP = PER * W, PL = (NP + 31) / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int i = 1; i < PER; ++i) v[i] += v[i - 1];
-    long long x = v[PER - 1];
+    for (int i = 0; i < PER; ++i) {
 #pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-        const long long o = __shfl_up_sync(~0u, x, w);
-        if (lane >= w) x += o;
+        for (int w = 1; w < 32; w <<= 1) {
+            const long long o = __shfl_up_sync(~0u, v[i], w);
+            if (lane >= w) v[i] += o;
+        }
+        if (lane == 31) part[i * W + warp] = v[i];
     }
-    if (lane == 31) part[warp] = x;
     __syncthreads();
-    long long before = 0, total = 0;
+    if (warp == 0) {                                     // the warps' totals, PL neighbours a lane
+        long long x[PL], sum = 0;
 #pragma unroll
-    for (int w = 0; w < T / 32; ++w) {
-        const long long p = part[w];
-        before += w < warp ? p : 0;
-        total += p;
+        for (int i = 0; i < PL; ++i) {
+            x[i] = lane * PL + i < NP ? part[lane * PL + i] : 0;
+            sum += x[i];
+        }
+        long long incl = sum;
+#pragma unroll
+        for (int w = 1; w < 32; w <<= 1) {
+            const long long o = __shfl_up_sync(~0u, incl, w);
+            if (lane >= w) incl += o;
+        }
+        incl -= sum;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            incl += x[i];
+            if (lane * PL + i < NP) part[lane * PL + i] = incl;
+        }
     }
-    const long long base = before + x - v[PER - 1];
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] += base;
-    return total;
+    for (int i = 0; i < PER; ++i)
+        if (i * W + warp > 0) v[i] += part[i * W + warp - 1];
+    return part[NP - 1];
 }
 
 // The first sequence whose sum ends past x (x is below the last sum).
@@ -79,13 +95,20 @@ __device__ uint32_t plan_lists(const dsv4_paged_plan_args& p, const PlanSums& q,
         const int x = q.stack - 1 - k;
         return x < q.count ? p.free_pages[x] : given_page(x - q.count);
     };
-    for (int i = self; i < q.n_back; i += step) p.free_pages[q.count + i] = given_page(i);
-    for (int k = self; k < q.taken; k += step) {
-        const int s = find(take, B, k);
-        p.block_table[s * mp + q.held[s] + (k - (s ? take[s - 1] : 0))] = taken_page(k);
-    }
-    const int tokens = B > 0 ? tok[B - 1] : 0;
-    for (int t = self; t < p.total_q; t += step) {
+    const int tokens = B > 0 ? tok[B - 1] : 0, n_back = q.n_back, taken = q.taken;
+    const long long all = static_cast<long long>(p.total_q) + taken + n_back;   // (one behind the other, so that no thread has all three)
+    for (long long at = self; at < all; at += step) {
+        if (at >= p.total_q) {
+            const int k = static_cast<int>(at - p.total_q), i = k - taken;
+            if (i >= 0) {
+                p.free_pages[q.count + i] = given_page(i);
+            } else {
+                const int s = find(take, B, k);
+                p.block_table[s * mp + q.held[s] + (k - (s ? take[s - 1] : 0))] = taken_page(k);
+            }
+            continue;
+        }
+        const int t = static_cast<int>(at);
         long long slot = -1, pos = 0;
         int s = -1;
         if (t < tokens) {
@@ -112,7 +135,7 @@ __global__ void __launch_bounds__(T)
 plan_kernel(const __grid_constant__ dsv4_paged_plan_args p, PlanSums* out, int lists, uint32_t* eword) {
     constexpr int MOST = T * PER;
     __shared__ int s_tok[MOST], s_back[MOST], s_take[MOST];
-    __shared__ long long s_part[3][T / 32];
+    __shared__ long long s_part[3][MOST / 32];
     __shared__ int s_taken;
     __shared__ uint32_t s_err;
     const int tid = threadIdx.x, lane = tid & 31, B = p.batch;
@@ -128,13 +151,13 @@ plan_kernel(const __grid_constant__ dsv4_paged_plan_args p, PlanSums* out, int l
     bool off[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int s = tid * PER + i;
+        const int s = i * T + tid;
         n[i] = L[i] = h[i] = keep[i] = take[i] = 0;
         off[i] = false;
         next[i] = 0;
         if (s < B) {
             const int n0 = p.new_len ? p.new_len[s] : 0, L0 = p.kv_len[s], h0 = p.held[s], sh = p.shared ? p.shared[s] : 0;
-            n[i] = max(n0, 0);
+            n[i] = min(max(n0, 0), p.total_q + 1);       // (more than fit is more than fit)
             L[i] = min(max(L0, 0), p.max_pages * p.page_size);
             h[i] = min(max(h0, 0), p.max_pages);
             keep[i] = min(max(sh, 0), h[i]);
@@ -147,13 +170,13 @@ plan_kernel(const __grid_constant__ dsv4_paged_plan_args p, PlanSums* out, int l
     long long back[PER], ends[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int s = tid * PER + i;
-        const long long want = (static_cast<long long>(L[i]) + n[i] + p.page_size - 1) / p.page_size;
+        const int s = i * T + tid;
+        const int want = static_cast<int>(static_cast<unsigned>(L[i] + n[i] + p.page_size - 1) / static_cast<unsigned>(p.page_size));
         off[i] = (n[i] > 0 && sum[i] > p.total_q) || want > p.max_pages;
         if (off[i]) err |= DSV4_EWORD_BAD_INDEX;
-        keep[i] = off[i] ? h[i] : static_cast<int>(min(max(want, static_cast<long long>(keep[i])), static_cast<long long>(h[i])));
+        keep[i] = off[i] ? h[i] : min(max(want, keep[i]), h[i]);
         back[i] = h[i] - keep[i];
-        take[i] = off[i] ? 0 : static_cast<int>(max(want - h[i], 0ll));
+        take[i] = off[i] ? 0 : max(want - h[i], 0);
         ends[i] = take[i];
         if (s < B) s_tok[s] = static_cast<int>(min(sum[i], static_cast<long long>(p.total_q)));
     }
@@ -168,7 +191,7 @@ plan_kernel(const __grid_constant__ dsv4_paged_plan_args p, PlanSums* out, int l
     int top = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int s = tid * PER + i;
+        const int s = i * T + tid;
         if (take[i] > 0 && ends[i] > stack) {
             off[i] = true;
             err |= DSV4_EWORD_NO_PAGES;
@@ -182,17 +205,13 @@ plan_kernel(const __grid_constant__ dsv4_paged_plan_args p, PlanSums* out, int l
         q.from[s] = keep[i];
         q.next[s] = next[i];
     }
+    top = __reduce_max_sync(~0u, top);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {                      // (bits of a word: 32 / PER neighbouring threads)
-        uint32_t bit = off[i] ? 1u << ((tid * PER + i) & 31) : 0;
-        if (i == 0) top = __reduce_max_sync(~0u, top);
-#pragma unroll
-        for (int w = 1; w < 32 / PER; w <<= 1) bit |= __shfl_xor_sync(~0u, bit, w);
-        n[i] = off[i] ? 0 : n[i];                        // what is added to the state
-        if (i == 0) sum[0] = bit;
-        else sum[0] |= bit;
+    for (int i = 0; i < PER; ++i) {
+        const uint32_t word = __ballot_sync(~0u, off[i]);
+        if (lane == 0) q.off[(i * T + tid) / 32] = word;
+        if (off[i]) n[i] = 0;                            // what is added to the state
     }
-    if (tid % (32 / PER) == 0) q.off[tid * PER / 32] = static_cast<uint32_t>(sum[0]);
     if (lane == 0 && top) atomicMax(&s_taken, top);
     __syncthreads();
     const int taken = s_taken;
@@ -212,7 +231,7 @@ plan_kernel(const __grid_constant__ dsv4_paged_plan_args p, PlanSums* out, int l
     // the state (every thread has read it)
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int s = tid * PER + i;
+        const int s = i * T + tid;
         if (s >= B) continue;
         p.cu_q[s + 1] = s_tok[s];
         p.kv_len_out[s] = L[i] + n[i];
@@ -258,10 +277,10 @@ int launch_paged_plan(const dsv4_paged_plan_args& a, uint8_t* ws, uint32_t* ewor
     const int lists = a.total_q <= 2048;
     count_launch();
     const cudaError_t e = a.batch <= 128 ? launch_k(plan_kernel<128, 1>, dim3(1), dim3(128), 0, st, true, a, q, lists, eword)
-                                         : launch_k(plan_kernel<512, 4>, dim3(1), dim3(512), 0, st, true, a, q, lists, eword);
+                                         : launch_k(plan_kernel<1024, 2>, dim3(1), dim3(1024), 0, st, true, a, q, lists, eword);
     if (e != cudaSuccess) return DSV4_ERR_LAUNCH;
     if (lists) return DSV4_OK;
-    const int sms = sm_count() > 0 ? sm_count() : 152, most = 4 * sms, need = (a.total_q + kListT - 1) / kListT;
+    const int sms = sm_count() > 0 ? sm_count() : 152, most = 4 * sms, need = (a.total_q + kListT - 1) / kListT + 32;
     count_launch();
     return launch_k(plan_lists_kernel, dim3(need < most ? need : most), dim3(kListT), 0, st, true, a, q, eword) == cudaSuccess
                ? DSV4_OK : DSV4_ERR_LAUNCH;
