@@ -945,8 +945,28 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
 }
 
 // Joins each query's parts, and gathers the error bits. An item is 128 channels of one query: one warp, four
-// channels per lane.
+// channels per lane. Up to 16 parts of the prefix's rows and 16 of the query's own take one look: a lane each has a part's maximum
+// and sum, and the first parts' outputs are on their way meanwhile. (Looking at up to 160 parts of either, as for a few
+// queries over a long prefix, issued 300 instructions an item: 54 us for 1,415 tokens of 32 heads.)
 constexpr int kMergeThreads = 256;
+
+// One query's joined channels: rotated back, rounded, stored.
+template <int D>
+__device__ __forceinline__ void merge_store(const PrefixParams& p, size_t at, int tok, int ch, float (&o)[4]) {
+    const int r0 = D - 2 * p.or_pairs;
+    if (p.orp && ch + 3 >= r0) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            if (ch + i < r0) continue;
+            const float2 cs = out_rope_angle(static_cast<double>(p.orp[tok]) * p.or_freq[(ch + i - r0) >> 1]);
+            const float e = o[i], b = o[i + 1];
+            o[i] = e * cs.x + b * cs.y;
+            o[i + 1] = -e * cs.y + b * cs.x;
+        }
+    }
+    *reinterpret_cast<uint2*>(p.out + at * D + ch) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
 prefix_merge_kernel(const __grid_constant__ PrefixParams p, int ctas, uint32_t* eword) {
@@ -963,95 +983,142 @@ prefix_merge_kernel(const __grid_constant__ PrefixParams p, int ctas, uint32_t* 
     const PagedGeom& g = p.g.p;
     const int first = min(max(g.cu_q[0], 0), g.total_q), end = min(max(g.cu_q[g.batch], 0), g.total_q);
     constexpr int WB = kMergeThreads / 32;
-    const long long items = static_cast<long long>(max(end - first, 0)) * g.H * CH;
-    for (long long it = static_cast<long long>(blockIdx.x) * WB + warp; it < items; it += static_cast<long long>(gridDim.x) * WB) {
+    const long long items = static_cast<long long>(max(end - first, 0)) * g.H * CH, step = static_cast<long long>(gridDim.x) * WB;
+    const size_t kind = static_cast<size_t>(g.total_q) * g.H, row0 = static_cast<size_t>(first) * g.H;
+    // an item's two records (the prefix's may be anything where the query has none)
+    auto records = [&](long long it, float4& mp, float4& mo) {
+        if (it >= items) return;
+        const long long qh = it / CH;
+        const int half = C::HALVES == 2 ? static_cast<int>(it - qh * CH) >> 1 : 0;
+        mp = p.home_ml[half * kind + row0 + qh];
+        mo = p.home_ml[(C::HALVES + half) * kind + row0 + qh];
+    };
+    long long it = static_cast<long long>(blockIdx.x) * WB + warp;
+    float4 mp_next, mo_next;
+    records(it, mp_next, mo_next);
+    for (; it < items; it += step) {
+        const float4 mp = mp_next, mo = mo_next;
+        records(it + step, mp_next, mo_next);
         const long long qh = it / CH;
         const int chunk = static_cast<int>(it - qh * CH), half = C::HALVES == 2 ? chunk >> 1 : 0, ch = chunk * 128 + lane * 4;
-        const size_t at = static_cast<size_t>(first) * g.H + qh;
+        const size_t at = row0 + qh;
         const int tok = static_cast<int>(at / g.H), h = static_cast<int>(at - static_cast<size_t>(tok) * g.H);
-        const size_t kind = static_cast<size_t>(g.total_q) * g.H;
-        const float4 own = p.home_ml[(C::HALVES + half) * kind + at];
-        float4 pre = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-        const bool two = __float_as_int(own.w) == 1;
-        if (two) pre = p.home_ml[half * kind + at];
+        const bool two = __float_as_int(mo.w) == 1;
         const float snk = p.sink ? p.sink[h] * kLog2e : -INFINITY;
-        float w[2][PL], l[2][PL], M = -INFINITY;
         int c0[2], np[2], row[2];
+        const float* home[2], *cont[2];
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-            const float4 ml = a ? own : pre;
-            const int info = __float_as_int(ml.z);
+            const int info = __float_as_int(a ? mo.z : mp.z);
             c0[a] = info & 255;
             row[a] = min((info >> 16) & 0x7FFF, C::TILES * 128 - 1);
             np[a] = a || two ? min((info >> 8) & 255, ctas - c0[a]) : 0;
-#pragma unroll
-            for (int k = 0; k < PL; ++k) {
-                const int i = lane + 32 * k;
-                float2 x = make_float2(-INFINITY, 0.f);
-                if (i == 0 && np[a] > 0) x = make_float2(ml.x, ml.y);
-                else if (i < np[a]) x = p.cont_ml[static_cast<size_t>(c0[a] + i) * C::TILES * 128 + row[a]];
-                w[a][k] = x.x;
-                l[a][k] = x.y;
-                M = fmaxf(M, x.x);
-            }
+            home[a] = p.home_o + (a * kind + at) * D + ch;
+            cont[a] = p.cont_o + (static_cast<size_t>(c0[a]) * C::TILES * 128 + row[a]) * C::DV + (ch - half * 256);
         }
-#pragma unroll
-        for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
-        const float top = fmaxf(M, snk);
-        float sum = 0.f;
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int k = 0; k < PL; ++k) {
-                w[a][k] = w[a][k] == -INFINITY ? 0.f : exp2f(w[a][k] - top);
-                // (a part whose pages were all hidden holds no sum; one that holds NaN keeps it, also beside a weight of 0)
-                sum += l[a][k] * w[a][k];
+        auto part = [&](int a, int i) {
+            return *reinterpret_cast<const float4*>(i ? cont[a] + static_cast<size_t>(i) * C::TILES * 128 * C::DV : home[a]);
+        };
+        float o[4] = {0.f, 0.f, 0.f, 0.f}, f;
+        auto add = [&](float e, const float4& v) {       // (a part that saw nothing may hold anything)
+            if (e == 0.f) return;
+            o[0] = fmaf(e, v.x, o[0]); o[1] = fmaf(e, v.y, o[1]);
+            o[2] = fmaf(e, v.z, o[2]); o[3] = fmaf(e, v.w, o[3]);
+        };
+        auto finish = [&](float M, float top, float sum) {
+            const float den = sum + (snk == -INFINITY ? 0.f : exp2f(snk - top));
+            if (chunk == 0 && lane == 0 && p.lse)
+                p.lse[at] = M == -INFINITY ? (p.sink ? p.sink[h] : -INFINITY) : top * kLn2 + logf(den);
+            f = M == -INFINITY ? 0.f : 1.f / den;        // (-inf: no part had a row of the query's)
+        };
+        if (np[0] <= 16 && np[1] <= 16) {
+            const int a = lane >> 4, i = lane & 15;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (i < (a ? np[1] : np[0])) {
+                if (i == 0) ml = a ? make_float2(mo.x, mo.y) : make_float2(mp.x, mp.y);
+                else ml = p.cont_ml[static_cast<size_t>((a ? c0[1] : c0[0]) + i) * C::TILES * 128 + (a ? row[1] : row[0])];
             }
+            float4 v0[2], v1[2];
 #pragma unroll
-        for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
-        const float den = sum + (snk == -INFINITY ? 0.f : exp2f(snk - top));
-        if (chunk == 0 && lane == 0 && p.lse)
-            p.lse[at] = M == -INFINITY ? (p.sink ? p.sink[h] : -INFINITY) : top * kLn2 + logf(den);
-        const float f = M == -INFINITY ? 0.f : 1.f / den;            // (-inf: no part had a row of the query's)
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < 2; ++k) {
+                if (k < np[0]) v0[k] = part(0, k);
+                if (k < np[1]) v1[k] = part(1, k);
+            }
+            float M = ml.x;
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            const float* home = p.home_o + (a * kind + at) * D + ch;
-            const float* cont = p.cont_o + (static_cast<size_t>(c0[a]) * C::TILES * 128 + row[a]) * C::DV + (ch - half * 256);
-            for (int i0 = 0; i0 < np[a]; i0 += 8) {
-                float wk = w[a][0];
+            for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
+            const float top = fmaxf(M, snk), w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+            float sum = ml.y * w;                        // (a part that holds NaN keeps it, also beside a weight of 0)
 #pragma unroll
-                for (int k = 1; k < PL; ++k)
-                    if (i0 >= 32 * k) wk = w[a][k];
-                float4 v[8];
+            for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
+            finish(M, top, sum);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll 1
+                for (int k = 0; k < np[b]; k += 2) {
+                    if (k) {
+                        v0[0] = part(b, k);
+                        if (k + 1 < np[b]) v0[1] = part(b, k + 1);
+                    }
+                    const float e0 = __shfl_sync(~0u, w, 16 * b + k), e1 = __shfl_sync(~0u, w, 16 * b + ((k + 1) & 15));
+                    add(e0, b && !k ? v1[0] : v0[0]);
+                    if (k + 1 < np[b]) add(e1, b && !k ? v1[1] : v0[1]);
+                }
+        } else {
+            float w[2][PL], l[2][PL], M = -INFINITY;
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int k = 0; k < PL; ++k) {
+                    const int i = lane + 32 * k;
+                    float2 x = make_float2(-INFINITY, 0.f);
+                    if (i == 0 && np[a] > 0) x = a ? make_float2(mo.x, mo.y) : make_float2(mp.x, mp.y);
+                    else if (i < np[a]) x = p.cont_ml[static_cast<size_t>(c0[a] + i) * C::TILES * 128 + row[a]];
+                    w[a][k] = x.x;
+                    l[a][k] = x.y;
+                    M = fmaxf(M, x.x);
+                }
+            float4 v[8];
+            auto fetch = [&](int a, int i0) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (i0 + i < np[a])
-                        v[i] = *reinterpret_cast<const float4*>(i0 + i ? cont + static_cast<size_t>(i0 + i) * C::TILES * 128 * C::DV : home);
+                    if (i0 + i < np[a]) v[i] = part(a, i0 + i);
+            };
+            fetch(0, 0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float e = __shfl_sync(~0u, wk, (i0 + i) & 31);
-                    if (i0 + i < np[a] && e != 0.f) {                // (a part that saw nothing may hold anything)
-                        o[0] = fmaf(e, v[i].x, o[0]); o[1] = fmaf(e, v[i].y, o[1]);
-                        o[2] = fmaf(e, v[i].z, o[2]); o[3] = fmaf(e, v[i].w, o[3]);
+            for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
+            const float top = fmaxf(M, snk);
+            float sum = 0.f;
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int k = 0; k < PL; ++k) {
+                    w[a][k] = w[a][k] == -INFINITY ? 0.f : exp2f(w[a][k] - top);
+                    sum += l[a][k] * w[a][k];
+                }
+#pragma unroll
+            for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
+            finish(M, top, sum);
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                if (a) fetch(1, 0);
+                for (int i0 = 0; i0 < np[a]; i0 += 8) {
+                    float wk = w[a][0];
+#pragma unroll
+                    for (int k = 1; k < PL; ++k)
+                        if (i0 >= 32 * k) wk = w[a][k];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float e = __shfl_sync(~0u, wk, (i0 + i) & 31);
+                        if (i0 + i < np[a]) add(e, v[i]);
                     }
+                    fetch(a, i0 + 8);
                 }
             }
         }
-        const int r0 = D - 2 * p.or_pairs;
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = f == 0.f ? 0.f : o[i] * f;
-        if (p.orp && ch + 3 >= r0) {
-#pragma unroll 1
-            for (int i = 0; i < 4; i += 2) {
-                if (ch + i < r0) continue;
-                const float2 cs = out_rope_angle(static_cast<double>(p.orp[tok]) * p.or_freq[(ch + i - r0) >> 1]);
-                const float e = i ? o[2] : o[0], b = i ? o[3] : o[1];
-                const float e1 = e * cs.x + b * cs.y, b1 = -e * cs.y + b * cs.x;
-                if (i) { o[2] = e1; o[3] = b1; } else { o[0] = e1; o[1] = b1; }
-            }
-        }
-        *reinterpret_cast<uint2*>(p.out + at * D + ch) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+        merge_store<D>(p, at, tok, ch, o);
     }
 }
 
