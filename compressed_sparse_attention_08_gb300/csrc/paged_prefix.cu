@@ -18,8 +18,8 @@
 // are that many queries), else two units; then both groups add to one O and hand each other the reference maximum.
 // Of 512 channels tensor memory holds 256 beside the scores, so a tile is taken twice, each time
 // with the scores over all channels and the product with half of V's (1.5 times the products' time).
-// Roles: warps 0, 2 and 3 move pages by TMA into a ring of slots of 128 rows x 128 channels, warp 1 issues
-// tcgen05.mma, warps 4-11 do the softmax and write the parts.
+// Roles: warps 0, 2 and 3 move pages by TMA into a ring of slots of 128 rows x 128 channels, warp 1 issues tcgen05.mma,
+// warps 4-11 do the softmax, write the parts and, once a segment's last scores have come, ask for the next one's queries.
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -203,17 +203,17 @@ struct PrefixParams {
     double or_freq[64];                  // theta^(-2j / out_rope_dim)
 };
 
-constexpr int kMaxSlots = 8, kSegs = 4;  // (the loads run at most two segments ahead of the outputs)
+constexpr int kMaxSlots = 8, kSegs = 8;  // (the loads start a segment while the outputs are at most five behind: one unit each, a slot each)
 struct PrefixCtl {
-    uint64_t q_full, q_empty, empty[kMaxSlots];
+    uint64_t q_full, empty[kMaxSlots];
     // A slot's copies, counted apart for K (and tiles that are both) and for V.
     uint64_t full[2][kMaxSlots];
     uint8_t last[kMaxSlots];             // a slot's last copy: 4 | parity << 1 | V
     uint64_t seg_full[kSegs], s_full[2], p_full[2], pv_done[2], o_done[2], ref_done[2][4], l_ready[2][4], o_empty;
     uint64_t drained;                    // products in flight when a wait ran out
-    uint32_t seg_end[kLoadWarps];
+    uint32_t seg_end;                    // query tiles that were copied
     PagedSchedOf<PrefixLine> sched;
-    PrefixSeg segs[kSegs];               // written by a load warp for the softmax
+    PrefixSeg segs[kSegs];               // written by a load warp
     float ref[128];                      // reference maxima (base-2 units), where two groups share a tile
     float l[2][128];
     unsigned bad[8];
@@ -234,7 +234,8 @@ struct XCfg {
     static constexpr int OFF_Q = ST * SLOT, OFF_C = OFF_Q + QB, SMEM = OFF_C + static_cast<int>(sizeof(PrefixCtl));
     static constexpr bool KEEP = HALVES == 1;                // a shared K/V tile stays for both products
     static constexpr int OCOL = 256;                         // scores: columns 0 and 128; P over their first 64
-    static_assert(SMEM <= 232448 && ST >= 3 && (!KEEP || ST > 2 * KS) && OCOL + TILES * DV <= 512, "fits");
+    static_assert(ST == (D == 512 ? 3 : 5), "slots");
+    static_assert(SMEM <= 232448 && (!KEEP || ST > 2 * KS) && OCOL + TILES * DV <= 512, "fits");
 };
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -349,8 +350,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         tma_prefetch_desc(&qmap);
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
-        mbar_init(&ctl.q_full, kLoadWarps);
-        mbar_init(&ctl.q_empty, 1);
+        mbar_init(&ctl.q_full, 1);
         for (int i = 0; i < ST; ++i) {
             mbar_init(&ctl.full[0][i], 1);
             mbar_init(&ctl.full[1][i], 1);
@@ -369,6 +369,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         mbar_init(&ctl.drained, 1);
         ctl.abort = 0;
         ctl.err = 0;
+        ctl.seg_end = 0;
         fence_barrier_init();
     }
     if (warp == 2) tmem_alloc(&ctl.tmem, 512);
@@ -393,14 +394,14 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     if (warp == 0 || warp == 2 || warp == 3) {
         // ---------------------------------------------------------------- pages and queries
         // Three warps walk the same slots and take them in turn. Order: as the products need them, K0 V0 K1
-        // V1 .. with two tiles of queries, K0 K1 V0 K2 V1 .. with one, K0 K1 .. where a tile is both.
+        // V1 .. with two tiles of queries, K0 K1 V0 K2 V1 .. with one, K0 K1 .. where a tile is both. They go on into the next
+        // segment as far as the ring lets them; its description is formed a segment ahead (it takes a few dependent loads).
         const int mine = warp == 0 ? 0 : warp - 1;
         PrefixWalk w(line, sched);
-        PrefixSeg sg;
-        const uint32_t qtile = static_cast<uint32_t>(g.hb) * g.tpt * D * 2;
+        PrefixSeg sg, after;
         const int piece = lane >> 1, box = lane & 1;
         uint32_t ring = 0, seg = 0, turn[2] = {0, 0};    // (a bit per slot: the parity of its next copy)
-        bool dead = false, more = w.next(sg);
+        bool dead = false, more = w.next(sg), then = more && w.next(after);
         PagedLook cur{0, 0, false}, prev{0, 0, false};
         if (more) cur = prefix_look(g, sg, sg.row0 + sg.kb * kUnit, lane);
         int k = more ? sg.kb : 0;
@@ -432,22 +433,10 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             }
         };
         for (int u = 0; !dead && more; ++u) {
-            if (k == sg.kb) {                        // a new segment
-                if (seg > 0) dead = __any_sync(~0u, !wait_for(&ctl.q_empty, (seg - 1) & 1, abort_flag, p.wait_ns));
-                if (dead) break;
-                if (lane == 0) {
-                    if (mine == 0) {
-                        ctl.segs[seg % kSegs] = sg;
-                        mbar_arrive(&ctl.seg_full[seg % kSegs]);
-                    }
-                    const bool skip = p.fault && seg == 0;
-                    if (!skip && mine == 0) mbar_arrive_expect_tx(&ctl.q_full, qtile * sg.nt);
-                    else if (!skip) mbar_arrive(&ctl.q_full);
-#pragma unroll 1
-                    for (int b = skip ? 4 * KS : mine; b < 2 * KS * sg.nt; b += kLoadWarps) {
-                        const int tile = b >= 2 * KS ? 1 : 0, c = b - tile * 2 * KS;
-                        tma_load_3d(sQ + b * C::QBOX, &qmap, &ctl.q_full, c * 64, sg.head0, sg.tok0 + tile * g.tpt);
-                    }
+            if (k == sg.kb) {                        // a new segment, for the other roles
+                if (lane == 0 && mine == 0) {
+                    ctl.segs[seg % kSegs] = sg;
+                    mbar_arrive(&ctl.seg_full[seg % kSegs]);
                 }
                 ++seg;
             }
@@ -456,7 +445,8 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             const bool first = k == sg.kb, last = k + 1 == sg.ke, two = sg.nt == 2;
             PagedLook next{0, 0, false};
             if (++k >= sg.ke) {
-                more = w.next(sg);
+                more = then;
+                sg = after;
                 k = more ? sg.kb : 0;
             }
             if (more) next = prefix_look(g, sg, sg.row0 + k * kUnit, lane);
@@ -469,15 +459,13 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                     if (!dead && last) load(&vmap, cur, VS, v0, kvh, -1);
                 }
             }
+            if (last && more) then = w.next(after);
             prev = cur;
             cur = next;
         }
-        if (lane == 0) {
-            ctl.seg_end[mine] = seg;
-            if (dead) {
-                atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
-                ctl.abort = 1;
-            }
+        if (dead && lane == 0) {
+            atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
+            ctl.abort = 1;
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- tensor core
@@ -492,9 +480,8 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         // the core idled.) Votes and exchanges tell the compiler that the warp stays together.
         // (Every wait of the kernel is for a phase whose predecessor the waiter has seen, itself or through what it waited for
         // before, and whose successor cannot end before it goes on: parity tells no more.)
-        PrefixWalk w(line, sched);
-        PrefixSeg sg{};
-        uint32_t u = 0, seg = 0, i0 = 0, ends = 0;       // units, segments, steps, steps with pv_done before this segment
+        struct { int row0, kb, ke, lo, hi_u; } sg{};
+        uint32_t at = 0, u = 0, seg = 0, i0 = 0, ends = 0;   // place on the line; units, segments, steps, steps with pv_done before this segment
         bool dead = false;
         const bool one = elect_one();
         // (a wait that runs out does so for all lanes)
@@ -526,26 +513,26 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         auto edge = [&](uint32_t x) {
             const int j0 = sg.row0 + (sg.kb + static_cast<int>(x)) * kUnit;
             const unsigned bad = *reinterpret_cast<volatile unsigned*>(&ctl.bad[(u + x) & 7]);
-            return __any_sync(~0u, j0 < sg.q.lo || j0 + kUnit > sg.hi_u || bad);
+            return __any_sync(~0u, j0 < sg.lo || j0 + kUnit > sg.hi_u || bad);
         };
         // Such rows hold anything: as V they must not meet P = 0.
         auto clear_rows = [&](uint32_t x) {
             const int j0 = sg.row0 + (sg.kb + static_cast<int>(x)) * kUnit;
             const unsigned bad = *reinterpret_cast<volatile unsigned*>(&ctl.bad[(u + x) & 7]);
-            auto clear = [&](int row0, int rows) {
-                for (int c = lane; c < rows * (VS * 16); c += 32) {
-                    const int row = row0 + c / (VS * 16), x16 = c % (VS * 16);
-                    uint32_t slot = vat.slot + (x16 >> 4);
-                    if (slot >= ST) slot -= ST;
-                    *reinterpret_cast<uint4*>(sm + slot * C::SLOT + ((x16 >> 3) & 1) * C::BOX + row * 128 + (x16 & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-                }
+            constexpr int per = VS * 16;                 // 16-byte pieces of a row, a lane each (two rows at a time of 128 channels)
+            const int x16 = lane % per;
+            uint32_t slot = vat.slot + (x16 >> 4);
+            if (slot >= ST) slot -= ST;
+            uint8_t* z = sm + slot * C::SLOT + ((x16 >> 3) & 1) * C::BOX + (x16 & 7) * 16;
+            auto clear = [&](int row, int end) {
+#pragma unroll 4
+                for (row += lane / per; row < end; row += 32 / per) *reinterpret_cast<uint4*>(z + row * 128) = make_uint4(0, 0, 0, 0);
             };
-            const int z0 = min(max(sg.q.lo - j0, 0), kUnit), z1 = min(max(sg.hi_u - j0, z0), kUnit);
+            const int z0 = min(max(sg.lo - j0, 0), kUnit), z1 = min(max(sg.hi_u - j0, z0), kUnit);
             clear(0, z0);
-            clear(z1, kUnit - z1);
+            clear(z1, kUnit);
             for (int r = 0; bad && r < (kUnit >> g.br_log2); ++r)
-                if (bad >> (2 * r) & 1) clear(r << g.br_log2, g.br);
+                if (bad >> (2 * r) & 1) clear(r << g.br_log2, (r + 1) << g.br_log2);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
         };
@@ -563,19 +550,21 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 mul_k(b1, 1, 0, kat.slot);
                 umma_commit(&ctl.s_full[b1]);
                 if (!keep) umma_commit(&ctl.empty[kat.slot]);
-                if (n == 1) umma_commit(&ctl.q_empty);
             }
             __syncwarp();
             kat.next();
             if (!keep) kat.template skip<1>();
             for (uint32_t x = 0; x < n; ++x, ++pp0, ++pp1) {
                 const bool more = x + 1 < n;
+                if (edgy) {                              // (before P is waited for)
+                    if (!keep && !wait(&ctl.full[1][vat.slot], vat.parity())) return false;
+                    clear_rows(x);
+                }
                 // lane 0: the first tile's P; 1: the next K; others: V
                 if (!look(lane == 0 ? &ctl.p_full[b0] : lane == 1 ? &ctl.full[0][kat.slot] : &ctl.full[1][vat.slot],
                           lane == 0 ? pp0 : lane == 1 ? kat.parity() : vat.parity(), lane == 0 || (lane == 1 ? more : !keep)))
                     return false;
                 tc_fence_after();
-                if (edgy) clear_rows(x);
                 if (x == 0 && seg > 0 && !wait(&ctl.o_empty, seg - 1)) return false;
                 if (one) {
                     mul_v(0, b0, vat.slot, x);
@@ -596,7 +585,6 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                         mul_k(b1, 1, 0, kat.slot);
                         umma_commit(&ctl.s_full[b1]);
                         if (!keep) umma_commit(&ctl.empty[kat.slot]);
-                        if (x + 2 == n) umma_commit(&ctl.q_empty);
                     } else {
                         umma_commit(&ctl.o_done[b1]);
                     }
@@ -627,10 +615,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                     if (one) {
                         mul_k(buf, 0, s, kat.slot);
                         if (!keep) umma_commit(&ctl.empty[kat.slot]);
-                        if (s + 1 == KS) {
-                            umma_commit(&ctl.s_full[buf]);
-                            if (x + 1 == n) umma_commit(&ctl.q_empty);
-                        }
+                        if (s + 1 == KS) umma_commit(&ctl.s_full[buf]);
                     }
                     __syncwarp();
                     kat.next();
@@ -648,13 +633,16 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 const uint32_t i = i0 + x, buf = i & 1;
                 RingAt<ST> v1 = vat;
                 if (VS == 2) v1.template skip<1>();
-                // lane 0: P; others: V
                 const bool odd = VS == 2 && (lane & 1);
+                if (edges >> (x + 1 < n ? 1 : 0) & 1) {  // (before P is waited for)
+                    if (!look(&ctl.full[1][odd ? v1.slot : vat.slot], odd ? v1.parity() : vat.parity(), !keep)) return false;
+                    clear_rows(x);
+                }
+                // lane 0: P; others: V
                 if (!look(lane == 0 ? &ctl.p_full[buf] : &ctl.full[1][odd ? v1.slot : vat.slot],
                           lane == 0 ? i >> 1 : odd ? v1.parity() : vat.parity(), lane == 0 || !keep))
                     return false;
                 tc_fence_after();
-                if (edges >> (x + 1 < n ? 1 : 0) & 1) clear_rows(x);
                 if (x == 0 && seg > 0 && !wait(&ctl.o_empty, seg - 1)) return false;
                 if (one) {
                     mul_v(0, buf, vat.slot, x);
@@ -677,17 +665,22 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             ends += n;
             return true;
         };
-        for (; __any_sync(~0u, w.next(sg)); ++seg) {
-            dead = !wait(&ctl.q_full, seg);
+        for (; at < share; ++seg) {
+            // the segment's description and its queries
+            dead = !look(lane == 0 ? &ctl.seg_full[seg % kSegs] : &ctl.q_full, lane == 0 ? seg / kSegs : seg, true);
             if (dead) break;
-            const bool two = C::TILES == 2 && __any_sync(~0u, sg.nt == 2);
+            const PrefixSeg& d = ctl.segs[seg % kSegs];
+            sg = {d.row0, d.kb, d.ke, d.q.lo, d.hi_u};
+            const uint32_t nt = d.nt, units = d.ke - d.kb, cost = d.cost;
+            const bool two = C::TILES == 2 && __any_sync(~0u, nt == 2);
             if constexpr (C::TILES == 2) {
                 if (two) dead = !two_tiles();
             }
             if (!two) dead = !one_tile();
             if (dead) break;
-            u += sg.ke - sg.kb;
-            i0 += (sg.ke - sg.kb) * sg.nt;
+            at += __shfl_sync(~0u, cost, 0);
+            u += units;
+            i0 += __shfl_sync(~0u, units * nt, 0);
         }
         if (dead && lane == 0) {
             atomicOr(&ctl.err, DSV4_EWORD_TIMEOUT);
@@ -701,6 +694,23 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         const uint32_t sbuf = lane_base + grp * 128;
         const uint64_t scale22 = pack_f32x2(p.scale2, p.scale2);
         const int rt = row / g.hb, rh = row - rt * g.hb;             // this row's token in a tile, and head
+        // Queries of segment `next` (one warp, when the products with the ones before are done).
+        const uint32_t qtile = static_cast<uint32_t>(g.hb) * g.tpt * D * 2;
+        auto fetch_queries = [&](uint32_t next) {
+            if (__any_sync(~0u, !wait_for(&ctl.seg_full[next % kSegs], (next / kSegs) & 1, abort_flag, p.wait_ns))) return;
+            if (p.fault && next == 0) return;
+            const PrefixSeg& d = ctl.segs[next % kSegs];
+            if (lane == 0) {
+                ctl.seg_end = next + 1;
+                mbar_arrive_expect_tx(&ctl.q_full, qtile * d.nt);
+            }
+            __syncwarp();
+            if (lane < 2 * KS * d.nt) {                              // 64 channels of a tile each
+                const int tile = lane >= 2 * KS ? 1 : 0, c = lane - tile * 2 * KS;
+                tma_load_3d(sQ + lane * C::QBOX, &qmap, &ctl.q_full, c * 64, d.head0, d.tok0 + tile * g.tpt);
+            }
+        };
+        if (share > 0 && warp == 4) fetch_queries(0);
         uint32_t at = 0, u = 0, i0 = 0, ends = 0, twos = 0;          // place on the line; units, steps, steps with pv_done, segments of two tiles
         bool dead = false;
         for (uint32_t seg = 0; at < share; ++seg) {
@@ -841,10 +851,12 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             dead = __any_sync(~0u, dead);
             if (dead) break;
             // ---------------------------------------------------------------- the segment's part
+            // (The segment's last scores have come to the warps of this group: its queries are read.)
             // The end of the last product, once the last step is known to have come to its softmax (the phase before is over
             // then). The warps of the same rows in both groups meet here: all that either waits for in the next segment comes
             // after all of this one.
             const uint32_t il = i0 + steps - 1 - (nt == 2 ? 1 - tile : 0);
+            if (q4 == 0 && ((i0 + steps - 1) & 1) == static_cast<uint32_t>(grp) && at + sg.cost < share) fetch_queries(seg + 1);
             if ((il & 1) != static_cast<uint32_t>(grp))
                 dead = !wait_for(&ctl.ref_done[grp ^ 1][q4], (il >> 1) & 1, abort_flag, p.wait_ns);
             const uint32_t e = ends + steps - 1;
@@ -933,7 +945,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             mbar_wait(&ctl.drained, 0, nullptr, kDrainNs);
         }
         if (tid == 0) {
-            const uint32_t seg = max(max(ctl.seg_end[0], ctl.seg_end[1]), ctl.seg_end[2]);
+            const uint32_t seg = ctl.seg_end;
             if (seg && !p.fault) mbar_wait(&ctl.q_full, (seg - 1) & 1, nullptr, kDrainNs);
             for (int i = 0; i < ST; ++i)
                 if (ctl.last[i]) mbar_wait(&ctl.full[ctl.last[i] & 1][i], ctl.last[i] >> 1 & 1, nullptr, kDrainNs);
