@@ -55,33 +55,36 @@ struct PrefixGeom {
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// The geometry with the prefix lengths as they are used (by this CTA: each forms its own copy).
+// The geometry with the prefix lengths as they are used (by this CTA: each forms its own copy). While the schedule is made,
+// lengths, groups and sequences lie in shared memory; afterwards they are read again where they are needed.
 struct PrefixLine {
     using Seq = PrefixSeq;
     const PrefixGeom& g;
     const int32_t* plen;
+    const int32_t* start;                // group_start, or null
+    const PagedSeq* seqs;                // or null
 };
 
-__device__ __forceinline__ int group_first(const PrefixGeom& g, int i) {
-    const int b = g.group_start ? g.group_start[i] : (i ? g.p.batch : 0);
-    return min(max(b, 0), g.p.batch);
+__device__ __forceinline__ int group_first(const PrefixLine& l, int i) {
+    const int b = l.start ? l.start[i] : (i ? l.g.p.batch : 0);
+    return min(max(b, 0), l.g.p.batch);
 }
 // The group of sequence s, or -1.
-__device__ __forceinline__ int group_of(const PrefixGeom& g, int s) {
-    if (!g.group_start) return 0;
-    int lo = 0, hi = g.groups;           // the last group that starts at or before s
+__device__ __forceinline__ int group_of(const PrefixLine& l, int s) {
+    if (!l.start) return 0;
+    int lo = 0, hi = l.g.groups;         // the last group that starts at or before s
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (g.group_start[mid] <= s) lo = mid; else hi = mid;
+        if (l.start[mid] <= s) lo = mid; else hi = mid;
     }
-    return group_first(g, lo) <= s && s < group_first(g, lo + 1) ? lo : -1;
+    return group_first(l, lo) <= s && s < group_first(l, lo + 1) ? lo : -1;
 }
 
 __device__ __forceinline__ PrefixSeq paged_seq(const PrefixLine& l, int v, bool& bad) {
     const PrefixGeom& g = l.g;
     PrefixSeq q;
     if (v < g.groups) {
-        const int a = group_first(g, v), b = group_first(g, v + 1), P = l.plen[v];
+        const int a = group_first(l, v), b = group_first(l, v + 1), P = l.plen[v];
         q.q0 = min(max(g.p.cu_q[a], 0), g.p.total_q);
         q.n = P > 0 ? max(min(max(g.p.cu_q[b], 0), g.p.total_q) - q.q0, 0) : 0;
         q.L = P;
@@ -91,8 +94,8 @@ __device__ __forceinline__ PrefixSeq paged_seq(const PrefixLine& l, int v, bool&
         return q;
     }
     const int s = v - g.groups;
-    const PagedSeq o = paged_seq(g.p, s, bad);
-    const int grp = group_of(g, s);
+    const PagedSeq o = l.seqs ? l.seqs[s] : paged_seq(g.p, s, bad);
+    const int grp = group_of(l, s);
     q.q0 = o.q0;
     q.n = o.n;
     q.L = o.L;
@@ -308,29 +311,39 @@ __device__ __forceinline__ PagedLook prefix_look(const PagedGeom& g, const Prefi
     return t;
 }
 
-// The prefix lengths that the groups use: no row that some token of the group does not see. `s_len`: scratch.
-__device__ void prefix_lengths(const PrefixGeom& g, int* s_len, int32_t* out, uint32_t* err) {
+// Scratch of the schedule, in the ring's place.
+struct PrefixScratch {
+    long long pref[4096];
+    PagedSeq seqs[2048];
+    int32_t plen[2048], start[2052];
+};
+
+// The prefix lengths that the groups use: no row that some token of the group does not see.
+__device__ void prefix_lengths(const PrefixGeom& g, PrefixScratch& z, int32_t* out, uint32_t* err) {
     bool bad = false;
     const int cap = g.p.max_pages * g.p.page_size;
     for (int i = threadIdx.x; i < g.groups; i += kThreads) {
         const int x = g.prefix_len[i];
-        s_len[i] = min(max(x, 0), cap);
-        bad |= x != s_len[i];
+        z.plen[i] = min(max(x, 0), cap);
+        bad |= x != z.plen[i];
         if (g.group_start) {
             const int a = g.group_start[i], b = g.group_start[i + 1];
             bad |= a < 0 || b < a || b > g.p.batch;
+            z.start[i] = a;
+            if (i + 1 == g.groups) z.start[i + 1] = b;
         }
     }
+    for (int s = threadIdx.x; s < g.p.batch; s += kThreads) z.seqs[s] = paged_seq(g.p, s, bad);
     __syncthreads();
+    const PrefixLine l{g, z.plen, g.group_start ? z.start : nullptr, z.seqs};
     for (int s = threadIdx.x; s < g.p.batch; s += kThreads) {
-        const PagedSeq q = paged_seq(g.p, s, bad);
-        const int grp = group_of(g, s);
-        if (grp >= 0 && q.n > 0 && q.L - q.n < s_len[grp]) atomicMin(&s_len[grp], max(q.L - q.n, 0));
+        const PagedSeq q = z.seqs[s];
+        const int grp = group_of(l, s);
+        if (grp >= 0 && q.n > 0 && q.L - q.n < z.plen[grp]) atomicMin(&z.plen[grp], max(q.L - q.n, 0));
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < g.groups; i += kThreads) out[i] = s_len[i];
     if (bad) atomicOr(err, DSV4_EWORD_BAD_INDEX);
     __syncthreads();
+    for (int i = threadIdx.x; i < g.groups; i += kThreads) out[i] = z.plen[i];
 }
 
 template <int D>
@@ -380,9 +393,12 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
     int32_t* plen = p.plen + static_cast<size_t>(worker) * p.g.groups;
-    prefix_lengths(p.g, reinterpret_cast<int*>(sm), plen, &ctl.err);
-    const PrefixLine line{p.g, plen};
-    paged_schedule<kThreads>(line, worker, workers, p.min_units, reinterpret_cast<long long*>(sm), &ctl.sched, &ctl.err);
+    PrefixScratch& scratch = *reinterpret_cast<PrefixScratch*>(sm);
+    static_assert(sizeof(PrefixScratch) <= static_cast<size_t>(C::OFF_Q), "in the ring's place");
+    prefix_lengths(p.g, scratch, plen, &ctl.err);
+    paged_schedule<kThreads>(PrefixLine{p.g, scratch.plen, p.g.group_start ? scratch.start : nullptr, scratch.seqs}, worker, workers,
+                             p.min_units, scratch.pref, &ctl.sched, &ctl.err);
+    const PrefixLine line{p.g, plen, p.g.group_start, nullptr};
     // the schedule's scratch is overwritten by TMA next
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
@@ -401,7 +417,15 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         PrefixSeg sg, after;
         const int piece = lane >> 1, box = lane & 1;
         uint32_t ring = 0, seg = 0, turn[2] = {0, 0};    // (a bit per slot: the parity of its next copy)
-        bool dead = false, more = w.next(sg), then = more && w.next(after);
+        bool dead = false, more = w.next(sg), then = false, known = false;   // (whether `then` and `after` are)
+        auto describe = [&] {                            // a new segment, for the other roles
+            if (lane == 0 && mine == 0) {
+                ctl.segs[seg % kSegs] = sg;
+                mbar_arrive(&ctl.seg_full[seg % kSegs]);
+            }
+            ++seg;
+        };
+        if (more) describe();
         PagedLook cur{0, 0, false}, prev{0, 0, false};
         if (more) cur = prefix_look(g, sg, sg.row0 + sg.kb * kUnit, lane);
         int k = more ? sg.kb : 0;
@@ -433,21 +457,17 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             }
         };
         for (int u = 0; !dead && more; ++u) {
-            if (k == sg.kb) {                        // a new segment, for the other roles
-                if (lane == 0 && mine == 0) {
-                    ctl.segs[seg % kSegs] = sg;
-                    mbar_arrive(&ctl.seg_full[seg % kSegs]);
-                }
-                ++seg;
-            }
             // the pages of the next unit are looked up while this one's copies wait
             const int kvh = sg.kvh, v0 = sg.half * 256;
             const bool first = k == sg.kb, last = k + 1 == sg.ke, two = sg.nt == 2;
             PagedLook next{0, 0, false};
             if (++k >= sg.ke) {
+                if (!known) then = w.next(after);
+                known = false;
                 more = then;
                 sg = after;
                 k = more ? sg.kb : 0;
+                if (more) describe();
             }
             if (more) next = prefix_look(g, sg, sg.row0 + k * kUnit, lane);
             load(&kmap, cur, KS, 0, kvh, u);
@@ -459,7 +479,10 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                     if (!dead && last) load(&vmap, cur, VS, v0, kvh, -1);
                 }
             }
-            if (last && more) then = w.next(after);
+            if (!known && more) {
+                then = w.next(after);
+                known = true;
+            }
             prev = cur;
             cur = next;
         }
