@@ -171,11 +171,11 @@ __device__ void paged_schedule(const Geom& g, int self, int count, int min_units
     // either side, more than the imbalance of at most 2 units or 1/32 of a share.
     if (warp < 2) {
         const long long T = batch > 0 ? pref[batch - 1] : 0;
-        const long long most = T / min_units < 1 ? 1 : T / min_units;
-        const int ge = most < count ? static_cast<int>(most) : count;
-        const long long share32 = T / ge / 32, small = share32 > 2 ? share32 : 2;
-        const int c = self + warp;
-        long long u = c < ge ? T * c / ge : T;
+        // (one division of 64 bits: they take hundreds of instructions; T c / ge in parts)
+        const int ge = T >= static_cast<long long>(count) * min_units ? count : max(static_cast<int>(T) / min_units, 1);
+        const long long share = T >> 31 ? T / ge : static_cast<int>(T) / ge, share32 = share / 32, small = share32 > 2 ? share32 : 2;
+        const int c = self + warp, over = static_cast<int>(T - share * ge);
+        long long u = c < ge ? share * c + over * c / ge : T;
         int s = 0, tt = 0, inner = 0, k = 0;
         Seq q{};
         bool dummy = false;
@@ -204,7 +204,7 @@ __device__ void paged_schedule(const Geom& g, int self, int count, int min_units
                     const int nf = __shfl_sync(~0u, n, f);
                     const long long r = rem - cum - (__shfl_sync(~0u, v, f) - static_cast<long long>(nf) * mult);
                     tt = tt0 + f;
-                    inner = static_cast<int>(r / nf);
+                    inner = r >> 31 ? static_cast<int>(r / nf) : static_cast<int>(r) / nf;
                     k = static_cast<int>(r - static_cast<long long>(inner) * nf);
                     const int part = k % paged_weight(g, q, tt);
                     u -= part;

@@ -173,8 +173,7 @@ struct PrefixWalk {
         o.n = segment_units(g, q, o.t0 + o.tn - 1);
         o.weight = paged_weight(l, q, tt);
         o.kb = k / o.weight;
-        const long long rest = left / o.weight;
-        o.ke = rest < o.n - o.kb ? o.kb + static_cast<int>(rest) : o.n;
+        o.ke = left >= static_cast<long long>(o.n - o.kb) * o.weight ? o.n : o.kb + static_cast<int>(left) / o.weight;
         o.cost = (o.ke - o.kb) * o.weight + (o.ke == o.n ? paged_over(l, q, tt) : 0);
         left -= o.cost;
         k = 0;
