@@ -209,7 +209,8 @@ __device__ void paged_schedule(const Geom& g, int self, int count, int min_units
                     const int part = k % paged_weight(g, q, tt);
                     u -= part;
                     k -= part;
-                    if (k > 0 && (nf <= small || k >= nf - paged_over(g, q, tt))) {   // the next tile's start
+                    const int rows = nf - paged_over(g, q, tt);
+                    if (k > 0 && (rows <= small || k >= rows)) {   // the next tile's start
                         u += nf - k;
                         k = 0;
                         if (++inner == mult) { inner = 0; ++tt; }

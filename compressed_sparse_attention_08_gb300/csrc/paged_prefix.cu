@@ -117,13 +117,14 @@ __device__ __forceinline__ int segment_units(const PrefixGeom& g, const PrefixSe
     return max((seen(q, t_last) - unit_row0(g, q) + kUnit - 1) / kUnit, 1);
 }
 // The line counts time, in 600 cycles or so: a unit of two tiles takes 5, of one tile 3 (at 256 and 512 channels all
-// have one, and take longer: only ratios count), a segment's start and end 21 and 11 (6 of longer units).
+// have one, and take longer: only ratios count), a segment's start and end 25 and 11 (4 of longer units).
+// Measured at 16 sequences of 256 tokens of 32 heads behind 32,768 shared rows: 590 us; with 21, 11 and 6 596, with 30 657, with 18 and 9 640.
 __device__ __forceinline__ bool two_tiles(const PrefixLine& l, const PrefixSeq& q, int tt) {
     return l.g.tiles == 2 && q.n - tt * paged_tokens(l) > l.g.p.tpt;
 }
 __device__ __forceinline__ int paged_weight(const PrefixLine& l, const PrefixSeq& q, int tt) { return two_tiles(l, q, tt) ? 5 : 3; }
 __device__ __forceinline__ int paged_over(const PrefixLine& l, const PrefixSeq& q, int tt) {
-    return l.g.tiles == 1 ? 6 : two_tiles(l, q, tt) ? 21 : 11;
+    return l.g.tiles == 1 ? 4 : two_tiles(l, q, tt) ? 25 : 11;
 }
 __device__ __forceinline__ int paged_tile_units(const PrefixLine& l, const PrefixSeq& q, int tt) {
     return segment_units(l.g, q, min((tt + 1) * paged_tokens(l), q.n) - 1) * paged_weight(l, q, tt) + paged_over(l, q, tt);
