@@ -206,7 +206,7 @@ struct PrefixParams {
     double or_freq[64];                  // theta^(-2j / out_rope_dim)
 };
 
-constexpr int kMaxSlots = 8, kSegs = 8;  // (the loads start a segment while the outputs are at most five behind: one unit each, a slot each)
+constexpr int kMaxSlots = 8, kSegs = 10; // (see the static_assert beside the roles)
 struct PrefixCtl {
     uint64_t q_full, empty[kMaxSlots];
     // A slot's copies, counted apart for K (and tiles that are both) and for V.
@@ -405,6 +405,11 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
 
     const PagedGeom& g = p.g.p;
     const PagedSchedOf<PrefixLine>& sched = ctl.sched;
+    // Descriptions in use at once: those of the segments from s on, of which some warp still writes outputs, to the newest. No
+    // slot of s + 1 becomes free before all warps have arrived at o_empty for s. If every segment is one slot, place s + 1 +
+    // ST waits for that; the load warp that describes passes up to kLoadWarps - 1 places of the other warps before its
+    // own stops it, and has described the segment behind that place by then.
+    static_assert(kSegs >= ST + kLoadWarps + 2, "descriptions");
     const bool keep = C::KEEP && p.shared;               // K rows stay in place as V
     const uint32_t share = static_cast<uint32_t>(sched.u1 - sched.u0);
     if (warp == 0 || warp == 2 || warp == 3) {
@@ -741,7 +746,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             dead = __any_sync(~0u, dead);
             if (dead) break;
             const PrefixSeg& sg = ctl.segs[seg % kSegs];
-            const uint32_t nt = sg.nt, n = sg.ke - sg.kb, steps = n * nt;
+            const uint32_t nt = sg.nt, n = sg.ke - sg.kb, steps = n * nt, cost = sg.cost;
             const uint32_t tile = nt == 2 ? (grp ^ i0) & 1 : 0;
             const int tok = static_cast<int>(tile) * g.tpt + rt;     // in the segment
             const bool valid = rt < g.tpt && tok < sg.tn && rh < sg.hv;
@@ -879,7 +884,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             // then). The warps of the same rows in both groups meet here: all that either waits for in the next segment comes
             // after all of this one.
             const uint32_t il = i0 + steps - 1 - (nt == 2 ? 1 - tile : 0);
-            if (q4 == 0 && ((i0 + steps - 1) & 1) == static_cast<uint32_t>(grp) && at + sg.cost < share) fetch_queries(seg + 1);
+            if (q4 == 0 && ((i0 + steps - 1) & 1) == static_cast<uint32_t>(grp) && at + cost < share) fetch_queries(seg + 1);
             if ((il & 1) != static_cast<uint32_t>(grp))
                 dead = !wait_for(&ctl.ref_done[grp ^ 1][q4], (il >> 1) & 1, abort_flag, p.wait_ns);
             const uint32_t e = ends + steps - 1;
@@ -945,8 +950,8 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.o_empty);
-            at += sg.cost;
+            if (lane == 0) mbar_arrive(&ctl.o_empty);        // (sg is not read any more)
+            at += cost;
             u += n;
             i0 += steps;
         }

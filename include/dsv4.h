@@ -572,8 +572,12 @@ int dsv4_rope(const dsv4_rope_args* args, dsv4_stream_t stream);
  * together, the rows behind them are read through each sequence's own. The result is dsv4_paged_attn's
  * with window 0. Where a sequence of the group has a token that stands inside the prefix, the
  * group's prefix ends before that token; sequences outside every group have none. (Each sequence's table
- * names pages for all its rows. For the shared ones they need not be the same pages.)
- * Without a prefix the call is right but slower than dsv4_paged_attn. */
+ * names pages for all its rows. For the shared ones they need not be the same pages. The first
+ * sequence's table is read also when that sequence has no tokens: the prefix must not reach into
+ * pages that it has given back.)
+ * Without a prefix the call is right but up to a sixth slower than dsv4_paged_attn; it is no faster either
+ * with 64 or more heads per KV head of 512 channels and a prefix that stays in L2, as one token's heads
+ * fill dsv4_paged_attn's tile. */
 typedef struct dsv4_paged_prefix_args {
     const void* q;            /* bf16 [total_q, heads, dim]                                   */
     const void* k_pages;      /* bf16 [num_pages, page_size, kv_heads, dim]                   */
