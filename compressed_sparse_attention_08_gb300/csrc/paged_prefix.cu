@@ -18,6 +18,12 @@
 // are that many queries), else two units; then both groups add to one O and hand each other the reference maximum.
 // Of 512 channels tensor memory holds 256 beside the scores, so a tile is taken twice, each time
 // with the scores over all channels and the product with half of V's (1.5 times the products' time).
+// What bounds it: at 128 channels the chain of a unit of two tiles, 3,030 cycles against 2,048 of products (issue, the scores'
+// arrival 370, the softmax 1,128, P's arrival 450); at 512 the loads, whose three slots beside Q turn around in 2,350 cycles
+// each (a unit 4,700 cycles, products 3,072); with short own rows the segments' starts. Measured, merge included: 16 chunks
+// of up to 256 tokens behind 32,768 shared rows, 32 heads over 8 of 128, K and V apart, 590 us (1,290 TFLOP/s, tensor pipe 62 %
+// active); 64 single tokens behind them 74; 48 tokens behind 65,536 rows, 16 heads of 512, one row as K and V, 158 (48 %
+// active); 45 tokens in three groups behind 12,345 rows, 16 heads over 2 of 256, 45; 2 tokens behind 1,000, 8 heads, 13.7.
 // Roles: warps 0, 2 and 3 move pages by TMA into a ring of slots of 128 rows x 128 channels, warp 1 issues tcgen05.mma,
 // warps 4-11 do the softmax, write the parts and, once a segment's last scores have come, ask for the next one's queries.
 #include <cfloat>
@@ -987,7 +993,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
 // Joins each query's parts, and gathers the error bits. An item is 128 channels of one query: one warp, four
 // channels per lane. Up to 16 parts of the prefix's rows and 16 of the query's own take one look: a lane each has a part's maximum
 // and sum, and the first parts' outputs are on their way meanwhile. (Looking at up to 160 parts of either, as for a few
-// queries over a long prefix, issued 300 instructions an item: 54 us for 1,415 tokens of 32 heads.)
+// queries over a long prefix, issued 300 instructions an item: 54 us for 1,415 tokens of 32 heads, now 39.)
 constexpr int kMergeThreads = 256;
 
 // One query's joined channels: rotated back, rounded, stored.
