@@ -21,8 +21,8 @@
 // What bounds it: at 128 channels the chain of a unit of two tiles, 3,030 cycles against 2,048 of products (issue, the scores'
 // arrival 370, the softmax 1,128, P's arrival 450); at 512 the loads, whose three slots beside Q turn around in 2,350 cycles
 // each (a unit 4,700 cycles, products 3,072); with short own rows the segments' starts. Measured, merge included: 16 chunks
-// of up to 256 tokens behind 32,768 shared rows, 32 heads over 8 of 128, K and V apart, 590 us (1,290 TFLOP/s, tensor pipe 62 %
-// active); 64 single tokens behind them 74; 48 tokens behind 65,536 rows, 16 heads of 512, one row as K and V, 158 (48 %
+// of up to 256 tokens behind 32,768 shared rows, 32 heads over 8 of 128, K and V apart, 583 us (1,310 TFLOP/s, tensor pipe 62 %
+// active); 64 single tokens behind them 74; 48 tokens behind 65,536 rows, 16 heads of 512, one row as K and V, 155 (48 %
 // active); 45 tokens in three groups behind 12,345 rows, 16 heads over 2 of 256, 45; 2 tokens behind 1,000, 8 heads, 13.7.
 // Roles: warps 0, 2 and 3 move pages by TMA into a ring of slots of 128 rows x 128 channels, warp 1 issues tcgen05.mma,
 // warps 4-11 do the softmax, write the parts and, once a segment's last scores have come, ask for the next one's queries.
@@ -993,7 +993,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
 // Joins each query's parts, and gathers the error bits. An item is 128 channels of one query: one warp, four
 // channels per lane. Up to 16 parts of the prefix's rows and 16 of the query's own take one look: a lane each has a part's maximum
 // and sum, and the first parts' outputs are on their way meanwhile. (Looking at up to 160 parts of either, as for a few
-// queries over a long prefix, issued 300 instructions an item: 54 us for 1,415 tokens of 32 heads, now 39.)
+// queries over a long prefix, issued 300 instructions an item: 54 us for 1,415 tokens of 32 heads, now 33.)
 constexpr int kMergeThreads = 256;
 
 // One query's joined channels: rotated back, rounded, stored.
@@ -1013,8 +1013,8 @@ __device__ __forceinline__ void merge_store(const PrefixParams& p, size_t at, in
     *reinterpret_cast<uint2*>(p.out + at * D + ch) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads)
+template <int D, bool MANY>
+__global__ void __launch_bounds__(kMergeThreads, MANY ? 3 : 2)
 prefix_merge_kernel(const __grid_constant__ PrefixParams p, int ctas, uint32_t* eword) {
     using C = XCfg<D>;
     constexpr int CH = D / 128, PL = 5;  // chunks of a query; parts of a segment per lane (at most 160)
@@ -1110,6 +1110,38 @@ prefix_merge_kernel(const __grid_constant__ PrefixParams p, int ctas, uint32_t* 
                     add(e0, b && !k ? v1[0] : v0[0]);
                     if (k + 1 < np[b]) add(e1, b && !k ? v1[1] : v0[1]);
                 }
+        } else if (MANY) {
+            auto load = [&](int a, int i) {
+                if (i == 0 && np[a] > 0) return a ? make_float2(mo.x, mo.y) : make_float2(mp.x, mp.y);
+                return i < np[a] ? p.cont_ml[static_cast<size_t>(c0[a] + i) * C::TILES * 128 + row[a]] : make_float2(-INFINITY, 0.f);
+            };
+            float M = -INFINITY;
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll 1
+                for (int i = lane; i < np[a]; i += 32) M = fmaxf(M, load(a, i).x);
+#pragma unroll
+            for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
+            const float top = fmaxf(M, snk);
+            float sum = 0.f;
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll 1
+                for (int i0 = 0; i0 < np[a]; i0 += 32) {
+                    const float2 ml = load(a, i0 + lane);
+                    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+                    sum += ml.y * w;
+#pragma unroll 1
+                    for (int k = 0; k < 32 && i0 + k < np[a]; k += 2) {
+                        const float4 v0 = part(a, i0 + k), v1 = i0 + k + 1 < np[a] ? part(a, i0 + k + 1) : v0;
+                        const float e0 = __shfl_sync(~0u, w, k), e1 = __shfl_sync(~0u, w, k + 1);
+                        add(e0, v0);
+                        add(e1, v1);                     // (past the last part: a weight of 0)
+                    }
+                }
+#pragma unroll
+            for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
+            finish(M, top, sum);
         } else {
             float w[2][PL], l[2][PL], M = -INFINITY;
 #pragma unroll
@@ -1241,11 +1273,16 @@ int run(const dsv4_paged_prefix_args& a, uint8_t* ws, uint32_t* eword, cudaStrea
     p.wait_ns = wc.wait_ns;
     count_launch();
     if (launch_k(kern, dim3(ctas), dim3(kThreads), C::SMEM, st, true, qmap, kmap, vmap, p) != cudaSuccess) return DSV4_ERR_LAUNCH;
-    const long long warps = static_cast<long long>(a.total_q) * a.heads * (D / 128), most = ctas * 8;
-    const long long blocks = (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+    // With more items than two CTAs per SM have warps the merge takes three with fewer registers and two loads in flight per
+    // item, else two with eight. Whole call: 1,415 tokens of 32 heads 580 us (584 in the other form), 48 of 16 heads x 512 154
+    // (157). Left to itself the compiler takes 136 registers for the second form, and one CTA: 64 of 32 heads 76 us, not 73.
+    const long long items = static_cast<long long>(a.total_q) * a.heads * (D / 128), wb = kMergeThreads / 32;
+    const bool many = items > 2 * wb * ctas;
+    const long long blocks = (items + wb - 1) / wb, most = 6 * ctas;
+    auto merge = many ? prefix_merge_kernel<D, true> : prefix_merge_kernel<D, false>;
     count_launch();
-    if (launch_k(prefix_merge_kernel<D>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(kMergeThreads), 0, st, true, p,
-                 ctas, eword) != cudaSuccess)
+    if (launch_k(merge, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(kMergeThreads), 0, st, true, p, ctas, eword) !=
+        cudaSuccess)
         return DSV4_ERR_LAUNCH;
     return DSV4_OK;
 }

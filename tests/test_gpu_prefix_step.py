@@ -107,3 +107,16 @@ def test_many_segments_of_one_unit(H, KV, D, shared, q):
     for s in (0, 699, 700, batch - 1):
         one = ref.attention(x[s * q:(s + 1) * q], c.k, c.v, c.table[s:s + 1], [0, q], [lens[s]], D ** -0.5)
         ref.check_attention(out[s * q:(s + 1) * q], lse[s * q:(s + 1) * q], one)
+
+
+@pytest.mark.parametrize("H, KV, D, shared, batch", [(32, 1, 128, True, 82), (32, 2, 256, False, 42), (64, 1, 512, True, 12)])
+def test_many_queries_beside_one_that_is_cut_into_many_parts(H, KV, D, shared, batch):
+    """Two sequences behind a prefix that most of the device works on, the rest behind a short one."""
+    g = gen(batch)
+    lens = [20011, 20060] + [21 + (s * 13) % 150 for s in range(batch - 2)]
+    c = Cache(g, lens, [0, 2, batch], [20000, 20], 64, KV, D, shared)
+    q = normal(g, batch, H, D, std=2.0)
+    sink = normal(g, H, dtype=torch.float32)
+    cu = cu_of([1] * batch)
+    out, lse = attend(c, q, cu, sink=sink)
+    ref.check_attention(out, lse, ref.attention(q, c.k, c.v, c.table, cu, lens, D ** -0.5, sink=sink))
