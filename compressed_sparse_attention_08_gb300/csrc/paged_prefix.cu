@@ -19,11 +19,11 @@
 // Of 512 channels tensor memory holds 256 beside the scores, so a tile is taken twice, each time
 // with the scores over all channels and the product with half of V's (1.5 times the products' time).
 // What bounds it: at 128 channels the chain of a unit of two tiles, 3,030 cycles against 2,048 of products (issue, the scores'
-// arrival 370, the softmax 1,128, P's arrival 450); at 512 the loads, whose three slots beside Q turn around in 2,350 cycles
-// each (a unit 4,700 cycles, products 3,072); with short own rows the segments' starts. Measured, merge included: 16 chunks
+// arrival 370, the softmax 1,128, P's arrival 450); at 512 shared memory, which gives 128 bytes a cycle: 4,096 cycles of a unit's 4,550 (Q
+// and K for the scores 2,048, V 512, the copies 1,536; products 3,072); with short own rows the segments' starts. Measured, merge included: 16 chunks
 // of up to 256 tokens behind 32,768 shared rows, 32 heads over 8 of 128, K and V apart, 583 us (1,310 TFLOP/s, tensor pipe 62 %
 // active); 64 single tokens behind them 74; 48 tokens behind 65,536 rows, 16 heads of 512, one row as K and V, 155 (48 %
-// active); 45 tokens in three groups behind 12,345 rows, 16 heads over 2 of 256, 45; 2 tokens behind 1,000, 8 heads, 13.7.
+// active); 45 tokens in three groups behind 12,345 rows, 16 heads over 2 of 256, 42; 2 tokens behind 1,000, 8 heads, 13.7.
 // Roles: warps 0, 2 and 3 move pages by TMA into a ring of slots of 128 rows x 128 channels, warp 1 issues tcgen05.mma,
 // warps 4-11 do the softmax, write the parts and, once a segment's last scores have come, ask for the next one's queries.
 #include <cfloat>
@@ -241,7 +241,10 @@ struct XCfg {
     static constexpr int ST_FIT = (232448 - static_cast<int>(sizeof(PrefixCtl)) - QB) / SLOT;
     static constexpr int ST = ST_FIT > kMaxSlots ? kMaxSlots : ST_FIT;
     static constexpr int OFF_Q = ST * SLOT, OFF_C = OFF_Q + QB, SMEM = OFF_C + static_cast<int>(sizeof(PrefixCtl));
-    static constexpr bool KEEP = HALVES == 1;                // a shared K/V tile stays for both products
+    // A shared K/V tile stays for both products where the ring then still holds five units. At 256 channels it would hold two
+    // and a half, and the next K waits for the product with V (45 tokens of 16 heads over 12,345 rows 44.5 us, loaded twice 42;
+    // 64 tokens over 32,768 67.6 and 63.5; 16 chunks of 128 over 8,192 369 and 379).
+    static constexpr bool KEEP = D == 128;
     static constexpr int OCOL = 256;                         // scores: columns 0 and 128; P over their first 64
     static_assert(ST == (D == 512 ? 3 : 5), "slots");
     static_assert(SMEM <= 232448 && (!KEEP || ST > 2 * KS) && OCOL + TILES * DV <= 512, "fits");
