@@ -20,7 +20,7 @@
 // with the scores over all channels and the product with half of V's (1.5 times the products' time).
 // What bounds it: at 128 channels the chain of a unit of two tiles, 3,030 cycles against 2,048 of products (issue, the scores'
 // arrival 370, the softmax 1,128, P's arrival 450); at 512 shared memory, which gives 128 bytes a cycle: 4,096 cycles of a unit's 4,550 (Q
-// and K for the scores 2,048, V 512, the copies 1,536; products 3,072); with short own rows the segments' starts. Measured, merge included: 16 chunks
+// and K for the scores 2,048, V 512, the copies 1,536; products 3,070); with short own rows the segments' starts. Measured, merge included: 16 chunks
 // of up to 256 tokens behind 32,768 shared rows, 32 heads over 8 of 128, K and V apart, 583 us (1,310 TFLOP/s, tensor pipe 62 %
 // active); 64 single tokens behind them 74; 48 tokens behind 65,536 rows, 16 heads of 512, one row as K and V, 155 (48 %
 // active); 45 tokens in three groups behind 12,345 rows, 16 heads over 2 of 256, 42; 2 tokens behind 1,000, 8 heads, 13.7.
