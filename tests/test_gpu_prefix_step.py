@@ -120,3 +120,33 @@ def test_many_queries_beside_one_that_is_cut_into_many_parts(H, KV, D, shared, b
     cu = cu_of([1] * batch)
     out, lse = attend(c, q, cu, sink=sink)
     ref.check_attention(out, lse, ref.attention(q, c.k, c.v, c.table, cu, lens, D ** -0.5, sink=sink))
+
+
+def test_pages_past_32_bit_offsets():
+    """A pool of 2^31 elements and more, of which the last pages are appended to and read."""
+    m = lib()
+    g = gen(9)
+    H, D, page, pool, pre, own = 16, 512, 64, 66000, 130, 70
+    kp = torch.empty(pool, page, 1, D, dtype=torch.bfloat16, device="cuda")
+    assert kp.numel() > 2 ** 31
+    ids = list(range(pool - 1, pool - 9, -1))
+    table = i32([[ids[0], ids[1], ids[2], ids[3]], [ids[0], ids[1], ids[4], ids[5]]])
+    lens = [pre + own, pre + own - 9]
+    slots, x = [], []
+    shared = normal(g, pre, 1, D)
+    for s in range(2):                       # both append the prefix's rows where their pages are their own
+        first = 0 if s == 0 else 128
+        slots += [int(table[s, r // page]) * page + r % page for r in range(first, lens[s])]
+        x += [shared[first:], normal(g, lens[s] - pre, 1, D)]
+    x, T = torch.cat(x), len(slots)
+    pos = torch.zeros(T, dtype=torch.int64, device="cuda")
+    m.dsv4_rope(m.rope_args(None, None, pos, k=x, k_out=kp, slots=torch.tensor(slots, device="cuda"), rope_dim=64))
+    at = torch.tensor(slots, device="cuda")
+    assert torch.equal(kp[at // page, at % page], x)          # (at position 0 nothing turns)
+    q = normal(g, 2, H, D, std=2.0)
+    out, lse = torch.empty_like(q), torch.empty(2, H, device="cuda")
+    a = m.paged_prefix_args(q, out, kp, table, i32([0, 1, 2]), i32(lens), i32([pre]), lse=lse)
+    ws = torch.empty(m.dsv4_paged_prefix_attn_workspace_size(a), dtype=torch.uint8, device="cuda")
+    m.dsv4_paged_prefix_attn(a, ws)
+    assert m.dsv4_read_error_word(ws) == (0, 0)
+    ref.check_attention(out, lse, ref.attention(q, kp, None, table, [0, 1, 2], lens, D ** -0.5))
