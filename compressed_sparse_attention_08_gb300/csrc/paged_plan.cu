@@ -7,7 +7,7 @@
 // pages held, the stack's height; in place too: it has read them all by then). What is left are three flat lists,
 // tokens, pages given back and pages taken, whose entries find their sequence by bisection in the sums. A page
 // that is given back and taken again is read where it stands in its table, so the lists need no order among
-// them. With few tokens the same CTA goes through them; with many a second launch does, from the sums in the
+// them. Where they must be short the same CTA goes through them; else a second launch does, from the sums in the
 // workspace, on the whole device.
 // Latency bounds both: a launch, the lengths' loads, three sums, then a token's search, its sequence's numbers, its page and its
 // slot, one after the other. Measured: 16 sequences of one token 4.0 us, 2,000 sequences with 44,483 tokens 11.4.
@@ -18,6 +18,7 @@ namespace dsv4 {
 namespace {
 
 constexpr int kMaxBatch = 2048, kListT = 256;
+constexpr int kFewTokens = 256, kFewPages = 4096;    // up to these one launch (see launch_paged_plan)
 
 // What the lists need of a batch: sums (inclusive) and numbers per sequence.
 struct PlanSums {
@@ -273,16 +274,22 @@ size_t paged_plan_ws_bytes() { return sizeof(PlanSums); }
 
 int launch_paged_plan(const dsv4_paged_plan_args& a, uint8_t* ws, uint32_t* eword, cudaStream_t st) {
     PlanSums* q = reinterpret_cast<PlanSums*>(ws);
-    // One launch while a thread has a few tokens; a second one for more costs less than they do then.
-    const int lists = a.total_q <= 2048;
+    // One CTA goes through the lists in passes of its threads, 0.4 us each with tables in L2 and 0.7 without (a search, a table
+    // entry, a store); a second launch costs 1.2 us whatever they hold. 16 sequences (back to back, one launch and two): 16
+    // tokens 3.0 and 4.2 us, 256 4.3 and 4.5, 1,024 8.5 and 4.9. How many pages go back and forth only the device knows: as many
+    // as the tables and the stack have room for, as when all requests end at once. One request of 8,192 pages took 53 us in one
+    // CTA, 128 of them 6.9 ms; in two launches 10 and 16. So one launch is for what is short at its most (4,096 pages: 22 us).
+    const long long tables = static_cast<long long>(a.batch) * a.max_pages, pages = tables < a.free_cap ? tables : a.free_cap;
+    const int lists = a.total_q <= kFewTokens && pages <= kFewPages;
     count_launch();
     const cudaError_t e = a.batch <= 128 ? launch_k(plan_kernel<128, 1>, dim3(1), dim3(128), 0, st, true, a, q, lists, eword)
                                          : launch_k(plan_kernel<1024, 2>, dim3(1), dim3(1024), 0, st, true, a, q, lists, eword);
     if (e != cudaSuccess) return DSV4_ERR_LAUNCH;
     if (lists) return DSV4_OK;
-    const int sms = sm_count() > 0 ? sm_count() : 152, most = 4 * sms, need = (a.total_q + kListT - 1) / kListT + 32;
+    const int sms = sm_count() > 0 ? sm_count() : 152, most = 4 * sms;
+    const long long need = (a.total_q + pages + kListT - 1) / kListT;
     count_launch();
-    return launch_k(plan_lists_kernel, dim3(need < most ? need : most), dim3(kListT), 0, st, true, a, q, eword) == cudaSuccess
+    return launch_k(plan_lists_kernel, dim3(need < most ? static_cast<unsigned>(need) : most), dim3(kListT), 0, st, true, a, q, eword) == cudaSuccess
                ? DSV4_OK : DSV4_ERR_LAUNCH;
 }
 
