@@ -96,16 +96,20 @@ __device__ uint32_t plan_lists(const dsv4_paged_plan_args& p, const PlanSums& q,
         const int x = q.stack - 1 - k;
         return x < q.count ? p.free_pages[x] : given_page(x - q.count);
     };
+    auto known = [&](int page) { return page >= 0 && page < p.num_pages; };
     const int tokens = B > 0 ? tok[B - 1] : 0, n_back = q.n_back, taken = q.taken;
     const long long all = static_cast<long long>(p.total_q) + taken + n_back;   // (one behind the other, so that no thread has all three)
     for (long long at = self; at < all; at += step) {
         if (at >= p.total_q) {
             const int k = static_cast<int>(at - p.total_q), i = k - taken;
+            // (a page that is none moves as it stands, and is told of when it enters the stack, not only when a row meets it)
+            const int page = i >= 0 ? given_page(i) : taken_page(k);
+            if (!known(page)) err |= DSV4_EWORD_BAD_INDEX;
             if (i >= 0) {
-                p.free_pages[q.count + i] = given_page(i);
+                p.free_pages[q.count + i] = page;
             } else {
                 const int s = find(take, B, k);
-                p.block_table[s * mp + q.held[s] + (k - (s ? take[s - 1] : 0))] = taken_page(k);
+                p.block_table[s * mp + q.held[s] + (k - (s ? take[s - 1] : 0))] = page;
             }
             continue;
         }
@@ -119,7 +123,7 @@ __device__ uint32_t plan_lists(const dsv4_paged_plan_args& p, const PlanSums& q,
             if (!(q.off[s >> 5] >> (s & 31) & 1)) {
                 const int j = row / p.page_size;
                 const int page = j < held ? p.block_table[s * mp + j] : taken_page((s ? take[s - 1] : 0) + j - held);
-                if (page >= 0 && page < p.num_pages) slot = static_cast<long long>(page) * p.page_size + (row - j * p.page_size);
+                if (known(page)) slot = static_cast<long long>(page) * p.page_size + (row - j * p.page_size);
                 else err |= DSV4_EWORD_BAD_INDEX;
             }
         }

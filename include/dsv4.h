@@ -493,7 +493,9 @@ int dsv4_paged_evict(const dsv4_paged_evict_args* args, void* ws, size_t ws_byte
  * slot -1, position 0 and seq -1, up to total_q. cu_q and kv_len_out are what dsv4_paged_attn takes.
  * The *_out arrays may be the arrays they follow. Negative lengths and counts out of their arrays
  * are clamped, a sequence whose tokens or pages do not fit total_q or max_pages is not served, a page
- * number outside the pool gives slot -1; these set DSV4_EWORD_BAD_INDEX. batch: 0..2048. */
+ * number outside the pool gives slot -1 and is given back or taken as it stands, pages given back that
+ * do not fit free_cap are not pushed (held_out counts them no more: they are left in the table alone, from
+ * entry held_out[s] on); these set DSV4_EWORD_BAD_INDEX. batch: 0..2048. */
 typedef struct dsv4_paged_plan_args {
     const int32_t* new_len;   /* int32 [batch] tokens of this step, or NULL: 0 (pages are only given back) */
     const int32_t* kv_len;    /* int32 [batch] rows before the step                           */

@@ -94,3 +94,43 @@ def test_both_forms_at_their_border(B, total, cap):
     p.call()
     want, err = p.check()
     assert err == 0 and want["count"] > 90
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("what", ["returned", "returned_high", "taken", "passed_on"])
+def test_a_page_outside_the_pool_is_flagged_when_it_moves(what, wide):
+    """When it goes to the stack or comes from it, also where no row of the step lies on it; everything else is as if it were
+    a page."""
+    page, width = 16, 5000 if wide else 6
+    new, kv, held = [0, 0, 1], [0, 20, 16], [3, 2, 1]
+    table = [[1, 2, 3], [4, 5], [6]]
+    free, count = [7, 8, 9], 3
+    if what == "returned":
+        table[0][1] = -1
+    if what == "returned_high":
+        table[0][2] = 4200
+    if what == "taken":                                               # for rows that were there before: no new token on it
+        new, kv, held, free[2] = [0, 0, 0], [40, 20, 17], [3, 2, 1], -3
+    if what == "passed_on":                                           # from an ended request straight to another's old rows
+        new, kv, held, count = [0, 0, 0], [0, 20, 17], [1, 2, 1], 0
+        table[0][0] = 4200
+    table = [row + [-9] * (width - len(row)) for row in table]
+    free = free[:count] + [-5] * ((4200 if wide else 12) - count)
+    p = Plan(new, kv, held, None, None, table, free, count, page=page, pool=4200, total=4)
+    p.call()
+    assert lib().dsv4_last_launch_count() == (2 if wide else 1)
+    want, err = ref.plan(*p.lists, **p.kw)
+    # (the plain form looks at the rows' pages alone: the page of the one new row is the last that was given back)
+    assert err == (ref.BAD_INDEX if what == "returned_high" else 0)
+    assert lib().dsv4_read_error_word(p.ws)[1] == ref.BAD_INDEX
+    for k, t in dict(cu_q=p.cu, slots=p.slots, table=p.table, free=p.free, kv_len=p.kv_out, held=p.held_out).items():
+        assert t.tolist() == want[k], k
+    assert p.count_out.tolist() == [want["count"]]
+
+
+def test_pages_that_do_not_fit_the_stack_stay_in_the_table():
+    p = Plan([0, 0], [5, 0], [4, 3], None, None, [[1, 2, 3, 4], [5, 6, 7, -9]], [8, 9, -5, -5], 2, page=16, pool=10, total=0)
+    p.call()
+    want, err = p.check()
+    assert err == ref.BAD_INDEX and want["free"] == [8, 9, 2, 3] and want["held"] == [1, 0]
+    assert p.table.tolist() == [[1, 2, 3, 4], [5, 6, 7, -9]]
