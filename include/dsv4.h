@@ -600,7 +600,9 @@ typedef struct dsv4_paged_prefix_args {
     double out_rope_theta;
 } dsv4_paged_prefix_args;
 
-/* The workspace holds fp32 partial outputs: 2 * total_q * heads * (dim + 8) numbers at most, and one tile per SM. */
+/* The workspace holds fp32 partial results: 2 * total_q * heads * (dim + 8) numbers at most; for each SM (160 where their
+ * number is not known) a tile of 128 queries x (min(dim, 256) + 2) numbers, two at dim 128; and an int per group and SM. The
+ * size does not depend on the lengths. */
 size_t dsv4_paged_prefix_attn_workspace_size(const dsv4_paged_prefix_args* args);
 int dsv4_paged_prefix_attn(const dsv4_paged_prefix_args* args, void* ws, size_t ws_bytes, dsv4_stream_t stream);
 
