@@ -28,7 +28,6 @@
 // warps 4-11 do the softmax, write the parts and, once a segment's last scores have come, ask for the next one's queries.
 #include <cfloat>
 #include <cmath>
-#include <type_traits>
 
 #include "internal.h"
 #include "paged.cuh"
@@ -57,9 +56,6 @@ struct PrefixGeom {
     const int32_t* group_start;          // [groups + 1] or null: one group of all
     int groups, tiles, halves;           // tiles of queries per segment, passes over V's channels
 };
-
-template <int N>
-using Int = std::integral_constant<int, N>;
 
 // The geometry with the prefix lengths as they are used (by this CTA: each forms its own copy). While the schedule is made,
 // lengths, groups and sequences lie in shared memory; afterwards they are read again where they are needed.
