@@ -10,7 +10,7 @@
 // them. Where they must be short the same CTA goes through them; else a second launch does, from the sums in the
 // workspace, on the whole device.
 // Latency bounds both: a launch, the lengths' loads, three sums, then a token's search, its sequence's numbers, its page and its
-// slot, one after the other. Measured: 16 sequences of one token 4.0 us, 2,000 sequences with 44,483 tokens 11.4.
+// slot, one after the other. Measured: 16 sequences of one token 3.9 us, 2,000 sequences with 44,483 tokens 11.3.
 #include "internal.h"
 #include "common.cuh"
 
@@ -282,7 +282,7 @@ int launch_paged_plan(const dsv4_paged_plan_args& a, uint8_t* ws, uint32_t* ewor
     // entry, a store); a second launch costs 1.2 us whatever they hold. 16 sequences (back to back, one launch and two): 16
     // tokens 3.0 and 4.2 us, 256 4.3 and 4.5, 1,024 8.5 and 4.9. How many pages go back and forth only the device knows: as many
     // as the tables and the stack have room for, as when all requests end at once. One request of 8,192 pages took 53 us in one
-    // CTA, 128 of them 6.9 ms; in two launches 10 and 16. So one launch is for what is short at its most (4,096 pages: 22 us).
+    // CTA, 128 of them 6.9 ms; in two launches 10 and 22. So one launch is for what is short at its most (4,096 pages: 22 us).
     const long long tables = static_cast<long long>(a.batch) * a.max_pages, pages = tables < a.free_cap ? tables : a.free_cap;
     const int lists = a.total_q <= kFewTokens && pages <= kFewPages;
     count_launch();
@@ -290,7 +290,8 @@ int launch_paged_plan(const dsv4_paged_plan_args& a, uint8_t* ws, uint32_t* ewor
                                          : launch_k(plan_kernel<1024, 2>, dim3(1), dim3(1024), 0, st, true, a, q, lists, eword);
     if (e != cudaSuccess) return DSV4_ERR_LAUNCH;
     if (lists) return DSV4_OK;
-    const int sms = sm_count() > 0 ? sm_count() : 152, most = 4 * sms;
+    // (each CTA copies the sums first: 2,000 sequences of 44,483 tokens warm 11.1 us with four CTAs per SM, 10.5 with two, 10.8 with one)
+    const int sms = sm_count() > 0 ? sm_count() : 152, most = 2 * sms;
     const long long need = (a.total_q + pages + kListT - 1) / kListT;
     count_launch();
     return launch_k(plan_lists_kernel, dim3(need < most ? static_cast<unsigned>(need) : most), dim3(kListT), 0, st, true, a, q, eword) == cudaSuccess
