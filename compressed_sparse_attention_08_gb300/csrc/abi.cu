@@ -3,6 +3,7 @@
 // No entry point allocates, frees, synchronises or reads device memory on the host,
 // except dsv4_read_error_word, which exists for tests and diagnostics.
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -272,7 +273,7 @@ bool rope_ok(const dsv4_rope_args* a) {
     if (a->rope_dim < 2 || a->rope_dim > a->dim || a->rope_dim > 512 || (a->rope_dim & 1)) return false;
     if (a->layout < 0 || a->layout > 1 || a->inverse < 0 || a->inverse > 1) return false;
     if (a->first < 0 || a->first > a->dim - a->rope_dim || (a->layout == 0 && (a->first & 1))) return false;
-    if (!std::isfinite(a->rope_theta) || a->rope_theta <= 0.0 || !std::isfinite(a->magnitude)) return false;
+    if (!std::isfinite(a->rope_theta) || a->rope_theta <= 0.0 || !(std::fabs(a->magnitude) <= FLT_MAX)) return false;
     if (a->scaling < DSV4_ROPE_PLAIN || a->scaling > DSV4_ROPE_BY_INDEX) return false;
     if (a->scaling != DSV4_ROPE_PLAIN && !(a->factor > 0.0 && std::isfinite(a->factor))) return false;
     if (a->scaling >= DSV4_ROPE_BY_TURNS &&

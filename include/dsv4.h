@@ -562,7 +562,7 @@ typedef struct dsv4_rope_args {
     int layout, inverse;
     int scaling;              /* DSV4_ROPE_*                                                  */
     double rope_theta, factor, original_len, beta_fast, beta_slow;
-    double magnitude;         /* 1 without                                                    */
+    double magnitude;         /* 1 without; within fp32's range                               */
 } dsv4_rope_args;
 
 int dsv4_rope(const dsv4_rope_args* args, dsv4_stream_t stream);
