@@ -20,10 +20,11 @@
 // with the scores over all channels and the product with half of V's (1.5 times the products' time).
 // What bounds it: at 128 channels the chain of a unit of two tiles, 3,030 cycles against 2,048 of products (issue, the scores'
 // arrival 370, the softmax 1,128, P's arrival 450); at 512 shared memory, which gives 128 bytes a cycle: 4,096 cycles of a unit's 4,550 (Q
-// and K for the scores 2,048, V 512, the copies 1,536; products 3,070); with short own rows the segments' starts. Measured, merge included: 16 chunks
-// of up to 256 tokens behind 32,768 shared rows, 32 heads over 8 of 128, K and V apart, 583 us (1,310 TFLOP/s, tensor pipe 62 %
-// active); 64 single tokens behind them 74; 48 tokens behind 65,536 rows, 16 heads of 512, one row as K and V, 155 (48 %
-// active); 45 tokens in three groups behind 12,345 rows, 16 heads over 2 of 256, 42; 2 tokens behind 1,000, 8 heads, 13.7.
+// and K for the scores 2,048, V 512, the copies 1,536; products 3,070); with short own rows the segments' starts and ends; in
+// small calls, cold (L2 flushed), the schedule's loads (10,000 cycles) and those until the first scores (14,000). Measured, merge included: 16
+// chunks of up to 256 tokens behind 32,768 shared rows, 32 heads over 8 of 128, K and V apart, 583 us (1,310 TFLOP/s, tensor pipe 62 %
+// active); 64 single tokens behind them 73; 48 tokens behind 65,536 rows, 16 heads of 512, one row as K and V, 153 (48 %
+// active); 45 tokens in three groups behind 12,345 rows, 16 heads over 2 of 256, 42; 2 tokens behind 1,000, 8 heads, 14.3.
 // Roles: warps 0, 2 and 3 move pages by TMA into a ring of slots of 128 rows x 128 channels, warp 1 issues tcgen05.mma,
 // warps 4-11 do the softmax, write the parts and, once a segment's last scores have come, ask for the next one's queries.
 #include <cfloat>
@@ -121,6 +122,9 @@ __device__ __forceinline__ int segment_units(const PrefixGeom& g, const PrefixSe
 // The line counts time, in 600 cycles or so: a unit of two tiles takes 5, of one tile 3 (at 256 and 512 channels all
 // have one, and take longer: only ratios count), a segment's start and end 25 and 11 (4 of longer units).
 // Measured at 16 sequences of 256 tokens of 32 heads behind 32,768 shared rows: 590 us; with 21, 11 and 6 596, with 30 657, with 18 and 9 640.
+// On 20 other batches at 128 channels (2 to 63 sequences of 1 to 168 tokens in 1 to 4 groups) 17 to 30 in the first place and 8 to 14
+// in the second come to the same within 1 % on average (single ones within 7 %): what they decide is how a batch falls on the
+// CTAs. On 20 at 256 and 512, with 2 in place of 4 3 to 5 % slower, with 3 0 to 2 %, with 6 and 8 1 to 2 % faster.
 __device__ __forceinline__ bool two_tiles(const PrefixLine& l, const PrefixSeq& q, int tt) {
     return l.g.tiles == 2 && q.n - tt * paged_tokens(l) > l.g.p.tpt;
 }

@@ -15,8 +15,8 @@
 // Waite reduced), while the first rows are already on their way.
 // What matters is how many such CTAs an SM holds (each waits for a position, then for its loads and angles): 128
 // threads held to 72 registers where a column is two vectors and to 48 where it is one. Measured: 2,039 tokens of 64 + 8 + 8
-// heads x 128 with the append 17.2 us, 4.8 TB/s (with 256 threads 19.2); 1,023 tokens of 64 + 1 x 512, 64 channels
-// turning, 28.2 us, 4.8 TB/s; 8,192 tokens of 32 + 8 x 128 in fp32 60.8 us, 5.5 TB/s of 6.8; 16 tokens 4.1 us. CTAs that walk
+// heads x 128 with the append 17.0 us, 4.9 TB/s (with 256 threads 19.2); 1,023 tokens of 64 + 1 x 512, 64 channels
+// turning, 27.8 us, 4.9 TB/s; 8,192 tokens of 32 + 8 x 128 in fp32 59.9 us, 5.6 TB/s of 6.8; 16 tokens 4.3 us. CTAs that walk
 // the tokens with the next one's loads in registers were slower (23, 37 and 83 us): fewer fit, and a barrier a token
 // ties their threads together.
 #include <cmath>
